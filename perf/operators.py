@@ -334,8 +334,8 @@ def _prepare_attention(c, seed):
         s["partition"], s["workspace"] = c["partition"], None
         most = min(s["max_ctx"], -(-c["sinks"] // 16) * 16 + -(-c["window"] // 16) * 16 + 16)
         parts = -(-most // c["partition"]) if c["partition"] else 1
-        if parts > 1:  # arrival counters, then (m, l, o) of every partition
-            size = (1 << 20) + 4 * c["seqs"] * H * parts * (D + 2) + 1024
+        if parts > 1:  # arrival counters, (m, l, o) of every partition, lengths
+            size = (1 << 20) + 4 * c["seqs"] * (H * parts * (D + 2) + 1) + 2048
             s["workspace"] = torch.zeros(size, dtype=torch.uint8, device=_dev())
     return s
 
