@@ -77,6 +77,10 @@ typedef enum {
 #define PA_DEVERR_TIMEOUT       0x20 /* a bounded wait on staged data gave up */
 #define PA_DEVERR_PREFIX_PLAN   0x40 /* prefix plan inconsistent with the tables or contexts */
 #define PA_DEVERR_QUERY_RANGE   0x80 /* FP8 pools: a bf16 query element beyond the fp16 range */
+#define PA_DEVERR_OUT_OF_BLOCKS 0x100 /* step maps: more new blocks than free ones */
+
+/* query_lens value of a sequence that has finished (pa_build_step_maps). */
+#define PA_STEP_FINISHED (-1)
 
 /*
  * pa_slot_mapping -- [GAO] §1.5.  For every token t, writes
@@ -159,6 +163,109 @@ PA_API pa_status pa_slot_mapping_and_cache_fp8(int32_t *slot_mapping,
                                                pa_dtype src_dtype, float k_scale,
                                                float v_scale, int32_t *error_word,
                                                void *stream);
+
+/*
+ * pa_build_step_maps -- the index arrays of one serving step, built on the
+ * device from each sequence's length and number of new tokens, so that a step
+ * needs no block table or slot from the host ([GAO] §1.4 and §1.5, [FEI]
+ * "Block Table 实现": a block is allocated when a token needs it).  With
+ * c = context_lens[s] tokens cached and n = query_lens[s] new ones, and
+ * b = block_size:
+ *   n == PA_STEP_FINISHED : the sequence ends; its ceil(c / b) blocks go back
+ *                           to the free stack, its length becomes 0
+ *   n >= 0                : it takes ceil((c + n) / b) - ceil(c / b) blocks,
+ *                           stored in the next entries of its table row; its
+ *                           length becomes c + n
+ *   block_tables   : int32 [num_seqs][max_blocks_per_seq] (in and out)
+ *   free_blocks    : int32 [num_blocks] (in and out), a stack of free blocks,
+ *                    the top at entry *free_count - 1.  Blocks of finished
+ *                    sequences are pushed first (batch order, a sequence's
+ *                    blocks in logical order), then new blocks are popped in
+ *                    the same order, so the result does not depend on timing.
+ *                    Entries below *free_count and from the pushed ones on are
+ *                    left as they were.
+ *   free_count     : int32 [1]; free_count_out: int32 [1] (may be the same)
+ *   context_lens   : int32 [num_seqs]; context_lens_out: int32 [num_seqs] (may
+ *                    be the same array: a captured graph of the call then
+ *                    steps its own state)
+ *   query_lens     : int32 [num_seqs]
+ *   query_start    : int32 [num_seqs + 1] (output), as pa_prefill_attention
+ *                    takes it
+ *   token_seq, token_pos, slot_mapping : int32 [num_tokens] (outputs) of the
+ *                    new tokens in batch order, as pa_slot_mapping computes
+ *                    them; num_tokens is their capacity, and entries past the
+ *                    step's tokens get -1 (which the cache writes skip).
+ * A table entry or a stack entry outside [0, num_blocks) sets
+ * PA_DEVERR_BLOCK_RANGE; its tokens get slot -1 (a popped one is stored as -1).
+ * The step is refused as a whole, with the lengths, tables and stack as they
+ * were, query_start all 0 and the token arrays all -1, when a length is
+ * negative or c + n passes max_blocks_per_seq * b (PA_DEVERR_CONTEXT_RANGE),
+ * the new tokens pass num_tokens (PA_DEVERR_TOKEN_RANGE), the stack would pass
+ * num_blocks or its count is negative (PA_DEVERR_BLOCK_RANGE), or it holds too
+ * few blocks (PA_DEVERR_OUT_OF_BLOCKS).  Blocks are taken to have one owner
+ * (shared prefixes are the host block manager's).  No other arrays may
+ * overlap.  num_tokens <= 2^30.
+ */
+PA_API pa_status pa_build_step_maps(int32_t *query_start, int32_t *token_seq,
+                                    int32_t *token_pos, int32_t *slot_mapping,
+                                    int32_t *context_lens_out, int32_t *free_count_out,
+                                    int32_t *block_tables, int max_blocks_per_seq,
+                                    const int32_t *context_lens, const int32_t *query_lens,
+                                    int32_t *free_blocks, const int32_t *free_count,
+                                    int num_seqs, int num_tokens, int block_size,
+                                    int num_blocks, int32_t *error_word, void *stream);
+
+/*
+ * pa_rope_and_cache, pa_rope_and_cache_fp8 -- rotary positions of the new
+ * tokens' queries and keys, fused with pa_reshape_and_cache(_fp8) ([GAO] §1.5;
+ * the pages say nothing of positions, the engine's model applies them just
+ * before the cache write).  For token t and pair i of rot_dim / 2
+ *     phi = positions[axis_of_pair[i]][t] * inv_freq[i]
+ *     (u, v) -> (u cos phi - v sin phi, v cos phi + u sin phi)
+ * on elements (i, i + rot_dim / 2) of every query and key head, or (2i, 2i + 1)
+ * when interleaved; elements from rot_dim on pass through.  Computed in fp32
+ * and rounded once: the query to dtype, keys to dtype (16-bit pools) or to the
+ * code e4m3(x * (1 / k_scale)) (FP8 pools); values as pa_reshape_and_cache(_fp8)
+ * writes them.  The angle is right to 2e-6 for turns phi / 2 pi below 2^21 and
+ * to 1e-4 at any int32 position with inv_freq <= 1.
+ *   query, key, value : dtype, [num_tokens] rows of [num_heads or
+ *                       num_kv_heads][head_dim], *_stride elements from token
+ *                       to token (a multiple of 8, at most 2^28): the parts of
+ *                       a fused QKV row as they are
+ *   query_out         : rows like query's; query itself with its stride (in
+ *                       place), or rows that share no byte with query, key and
+ *                       value (PA_ERR_INVALID_ARG)
+ *   positions         : int32 [num_axes][num_tokens] (device): one axis for
+ *                       text, three (time, height, width) for images and video
+ *   axis_of_pair      : int32 [rot_dim / 2] (HOST; read before the call
+ *                       returns), each pair's axis, in [0, num_axes); NULL: axis 0
+ *   inv_freq          : float [rot_dim / 2] (device), radians per position
+ *   slot_mapping      : int32 [num_tokens]; slot < 0: the token's key and value
+ *                       are not written (its query is rotated all the same);
+ *                       slot >= num_blocks * block_size likewise, and sets
+ *                       PA_DEVERR_SLOT_RANGE.  Two tokens with one slot race.
+ * Supported: head_dim and rot_dim multiples of 16, rot_dim <= head_dim <= 256;
+ * num_axes <= 255; num_blocks * block_size < 2^31.  Addresses 16-byte aligned.
+ */
+PA_API pa_status pa_rope_and_cache(void *query_out, int64_t query_out_stride, const void *query,
+                                   int64_t query_stride, const void *key, int64_t key_stride,
+                                   const void *value, int64_t value_stride, void *key_cache,
+                                   void *value_cache, const int32_t *slot_mapping,
+                                   const int32_t *positions, int num_axes,
+                                   const int32_t *axis_of_pair, const float *inv_freq,
+                                   int rot_dim, int interleaved, int num_tokens, int num_heads,
+                                   int num_kv_heads, int head_dim, int block_size,
+                                   int num_blocks, pa_dtype dtype, int32_t *error_word,
+                                   void *stream);
+
+PA_API pa_status pa_rope_and_cache_fp8(
+    void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+    const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+    void *key_cache, void *value_cache, const int32_t *slot_mapping, const int32_t *positions,
+    int num_axes, const int32_t *axis_of_pair, const float *inv_freq, int rot_dim,
+    int interleaved, int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, pa_dtype dtype, float k_scale, float v_scale,
+    int32_t *error_word, void *stream);
 
 /*
  * pa_copy_blocks -- the "copy the contents" step of copy-on-write
@@ -364,6 +471,74 @@ PA_API pa_status pa_prefill_attention_fp8(void *out, const void *query, const vo
                                           int num_blocks, float scale, float k_scale,
                                           float v_scale, pa_dtype dtype, int32_t *error_word,
                                           void *stream);
+
+/*
+ * pa_decode_attention_window, pa_decode_attention_window_fp8 -- paged decode
+ * with a sliding window and a few first tokens that stay visible (no
+ * counterpart on the pages, which attend the whole context): as
+ * pa_decode_attention(_fp8), over the visible positions only.  The query of
+ * sequence s sits at position context_lens[s] - 1 and sees
+ *     p in [0, context_lens[s])  with  p >= context_lens[s] - window
+ *                                or    p < num_sinks
+ * (the window counts the query's own token; window >= the context: plain
+ * decode).  Blocks that hold no visible token are not read and their table
+ * entries are not looked at, so an engine may free them as the window moves
+ * on; what hidden positions of a visible block hold has no influence.
+ *   window         : >= 1;  num_sinks : >= 0 (PA_ERR_INVALID_ARG otherwise)
+ *   partition_size : as pa_decode_attention, in visible tokens rounded to
+ *                    16-token tiles, so the number of partitions is bounded
+ *                    by window and num_sinks, not by the context
+ *   workspace      : >= pa_window_workspace_bytes(...) bytes, 256-byte
+ *                    aligned, its first bytes (the arrival counters of
+ *                    pa_decode_workspace_bytes, the same region) zeroed
+ *                    before first use; may be NULL when that size is 0
+ * Other arguments, limits and errors as pa_decode_attention(_fp8).
+ */
+PA_API size_t pa_window_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                        int head_dim, int max_context_len, int window,
+                                        int num_sinks, int partition_size);
+
+PA_API pa_status pa_decode_attention_window(
+    void *out, const void *query, const void *key_cache, const void *value_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int max_context_len, int window, int num_sinks, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    int partition_size, void *workspace, size_t workspace_bytes, pa_dtype dtype,
+    int32_t *error_word, void *stream);
+
+PA_API pa_status pa_decode_attention_window_fp8(
+    void *out, const void *query, const void *key_cache, const void *value_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int max_context_len, int window, int num_sinks, int num_seqs, int num_heads,
+    int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale, float k_scale,
+    float v_scale, int partition_size, void *workspace, size_t workspace_bytes, pa_dtype dtype,
+    int32_t *error_word, void *stream);
+
+/*
+ * pa_prefill_attention_window, pa_prefill_attention_window_fp8 -- chunked
+ * prefill and mixed batches with the same window: as pa_prefill_attention(_fp8),
+ * where the chunk row at position pos sees
+ *     p in [0, pos]  with  p > pos - window  or  p < num_sinks.
+ * A row at a negative position gets a zero row; rows of out past
+ * query_start[num_seqs] are left as they were.  query_start entries outside
+ * [0, num_tokens] are clipped and flagged PA_DEVERR_TOKEN_RANGE.
+ * num_tokens * num_heads < 2^31 - 128.  Other arguments, limits and errors as
+ * pa_prefill_attention(_fp8) (scale positive).  No workspace.
+ */
+PA_API pa_status pa_prefill_attention_window(
+    void *out, const void *query, const void *key_cache, const void *value_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *query_start,
+    const int32_t *context_lens, int max_context_len, int window, int num_sinks, int num_seqs,
+    int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+    int num_blocks, float scale, pa_dtype dtype, int32_t *error_word, void *stream);
+
+PA_API pa_status pa_prefill_attention_window_fp8(
+    void *out, const void *query, const void *key_cache, const void *value_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *query_start,
+    const int32_t *context_lens, int max_context_len, int window, int num_sinks, int num_seqs,
+    int num_tokens, int num_heads, int num_kv_heads, int head_dim, int block_size,
+    int num_blocks, float scale, float k_scale, float v_scale, pa_dtype dtype,
+    int32_t *error_word, void *stream);
 
 /*
  * Prefix plan -- which sequences of a decode batch share leading physical

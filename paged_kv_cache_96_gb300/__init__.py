@@ -16,7 +16,8 @@ __all__ = [
     "pa_slot_mapping", "pa_reshape_and_cache", "pa_copy_blocks",
     "pa_decode_attention", "pa_decode_workspace_bytes", "PAError",
     "pa_reshape_and_cache_fp8", "pa_decode_attention_fp8", "pa_decode_attention_noalloc",
-    "library_path",
+    "pa_build_step_maps", "pa_rope_and_cache", "pa_decode_attention_window",
+    "pa_prefill_attention_window", "pa_window_workspace_bytes", "library_path",
 ]
 
 

@@ -31,6 +31,9 @@ DEVERR_TOKEN_RANGE = 0x10
 DEVERR_TIMEOUT = 0x20
 DEVERR_PREFIX_PLAN = 0x40
 DEVERR_QUERY_RANGE = 0x80
+DEVERR_OUT_OF_BLOCKS = 0x100
+
+STEP_FINISHED = -1  # query_lens value of a sequence that has finished
 
 
 class PAError(RuntimeError):
@@ -54,7 +57,15 @@ def _load() -> ctypes.CDLL:
             "`python -m paged_kv_cache_96_gb300.build` (no CPU fallback exists)")
     lib = ctypes.CDLL(_LIB_PATH)
     P, i32, f32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    i64 = ctypes.c_int64
     sigs = {
+        "pa_build_step_maps": (i32, [P, P, P, P, P, P, P, i32, P, P, P, P, i32, i32, i32, i32,
+                                     P, P]),
+        "pa_rope_and_cache": (i32, [P, i64, P, i64, P, i64, P, i64, P, P, P, P, i32, P, P, i32,
+                                    i32, i32, i32, i32, i32, i32, i32, i32, P, P]),
+        "pa_rope_and_cache_fp8": (i32, [P, i64, P, i64, P, i64, P, i64, P, P, P, P, i32, P, P,
+                                        i32, i32, i32, i32, i32, i32, i32, i32, i32, f32, f32,
+                                        P, P]),
         "pa_slot_mapping": (i32, [P, P, i32, P, P, i32, i32, i32, i32, P, P]),
         "pa_reshape_and_cache": (i32, [P, P, P, P, P, i32, i32, i32, i32, i32, i32, P, P]),
         "pa_copy_blocks": (i32, [P, P, P, i32, i32, i32, i32, i32, i32, P, P]),
@@ -80,6 +91,17 @@ def _load() -> ctypes.CDLL:
                                        i32, i32, i32, f32, i32, P, P]),
         "pa_prefill_attention_fp8": (i32, [P, P, P, P, P, i32, P, P, i32, i32, i32, i32,
                                            i32, i32, i32, i32, f32, f32, f32, i32, P, P]),
+        "pa_window_workspace_bytes": (sz, [i32] * 8),
+        "pa_decode_attention_window": (i32, [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32,
+                                             i32, i32, i32, i32, f32, i32, P, sz, i32, P, P]),
+        "pa_decode_attention_window_fp8": (i32, [P, P, P, P, P, i32, P, i32, i32, i32, i32, i32,
+                                                 i32, i32, i32, i32, f32, f32, f32, i32, P, sz,
+                                                 i32, P, P]),
+        "pa_prefill_attention_window": (i32, [P, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32,
+                                              i32, i32, i32, i32, i32, f32, i32, P, P]),
+        "pa_prefill_attention_window_fp8": (i32, [P, P, P, P, P, i32, P, P, i32, i32, i32, i32,
+                                                  i32, i32, i32, i32, i32, i32, f32, f32, f32,
+                                                  i32, P, P]),
         "pa_prefix_plan_ints": (sz, [i32, i32, i32]),
         "pa_plan_prefix_groups": (i32, [P, i32, P, i32, i32, i32, P, sz, P, P]),
         "pa_cascade_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
@@ -184,6 +206,114 @@ def _stream(stream) -> ctypes.c_void_p:
 def _check(fn: str, status: int) -> None:
     if status != PA_OK:
         raise PAError(fn, status)
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    """The tensors of one call live on one device, the current one (whose
+    stream the call is queued on)."""
+    dev = first.get_device()
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors of one call must be on one device")
+    if dev >= 0 and dev != torch.cuda.current_device():
+        raise ValueError(f"tensors are on device {dev}, which is not the current device")
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype):
+    """Pointer and token stride of [T, heads, d] whose token rows are dense
+    (a view into a wider row, as the parts of a fused QKV projection are)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: torch.Tensor expected")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
+    st, sh = t.stride(), t.shape
+    if (sh[2] > 1 and st[2] != 1) or (sh[1] > 1 and st[1] != sh[2]):
+        raise ValueError(f"{name}: heads and elements of a token must be dense")
+    return ctypes.c_void_p(t.data_ptr()), st[0] if sh[0] > 1 else sh[1] * sh[2]
+
+
+def pa_build_step_maps(block_tables: torch.Tensor, context_lens: torch.Tensor,
+                       query_lens: torch.Tensor, free_blocks: torch.Tensor,
+                       free_count: torch.Tensor, block_size: int, num_blocks: int,
+                       query_start: torch.Tensor, token_seq: torch.Tensor,
+                       token_pos: torch.Tensor, slot_mapping: torch.Tensor,
+                       context_lens_out: torch.Tensor, free_count_out: torch.Tensor,
+                       error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The index arrays of one step from the requests' lengths: block_tables
+    [S, MB] and the stack free_blocks [num_blocks] are extended in place,
+    query_start [S + 1] and the token arrays [T] (a capacity; -1 past the
+    step's tokens) are outputs.  query_lens: new tokens of each sequence, or
+    STEP_FINISHED.  context_lens_out / free_count_out may be the inputs."""
+    S, MB = block_tables.shape
+    T = token_seq.shape[0]
+    if (context_lens.shape[0] != S or query_lens.shape[0] != S or
+            context_lens_out.shape[0] != S or query_start.shape[0] != S + 1):
+        raise ValueError("one length per sequence and num_seqs + 1 offsets expected")
+    if token_pos.shape[0] != T or slot_mapping.shape[0] != T:
+        raise ValueError("token_seq, token_pos and slot_mapping must have one length")
+    if free_blocks.numel() < num_blocks or free_count.numel() < 1 or free_count_out.numel() < 1:
+        raise ValueError("a stack of num_blocks entries and its count expected")
+    _same_device(block_tables, context_lens, query_lens, free_blocks, free_count, query_start,
+                 token_seq, token_pos, slot_mapping, context_lens_out, free_count_out,
+                 error_word)
+    i32 = torch.int32
+    _check("pa_build_step_maps", _lib.pa_build_step_maps(
+        _dev(query_start, "query_start", i32), _dev(token_seq, "token_seq", i32),
+        _dev(token_pos, "token_pos", i32), _dev(slot_mapping, "slot_mapping", i32),
+        _dev(context_lens_out, "context_lens_out", i32),
+        _dev(free_count_out, "free_count_out", i32), _dev(block_tables, "block_tables", i32),
+        MB, _dev(context_lens, "context_lens", i32), _dev(query_lens, "query_lens", i32),
+        _dev(free_blocks, "free_blocks", i32), _dev(free_count, "free_count", i32), S, T,
+        block_size, num_blocks, _opt(error_word, "error_word"), _stream(stream)))
+
+
+def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
+                      value: torch.Tensor, key_cache: torch.Tensor, value_cache: torch.Tensor,
+                      slot_mapping: torch.Tensor, positions: torch.Tensor,
+                      inv_freq: torch.Tensor, axis_of_pair: Optional[torch.Tensor] = None,
+                      interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
+                      error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rotate query [T, H, d] (into query_out, which may be query) and key
+    [T, Hkv, d] by positions ([T], or [axes, T] with axis_of_pair, an int32
+    CPU tensor of one axis per rotary pair), and write key and value to the
+    pools at their slots (e4m3 codes with the scales when they are uint8).
+    query, key and value may be views into wider token rows.  inv_freq:
+    float32 [rot_dim / 2]."""
+    T, H, d = query.shape
+    N, bs, Hkv, d2 = key_cache.shape
+    if (d != d2 or query_out.shape != query.shape or key.shape != (T, Hkv, d) or
+            value.shape != key.shape or value_cache.shape != key_cache.shape):
+        raise ValueError("shape mismatch between new tokens and pools")
+    if slot_mapping.shape[0] != T or positions.shape[-1] != T or positions.dim() > 2:
+        raise ValueError("one slot and, per axis, one position per new token expected")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    half = inv_freq.shape[0]
+    axis_ptr = None
+    if axis_of_pair is not None:
+        if (axis_of_pair.dtype != torch.int32 or axis_of_pair.is_cuda or
+                axis_of_pair.shape != (half,) or not axis_of_pair.is_contiguous()):
+            raise ValueError("axis_of_pair: int32 CPU tensor, one axis per rotary pair")
+        axis_ptr = ctypes.c_void_p(axis_of_pair.data_ptr())
+    _same_device(query, query_out, key, value, key_cache, value_cache, slot_mapping, positions,
+                 inv_freq, error_word)
+    fp8 = key_cache.dtype == torch.uint8
+    dt = query.dtype
+    args = (*_rows(query_out, "query_out", dt), *_rows(query, "query", dt),
+            *_rows(key, "key", dt), *_rows(value, "value", dt),
+            _dev(key_cache, "key_cache", torch.uint8 if fp8 else dt),
+            _dev(value_cache, "value_cache", torch.uint8 if fp8 else dt),
+            _dev(slot_mapping, "slot_mapping", torch.int32),
+            _dev(positions, "positions", torch.int32), axes, axis_ptr,
+            _dev(inv_freq, "inv_freq", torch.float32), 2 * half, 1 if interleaved else 0, T, H,
+            Hkv, d, bs, N, _dtype_code(query))
+    tail = (_opt(error_word, "error_word"), _stream(stream))
+    if fp8:
+        _check("pa_rope_and_cache_fp8", _lib.pa_rope_and_cache_fp8(
+            *args, float(k_scale), float(v_scale), *tail))
+        return
+    _check("pa_rope_and_cache", _lib.pa_rope_and_cache(*args, *tail))
 
 
 def pa_slot_mapping(slot_mapping: torch.Tensor, block_tables: torch.Tensor,
@@ -461,6 +591,96 @@ def pa_prefill_attention(out: torch.Tensor, query: torch.Tensor, key_cache: torc
         return
     _check("pa_prefill_attention", _lib.pa_prefill_attention(
         *head, _dtype_code(key_cache), _opt(error_word, "error_word"), _stream(stream)))
+
+
+def _reach(n: int) -> int:
+    """A window or a number of first tokens as a C int: what passes the int32
+    range hides as little as its largest value, negative ones are refused."""
+    return max(-1, min(int(n), 0x7FFFFFFF))
+
+
+def pa_window_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                              max_context_len: int, window: int, num_sinks: int,
+                              partition_size: int) -> int:
+    return int(_lib.pa_window_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                              max_context_len, _reach(window),
+                                              _reach(num_sinks), partition_size))
+
+
+def pa_decode_attention_window(out: torch.Tensor, query: torch.Tensor,
+                               key_cache: torch.Tensor, value_cache: torch.Tensor,
+                               block_tables: torch.Tensor, context_lens: torch.Tensor,
+                               max_context_len: int, scale: float, window: int,
+                               num_sinks: int = 0, partition_size: int = 0,
+                               workspace: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+                               v_scale: float = 1.0,
+                               error_word: Optional[torch.Tensor] = None,
+                               stream=None) -> None:
+    """Paged decode over the last `window` tokens and the first num_sinks; out
+    and query are [S, H, d].  uint8 pools take the e4m3 path with k_scale /
+    v_scale."""
+    S, H, d = query.shape
+    N, bs, Hkv, d2 = key_cache.shape
+    if (d != d2 or out.shape != query.shape or value_cache.shape != key_cache.shape or
+            block_tables.shape[0] != S or context_lens.shape[0] != S):
+        raise ValueError("shape mismatch")
+    _same_device(query, out, key_cache, value_cache, block_tables, context_lens, workspace,
+                 error_word)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr = _dev(workspace, "workspace")
+        ws_bytes = workspace.numel() * workspace.element_size()
+    fp8 = key_cache.dtype == torch.uint8
+    pool = torch.uint8 if fp8 else query.dtype
+    i32 = torch.int32
+    head = (_dev(out, "out", query.dtype), _dev(query, "query"),
+            _dev(key_cache, "key_cache", pool), _dev(value_cache, "value_cache", pool),
+            _dev(block_tables, "block_tables", i32), block_tables.shape[1],
+            _dev(context_lens, "context_lens", i32), int(max_context_len),
+            _reach(window), _reach(num_sinks), S, H, Hkv, d, bs, N, float(scale))
+    tail = (int(partition_size), ws_ptr, ws_bytes, _dtype_code(query),
+            _opt(error_word, "error_word"), _stream(stream))
+    if fp8:
+        _check("pa_decode_attention_window_fp8", _lib.pa_decode_attention_window_fp8(
+            *head, float(k_scale), float(v_scale), *tail))
+        return
+    _check("pa_decode_attention_window", _lib.pa_decode_attention_window(*head, *tail))
+
+
+def pa_prefill_attention_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                                value_cache: torch.Tensor, block_tables: torch.Tensor,
+                                query_start: torch.Tensor, context_lens: torch.Tensor,
+                                max_context_len: int, scale: float, window: int,
+                                num_sinks: int = 0, k_scale: float = 1.0, v_scale: float = 1.0,
+                                error_word: Optional[torch.Tensor] = None,
+                                stream=None) -> None:
+    """Chunked prefill / mixed batch with a sliding window: out and query are
+    [T, H, d], sequence s owns rows [query_start[s], query_start[s + 1]), its
+    newest tokens; each row sees the last `window` tokens up to its own and the
+    first num_sinks.  uint8 pools take the e4m3 path with k_scale / v_scale."""
+    T, H, d = query.shape
+    N, bs, Hkv, d2 = key_cache.shape
+    S = context_lens.shape[0]
+    if (d != d2 or out.shape != query.shape or value_cache.shape != key_cache.shape or
+            query_start.shape[0] != S + 1 or block_tables.shape[0] != S):
+        raise ValueError("shape mismatch")
+    _same_device(query, out, key_cache, value_cache, block_tables, query_start, context_lens,
+                 error_word)
+    fp8 = key_cache.dtype == torch.uint8
+    pool = torch.uint8 if fp8 else query.dtype
+    i32 = torch.int32
+    head = (_dev(out, "out", query.dtype), _dev(query, "query"),
+            _dev(key_cache, "key_cache", pool), _dev(value_cache, "value_cache", pool),
+            _dev(block_tables, "block_tables", i32), block_tables.shape[1],
+            _dev(query_start, "query_start", i32), _dev(context_lens, "context_lens", i32),
+            int(max_context_len), _reach(window), _reach(num_sinks), S, T, H, Hkv, d, bs, N,
+            float(scale))
+    tail = (_dtype_code(query), _opt(error_word, "error_word"), _stream(stream))
+    if fp8:
+        _check("pa_prefill_attention_window_fp8", _lib.pa_prefill_attention_window_fp8(
+            *head, float(k_scale), float(v_scale), *tail))
+        return
+    _check("pa_prefill_attention_window", _lib.pa_prefill_attention_window(*head, *tail))
 
 
 def pa_plan_prefix_groups(block_tables, context_lens, block_size: int,
