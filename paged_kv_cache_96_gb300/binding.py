@@ -208,30 +208,70 @@ def _check(fn: str, status: int) -> None:
         raise PAError(fn, status)
 
 
-def _same_device(first: torch.Tensor, *others) -> None:
-    """The tensors of one call live on one device, the current one (whose
+# The wrappers below check a tensor and take its address in one step: type,
+# device and layout are three attribute reads on the way to the pointer, which
+# for a call of a dozen small tensors is most of what the host spends.
+
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _device(t: torch.Tensor, name: str) -> int:
+    """The device of a call's tensors, which has to be the current one (whose
     stream the call is queued on)."""
-    dev = first.get_device()
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("tensors of one call must be on one device")
-    if dev >= 0 and dev != torch.cuda.current_device():
-        raise ValueError(f"tensors are on device {dev}, which is not the current device")
-
-
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype):
-    """Pointer and token stride of [T, heads, d] whose token rows are dense
-    (a view into a wider row, as the parts of a fused QKV projection are)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: torch.Tensor expected")
     if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor")
-    if t.dtype != dtype:
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name}: on device {dev}, which is not the current device")
+    return dev
+
+
+def _at(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
+    """Address of a contiguous tensor of `dtype` on device `dev`."""
+    try:
+        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _dev(t, name, dtype)
+    raise ValueError(f"{name}: tensors of one call must be on one device")
+
+
+def _opt_at(t: Optional[torch.Tensor], name: str, dev: int) -> Optional[int]:
+    return None if t is None else _at(t, name, torch.int32, dev)
+
+
+def _space(t: Optional[torch.Tensor], dev: int):
+    """Address and bytes of a workspace of any type."""
+    if t is None:
+        return None, 0
+    return _at(t, "workspace", t.dtype, dev), t.numel() * t.element_size()
+
+
+def _queue(stream, dev: int) -> int:
+    if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("the stream is on another device than the tensors")
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int):
+    """Address and token stride of [T, heads, d] whose token rows are dense
+    (a view into a wider row, as the parts of a fused QKV projection are)."""
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
-    st, sh = t.stride(), t.shape
-    if (sh[2] > 1 and st[2] != 1) or (sh[1] > 1 and st[1] != sh[2]):
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: tensors of one call must be on one device")
+    a, b, c = t.stride()
+    n, h, d = t.shape
+    if (c != 1 and d > 1) or (b != d and h > 1):
         raise ValueError(f"{name}: heads and elements of a token must be dense")
-    return ctypes.c_void_p(t.data_ptr()), st[0] if sh[0] > 1 else sh[1] * sh[2]
+    return t.data_ptr(), a if n > 1 else h * d
 
 
 def pa_build_step_maps(block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -255,18 +295,16 @@ def pa_build_step_maps(block_tables: torch.Tensor, context_lens: torch.Tensor,
         raise ValueError("token_seq, token_pos and slot_mapping must have one length")
     if free_blocks.numel() < num_blocks or free_count.numel() < 1 or free_count_out.numel() < 1:
         raise ValueError("a stack of num_blocks entries and its count expected")
-    _same_device(block_tables, context_lens, query_lens, free_blocks, free_count, query_start,
-                 token_seq, token_pos, slot_mapping, context_lens_out, free_count_out,
-                 error_word)
-    i32 = torch.int32
+    dev, i32 = _device(block_tables, "block_tables"), torch.int32
     _check("pa_build_step_maps", _lib.pa_build_step_maps(
-        _dev(query_start, "query_start", i32), _dev(token_seq, "token_seq", i32),
-        _dev(token_pos, "token_pos", i32), _dev(slot_mapping, "slot_mapping", i32),
-        _dev(context_lens_out, "context_lens_out", i32),
-        _dev(free_count_out, "free_count_out", i32), _dev(block_tables, "block_tables", i32),
-        MB, _dev(context_lens, "context_lens", i32), _dev(query_lens, "query_lens", i32),
-        _dev(free_blocks, "free_blocks", i32), _dev(free_count, "free_count", i32), S, T,
-        block_size, num_blocks, _opt(error_word, "error_word"), _stream(stream)))
+        _at(query_start, "query_start", i32, dev), _at(token_seq, "token_seq", i32, dev),
+        _at(token_pos, "token_pos", i32, dev), _at(slot_mapping, "slot_mapping", i32, dev),
+        _at(context_lens_out, "context_lens_out", i32, dev),
+        _at(free_count_out, "free_count_out", i32, dev),
+        _at(block_tables, "block_tables", i32, dev), MB,
+        _at(context_lens, "context_lens", i32, dev), _at(query_lens, "query_lens", i32, dev),
+        _at(free_blocks, "free_blocks", i32, dev), _at(free_count, "free_count", i32, dev), S, T,
+        block_size, num_blocks, _opt_at(error_word, "error_word", dev), _queue(stream, dev)))
 
 
 def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -295,20 +333,18 @@ def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.T
         if (axis_of_pair.dtype != torch.int32 or axis_of_pair.is_cuda or
                 axis_of_pair.shape != (half,) or not axis_of_pair.is_contiguous()):
             raise ValueError("axis_of_pair: int32 CPU tensor, one axis per rotary pair")
-        axis_ptr = ctypes.c_void_p(axis_of_pair.data_ptr())
-    _same_device(query, query_out, key, value, key_cache, value_cache, slot_mapping, positions,
-                 inv_freq, error_word)
-    fp8 = key_cache.dtype == torch.uint8
-    dt = query.dtype
-    args = (*_rows(query_out, "query_out", dt), *_rows(query, "query", dt),
-            *_rows(key, "key", dt), *_rows(value, "value", dt),
-            _dev(key_cache, "key_cache", torch.uint8 if fp8 else dt),
-            _dev(value_cache, "value_cache", torch.uint8 if fp8 else dt),
-            _dev(slot_mapping, "slot_mapping", torch.int32),
-            _dev(positions, "positions", torch.int32), axes, axis_ptr,
-            _dev(inv_freq, "inv_freq", torch.float32), 2 * half, 1 if interleaved else 0, T, H,
-            Hkv, d, bs, N, _dtype_code(query))
-    tail = (_opt(error_word, "error_word"), _stream(stream))
+        axis_ptr = axis_of_pair.data_ptr()
+    dev = _device(query, "query")
+    dt, fp8 = query.dtype, key_cache.dtype is torch.uint8
+    pool = torch.uint8 if fp8 else dt
+    args = (*_rows(query_out, "query_out", dt, dev), *_rows(query, "query", dt, dev),
+            *_rows(key, "key", dt, dev), *_rows(value, "value", dt, dev),
+            _at(key_cache, "key_cache", pool, dev), _at(value_cache, "value_cache", pool, dev),
+            _at(slot_mapping, "slot_mapping", torch.int32, dev),
+            _at(positions, "positions", torch.int32, dev), axes, axis_ptr,
+            _at(inv_freq, "inv_freq", torch.float32, dev), 2 * half, 1 if interleaved else 0, T,
+            H, Hkv, d, bs, N, _dtype_code(query))
+    tail = (_opt_at(error_word, "error_word", dev), _queue(stream, dev))
     if fp8:
         _check("pa_rope_and_cache_fp8", _lib.pa_rope_and_cache_fp8(
             *args, float(k_scale), float(v_scale), *tail))
@@ -624,22 +660,16 @@ def pa_decode_attention_window(out: torch.Tensor, query: torch.Tensor,
     if (d != d2 or out.shape != query.shape or value_cache.shape != key_cache.shape or
             block_tables.shape[0] != S or context_lens.shape[0] != S):
         raise ValueError("shape mismatch")
-    _same_device(query, out, key_cache, value_cache, block_tables, context_lens, workspace,
-                 error_word)
-    ws_ptr, ws_bytes = None, 0
-    if workspace is not None:
-        ws_ptr = _dev(workspace, "workspace")
-        ws_bytes = workspace.numel() * workspace.element_size()
-    fp8 = key_cache.dtype == torch.uint8
-    pool = torch.uint8 if fp8 else query.dtype
-    i32 = torch.int32
-    head = (_dev(out, "out", query.dtype), _dev(query, "query"),
-            _dev(key_cache, "key_cache", pool), _dev(value_cache, "value_cache", pool),
-            _dev(block_tables, "block_tables", i32), block_tables.shape[1],
-            _dev(context_lens, "context_lens", i32), int(max_context_len),
-            _reach(window), _reach(num_sinks), S, H, Hkv, d, bs, N, float(scale))
-    tail = (int(partition_size), ws_ptr, ws_bytes, _dtype_code(query),
-            _opt(error_word, "error_word"), _stream(stream))
+    dev, dt, i32 = _device(query, "query"), query.dtype, torch.int32
+    fp8 = key_cache.dtype is torch.uint8
+    pool = torch.uint8 if fp8 else dt
+    head = (_at(out, "out", dt, dev), _at(query, "query", dt, dev),
+            _at(key_cache, "key_cache", pool, dev), _at(value_cache, "value_cache", pool, dev),
+            _at(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+            _at(context_lens, "context_lens", i32, dev), int(max_context_len),
+            _reach(window), _reach(num_sinks), S, H, Hkv, d, bs, N, scale)
+    tail = (int(partition_size), *_space(workspace, dev), _dtype_code(query),
+            _opt_at(error_word, "error_word", dev), _queue(stream, dev))
     if fp8:
         _check("pa_decode_attention_window_fp8", _lib.pa_decode_attention_window_fp8(
             *head, float(k_scale), float(v_scale), *tail))
@@ -664,18 +694,16 @@ def pa_prefill_attention_window(out: torch.Tensor, query: torch.Tensor, key_cach
     if (d != d2 or out.shape != query.shape or value_cache.shape != key_cache.shape or
             query_start.shape[0] != S + 1 or block_tables.shape[0] != S):
         raise ValueError("shape mismatch")
-    _same_device(query, out, key_cache, value_cache, block_tables, query_start, context_lens,
-                 error_word)
-    fp8 = key_cache.dtype == torch.uint8
-    pool = torch.uint8 if fp8 else query.dtype
-    i32 = torch.int32
-    head = (_dev(out, "out", query.dtype), _dev(query, "query"),
-            _dev(key_cache, "key_cache", pool), _dev(value_cache, "value_cache", pool),
-            _dev(block_tables, "block_tables", i32), block_tables.shape[1],
-            _dev(query_start, "query_start", i32), _dev(context_lens, "context_lens", i32),
-            int(max_context_len), _reach(window), _reach(num_sinks), S, T, H, Hkv, d, bs, N,
-            float(scale))
-    tail = (_dtype_code(query), _opt(error_word, "error_word"), _stream(stream))
+    dev, dt, i32 = _device(query, "query"), query.dtype, torch.int32
+    fp8 = key_cache.dtype is torch.uint8
+    pool = torch.uint8 if fp8 else dt
+    head = (_at(out, "out", dt, dev), _at(query, "query", dt, dev),
+            _at(key_cache, "key_cache", pool, dev), _at(value_cache, "value_cache", pool, dev),
+            _at(block_tables, "block_tables", i32, dev), block_tables.shape[1],
+            _at(query_start, "query_start", i32, dev),
+            _at(context_lens, "context_lens", i32, dev), int(max_context_len), _reach(window),
+            _reach(num_sinks), S, T, H, Hkv, d, bs, N, scale)
+    tail = (_dtype_code(query), _opt_at(error_word, "error_word", dev), _queue(stream, dev))
     if fp8:
         _check("pa_prefill_attention_window_fp8", _lib.pa_prefill_attention_window_fp8(
             *head, float(k_scale), float(v_scale), *tail))
