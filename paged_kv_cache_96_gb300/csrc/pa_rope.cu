@@ -26,6 +26,7 @@
 // rounding error is recovered with a fused multiply-add, and only then are
 // whole turns dropped: the phase is right to 10^-6 turns at position 2^31 and
 // to 10^-8 below a million.
+#include <algorithm>
 #include <cmath>
 
 #include <cuda_bf16.h>
@@ -37,7 +38,8 @@
 namespace pa {
 
 constexpr int kRopeMaxPairs = 128;  // head_dim up to 256
-constexpr int kRopeThreads = 256;
+constexpr int kRopeMaxThreads = 256;
+constexpr int kAhead = 3;  // rotary items of a thread whose loads go out first
 
 struct RopeParams {
     void *query_out;
@@ -73,6 +75,17 @@ __device__ __forceinline__ float rope_turns(int pos, float f)
 __device__ __forceinline__ float rope_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float rope_float(__half x) { return __half2float(x); }
 
+// A 16-byte word that is read once: not kept in L1.
+__device__ __forceinline__ uint4 load_word(const void *p)
+{
+    uint4 w;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+                 : "l"(p)
+                 : "memory");
+    return w;
+}
+
 template <typename T> __device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8])
 {
     const T *e = reinterpret_cast<const T *>(&w);
@@ -102,11 +115,11 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv)
 // key, then single words to pass on (elements from rot_dim on) and to cache
 // (values).
 template <typename T, bool kFp8, bool kInterleaved>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeMaxThreads)
     rope_and_cache_kernel(const __grid_constant__ RopeParams p)
 {
     __shared__ __align__(16) float cos_s[kRopeMaxPairs], sin_s[kRopeMaxPairs];
-    const int t = blockIdx.x, tid = threadIdx.x;
+    const int t = blockIdx.x, tid = threadIdx.x, threads = blockDim.x;
     pdl_wait_primary();
     pdl_launch_dependents();
 
@@ -131,18 +144,21 @@ __global__ void __launch_bounds__(kRopeThreads)
         int h, lo, hi;
         locate(it, h, lo, hi);
         const T *row = h < H ? q + h * D : k + (h - H) * D;
-        a = *reinterpret_cast<const uint4 *>(row + lo);
-        b = *reinterpret_cast<const uint4 *>(row + hi);
+        a = load_word(row + lo);
+        b = load_word(row + hi);
     };
     // the first items' loads go out before the angles are needed
-    constexpr int kAhead = 3;
-    uint4 wa[kAhead], wb[kAhead];
+        uint4 wa[kAhead], wb[kAhead];
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-        const int it = tid + u * kRopeThreads;
+        const int it = tid + u * threads;
         if (it < rot_items)
             load2(it, wa[u], wb[u]);
     }
+    const int v_items = K * (D >> 3);
+    uint4 wv0 = make_uint4(0, 0, 0, 0);
+    if (tid < v_items)
+        wv0 = load_word(v + 8 * tid);
     long long slot = p.slot_mapping[t];
     if (slot >= p.num_slots) {
         if (tid == 0)
@@ -205,11 +221,11 @@ __global__ void __launch_bounds__(kRopeThreads)
     };
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
-        const int it = tid + u * kRopeThreads;
+        const int it = tid + u * threads;
         if (it < rot_items)
             turn(it, wa[u], wb[u]);
     }
-    for (int it = tid + kAhead * kRopeThreads; it < rot_items; it += kRopeThreads) {
+    for (int it = tid + kAhead * threads; it < rot_items; it += threads) {
         uint4 a, b;
         load2(it, a, b);
         turn(it, a, b);
@@ -217,10 +233,10 @@ __global__ void __launch_bounds__(kRopeThreads)
     // elements past the rotary ones
     const int rest = (D - p.rot_dim) >> 3;
     if (rest > 0) {
-        for (int it = tid; it < (H + K) * rest; it += kRopeThreads) {
+        for (int it = tid; it < (H + K) * rest; it += threads) {
             const int h = it / rest, d = p.rot_dim + 8 * (it - h * rest);
             const T *row = h < H ? q + h * D : k + (h - H) * D;
-            const uint4 w = *reinterpret_cast<const uint4 *>(row + d);
+            const uint4 w = load_word(row + d);
             if (h < H) {
                 *reinterpret_cast<uint4 *>(qo + h * D + d) = w;
             } else if constexpr (kFp8) {
@@ -234,8 +250,8 @@ __global__ void __launch_bounds__(kRopeThreads)
         }
     }
     if (slot >= 0) {
-        for (int it = tid; it < K * (D >> 3); it += kRopeThreads) {
-            const uint4 w = *reinterpret_cast<const uint4 *>(v + 8 * it);
+        for (int it = tid; it < v_items; it += threads) {
+            const uint4 w = it == tid ? wv0 : load_word(v + 8 * it);
             if constexpr (kFp8) {
                 float x[8];
                 unpack8<T>(w, x);
@@ -253,7 +269,14 @@ static pa_status launch_rope(const RopeParams &p, bool interleaved, cudaStream_t
 {
     auto kernel = interleaved ? rope_and_cache_kernel<T, kFp8, true>
                               : rope_and_cache_kernel<T, kFp8, false>;
-    return launch_pdl(kernel, dim3((unsigned)p.num_tokens), dim3(kRopeThreads), 0, stream, p);
+    // Threads that share the rotary items evenly, kAhead or fewer each for rows
+    // of up to 96 heads of 128 (72 heads: 192 threads with 3 items), and one a
+    // rotary pair at least.
+    const int items = (p.num_heads + p.num_kv_heads) * (p.rot_dim / 16);
+    const int rounds = (items + kRopeMaxThreads - 1) / kRopeMaxThreads;
+    const int even = (items + rounds - 1) / rounds;
+    const int threads = (std::max(even, p.rot_dim / 2) + 31) / 32 * 32;
+    return launch_pdl(kernel, dim3((unsigned)p.num_tokens), dim3(threads), 0, stream, p);
 }
 
 static bool stride_ok(long long stride, int heads, int head_dim, int tokens)
