@@ -46,69 +46,9 @@
 #include <mutex>
 #include <type_traits>
 
-#include "pa_decode_common.cuh"
-#include "pa_tcgen05.cuh"
+#include "pa_window.cuh"
 
 namespace pa {
-
-struct WindowMqParams {
-    void *out;          // [T][H][D]
-    const void *query;  // [T][H][D]
-    const int32_t *block_tables;
-    const int32_t *context_lens;
-    const int32_t *query_start;  // [S + 1]
-    int32_t *error_word;
-    uint64_t wait_ns;   // limit of one stage wait (PA_DEVERR_TIMEOUT past it)
-    int withhold_fill;  // test hook: each CTA's key warp never issues its first fill
-    int num_segments;   // sequences
-    int num_heads, num_kv_heads, group;
-    int max_blocks_per_seq, num_blocks, block_size, block_shift, max_context_len;
-    int window, num_sinks;
-    int sink_tokens;    // num_sinks rounded up to 16-token boxes
-    float scale_log2;   // scale * log2(e) (times the K scale for FP8 pools)
-    float out_scale;    // applied to the output (the V scale for FP8 pools)
-    int num_tokens;     // rows of query and out (T)
-    int q_tma;          // 1: each unit's query tile arrives by TMA (the query map)
-};
-
-// ---- fp32 helpers for the softmax ---------------------------------------------
-
-// Maximum of three (max.f32 with three sources; a NaN source is ignored as
-// in fmaxf).
-__device__ __forceinline__ float fmax3(float a, float b, float c)
-{
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-// Two fp32 values in one 64-bit register, and packed fp32 FMA / add on them
-// (fma.rn.f32x2 / add.rn.f32x2: each lane rounds as its scalar form).
-__device__ __forceinline__ uint64_t pack_f32x2(float lo, float hi)
-{
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float &lo, float &hi)
-{
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t ffma_f32x2(uint64_t a, uint64_t b, uint64_t c)
-{
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-
-__device__ __forceinline__ uint64_t fadd_f32x2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
 
 constexpr int kTcRows = 128;     // query rows per CTA (M of the MMAs)
 constexpr int kRowWarps = 4;     // warps 0-3: one thread per row (softmax, epilogue)
@@ -158,45 +98,7 @@ template <int D, bool kFp8> struct WindowTcLayout {
     static_assert(kStageBytes % 1024 == 0 && kQ % 1024 == 0, "1024-byte aligned operands");
 };
 
-// 3-D tiled bulk tensor load global -> shared, completion on an mbarrier.
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *tmap, uint32_t bar,
-                                            int c0, int c1, int c2)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
-        : "memory");
-}
-
-// Context length of a chunked-prefill sequence, clamped like the decode pass.
-__device__ __forceinline__ int window_context(const WindowMqParams &p, int s)
-{
-    const int limit = min(p.max_context_len, p.max_blocks_per_seq * p.block_size);
-    int c = p.context_lens[s];
-    if (c < 0 || c > limit) {
-        flag_error(p.error_word, PA_DEVERR_CONTEXT_RANGE);
-        c = c < 0 ? 0 : limit;
-    }
-    return c;
-}
-
-// First row of sequence s, kept inside the query; offsets that are not are
-// flagged by the caller that passes `flag`.
-__device__ __forceinline__ int window_row0(const WindowMqParams &p, int s, bool flag)
-{
-    const int r = p.query_start[s];
-    if (flag && (r < 0 || r > p.num_tokens))
-        flag_error(p.error_word, PA_DEVERR_TOKEN_RANGE);
-    return min(max(r, 0), p.num_tokens);
-}
-
-// Rows of one sequence's chunk, and its row tiles (work units per KV head).
-__device__ __forceinline__ int window_rows(const WindowMqParams &p, int s, bool flag = false)
-{
-    return max(0, window_row0(p, s + 1, flag) - window_row0(p, s, flag));
-}
-
+// Row tiles of a sequence (work units per KV head).
 __device__ __forceinline__ int window_units(const WindowMqParams &p, int s)
 {
     return (window_rows(p, s, true) * p.group + kTcRows - 1) / kTcRows;
@@ -332,11 +234,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             hist[lane + 32] = 0;
             __syncwarp();
             for (int sg = lane; sg < nseg; sg += 32) {
-                const int ctx = window_context(p, sg);
-                const unsigned keys = min((unsigned)ctx, (unsigned)min(p.sink_tokens, ctx) +
-                                                             (unsigned)min(p.window, ctx));
-                const int tiles = (int)((keys + kTcTokens - 1) / kTcTokens);
-                const int key = kWinOrderBuckets - 1 - min(tiles, kWinOrderBuckets - 1);
+                const int key = window_order_key(p, sg, kWinOrderBuckets);
                 seg_units[sg] = window_units(p, sg);
                 seg_key[sg] = key;
                 atomicAdd(&hist[key], 1);
@@ -1351,6 +1249,9 @@ static pa_status run_window_prefill(
     // row tiles: at most one partial tile per sequence beyond the full ones
     const long long max_units =
         ((long long)num_tokens * group / kTcRows + num_seqs) * num_kv_heads;
+    if (!fp8)
+        return launch_window_tiles(prm, dtype, key_cache, value_cache, head_dim,
+                                  as_stream(stream));
     return dispatch_window_mq(prm, fp8 ? PA_FP8_E4M3 : dtype, dtype, key_cache, value_cache,
                               head_dim, as_stream(stream), max_units);
 }

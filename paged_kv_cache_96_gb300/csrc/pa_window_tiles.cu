@@ -1,0 +1,917 @@
+// pa_window_tiles.cu -- chunked prefill and mixed batches over 16-bit paged pools
+// with a sliding window and a few first tokens that stay visible, for sm_103a,
+// on the 5th-generation tensor cores.
+//
+// Row of sequence s at position pos, window W, first tokens N:
+//     seen = { p <= pos : p > pos - W  or  p < N }
+//     out = sum_{p seen} softmax_p(scale * q . k_p) v_p
+// ("PagedAttention & Continuous Batching" §2.4, §2.5 for the chunk; the window
+// is an addition).
+//
+// What bounds it: the tensor cores (4 d flop a row and key), and beside them
+// the softmax of every score.  A CTA (one an SM, all of its tensor memory) works
+// through 128 query rows of one KV head at a time, in steps of 128 keys:
+//  * A score product reads its query rows from shared memory for every step,
+//    so N = 128 keys cost what 64 do (128 bytes a cycle: 8 MMAs take ~480
+//    cycles for either); 64-key steps pay that, and every barrier and commit,
+//    twice.
+//  * Tensor memory: two S buffers (128 fp32 columns each) and two O buffers.  The
+//    scores of step g + 1 are computed while the softmax of step g runs; P
+//    goes over the upper half of its S as 16-bit pairs, in two halves of 64
+//    keys, so the value product starts on the first while the second is
+//    computed.  The next unit's products start into the other O buffer while
+//    warps of their own write this unit's rows: with windows a unit has few
+//    steps, and its end would cost as much as several of them.
+//  * Keys are counted without a gap ("compact positions", at the grain of one
+//    TMA box): the first tokens' boxes, then the window's, `skip` tokens further
+//    on; row r sees c with c < lim_r and (c >= low_r or c < N).  Steps past the
+//    window do not exist, and a last step of 64 keys or fewer is done at half
+//    size.
+//  * Twelve warps: 0-3 the softmax (one thread a row, a reference maximum that
+//    moves only when a score passes it by 2^8), 4-7 the output rows, 8 loads
+//    keys and query tiles, 9 values, 10 issues the MMAs, 11 zeroes value rows
+//    that no row of the unit sees (so that NaN or another sequence's rows never
+//    meet a zero weight) in the few steps that have such rows.  They meet only
+//    at mbarriers; every wait is bounded, the first to run out stops all roles,
+//    and tensor memory is released on every path.
+//  * Query tiles hold floor(128 / G) whole tokens, so that any group size
+//    arrives by one TMA box a d-half.
+// P is rounded to the pools' type as an MMA operand, relative error 2^-9
+// (bf16) or 2^-12: about that of the rounded output; the sum keeps the
+// unrounded fp32 weights.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <mutex>
+#include <type_traits>
+
+#include "pa_window.cuh"
+
+namespace pa {
+
+constexpr int kWtRows = 128;      // rows of a tile (M of the MMAs)
+constexpr int kWtKeys = 128;      // keys of a step
+constexpr int kWtHalf = 64;       // keys of a half step
+constexpr int kWtOutWarp = 4;       // warps 0-3: softmax, 4-7: output rows
+constexpr int kWtKeyWarp = 8;
+constexpr int kWtValueWarp = 9;
+constexpr int kWtFixWarp = 11;      // (10: tensor cores)
+constexpr int kWtThreads = 384;
+constexpr uint32_t kWtTmemCols = 512;  // S at 0 and 128, O at 256 and 384
+constexpr uint32_t kWtTmemO = 256;
+constexpr int kWtOrderBuckets = 64;
+constexpr int kWtOrderSegs = 512;
+
+// A work unit: the tokens of a tile of one KV head, and their keys.
+struct WtUnit {
+    int row0;           // first query row (token) of the unit
+    int kh;             // KV head
+    int count;          // tokens
+    int pos0;           // position of the first token
+    int skip;           // real minus compact position, from the window on
+    int kend;           // compact keys
+    int hide0, hide1;   // compact keys that no row sees: [hide0, hide1)
+    int seq;            // sequence (its table)
+    __device__ int steps() const { return (kend + kWtKeys - 1) / kWtKeys; }
+    // a last step of 64 keys or fewer
+    __device__ bool half(int si) const { return kend - si * kWtKeys <= kWtHalf; }
+    // value rows of step si that no row sees
+    __device__ bool hidden(int si) const
+    {
+        const int c0 = si * kWtKeys;
+        return c0 + kWtKeys > kend || (hide1 > max(hide0, c0) && hide0 < c0 + kWtKeys);
+    }
+};
+// units of a CTA kept in shared memory; later ones are worked out by each role
+constexpr int kWtUnits = 192;
+
+template <int D> struct WtLayout {
+    static constexpr int kHalves = D / 64;               // 128-byte rows of 64 elements
+    static constexpr int kHalfBytes = 128 * 128;         // 128 rows of one d-half
+    static constexpr int kTile = kHalves * kHalfBytes;   // a query tile, or K or V of a step
+    static constexpr int kK = 0;                         // 2 stages
+    static constexpr int kV = 2 * kTile;                 // 2 stages
+    static constexpr int kQ = 4 * kTile;                 // 2 query tiles
+    static constexpr int kInv = 6 * kTile;               // float 1 / l [2][128]
+    static constexpr int kBars = kInv + 2 * 128 * 4;     // 23 mbarriers
+    static constexpr int kTmemSlot = kBars + 24 * 8;
+    static constexpr int kAbort = kTmemSlot + 8;
+    static constexpr int kUnits = kTmemSlot + 16;        // the CTA's first units
+    // int unit prefix[n + 1], then (ordered) order[n], units[n], key[n] and
+    // the sort's buckets
+    static constexpr int kSeg = kUnits + kWtUnits * (int)sizeof(WtUnit);
+    static size_t bytes(int segments, bool ordered)
+    {
+        return 1024 + kSeg + 4 * ((size_t)segments + 1) +
+               (ordered ? 4 * (3 * (size_t)segments + kWtOrderBuckets) : 0);
+    }
+};
+
+// Registers a thread of each warpgroup: softmax, output, the others.  The
+// block is launched with 168 a thread: 128 x (240 + 144 + 96) <= 384 x 168.
+__device__ __forceinline__ void wt_regs_softmax()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+}
+__device__ __forceinline__ void wt_regs_output()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 144;");
+}
+__device__ __forceinline__ void wt_regs_others()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+}
+
+template <typename T, int D, int kBox>
+__global__ void __launch_bounds__(kWtThreads, 1)
+    window_tiles_kernel(const __grid_constant__ WindowMqParams p,
+                       const __grid_constant__ CUtensorMap tmap_k,
+                       const __grid_constant__ CUtensorMap tmap_v,
+                       const __grid_constant__ CUtensorMap tmap_q)
+{
+    using L = WtLayout<D>;
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t kIdescS = idesc_f16(kBf16, kWtRows, kWtKeys, false, false);
+    constexpr uint32_t kIdescSHalf = idesc_f16(kBf16, kWtRows, kWtHalf, false, false);
+    constexpr uint32_t kIdescO = idesc_f16(kBf16, kWtRows, D, false, true);
+    constexpr int KT = D / 16;
+    constexpr int kSubs = kWtKeys / kBox;  // boxes of a step and d-half
+
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    uint8_t *smem = smem_raw + (((raw_addr + 1023u) & ~1023u) - raw_addr);
+    const uint32_t sbase = smem_addr(smem);
+    int *pref = reinterpret_cast<int *>(smem + L::kSeg);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
+    // mbarriers, [parity of the step]: K / V of a stage ready; V landed before
+    // its hidden rows are zeroed; S computed (frees the K stage); half h of P
+    // stored by the 4 softmax warps; value product done (frees S, P and the V
+    // stage).  [parity of the unit]: query tile landed; the unit's last value
+    // product done; its 1 / l stored by the 4 softmax warps; its O and 1 / l
+    // read by the 4 output warps.  Every tensor-core operation done.
+    auto bar = [&](int i) { return sbase + L::kBars + 8 * i; };
+    auto kfull = [&](int st) { return bar(st); };
+    auto vfull = [&](int st) { return bar(2 + st); };
+    auto vland = [&](int st) { return bar(4 + st); };
+    auto sfull = [&](int st) { return bar(6 + st); };
+    auto pfull = [&](int h, int st) { return bar(8 + 2 * h + st); };
+    auto ofull = [&](int st) { return bar(12 + st); };
+    auto qfull = [&](int b) { return bar(14 + b); };
+    auto ufull = [&](int b) { return bar(16 + b); };
+    auto lfull = [&](int b) { return bar(18 + b); };
+    auto ufree = [&](int b) { return bar(20 + b); };
+    const uint32_t mma_drain = bar(22);
+    float *inv_s = reinterpret_cast<float *>(smem + L::kInv);
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int G = p.group, Hkv = p.num_kv_heads, H = p.num_heads;
+    const int nseg = p.num_segments;
+    const int tok_unit = kWtRows / G;  // whole tokens of a tile
+
+    if (tid == 0) {
+        for (int st = 0; st < 2; ++st) {
+            mbar_init(kfull(st), 1);
+            mbar_init(vfull(st), 1);
+            mbar_init(vland(st), 1);
+            mbar_init(sfull(st), 1);
+            mbar_init(pfull(0, st), 4);
+            mbar_init(pfull(1, st), 4);
+            mbar_init(ofull(st), 1);
+            mbar_init(qfull(st), 1);
+            mbar_init(ufull(st), 1);
+            mbar_init(lfull(st), 4);
+            mbar_init(ufree(st), 4);
+        }
+        mbar_init(mma_drain, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+        prefetch_tensormap(&tmap_q);
+    }
+    pdl_wait_primary();
+    if (warp == 0) {
+        tmem_alloc(sbase + L::kTmemSlot, kWtTmemCols);
+        tmem_relinquish();
+    }
+
+    // ---- work units per sequence and their prefix sums --------------------------------
+    auto units_of = [&](int s) {
+        return (window_rows(p, s, true) + tok_unit - 1) / tok_unit;
+    };
+    int *order = pref + nseg + 1;  // k-th sequence of the unit order (ordered)
+    const bool ordered = p.ordered != 0;
+    if (warp == 1) {
+        int *seg_units = order + nseg;
+        if (ordered) {
+            // counting sort by the keys of the sequence's last row, most
+            // first, by index within a count; every CTA computes the same order
+            int *seg_key = seg_units + nseg;
+            int *hist = seg_key + nseg;
+            hist[lane] = 0;
+            hist[lane + 32] = 0;
+            __syncwarp();
+            for (int sg = lane; sg < nseg; sg += 32) {
+                const int key = window_order_key(p, sg, kWtOrderBuckets);
+                seg_units[sg] = units_of(sg);
+                seg_key[sg] = key;
+                atomicAdd(&hist[key], 1);
+            }
+            __syncwarp();
+            const int c0 = hist[2 * lane], c1 = hist[2 * lane + 1];
+            int x = c0 + c1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            __syncwarp();
+            hist[2 * lane] = x - c0 - c1;  // first place of each count
+            hist[2 * lane + 1] = x - c1;
+            __syncwarp();
+            for (int base = 0; base < nseg; base += 32) {
+                const int sg = base + lane;
+                const int key = sg < nseg ? seg_key[sg] : -1;
+                const unsigned same = __match_any_sync(kFull, key);
+                const int rank = __popc(same & ((1u << lane) - 1u));
+                const int off = key >= 0 ? hist[key] : 0;
+                __syncwarp();
+                if (key >= 0) {
+                    order[off + rank] = sg;
+                    if (rank == 0)
+                        hist[key] = off + __popc(same);
+                }
+                __syncwarp();
+            }
+        }
+        int carry = 0;
+        for (int base = 0; base < nseg; base += 32) {
+            const int k = base + lane;
+            const int n = k < nseg ? (ordered ? seg_units[order[k]] : units_of(k)) : 0;
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (k < nseg)
+                pref[k] = carry + x - n;
+            carry += __shfl_sync(kFull, x, 31);
+        }
+        if (lane == 0)
+            pref[nseg] = carry;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
+    const int total_units = pref[nseg] * Hkv;
+    // this CTA's unit after unit u in the deal (its first unit is blockIdx.x):
+    // round-robin, or boustrophedon over the ordered units
+    auto next_unit = [&](int u) -> int {
+        const int grid = gridDim.x;
+        if (!ordered)
+            return u + grid;
+        const int r = u / grid + 1;
+        return r * grid + ((r & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    };
+
+    // ---- unit -> (sequence, KV head, tokens, keys) -------------------------------------
+    // Every role walks the same units in the same order and counts the same
+    // steps, so step g (over this CTA's units) names its ring stage g % 2 and
+    // the phase g / 2 of every barrier of that stage.
+    const int sinks = p.num_sinks, sink_tokens = p.sink_tokens;
+    auto work_out = [&](int u) -> WtUnit {
+        WtUnit w;
+        const int q = u / Hkv;
+        w.kh = u - q * Hkv;
+        int lo = 0, hi = nseg - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (pref[mid] <= q)
+                lo = mid;
+            else
+                hi = mid - 1;
+        }
+        w.seq = ordered ? order[lo] : lo;
+        const int rows = window_rows(p, w.seq);
+        // ordered: the sequence's units last-first
+        const int tok0 = (ordered ? pref[lo + 1] - 1 - q : q - pref[lo]) * tok_unit;
+        w.row0 = window_row0(p, w.seq, false) + tok0;
+        w.count = min(tok_unit, rows - tok0);
+        const int ctx = window_context(p, w.seq);
+        w.pos0 = ctx - rows + tok0;
+        const int end = max(0, w.pos0 + w.count);        // one past the last key
+        const int low = max(0, w.pos0 + 1 - p.window);   // the first row's window
+        w.skip = max(0, (low & ~(kBox - 1)) - sink_tokens);
+        w.kend = end - w.skip;
+        w.hide0 = sinks;
+        w.hide1 = min(low - w.skip, w.kend);
+        return w;
+    };
+    // the CTA's units, worked out once, a thread each (a role that did it at
+    // each unit's start would add a few trips to L2 to every unit)
+    WtUnit *unit_s = reinterpret_cast<WtUnit *>(smem + L::kUnits);
+    {
+        int u = blockIdx.x;
+        for (int k = 0; k < kWtUnits && u < total_units; ++k, u = next_unit(u))
+            if (k % kWtThreads == tid)
+                unit_s[k] = work_out(u);
+    }
+    __syncthreads();
+    // the CTA's k-th unit, u its number
+    auto unit_at = [&](int k, int u) -> WtUnit {
+        return k < kWtUnits ? unit_s[k] : work_out(u);
+    };
+    // a bounded wait, warp-uniform; the first one to run out stops every role
+    auto wait = [&](uint32_t b, uint32_t parity) -> bool {
+        if (__all_sync(kFull, mbar_try_wait(b, parity)))
+            return true;
+        bool ok = *abort_flag == 0 && mbar_wait_bounded(b, parity, p.wait_ns);
+        ok = __all_sync(kFull, ok);
+        if (!ok)
+            *abort_flag = 1;
+        return ok;
+    };
+
+    // rows of a unit: row r is token r / G, head r % G of the group
+    const int r = tid & (kWtRows - 1);
+    const int tok = r / G, hg = r - (r / G) * G;
+    const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+
+    if (warp < kWtOutWarp) {
+        // ===== softmax warps ==============================================================
+        wt_regs_softmax();
+        uint32_t g = 0, nu = 0;  // steps, units with keys
+        bool ok = true;
+        for (int u = blockIdx.x, ku = 0; u < total_units && ok; u = next_unit(u), ++ku) {
+            const WtUnit w = unit_at(ku, u);
+            const int steps = w.steps();
+            if (steps == 0)
+                continue;  // (the output warps write its zero rows)
+            const bool row = r < tok_unit * G && tok < w.count;
+            // compact: one past the row's own position, its window's start
+            const int lim = row ? w.pos0 + tok + 1 - w.skip : 0;
+            const int low = max(0, w.pos0 + tok + 1 - p.window) - w.skip;
+            const uint32_t o_at = tmem + lanes + kWtTmemO + (nu & 1) * 128;
+            float m_ref = -INFINITY, l_run = 0.f;
+            for (int si = 0; si < steps; ++si, ++g) {
+                const int st = g & 1;
+                const uint32_t ph = (g >> 1) & 1;
+                const uint32_t s_at = tmem + lanes + st * kWtKeys;
+                const int c0 = si * kWtKeys;
+                const bool full = !w.half(si);
+                ok = wait(sfull(st), ph);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                float sv[kWtKeys];
+                {
+                    uint32_t v[64];
+                    tmem_ld_32x32b_x64(s_at, v);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        sv[i] = __uint_as_float(v[i]);
+                }
+                if (full) {
+                    uint32_t v[64];
+                    tmem_ld_32x32b_x64(s_at + 64, v);
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        sv[64 + i] = __uint_as_float(v[i]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 64; ++i)
+                        sv[64 + i] = -INFINITY;
+                }
+                // hidden keys (steps at a border only): bits of each 32 seen
+                if (lim < c0 + kWtKeys || (low > max(c0, sinks) && sinks < c0 + kWtKeys)) {
+#pragma unroll
+                    for (int b = 0; b < kWtKeys / 32; ++b) {
+                        const int cb = c0 + 32 * b;
+                        auto below = [&](int c) -> uint32_t {  // bits of keys < c
+                            const int k = c - cb;
+                            return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
+                        };
+                        const uint32_t seen = below(lim) & (~below(low) | below(sinks));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            sv[32 * b + i] = (seen >> i) & 1u ? sv[32 * b + i] : -INFINITY;
+                    }
+                }
+                // maximum raw score (the scale is positive)
+                float mx;
+                {
+                    float m[43];
+#pragma unroll
+                    for (int k = 0; k < 42; ++k)
+                        m[k] = fmax3(sv[3 * k], sv[3 * k + 1], sv[3 * k + 2]);
+                    m[42] = fmaxf(sv[126], sv[127]);
+                    float m2[15];
+#pragma unroll
+                    for (int k = 0; k < 14; ++k)
+                        m2[k] = fmax3(m[3 * k], m[3 * k + 1], m[3 * k + 2]);
+                    m2[14] = m[42];
+                    float m3[5];
+#pragma unroll
+                    for (int k = 0; k < 5; ++k)
+                        m3[k] = fmax3(m2[3 * k], m2[3 * k + 1], m2[3 * k + 2]);
+                    mx = fmax3(fmax3(m3[0], m3[1], m3[2]), m3[3], m3[4]) * p.scale_log2;
+                }
+                const bool moved = mx > m_ref + kSlack;
+                float alpha = 1.f;
+                if (moved) {
+                    alpha = exp2f(m_ref - mx);  // 0 while m_ref is -inf
+                    m_ref = mx;
+                    l_run *= alpha;
+                }
+                // a reference moved: rescale O once the value product before is done
+                if (si > 0 && __any_sync(kFull, moved)) {
+                    const uint32_t gp = g - 1;
+                    ok = wait(ofull(gp & 1), (gp >> 1) & 1);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < D / 32; ++c) {
+                        uint32_t o[32];
+                        tmem_ld_32x32b_x32(o_at + c * 32, o);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+                        tmem_st_32x32b_x32(o_at + c * 32, o);
+                    }
+                }
+                const float neg_mu = m_ref == -INFINITY ? 0.f : -m_ref;
+                const uint64_t sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
+                const uint64_t nm2 = pack_f32x2(neg_mu, neg_mu);
+                uint64_t acc[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (h == 1 && !full) {
+                        // (nobody waits for this half; its barrier keeps step)
+                        if (lane == 0)
+                            mbar_arrive(pfull(h, st));
+                        break;
+                    }
+                    uint32_t pw[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        float e0, e1;
+                        unpack_f32x2(ffma_f32x2(pack_f32x2(sv[64 * h + 2 * i],
+                                                           sv[64 * h + 2 * i + 1]),
+                                                sl2, nm2),
+                                     e0, e1);
+                        const float p0 = exp2f(e0), p1 = exp2f(e1);
+                        acc[i & 1] = fadd_f32x2(acc[i & 1], pack_f32x2(p0, p1));
+                        pw[i] = MmaOp<T>::pack(p0, p1);
+                    }
+                    tmem_st_32x32b_x32(s_at + 64 + 32 * h, pw);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(pfull(h, st));
+                }
+                {
+                    float a0, a1, b0, b1;
+                    unpack_f32x2(acc[0], a0, a1);
+                    unpack_f32x2(acc[1], b0, b1);
+                    l_run += (a0 + a1) + (b0 + b1);
+                }
+            }
+            if (!ok)
+                break;
+            // this unit's 1 / l, once unit nu - 2's has been read
+            const int b = nu & 1;
+            if (nu >= 2) {
+                ok = wait(ufree(b), ((nu - 2) >> 1) & 1);
+                if (!ok)
+                    break;
+            }
+            inv_s[b * kWtRows + r] = l_run > 0.f ? p.out_scale / l_run : l_run;
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(lfull(b));
+            ++nu;
+        }
+    } else if (warp < kWtKeyWarp) {
+        // ===== output warps: O / l of a unit, while the next one is computed ==============
+        wt_regs_output();
+        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+        uint32_t nu = 0;
+        for (int u = blockIdx.x, ku = 0; u < total_units; u = next_unit(u), ++ku) {
+            const WtUnit w = unit_at(ku, u);
+            const bool row = r < tok_unit * G && tok < w.count;
+            T *dst = static_cast<T *>(p.out) +
+                     (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
+            if (w.steps() == 0) {  // no keys: zero rows
+                if (row)
+                    for (int c = 0; c < D / 8; ++c)
+                        reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            const int b = nu & 1;
+            const uint32_t ph = (nu >> 1) & 1;
+            if (!wait(lfull(b), ph) || !wait(ufull(b), ph))
+                break;
+            tc_fence_after();
+            const float inv = inv_s[b * kWtRows + r];
+            const uint32_t o_at = tmem + lanes + kWtTmemO + b * 128;
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                uint32_t o[64];
+                tmem_ld_32x32b_x64(o_at + c * 64, o);
+                if (c == D / 64 - 1) {
+                    // the buffer is read: the unit after next may write it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(ufree(b));
+                }
+                if (!row)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = MmaOp<T>::pack(__uint_as_float(o[16 * i + 2 * k]) * inv,
+                                              __uint_as_float(o[16 * i + 2 * k + 1]) * inv);
+                    T *at = dst + c * 64 + 16 * i;
+                    if (out32) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                         at),
+                                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                                     "r"(v[5]), "r"(v[6]), "r"(v[7])
+                                     : "memory");
+                    } else {
+                        reinterpret_cast<uint4 *>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                        reinterpret_cast<uint4 *>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+            }
+            ++nu;
+        }
+    } else {
+        wt_regs_others();
+        if (warp == kWtKeyWarp || warp == kWtValueWarp) {
+            // ===== fetch warps: keys and query tiles (8), values (9) ====================
+            // Lane j owns box j / halves and d-half j % halves of every step: it
+            // looks up that box's physical block one step ahead and issues it.
+            const bool values = warp == kWtValueWarp;
+            const int my_sb = lane / L::kHalves, my_hf = lane % L::kHalves;
+            uint32_t g = 0;
+            int qk = 0, qu = blockIdx.x;  // next unit whose query tile goes out
+            uint32_t nq = 0, nu = 0;      // query tiles issued, units with keys begun
+            uint32_t nland0 = 0, nland1 = 0;    // fills of a value stage onto vland
+            uint32_t last0 = 0, last1 = 0;      // last fill's barrier per stage (0: none)
+            uint32_t last_ph0 = 0, last_ph1 = 0;  // and its phase
+            bool ok = true;
+            for (int u = blockIdx.x, ku = 0; u < total_units && ok; u = next_unit(u), ++ku) {
+                const WtUnit w = unit_at(ku, u);
+                const int steps = w.steps();
+                const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
+                auto lookup = [&](int si) -> int {
+                    const int c = si * kWtKeys + my_sb * kBox;
+                    if (my_sb >= kSubs || c >= w.kend)
+                        return 0;
+                    return __ldg(table + ((c + (c >= sink_tokens ? w.skip : 0)) >> p.block_shift));
+                };
+                int ent_next = steps > 0 ? lookup(0) : 0;
+                for (int si = 0; si < steps; ++si, ++g) {
+                    const int st = g & 1;
+                    const uint32_t ph = (g >> 1) & 1;
+                    int ent = ent_next;
+                    if (ent < 0 || ent >= p.num_blocks) {
+                        flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
+                        ent = 0;  // stays inside the pool; the rows' outputs are undefined
+                    }
+                    if (si + 1 < steps)
+                        ent_next = lookup(si + 1);
+                    // the stage's step g - 2 is consumed
+                    if (g >= 2) {
+                        ok = wait(values ? ofull(st) : sfull(st), ph ^ 1);
+                        if (!ok)
+                            break;
+                    }
+                    // test hook of the time-out path: a CTA's first key fill is
+                    // never issued, so the wait for it runs out
+                    if (!(p.withhold_fill != 0 && !values && g == 0)) {
+                        const int c0 = si * kWtKeys;
+                        const int nsub = min(kSubs, (w.kend - c0 + kBox - 1) / kBox);
+                        const bool fix = values && w.hidden(si);
+                        const uint32_t fb = !values ? kfull(st) : fix ? vland(st) : vfull(st);
+                        if (lane == 0)
+                            mbar_arrive_expect_tx(fb, (uint32_t)(nsub * L::kHalves * kBox * 128));
+                        __syncwarp();
+                        if (my_sb < nsub) {
+                            const int c = c0 + my_sb * kBox;
+                            const int tk = c + (c >= sink_tokens ? w.skip : 0);
+                            tma_load_4d(sbase + (values ? L::kV : L::kK) + st * L::kTile +
+                                            my_hf * L::kHalfBytes + my_sb * kBox * 128,
+                                        values ? &tmap_v : &tmap_k, fb, my_hf * 64, w.kh,
+                                        tk & (p.block_size - 1), ent);
+                        }
+                        (st ? last1 : last0) = fb;
+                        (st ? last_ph1 : last_ph0) = fix ? (st ? nland1 : nland0) & 1 : ph;
+                        if (fix)
+                            ++(st ? nland1 : nland0);
+                    }
+                    // Query tiles, two units deep: the tile of unit v goes into the
+                    // place of unit v - 2's, whose last S is step g - 2 at the
+                    // latest for this unit's own tile, and from its second step
+                    // on for the next unit's.
+                    if (!values) {
+                        const uint32_t due = nu + (si > 0 ? 2 : 1);
+                        while (nq < due && qu < total_units) {
+                            const WtUnit wq = unit_at(qk, qu);
+                            if (wq.kend > 0) {
+                                const uint32_t qb = qfull(nq & 1);
+                                if (lane == 0)
+                                    mbar_arrive_expect_tx(qb, L::kHalves * 128 * tok_unit * G);
+                                __syncwarp();
+                                if (lane < L::kHalves)
+                                    tma_load_3d(sbase + L::kQ + (nq & 1) * L::kTile +
+                                                    lane * L::kHalfBytes,
+                                                &tmap_q, qb, 64 * lane, wq.kh * G, wq.row0);
+                                ++nq;
+                            }
+                            qu = next_unit(qu);
+                            ++qk;
+                        }
+                    }
+                }
+                nu += steps > 0;
+            }
+            // fills still landing (after an abort the roles that wait for them
+            // may have left)
+            if (last0 != 0)
+                mbar_wait_bounded(last0, last_ph0, kDrainWaitNs);
+            if (last1 != 0)
+                mbar_wait_bounded(last1, last_ph1, kDrainWaitNs);
+            if (nq > 0)
+                mbar_wait_bounded(qfull((nq - 1) & 1), ((nq - 1) >> 1) & 1, kDrainWaitNs);
+            if (nq > 1)
+                mbar_wait_bounded(qfull((nq - 2) & 1), ((nq - 2) >> 1) & 1, kDrainWaitNs);
+        } else if (warp == kWtFixWarp) {
+            // ===== hidden value rows: zeroed once landed, before the MMA warp may read ====
+            uint32_t g = 0;
+            uint32_t nland0 = 0, nland1 = 0;
+            bool ok = true;
+            for (int u = blockIdx.x, ku = 0; u < total_units && ok; u = next_unit(u), ++ku) {
+                const WtUnit w = unit_at(ku, u);
+                const int steps = w.steps();
+                for (int si = 0; si < steps; ++si, ++g) {
+                    if (!w.hidden(si))
+                        continue;
+                    const int st = g & 1;
+                    ok = wait(vland(st), (st ? nland1 : nland0) & 1);
+                    if (!ok)
+                        break;
+                    ++(st ? nland1 : nland0);
+                    const int c0 = si * kWtKeys;
+                    const int rows = w.half(si) ? kWtHalf : kWtKeys;
+                    const uint32_t vb = sbase + L::kV + st * L::kTile;
+                    for (int i = lane; i < rows; i += 32) {
+                        const int c = c0 + i;
+                        if (!(c >= w.kend || (c >= w.hide0 && c < w.hide1)))
+                            continue;
+#pragma unroll
+                        for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                 vb + hf * L::kHalfBytes + i * 128 +
+                                                 (((k + i) & 7) << 4)),
+                                             "r"(0)
+                                             : "memory");
+                    }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(vfull(st));
+                }
+            }
+        } else {
+            // ===== tensor-core warp: one elected lane issues ================================
+            // S of step g + 1 goes out before the value product of step g, so it
+            // is computed while the softmax of step g runs.
+            const uint64_t desc_q0 = smem_desc_sw128(sbase + L::kQ, 16, 1024);
+            const uint64_t desc_k0 = smem_desc_sw128(sbase + L::kK, 16, 1024);
+            const uint64_t desc_v0 = smem_desc_sw128(sbase + L::kV, L::kHalfBytes, 1024);
+            struct Cursor {
+                int u, ku;    // unit and its number in this CTA
+                int kend, si; // its compact keys, step (kend 0: no more units)
+                uint32_t nu;  // units with keys before it
+            };
+            auto open = [&](Cursor &c) {  // the first unit from c.u on that has keys
+                c.kend = 0;
+                c.si = 0;
+                for (; c.u < total_units; c.u = next_unit(c.u), ++c.ku) {
+                    c.kend = unit_at(c.ku, c.u).kend;
+                    if (c.kend > 0)
+                        return;
+                }
+            };
+            auto advance = [&](Cursor &c) {
+                if (++c.si * kWtKeys >= c.kend) {
+                    c.u = next_unit(c.u);
+                    ++c.ku;
+                    ++c.nu;
+                    open(c);
+                }
+            };
+            // S of step gs, at cursor c
+            auto issue_s = [&](const Cursor &c, uint32_t gs) -> bool {
+                const int st = gs & 1;
+                if (!wait(kfull(st), (gs >> 1) & 1) ||
+                    (c.si == 0 && !wait(qfull(c.nu & 1), (c.nu >> 1) & 1)) ||
+                    (gs >= 2 && !wait(ofull(st), ((gs - 2) >> 1) & 1)))
+                    return false;
+                tc_fence_after();
+                const uint64_t dq = desc_q0 + (uint64_t)(((c.nu & 1) * L::kTile) >> 4);
+                const uint64_t dk = desc_k0 + (uint64_t)((st * L::kTile) >> 4);
+                const bool full = c.kend - c.si * kWtKeys > kWtHalf;
+                if (elect_one()) {
+#pragma unroll
+                    for (int kk = 0; kk < KT; ++kk) {
+                        const uint32_t o = ((kk >> 2) * L::kHalfBytes + (kk & 3) * 32) >> 4;
+                        tc_mma_ss(tmem + st * kWtKeys, dq + o, dk + o,
+                                  full ? kIdescS : kIdescSHalf, kk > 0 ? 1u : 0u);
+                    }
+                    tc_commit(sfull(st));
+                }
+                return true;
+            };
+            Cursor c{(int)blockIdx.x, 0, 0, 0, 0u};
+            open(c);
+            bool ok = c.kend == 0 || issue_s(c, 0);
+            for (uint32_t g = 0; ok && c.kend > 0; ++g) {
+                const int st = g & 1;
+                const uint32_t ph = (g >> 1) & 1;
+                Cursor n = c;
+                advance(n);
+                if (n.kend > 0 && !issue_s(n, g + 1)) {
+                    ok = false;
+                    break;
+                }
+                // the value product of step g; a unit's first waits until its O
+                // buffer has been read
+                const uint32_t b = c.nu & 1;
+                ok = wait(vfull(st), ph) &&
+                     (c.si > 0 || c.nu < 2 || wait(ufree(b), ((c.nu - 2) >> 1) & 1));
+                const bool full = c.kend - c.si * kWtKeys > kWtHalf;
+                const uint64_t dv = desc_v0 + (uint64_t)((st * L::kTile) >> 4);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (!ok || (h == 1 && !full))
+                        break;
+                    ok = wait(pfull(h, st), ph);
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    if (elect_one()) {
+#pragma unroll
+                        for (int ks = 0; ks < kWtHalf / 16; ++ks)
+                            tc_mma_ts(tmem + kWtTmemO + b * 128,
+                                      tmem + st * kWtKeys + 64 + 32 * h + ks * 8,
+                                      dv + (uint64_t)(((4 * h + ks) * 2048) >> 4), kIdescO,
+                                      (c.si > 0 || h > 0 || ks > 0) ? 1u : 0u);
+                        if (h == 1 || !full) {
+                            tc_commit(ofull(st));
+                            if ((c.si + 1) * kWtKeys >= c.kend)
+                                tc_commit(ufull(b));
+                        }
+                    }
+                }
+                c = n;
+            }
+            // every tensor-core operation this warp issued has finished
+            if (elect_one())
+                tc_commit(mma_drain);
+            __syncwarp();
+            mbar_wait_bounded(mma_drain, 0, kDrainWaitNs);
+        }
+    }
+    pdl_launch_dependents();
+
+    tc_fence_before();
+    __syncthreads();
+    if (tid == 0 && *abort_flag)
+        flag_error(p.error_word, PA_DEVERR_TIMEOUT);
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kWtTmemCols);
+    }
+}
+
+// ---- host side -------------------------------------------------------------------
+
+template <typename T, int D, int kBox>
+static pa_status launch_tiles_as(const WindowMqParams &prm, const CUtensorMap &mk,
+                                const CUtensorMap &mv, const CUtensorMap &mq,
+                                cudaStream_t stream, int grid, int optin)
+{
+    auto kernel = window_tiles_kernel<T, D, kBox>;
+    static size_t enabled[kMaxDevices];
+    static std::mutex mu;
+    const size_t smem = WtLayout<D>::bytes(prm.num_segments, prm.ordered != 0);
+    if (smem > (size_t)optin)
+        return PA_ERR_UNSUPPORTED;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return record_cuda(e);
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (smem > enabled[dev]) {
+            e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)smem);
+            if (e != cudaSuccess)
+                return record_cuda(e);
+            enabled[dev] = smem;
+        }
+    }
+    return launch_pdl(kernel, dim3((unsigned)grid), dim3(kWtThreads), smem, stream, prm, mk,
+                      mv, mq);
+}
+
+// A 4-D map of a 16-bit pool [num_blocks][block_size][num_kv_heads][head_dim]
+// with boxes of 64 elements x 1 head x `tokens` x 1 block, and a 3-D map of the
+// query [T][H][D] with boxes of 64 elements x G heads x whole tokens of a tile;
+// 128-byte swizzle, zero fill past the end.
+static bool encode_tiles_map(CUtensorMap *map, const void *base, pa_dtype dtype, int rank,
+                            const cuuint64_t *dims, const cuuint32_t *box)
+{
+    EncodeTiledFn fn = get_encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t strides[3];
+    cuuint64_t bytes = 2;
+    for (int i = 0; i + 1 < rank; ++i)
+        strides[i] = bytes *= dims[i];
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return fn(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+              (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+pa_status launch_window_tiles(const WindowMqParams &prm_in, pa_dtype dtype, const void *key_cache,
+                             const void *value_cache, int head_dim, cudaStream_t stream)
+{
+    WindowMqParams prm = prm_in;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return record_cuda(e);
+    DeviceInfo info;
+    const pa_status st = device_info(dev, &info);
+    if (st != PA_OK)
+        return st;
+    // boxes of 32 tokens where a block holds them (half the TMA instructions)
+    const int box_tokens = prm.block_size >= 32 ? 32 : 16;
+    prm.sink_tokens = (prm.num_sinks + box_tokens - 1) & ~(box_tokens - 1);
+    const int tok_tile = kWtRows / prm.group;
+    const long long units = ((long long)prm.num_tokens / tok_tile + prm.num_segments) *
+                            prm.num_kv_heads;
+    const int grid = (int)std::max(1ll, std::min((long long)info.sms, units));
+    // more than a round of units: longest first
+    prm.ordered = units > info.sms && prm.num_segments <= kWtOrderSegs;
+
+    CUtensorMap mk, mv, mq;
+    const cuuint64_t pool[4] = {(cuuint64_t)head_dim, (cuuint64_t)prm.num_kv_heads,
+                                (cuuint64_t)prm.block_size, (cuuint64_t)prm.num_blocks};
+    const cuuint32_t pool_box[4] = {64, 1, (cuuint32_t)box_tokens, 1};
+    const cuuint64_t rows[3] = {(cuuint64_t)head_dim, (cuuint64_t)prm.num_heads,
+                                (cuuint64_t)prm.num_tokens};
+    const cuuint32_t rows_box[3] = {64, (cuuint32_t)prm.group, (cuuint32_t)tok_tile};
+    if (!encode_tiles_map(&mk, key_cache, dtype, 4, pool, pool_box) ||
+        !encode_tiles_map(&mv, value_cache, dtype, 4, pool, pool_box) ||
+        !encode_tiles_map(&mq, prm.query, dtype, 3, rows, rows_box))
+        return PA_ERR_CUDA;
+    using B16 = __nv_bfloat16;
+    auto run = [&](auto kernel_launch) {
+        return kernel_launch(prm, mk, mv, mq, stream, grid, info.optin);
+    };
+    if (dtype == PA_BF16) {
+        if (head_dim == 128)
+            return box_tokens == 32 ? run(launch_tiles_as<B16, 128, 32>)
+                                    : run(launch_tiles_as<B16, 128, 16>);
+        return box_tokens == 32 ? run(launch_tiles_as<B16, 64, 32>)
+                                : run(launch_tiles_as<B16, 64, 16>);
+    }
+    if (head_dim == 128)
+        return box_tokens == 32 ? run(launch_tiles_as<__half, 128, 32>)
+                                : run(launch_tiles_as<__half, 128, 16>);
+    return box_tokens == 32 ? run(launch_tiles_as<__half, 64, 32>)
+                            : run(launch_tiles_as<__half, 64, 16>);
+}
+
+}  // namespace pa
