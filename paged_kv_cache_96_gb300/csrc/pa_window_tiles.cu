@@ -20,16 +20,21 @@
 //    goes over the upper half of its S as 16-bit pairs, in two halves of 64
 //    keys, so the value product starts on the first while the second is
 //    computed.  The next unit's products start into the other O buffer while
-//    warps of their own write this unit's rows: with windows a unit has few
-//    steps, and its end would cost as much as several of them.
+//    this unit's rows are written: with windows a unit has few steps, and its
+//    end would cost as much as several of them.
+//  * A step's softmax takes ~1,500 cycles of four warps, its products ~1,000 of
+//    the tensor cores, so two sets of four warps take the steps in turn.  The
+//    rows' reference maximum goes from one to the other through shared memory
+//    as soon as it is known; the sums are joined at the unit's end, by the set
+//    that did not have the last step, after its first step of the next unit.
 //  * Keys are counted without a gap ("compact positions", at the grain of one
 //    TMA box): the first tokens' boxes, then the window's, `skip` tokens further
 //    on; row r sees c with c < lim_r and (c >= low_r or c < N).  Steps past the
 //    window do not exist, and a last step of 64 keys or fewer is done at half
 //    size.
-//  * Twelve warps: 0-3 the softmax (one thread a row, a reference maximum that
-//    moves only when a score passes it by 2^8), 4-7 the output rows, 8 loads
-//    keys and query tiles, 9 values, 10 issues the MMAs, 11 zeroes value rows
+//  * Twelve warps: 0-3 and 4-7 the softmax (one thread a row, a reference maximum
+//    that moves only when a score passes it by 2^8) and the rows, 8 loads keys
+//    and query tiles, 9 values, 10 issues the MMAs, 11 zeroes value rows
 //    that no row of the unit sees (so that NaN or another sequence's rows never
 //    meet a zero weight) in the few steps that have such rows.  They meet only
 //    at mbarriers; every wait is bounded, the first to run out stops all roles,
@@ -54,13 +59,13 @@ namespace pa {
 constexpr int kWtRows = 128;      // rows of a tile (M of the MMAs)
 constexpr int kWtKeys = 128;      // keys of a step
 constexpr int kWtHalf = 64;       // keys of a half step
-constexpr int kWtOutWarp = 4;       // warps 0-3: softmax, 4-7: output rows
-constexpr int kWtKeyWarp = 8;
+constexpr int kWtKeyWarp = 8;       // warps 0-3 and 4-7: softmax of even and odd steps
 constexpr int kWtValueWarp = 9;
-constexpr int kWtFixWarp = 11;      // (10: tensor cores)
-constexpr int kWtThreads = 384;
-constexpr uint32_t kWtTmemCols = 512;  // S at 0 and 128, O at 256 and 384
-constexpr uint32_t kWtTmemO = 256;
+constexpr int kWtScoreWarp = 10;
+constexpr int kWtFixWarp = 12;      // (11: value products)
+constexpr int kWtThreads = 416;
+constexpr uint32_t kWtTmemCols = 512;  // S at 0, 128 and 256 (P over each), O at 384
+constexpr uint32_t kWtTmemO = 384;
 constexpr int kWtOrderBuckets = 64;
 constexpr int kWtOrderSegs = 512;
 
@@ -87,6 +92,20 @@ struct WtUnit {
 // units of a CTA kept in shared memory; later ones are worked out by each role
 constexpr int kWtUnits = 192;
 
+// Step g's slot g % 3 and the parity of g / 3, counted along.
+struct Slot3 {
+    int i = 0;
+    uint32_t ph = 0;
+    __device__ void next()
+    {
+        if (++i == 3) {
+            i = 0;
+            ph ^= 1;
+        }
+    }
+    __device__ Slot3 before() const { return i > 0 ? Slot3{i - 1, ph} : Slot3{2, ph ^ 1}; }
+};
+
 template <int D> struct WtLayout {
     static constexpr int kHalves = D / 64;               // 128-byte rows of 64 elements
     static constexpr int kHalfBytes = 128 * 128;         // 128 rows of one d-half
@@ -94,9 +113,11 @@ template <int D> struct WtLayout {
     static constexpr int kK = 0;                         // 2 stages
     static constexpr int kV = 2 * kTile;                 // 2 stages
     static constexpr int kQ = 4 * kTile;                 // 2 query tiles
-    static constexpr int kInv = 6 * kTile;               // float 1 / l [2][128]
-    static constexpr int kBars = kInv + 2 * 128 * 4;     // 23 mbarriers
-    static constexpr int kTmemSlot = kBars + 24 * 8;
+    static constexpr int kRef = 6 * kTile;               // float reference [2 steps][128]
+    static constexpr int kPartL = kRef + 2 * 128 * 4;    // float l, m [2 units][2][128]
+    static constexpr int kPartM = kPartL + 4 * 128 * 4;
+    static constexpr int kBars = kPartM + 4 * 128 * 4;   // 30 mbarriers
+    static constexpr int kTmemSlot = kBars + 30 * 8;
     static constexpr int kAbort = kTmemSlot + 8;
     static constexpr int kUnits = kTmemSlot + 16;        // the CTA's first units
     // int unit prefix[n + 1], then (ordered) order[n], units[n], key[n] and
@@ -109,19 +130,32 @@ template <int D> struct WtLayout {
     }
 };
 
-// Registers a thread of each warpgroup: softmax, output, the others.  The
-// block is launched with 168 a thread: 128 x (240 + 144 + 96) <= 384 x 168.
-__device__ __forceinline__ void wt_regs_softmax()
+// 16 columns of this warp's 32 lanes, without waiting for the store.
+__device__ __forceinline__ void tmem_st_x16_nowait(uint32_t taddr, const uint32_t (&r)[16])
 {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 240;");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, "
+                 "%9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+                 "r"(r[13]), "r"(r[14]), "r"(r[15])
+                 : "memory");
 }
-__device__ __forceinline__ void wt_regs_output()
+__device__ __forceinline__ void tmem_wait_st()
 {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 144;");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
-__device__ __forceinline__ void wt_regs_others()
+
+// The rest of a wait whose phase has not completed yet.  Out of line: it is
+// called from a dozen places, and the roles' loops have to stay short enough
+// for the instruction cache.
+__device__ __noinline__ bool wt_wait_slow(uint32_t b, uint32_t parity, uint64_t limit_ns,
+                                          volatile int *abort_flag)
 {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 96;");
+    bool ok = *abort_flag == 0 && mbar_wait_bounded(b, parity, limit_ns);
+    ok = __all_sync(kFull, ok);
+    if (!ok)
+        *abort_flag = 1;
+    return ok;
 }
 
 template <typename T, int D, int kBox>
@@ -145,25 +179,32 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const uint32_t sbase = smem_addr(smem);
     int *pref = reinterpret_cast<int *>(smem + L::kSeg);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
-    // mbarriers, [parity of the step]: K / V of a stage ready; V landed before
-    // its hidden rows are zeroed; S computed (frees the K stage); half h of P
-    // stored by the 4 softmax warps; value product done (frees S, P and the V
-    // stage).  [parity of the unit]: query tile landed; the unit's last value
-    // product done; its 1 / l stored by the 4 softmax warps; its O and 1 / l
-    // read by the 4 output warps.  Every tensor-core operation done.
+    // mbarriers.  [parity of the step]: K / V of a stage ready; V landed before
+    // its hidden rows are zeroed; the rows' references after the step stored.
+    // [step % 3]: S computed (frees the K stage); half h of P stored by the 4
+    // softmax warps; value product done (frees S, P and the V stage).  (A wait
+    // for a step's phase needs the next step on the same barrier to depend on
+    // the waiter: the products of step g + 2 do not depend on a wait for step
+    // g's, those of step g + 3 do.)
+    // [parity of the unit]: query tile landed; the unit's last value product
+    // done; its sums stored by the 8 softmax warps; its O and sums read by 4.
+    // Every tensor-core operation done.
     auto bar = [&](int i) { return sbase + L::kBars + 8 * i; };
     auto kfull = [&](int st) { return bar(st); };
     auto vfull = [&](int st) { return bar(2 + st); };
     auto vland = [&](int st) { return bar(4 + st); };
-    auto sfull = [&](int st) { return bar(6 + st); };
-    auto pfull = [&](int h, int st) { return bar(8 + 2 * h + st); };
-    auto ofull = [&](int st) { return bar(12 + st); };
-    auto qfull = [&](int b) { return bar(14 + b); };
-    auto ufull = [&](int b) { return bar(16 + b); };
-    auto lfull = [&](int b) { return bar(18 + b); };
-    auto ufree = [&](int b) { return bar(20 + b); };
-    const uint32_t mma_drain = bar(22);
-    float *inv_s = reinterpret_cast<float *>(smem + L::kInv);
+    auto mfull = [&](int st) { return bar(8 + st); };
+    auto qfull = [&](int b) { return bar(10 + b); };
+    auto ufull = [&](int b) { return bar(12 + b); };
+    auto lfull = [&](int b) { return bar(14 + b); };
+    auto ufree = [&](int b) { return bar(16 + b); };
+    auto sfull = [&](int i) { return bar(18 + i); };
+    auto pfull = [&](int h, int i) { return bar(21 + 3 * h + i); };
+    auto ofull = [&](int i) { return bar(27 + i); };
+    auto mma_drain = [&](int i) { return bar(6 + i); };
+    float *ref_s = reinterpret_cast<float *>(smem + L::kRef);
+    float *part_l = reinterpret_cast<float *>(smem + L::kPartL);
+    float *part_m = reinterpret_cast<float *>(smem + L::kPartM);
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int G = p.group, Hkv = p.num_kv_heads, H = p.num_heads;
@@ -175,16 +216,20 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             mbar_init(kfull(st), 1);
             mbar_init(vfull(st), 1);
             mbar_init(vland(st), 1);
-            mbar_init(sfull(st), 1);
-            mbar_init(pfull(0, st), 4);
-            mbar_init(pfull(1, st), 4);
-            mbar_init(ofull(st), 1);
             mbar_init(qfull(st), 1);
             mbar_init(ufull(st), 1);
-            mbar_init(lfull(st), 4);
+            mbar_init(lfull(st), 8);
+            mbar_init(mfull(st), 4);
             mbar_init(ufree(st), 4);
         }
-        mbar_init(mma_drain, 1);
+        for (int b = 0; b < 3; ++b) {
+            mbar_init(sfull(b), 1);
+            mbar_init(ofull(b), 1);
+            mbar_init(pfull(0, b), 4);
+            mbar_init(pfull(1, b), 4);
+        }
+        mbar_init(mma_drain(0), 1);
+        mbar_init(mma_drain(1), 1);
         *abort_flag = 0;
         fence_barrier_init();
         prefetch_tensormap(&tmap_k);
@@ -268,17 +313,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot);
+    // (a shuffle, so that the compiler knows it to be the same in every lane:
+    // MMA operands live in uniform registers)
+    const uint32_t tmem = __shfl_sync(
+        kFull, *reinterpret_cast<volatile uint32_t *>(smem + L::kTmemSlot), 0);
     const int total_units = pref[nseg] * Hkv;
-    // this CTA's unit after unit u in the deal (its first unit is blockIdx.x):
-    // round-robin, or boustrophedon over the ordered units
-    auto next_unit = [&](int u) -> int {
-        const int grid = gridDim.x;
-        if (!ordered)
-            return u + grid;
-        const int r = u / grid + 1;
-        return r * grid + ((r & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
+    // the number of this CTA's k-th unit in the deal: round-robin, or
+    // boustrophedon over the ordered units (k is kept below 2^31 / grid)
+    const int grid = gridDim.x;
+    auto unit_no = [&](int k) -> int {
+        return k * grid + (ordered && (k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x);
     };
+    const int my_units = total_units > (int)blockIdx.x ? (total_units - 1) / grid + 1 : 0;
 
     // ---- unit -> (sequence, KV head, tokens, keys) -------------------------------------
     // Every role walks the same units in the same order and counts the same
@@ -316,26 +362,21 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // the CTA's units, worked out once, a thread each (a role that did it at
     // each unit's start would add a few trips to L2 to every unit)
     WtUnit *unit_s = reinterpret_cast<WtUnit *>(smem + L::kUnits);
-    {
-        int u = blockIdx.x;
-        for (int k = 0; k < kWtUnits && u < total_units; ++k, u = next_unit(u))
-            if (k % kWtThreads == tid)
-                unit_s[k] = work_out(u);
-    }
+    if (tid < kWtUnits && tid < my_units && unit_no(tid) < total_units)
+        unit_s[tid] = work_out(unit_no(tid));
     __syncthreads();
-    // the CTA's k-th unit, u its number
-    auto unit_at = [&](int k, int u) -> WtUnit {
-        return k < kWtUnits ? unit_s[k] : work_out(u);
+    // the CTA's k-th unit; false past its last one (in the last round of the
+    // ordered deal, where the CTAs are taken backwards, it may have none)
+    auto unit_at = [&](int k, WtUnit &w) -> bool {
+        if (k >= my_units || unit_no(k) >= total_units)
+            return false;
+        w = k < kWtUnits ? unit_s[k] : work_out(unit_no(k));
+        return true;
     };
     // a bounded wait, warp-uniform; the first one to run out stops every role
     auto wait = [&](uint32_t b, uint32_t parity) -> bool {
-        if (__all_sync(kFull, mbar_try_wait(b, parity)))
-            return true;
-        bool ok = *abort_flag == 0 && mbar_wait_bounded(b, parity, p.wait_ns);
-        ok = __all_sync(kFull, ok);
-        if (!ok)
-            *abort_flag = 1;
-        return ok;
+        return __all_sync(kFull, mbar_try_wait(b, parity)) ||
+               wt_wait_slow(b, parity, p.wait_ns, abort_flag);
     };
 
     // rows of a unit: row r is token r / G, head r % G of the group
@@ -343,56 +384,107 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int tok = r / G, hg = r - (r / G) * G;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
 
-    if (warp < kWtOutWarp) {
-        // ===== softmax warps ==============================================================
-        wt_regs_softmax();
+    if (warp < kWtKeyWarp) {
+        // ===== softmax warps: warps 0-3 the even steps, 4-7 the odd ones ====================
+        const int wg = warp >> 2;
+        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t g = 0, nu = 0;  // steps, units with keys
+        Slot3 s3;
         bool ok = true;
-        for (int u = blockIdx.x, ku = 0; u < total_units && ok; u = next_unit(u), ++ku) {
-            const WtUnit w = unit_at(ku, u);
+        auto out_row = [&](const WtUnit &w) -> T * {
+            return static_cast<T *>(p.out) + (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
+        };
+        // A unit's rows, O / l, written by the warps that did not have its last
+        // step, after their first step of the next unit.
+        T *pend = nullptr;      // this thread's row (null: not a row)
+        int pend_nu = -1;       // unit waiting to be written (-1: none)
+        auto write_rows = [&]() -> bool {
+            const int b = pend_nu & 1;
+            const uint32_t ph = (pend_nu >> 1) & 1;
+            pend_nu = -1;
+            if (!wait(lfull(b), ph) || !wait(ufull(b), ph))
+                return false;
+            tc_fence_after();
+            // O is relative to the last step's reference, which the other
+            // warps' sum has, and this warp's reference is not above it
+            const float l0 = part_l[(2 * b + (wg ^ 1)) * kWtRows + r];
+            const float l1 = part_l[(2 * b + wg) * kWtRows + r];
+            const float m0 = part_m[(2 * b + (wg ^ 1)) * kWtRows + r];
+            const float m1 = part_m[(2 * b + wg) * kWtRows + r];
+            const float l = l1 == 0.f ? l0 : l0 + l1 * exp2f(m1 - m0);
+            const float inv = l > 0.f ? p.out_scale / l : l;  // (0 for a row without keys)
+            const uint32_t o_at = tmem + lanes + kWtTmemO;
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_at + c * 32, o);
+                if (c == D / 32 - 1) {
+                    // O is read: the next unit's value products may write it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(ufree(b));
+                }
+                if (pend == nullptr)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    uint32_t v[8];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        v[k] = MmaOp<T>::pack(__uint_as_float(o[16 * i + 2 * k]) * inv,
+                                              __uint_as_float(o[16 * i + 2 * k + 1]) * inv);
+                    T *at = pend + c * 32 + 16 * i;
+                    if (out32) {
+                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                         at),
+                                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
+                                     "r"(v[5]), "r"(v[6]), "r"(v[7])
+                                     : "memory");
+                    } else {
+                        reinterpret_cast<uint4 *>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+                        reinterpret_cast<uint4 *>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+                    }
+                }
+            }
+            return true;
+        };
+        WtUnit w;
+        for (int ku = 0; ok && unit_at(ku, w); ++ku) {
             const int steps = w.steps();
-            if (steps == 0)
-                continue;  // (the output warps write its zero rows)
+            if (steps == 0) {  // no keys: zero rows
+                if (wg == 0 && r < tok_unit * G && tok < w.count)
+                    for (int c = 0; c < D / 8; ++c)
+                        reinterpret_cast<uint4 *>(out_row(w))[c] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
             const bool row = r < tok_unit * G && tok < w.count;
             // compact: one past the row's own position, its window's start
             const int lim = row ? w.pos0 + tok + 1 - w.skip : 0;
             const int low = max(0, w.pos0 + tok + 1 - p.window) - w.skip;
-            const uint32_t o_at = tmem + lanes + kWtTmemO + (nu & 1) * 128;
-            float m_ref = -INFINITY, l_run = 0.f;
-            for (int si = 0; si < steps; ++si, ++g) {
+            const uint32_t o_at = tmem + lanes + kWtTmemO;
+            float m_own = -INFINITY, l_own = 0.f;  // reference, and sum relative to it
+            for (int si = 0; si < steps; ++si, ++g, s3.next()) {
+                if ((int)(g & 1) != wg)
+                    continue;  // the other warps' step
                 const int st = g & 1;
-                const uint32_t ph = (g >> 1) & 1;
-                const uint32_t s_at = tmem + lanes + st * kWtKeys;
+                const uint32_t s_at = tmem + lanes + s3.i * kWtKeys;
                 const int c0 = si * kWtKeys;
-                const bool full = !w.half(si);
-                ok = wait(sfull(st), ph);
-                if (!ok)
-                    break;
-                tc_fence_after();
-                float sv[kWtKeys];
-                {
-                    uint32_t v[64];
-                    tmem_ld_32x32b_x64(s_at, v);
+                const int halves = w.half(si) ? 1 : 2;
+                // 64 scores of a half, those hidden from this row -inf.  Hidden ones
+                // come in a few steps of a unit and there mostly in one place:
+                // each 32 keys are looked at by themselves.
+                auto load_half = [&](int h, float (&sv)[kWtHalf]) {
+                    uint32_t v[kWtHalf];
+                    tmem_ld_32x32b_x64(s_at + h * kWtHalf, v);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
+                    for (int i = 0; i < kWtHalf; ++i)
                         sv[i] = __uint_as_float(v[i]);
-                }
-                if (full) {
-                    uint32_t v[64];
-                    tmem_ld_32x32b_x64(s_at + 64, v);
 #pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        sv[64 + i] = __uint_as_float(v[i]);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 64; ++i)
-                        sv[64 + i] = -INFINITY;
-                }
-                // hidden keys (steps at a border only): bits of each 32 seen
-                if (lim < c0 + kWtKeys || (low > max(c0, sinks) && sinks < c0 + kWtKeys)) {
-#pragma unroll
-                    for (int b = 0; b < kWtKeys / 32; ++b) {
-                        const int cb = c0 + 32 * b;
+                    for (int q = 0; q < 2; ++q) {
+                        const int cb = c0 + h * kWtHalf + 32 * q;
+                        if (lim >= cb + 32 && (low <= cb || sinks >= cb + 32))
+                            continue;
                         auto below = [&](int c) -> uint32_t {  // bits of keys < c
                             const int k = c - cb;
                             return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
@@ -400,43 +492,65 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         const uint32_t seen = below(lim) & (~below(low) | below(sinks));
 #pragma unroll
                         for (int i = 0; i < 32; ++i)
-                            sv[32 * b + i] = (seen >> i) & 1u ? sv[32 * b + i] : -INFINITY;
+                            sv[32 * q + i] = (seen >> i) & 1u ? sv[32 * q + i] : -INFINITY;
                     }
+                };
+                ok = wait(sfull(s3.i), s3.ph);
+                if (!ok)
+                    break;
+                tc_fence_after();
+                // The loops over halves stay loops: unrolled, the step's code
+                // passes the instruction cache and both sets of warps wait for
+                // it (572 us against 505 for 8,192 rows behind 4,096 tokens).
+                // Reading S twice costs less than holding it.
+                float mx = -INFINITY;  // maximum raw score (the scale is positive)
+#pragma unroll 1
+                for (int h = 0; h < halves; ++h) {
+                    float sv[kWtHalf];
+                    load_half(h, sv);
+                    float m22[22], m8[8];
+#pragma unroll
+                    for (int k = 0; k < 21; ++k)
+                        m22[k] = fmax3(sv[3 * k], sv[3 * k + 1], sv[3 * k + 2]);
+                    m22[21] = fmaxf(sv[63], mx);
+#pragma unroll
+                    for (int k = 0; k < 7; ++k)
+                        m8[k] = fmax3(m22[3 * k], m22[3 * k + 1], m22[3 * k + 2]);
+                    m8[7] = m22[21];
+                    mx = fmax3(fmax3(m8[0], m8[1], m8[2]), fmax3(m8[3], m8[4], m8[5]),
+                               fmaxf(m8[6], m8[7]));
                 }
-                // maximum raw score (the scale is positive)
-                float mx;
-                {
-                    float m[43];
-#pragma unroll
-                    for (int k = 0; k < 42; ++k)
-                        m[k] = fmax3(sv[3 * k], sv[3 * k + 1], sv[3 * k + 2]);
-                    m[42] = fmaxf(sv[126], sv[127]);
-                    float m2[15];
-#pragma unroll
-                    for (int k = 0; k < 14; ++k)
-                        m2[k] = fmax3(m[3 * k], m[3 * k + 1], m[3 * k + 2]);
-                    m2[14] = m[42];
-                    float m3[5];
-#pragma unroll
-                    for (int k = 0; k < 5; ++k)
-                        m3[k] = fmax3(m2[3 * k], m2[3 * k + 1], m2[3 * k + 2]);
-                    mx = fmax3(fmax3(m3[0], m3[1], m3[2]), m3[3], m3[4]) * p.scale_log2;
+                mx *= p.scale_log2;
+                // the reference after the step before (a unit's first: none); it
+                // moves only when a score passes it by 2^kSlack
+                float m_in = -INFINITY;
+                if (g > 0) {
+                    const uint32_t gp = g - 1;
+                    ok = wait(mfull(gp & 1), (gp >> 1) & 1);
+                    if (!ok)
+                        break;
+                    if (si > 0)
+                        m_in = ref_s[(gp & 1) * kWtRows + r];
                 }
-                const bool moved = mx > m_ref + kSlack;
-                float alpha = 1.f;
-                if (moved) {
-                    alpha = exp2f(m_ref - mx);  // 0 while m_ref is -inf
-                    m_ref = mx;
-                    l_run *= alpha;
+                const bool moved = mx > m_in + kSlack;
+                const float m_ref = moved ? mx : m_in;
+                ref_s[st * kWtRows + r] = m_ref;
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(mfull(st));
+                if (m_ref != m_own) {
+                    l_own *= exp2f(m_own - m_ref);  // 0 while m_own is -inf
+                    m_own = m_ref;
                 }
                 // a reference moved: rescale O once the value product before is done
                 if (si > 0 && __any_sync(kFull, moved)) {
-                    const uint32_t gp = g - 1;
-                    ok = wait(ofull(gp & 1), (gp >> 1) & 1);
+                    const Slot3 sp = s3.before();
+                    ok = wait(ofull(sp.i), sp.ph);
                     if (!ok)
                         break;
                     tc_fence_after();
-#pragma unroll
+                    const float alpha = moved ? exp2f(m_in - m_ref) : 1.f;
+#pragma unroll 1
                     for (int c = 0; c < D / 32; ++c) {
                         uint32_t o[32];
                         tmem_ld_32x32b_x32(o_at + c * 32, o);
@@ -450,114 +564,69 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const uint64_t sl2 = pack_f32x2(p.scale_log2, p.scale_log2);
                 const uint64_t nm2 = pack_f32x2(neg_mu, neg_mu);
                 uint64_t acc[2] = {pack_f32x2(0.f, 0.f), pack_f32x2(0.f, 0.f)};
+#pragma unroll 1
+                for (int h = 0; h < halves; ++h) {
+                    float sv[kWtHalf];
+                    load_half(h, sv);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (h == 1 && !full) {
-                        // (nobody waits for this half; its barrier keeps step)
-                        if (lane == 0)
-                            mbar_arrive(pfull(h, st));
-                        break;
-                    }
-                    uint32_t pw[32];
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t pw[16];
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        float e0, e1;
-                        unpack_f32x2(ffma_f32x2(pack_f32x2(sv[64 * h + 2 * i],
-                                                           sv[64 * h + 2 * i + 1]),
-                                                sl2, nm2),
-                                     e0, e1);
-                        const float p0 = exp2f(e0), p1 = exp2f(e1);
-                        acc[i & 1] = fadd_f32x2(acc[i & 1], pack_f32x2(p0, p1));
-                        pw[i] = MmaOp<T>::pack(p0, p1);
+                        for (int i = 0; i < 16; ++i) {
+                            const int k = 32 * c + 2 * i;
+                            float e0, e1;
+                            unpack_f32x2(ffma_f32x2(pack_f32x2(sv[k], sv[k + 1]), sl2, nm2), e0,
+                                         e1);
+                            const float p0 = exp2f(e0), p1 = exp2f(e1);
+                            acc[i & 1] = fadd_f32x2(acc[i & 1], pack_f32x2(p0, p1));
+                            pw[i] = MmaOp<T>::pack(p0, p1);
+                        }
+                        // over the first half of S, which both passes have read
+                        tmem_st_x16_nowait(s_at + 32 * h + 16 * c, pw);
                     }
-                    tmem_st_32x32b_x32(s_at + 64 + 32 * h, pw);
+                    tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0)
-                        mbar_arrive(pfull(h, st));
+                        mbar_arrive(pfull(h, s3.i));
                 }
+                if (halves == 1 && lane == 0)
+                    mbar_arrive(pfull(1, s3.i));  // (nobody waits for it; it keeps step)
                 {
                     float a0, a1, b0, b1;
                     unpack_f32x2(acc[0], a0, a1);
                     unpack_f32x2(acc[1], b0, b1);
-                    l_run += (a0 + a1) + (b0 + b1);
+                    l_own += (a0 + a1) + (b0 + b1);
+                }
+                if (pend_nu >= 0) {
+                    ok = write_rows();
+                    if (!ok)
+                        break;
                 }
             }
             if (!ok)
                 break;
-            // this unit's 1 / l, once unit nu - 2's has been read
+            // this unit's sums, once unit nu - 2's have been read
             const int b = nu & 1;
             if (nu >= 2) {
                 ok = wait(ufree(b), ((nu - 2) >> 1) & 1);
                 if (!ok)
                     break;
             }
-            inv_s[b * kWtRows + r] = l_run > 0.f ? p.out_scale / l_run : l_run;
+            part_l[(2 * b + wg) * kWtRows + r] = l_own;
+            part_m[(2 * b + wg) * kWtRows + r] = m_own;
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(lfull(b));
-            ++nu;
-        }
-    } else if (warp < kWtKeyWarp) {
-        // ===== output warps: O / l of a unit, while the next one is computed ==============
-        wt_regs_output();
-        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-        uint32_t nu = 0;
-        for (int u = blockIdx.x, ku = 0; u < total_units; u = next_unit(u), ++ku) {
-            const WtUnit w = unit_at(ku, u);
-            const bool row = r < tok_unit * G && tok < w.count;
-            T *dst = static_cast<T *>(p.out) +
-                     (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
-            if (w.steps() == 0) {  // no keys: zero rows
-                if (row)
-                    for (int c = 0; c < D / 8; ++c)
-                        reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
-                continue;
-            }
-            const int b = nu & 1;
-            const uint32_t ph = (nu >> 1) & 1;
-            if (!wait(lfull(b), ph) || !wait(ufull(b), ph))
-                break;
-            tc_fence_after();
-            const float inv = inv_s[b * kWtRows + r];
-            const uint32_t o_at = tmem + lanes + kWtTmemO + b * 128;
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t o[64];
-                tmem_ld_32x32b_x64(o_at + c * 64, o);
-                if (c == D / 64 - 1) {
-                    // the buffer is read: the unit after next may write it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(ufree(b));
-                }
-                if (!row)
-                    continue;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = MmaOp<T>::pack(__uint_as_float(o[16 * i + 2 * k]) * inv,
-                                              __uint_as_float(o[16 * i + 2 * k + 1]) * inv);
-                    T *at = dst + c * 64 + 16 * i;
-                    if (out32) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                                         at),
-                                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-                                     "r"(v[5]), "r"(v[6]), "r"(v[7])
-                                     : "memory");
-                    } else {
-                        reinterpret_cast<uint4 *>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-                        reinterpret_cast<uint4 *>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-                    }
-                }
+            if ((int)((g - 1) & 1) != wg) {  // the last step was the other warps'
+                pend = row ? out_row(w) : nullptr;
+                pend_nu = (int)nu;
             }
             ++nu;
         }
+        if (ok && pend_nu >= 0)
+            write_rows();
     } else {
-        wt_regs_others();
         if (warp == kWtKeyWarp || warp == kWtValueWarp) {
             // ===== fetch warps: keys and query tiles (8), values (9) ====================
             // Lane j owns box j / halves and d-half j % halves of every step: it
@@ -565,14 +634,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const bool values = warp == kWtValueWarp;
             const int my_sb = lane / L::kHalves, my_hf = lane % L::kHalves;
             uint32_t g = 0;
-            int qk = 0, qu = blockIdx.x;  // next unit whose query tile goes out
+            Slot3 s2;                     // of step g - 2
+            int qk = 0;                   // next unit whose query tile goes out
             uint32_t nq = 0, nu = 0;      // query tiles issued, units with keys begun
             uint32_t nland0 = 0, nland1 = 0;    // fills of a value stage onto vland
             uint32_t last0 = 0, last1 = 0;      // last fill's barrier per stage (0: none)
             uint32_t last_ph0 = 0, last_ph1 = 0;  // and its phase
             bool ok = true;
-            for (int u = blockIdx.x, ku = 0; u < total_units && ok; u = next_unit(u), ++ku) {
-                const WtUnit w = unit_at(ku, u);
+            WtUnit w;
+            for (int ku = 0; ok && unit_at(ku, w); ++ku) {
                 const int steps = w.steps();
                 const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
                 auto lookup = [&](int si) -> int {
@@ -594,9 +664,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         ent_next = lookup(si + 1);
                     // the stage's step g - 2 is consumed
                     if (g >= 2) {
-                        ok = wait(values ? ofull(st) : sfull(st), ph ^ 1);
+                        ok = wait(values ? ofull(s2.i) : sfull(s2.i), s2.ph);
                         if (!ok)
                             break;
+                        s2.next();
                     }
                     // test hook of the time-out path: a CTA's first key fill is
                     // never issued, so the wait for it runs out
@@ -627,8 +698,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     // on for the next unit's.
                     if (!values) {
                         const uint32_t due = nu + (si > 0 ? 2 : 1);
-                        while (nq < due && qu < total_units) {
-                            const WtUnit wq = unit_at(qk, qu);
+                        WtUnit wq;
+                        while (nq < due && unit_at(qk, wq)) {
                             if (wq.kend > 0) {
                                 const uint32_t qb = qfull(nq & 1);
                                 if (lane == 0)
@@ -640,7 +711,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                                 &tmap_q, qb, 64 * lane, wq.kh * G, wq.row0);
                                 ++nq;
                             }
-                            qu = next_unit(qu);
                             ++qk;
                         }
                     }
@@ -662,8 +732,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             uint32_t g = 0;
             uint32_t nland0 = 0, nland1 = 0;
             bool ok = true;
-            for (int u = blockIdx.x, ku = 0; u < total_units && ok; u = next_unit(u), ++ku) {
-                const WtUnit w = unit_at(ku, u);
+            WtUnit w;
+            for (int ku = 0; ok && unit_at(ku, w); ++ku) {
                 const int steps = w.steps();
                 for (int si = 0; si < steps; ++si, ++g) {
                     if (!w.hidden(si))
@@ -697,104 +767,89 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 }
             }
         } else {
-            // ===== tensor-core warp: one elected lane issues ================================
-            // S of step g + 1 goes out before the value product of step g, so it
-            // is computed while the softmax of step g runs.
+            // ===== tensor-core warps: scores (10), value products (11) ======================
+            // One elected lane of each issues.  An MMA takes its warp ~60 cycles
+            // to issue, about what it takes to run, and every wait some tens:
+            // one warp for both would be what the kernel waits for.
+            const bool scores = warp == kWtScoreWarp;
             const uint64_t desc_q0 = smem_desc_sw128(sbase + L::kQ, 16, 1024);
             const uint64_t desc_k0 = smem_desc_sw128(sbase + L::kK, 16, 1024);
             const uint64_t desc_v0 = smem_desc_sw128(sbase + L::kV, L::kHalfBytes, 1024);
-            struct Cursor {
-                int u, ku;    // unit and its number in this CTA
-                int kend, si; // its compact keys, step (kend 0: no more units)
-                uint32_t nu;  // units with keys before it
-            };
-            auto open = [&](Cursor &c) {  // the first unit from c.u on that has keys
-                c.kend = 0;
-                c.si = 0;
-                for (; c.u < total_units; c.u = next_unit(c.u), ++c.ku) {
-                    c.kend = unit_at(c.ku, c.u).kend;
-                    if (c.kend > 0)
-                        return;
-                }
-            };
-            auto advance = [&](Cursor &c) {
-                if (++c.si * kWtKeys >= c.kend) {
-                    c.u = next_unit(c.u);
-                    ++c.ku;
-                    ++c.nu;
-                    open(c);
-                }
-            };
-            // S of step gs, at cursor c
-            auto issue_s = [&](const Cursor &c, uint32_t gs) -> bool {
-                const int st = gs & 1;
-                if (!wait(kfull(st), (gs >> 1) & 1) ||
-                    (c.si == 0 && !wait(qfull(c.nu & 1), (c.nu >> 1) & 1)) ||
-                    (gs >= 2 && !wait(ofull(st), ((gs - 2) >> 1) & 1)))
-                    return false;
-                tc_fence_after();
-                const uint64_t dq = desc_q0 + (uint64_t)(((c.nu & 1) * L::kTile) >> 4);
-                const uint64_t dk = desc_k0 + (uint64_t)((st * L::kTile) >> 4);
-                const bool full = c.kend - c.si * kWtKeys > kWtHalf;
-                if (elect_one()) {
+            uint32_t g = 0, nu = 0;
+            Slot3 s3;
+            bool ok = true;
+            WtUnit w;
+            for (int ku = 0; ok && unit_at(ku, w); ++ku) {
+                const int kend = w.kend;
+                if (kend <= 0)
+                    continue;
+                const int b = nu & 1;
+                const uint32_t bph = (nu >> 1) & 1;
+                if (scores) {
+                    ok = wait(qfull(b), bph);
+                    const uint64_t dq = desc_q0 + (uint64_t)((b * L::kTile) >> 4);
+#pragma unroll 1
+                    for (int rem = kend; rem > 0 && ok; rem -= kWtKeys, ++g, s3.next()) {
+                        const int st = g & 1;
+                        // keys landed; the columns' last value product is done
+                        ok = wait(kfull(st), (g >> 1) & 1) &&
+                             (g < 3 || wait(ofull(s3.i), s3.ph ^ 1));
+                        if (!ok)
+                            break;
+                        tc_fence_after();
+                        const uint64_t dk = desc_k0 + (uint64_t)((st * L::kTile) >> 4);
+                        const uint32_t at = tmem + s3.i * kWtKeys;
+                        const uint32_t idesc = rem > kWtHalf ? kIdescS : kIdescSHalf;
+                        if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < KT; ++kk) {
-                        const uint32_t o = ((kk >> 2) * L::kHalfBytes + (kk & 3) * 32) >> 4;
-                        tc_mma_ss(tmem + st * kWtKeys, dq + o, dk + o,
-                                  full ? kIdescS : kIdescSHalf, kk > 0 ? 1u : 0u);
+                            for (int kk = 0; kk < KT; ++kk) {
+                                const uint32_t o = ((kk >> 2) * L::kHalfBytes + (kk & 3) * 32) >> 4;
+                                tc_mma_ss(at, dq + o, dk + o, idesc, kk > 0 ? 1u : 0u);
+                            }
+                            tc_commit(sfull(s3.i));
+                        }
                     }
-                    tc_commit(sfull(st));
-                }
-                return true;
-            };
-            Cursor c{(int)blockIdx.x, 0, 0, 0, 0u};
-            open(c);
-            bool ok = c.kend == 0 || issue_s(c, 0);
-            for (uint32_t g = 0; ok && c.kend > 0; ++g) {
-                const int st = g & 1;
-                const uint32_t ph = (g >> 1) & 1;
-                Cursor n = c;
-                advance(n);
-                if (n.kend > 0 && !issue_s(n, g + 1)) {
-                    ok = false;
-                    break;
-                }
-                // the value product of step g; a unit's first waits until its O
-                // buffer has been read
-                const uint32_t b = c.nu & 1;
-                ok = wait(vfull(st), ph) &&
-                     (c.si > 0 || c.nu < 2 || wait(ufree(b), ((c.nu - 2) >> 1) & 1));
-                const bool full = c.kend - c.si * kWtKeys > kWtHalf;
-                const uint64_t dv = desc_v0 + (uint64_t)((st * L::kTile) >> 4);
+                } else {
+                    // a unit's first value product waits until the O of the unit
+                    // before has been read
+                    ok = nu == 0 || wait(ufree(b ^ 1), ((nu - 1) >> 1) & 1);
+#pragma unroll 1
+                    for (int rem = kend; rem > 0 && ok; rem -= kWtKeys, ++g, s3.next()) {
+                        const int st = g & 1;
+                        ok = wait(vfull(st), (g >> 1) & 1);
+                        const int halves = rem > kWtHalf ? 2 : 1;
+                        uint64_t dv = desc_v0 + (uint64_t)((st * L::kTile) >> 4);
+                        uint32_t p_at = tmem + s3.i * kWtKeys;
+#pragma unroll 1
+                        for (int h = 0; h < halves && ok; ++h) {
+                            ok = wait(pfull(h, s3.i), s3.ph);
+                            if (!ok)
+                                break;
+                            tc_fence_after();
+                            if (elect_one()) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (!ok || (h == 1 && !full))
-                        break;
-                    ok = wait(pfull(h, st), ph);
-                    if (!ok)
-                        break;
-                    tc_fence_after();
-                    if (elect_one()) {
-#pragma unroll
-                        for (int ks = 0; ks < kWtHalf / 16; ++ks)
-                            tc_mma_ts(tmem + kWtTmemO + b * 128,
-                                      tmem + st * kWtKeys + 64 + 32 * h + ks * 8,
-                                      dv + (uint64_t)(((4 * h + ks) * 2048) >> 4), kIdescO,
-                                      (c.si > 0 || h > 0 || ks > 0) ? 1u : 0u);
-                        if (h == 1 || !full) {
-                            tc_commit(ofull(st));
-                            if ((c.si + 1) * kWtKeys >= c.kend)
-                                tc_commit(ufull(b));
+                                for (int ks = 0; ks < kWtHalf / 16; ++ks)
+                                    tc_mma_ts(tmem + kWtTmemO, p_at + ks * 8,
+                                              dv + (uint64_t)((ks * 2048) >> 4), kIdescO,
+                                              (rem < kend || h > 0 || ks > 0) ? 1u : 0u);
+                                if (h == halves - 1) {
+                                    tc_commit(ofull(s3.i));
+                                    if (rem <= kWtKeys)
+                                        tc_commit(ufull(b));
+                                }
+                            }
+                            dv += (kWtHalf * 128) >> 4;
+                            p_at += 32;
                         }
                     }
                 }
-                c = n;
+                ++nu;
             }
             // every tensor-core operation this warp issued has finished
             if (elect_one())
-                tc_commit(mma_drain);
+                tc_commit(mma_drain(scores ? 0 : 1));
             __syncwarp();
-            mbar_wait_bounded(mma_drain, 0, kDrainWaitNs);
+            mbar_wait_bounded(mma_drain(scores ? 0 : 1), 0, kDrainWaitNs);
         }
     }
     pdl_launch_dependents();
