@@ -19,9 +19,7 @@
 //    scores of step g + 1 are computed while the softmax of step g runs; P
 //    goes over the upper half of its S as 16-bit pairs, in two halves of 64
 //    keys, so the value product starts on the first while the second is
-//    computed.  The next unit's products start into the other O buffer while
-//    this unit's rows are written: with windows a unit has few steps, and its
-//    end would cost as much as several of them.
+//    computed.
 //  * A step's softmax takes ~1,500 cycles of four warps, its products ~1,000 of
 //    the tensor cores, so two sets of four warps take the steps in turn.  The
 //    rows' reference maximum goes from one to the other through shared memory
@@ -59,11 +57,11 @@ namespace pa {
 constexpr int kWtRows = 128;      // rows of a tile (M of the MMAs)
 constexpr int kWtKeys = 128;      // keys of a step
 constexpr int kWtHalf = 64;       // keys of a half step
-constexpr int kWtKeyWarp = 8;       // warps 0-3 and 4-7: softmax of even and odd steps
-constexpr int kWtValueWarp = 9;
-constexpr int kWtScoreWarp = 10;
-constexpr int kWtFixWarp = 12;      // (11: value products)
-constexpr int kWtThreads = 416;
+constexpr int kWtOutWarp = 8;       // warps 0-3 and 4-7: softmax of even and odd steps
+constexpr int kWtKeyWarp = 12;      // 8-11: output rows (8: hidden value rows too)
+constexpr int kWtValueWarp = 13;
+constexpr int kWtScoreWarp = 14;
+constexpr int kWtThreads = 512;     // (15: value products)
 constexpr uint32_t kWtTmemCols = 512;  // S at 0, 128 and 256 (P over each), O at 384
 constexpr uint32_t kWtTmemO = 384;
 constexpr int kWtOrderBuckets = 64;
@@ -384,80 +382,17 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int tok = r / G, hg = r - (r / G) * G;
     const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
 
-    if (warp < kWtKeyWarp) {
+    if (warp < kWtOutWarp) {
         // ===== softmax warps: warps 0-3 the even steps, 4-7 the odd ones ====================
         const int wg = warp >> 2;
-        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
         uint32_t g = 0, nu = 0;  // steps, units with keys
         Slot3 s3;
         bool ok = true;
-        auto out_row = [&](const WtUnit &w) -> T * {
-            return static_cast<T *>(p.out) + (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
-        };
-        // A unit's rows, O / l, written by the warps that did not have its last
-        // step, after their first step of the next unit.
-        T *pend = nullptr;      // this thread's row (null: not a row)
-        int pend_nu = -1;       // unit waiting to be written (-1: none)
-        auto write_rows = [&]() -> bool {
-            const int b = pend_nu & 1;
-            const uint32_t ph = (pend_nu >> 1) & 1;
-            pend_nu = -1;
-            if (!wait(lfull(b), ph) || !wait(ufull(b), ph))
-                return false;
-            tc_fence_after();
-            // O is relative to the last step's reference, which the other
-            // warps' sum has, and this warp's reference is not above it
-            const float l0 = part_l[(2 * b + (wg ^ 1)) * kWtRows + r];
-            const float l1 = part_l[(2 * b + wg) * kWtRows + r];
-            const float m0 = part_m[(2 * b + (wg ^ 1)) * kWtRows + r];
-            const float m1 = part_m[(2 * b + wg) * kWtRows + r];
-            const float l = l1 == 0.f ? l0 : l0 + l1 * exp2f(m1 - m0);
-            const float inv = l > 0.f ? p.out_scale / l : l;  // (0 for a row without keys)
-            const uint32_t o_at = tmem + lanes + kWtTmemO;
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
-                tmem_ld_32x32b_x32(o_at + c * 32, o);
-                if (c == D / 32 - 1) {
-                    // O is read: the next unit's value products may write it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(ufree(b));
-                }
-                if (pend == nullptr)
-                    continue;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t v[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        v[k] = MmaOp<T>::pack(__uint_as_float(o[16 * i + 2 * k]) * inv,
-                                              __uint_as_float(o[16 * i + 2 * k + 1]) * inv);
-                    T *at = pend + c * 32 + 16 * i;
-                    if (out32) {
-                        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                                         at),
-                                     "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]),
-                                     "r"(v[5]), "r"(v[6]), "r"(v[7])
-                                     : "memory");
-                    } else {
-                        reinterpret_cast<uint4 *>(at)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-                        reinterpret_cast<uint4 *>(at)[1] = make_uint4(v[4], v[5], v[6], v[7]);
-                    }
-                }
-            }
-            return true;
-        };
         WtUnit w;
         for (int ku = 0; ok && unit_at(ku, w); ++ku) {
             const int steps = w.steps();
-            if (steps == 0) {  // no keys: zero rows
-                if (wg == 0 && r < tok_unit * G && tok < w.count)
-                    for (int c = 0; c < D / 8; ++c)
-                        reinterpret_cast<uint4 *>(out_row(w))[c] = make_uint4(0, 0, 0, 0);
-                continue;
-            }
+            if (steps == 0)
+                continue;  // (the output warps write its zero rows)
             const bool row = r < tok_unit * G && tok < w.count;
             // compact: one past the row's own position, its window's start
             const int lim = row ? w.pos0 + tok + 1 - w.skip : 0;
@@ -471,28 +406,36 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const uint32_t s_at = tmem + lanes + s3.i * kWtKeys;
                 const int c0 = si * kWtKeys;
                 const int halves = w.half(si) ? 1 : 2;
-                // 64 scores of a half, those hidden from this row -inf.  Hidden ones
-                // come in a few steps of a unit and there mostly in one place:
-                // each 32 keys are looked at by themselves.
                 auto load_half = [&](int h, float (&sv)[kWtHalf]) {
                     uint32_t v[kWtHalf];
                     tmem_ld_32x32b_x64(s_at + h * kWtHalf, v);
 #pragma unroll
                     for (int i = 0; i < kWtHalf; ++i)
                         sv[i] = __uint_as_float(v[i]);
+                };
+                // Scores hidden from this row become -inf, and go back so: they
+                // come in a few steps of a unit and there mostly in one place,
+                // so each 32 keys are looked at by themselves.
+                auto hide = [&](int h, float (&sv)[kWtHalf]) {
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
                         const int cb = c0 + h * kWtHalf + 32 * q;
-                        if (lim >= cb + 32 && (low <= cb || sinks >= cb + 32))
+                        const bool open = lim >= cb + 32 && (low <= cb || sinks >= cb + 32);
+                        if (__all_sync(kFull, open))
                             continue;
                         auto below = [&](int c) -> uint32_t {  // bits of keys < c
                             const int k = c - cb;
                             return k >= 32 ? 0xffffffffu : k <= 0 ? 0u : (1u << k) - 1u;
                         };
                         const uint32_t seen = below(lim) & (~below(low) | below(sinks));
+                        uint32_t v[32];
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            sv[32 * q + i] = (seen >> i) & 1u ? sv[32 * q + i] : -INFINITY;
+                        for (int i = 0; i < 32; ++i) {
+                            float &x = sv[32 * q + i];
+                            x = (seen >> i) & 1u ? x : -INFINITY;
+                            v[i] = __float_as_uint(x);
+                        }
+                        tmem_st_32x32b_x32(s_at + h * kWtHalf + 32 * q, v);
                     }
                 };
                 ok = wait(sfull(s3.i), s3.ph);
@@ -508,6 +451,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 for (int h = 0; h < halves; ++h) {
                     float sv[kWtHalf];
                     load_half(h, sv);
+                    hide(h, sv);
                     float m22[22], m8[8];
 #pragma unroll
                     for (int k = 0; k < 21; ++k)
@@ -598,11 +542,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     unpack_f32x2(acc[1], b0, b1);
                     l_own += (a0 + a1) + (b0 + b1);
                 }
-                if (pend_nu >= 0) {
-                    ok = write_rows();
-                    if (!ok)
-                        break;
-                }
             }
             if (!ok)
                 break;
@@ -618,14 +557,120 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(lfull(b));
-            if ((int)((g - 1) & 1) != wg) {  // the last step was the other warps'
-                pend = row ? out_row(w) : nullptr;
-                pend_nu = (int)nu;
-            }
             ++nu;
         }
-        if (ok && pend_nu >= 0)
-            write_rows();
+    } else if (warp < kWtKeyWarp) {
+        // ===== output warps: O / l of a unit, while the next one is computed ==============
+        // Warp 8 also zeroes, once landed, the value rows that no row of a unit
+        // sees, before the value-product warp may read them.
+        const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+        uint32_t g = 0, nu = 0;
+        uint32_t nland0 = 0, nland1 = 0;
+        bool ok = true;
+        auto zero_hidden = [&](const WtUnit &w, int si, int st) -> bool {
+            if (!wait(vland(st), (st ? nland1 : nland0) & 1))
+                return false;
+            ++(st ? nland1 : nland0);
+            const int c0 = si * kWtKeys;
+            const int rows = w.half(si) ? kWtHalf : kWtKeys;
+            const uint32_t vb = sbase + L::kV + st * L::kTile;
+#pragma unroll 1
+            for (int i = lane; i < rows; i += 32) {
+                const int c = c0 + i;
+                if (!(c >= w.kend || (c >= w.hide0 && c < w.hide1)))
+                    continue;
+#pragma unroll
+                for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                         vb + hf * L::kHalfBytes + i * 128 + (((k + i) & 7) << 4)),
+                                     "r"(0)
+                                     : "memory");
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(vfull(st));
+            return true;
+        };
+        // A unit's rounded rows are stored after the next unit's first step has
+        // its value rows: those are what the tensor cores may be waiting for.
+        uint32_t v[D / 2];
+        T *pend = nullptr;
+        auto store_rows = [&]() {
+            if (pend == nullptr)
+                return;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                T *at = pend + 16 * i;
+                if (out32) {
+                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
+                                     at),
+                                 "r"(v[8 * i]), "r"(v[8 * i + 1]), "r"(v[8 * i + 2]),
+                                 "r"(v[8 * i + 3]), "r"(v[8 * i + 4]), "r"(v[8 * i + 5]),
+                                 "r"(v[8 * i + 6]), "r"(v[8 * i + 7])
+                                 : "memory");
+                } else {
+                    reinterpret_cast<uint4 *>(at)[0] =
+                        make_uint4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
+                    reinterpret_cast<uint4 *>(at)[1] =
+                        make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+                }
+            }
+            pend = nullptr;
+        };
+        WtUnit w;
+        for (int ku = 0; ok && unit_at(ku, w); ++ku) {
+            const int steps = w.steps();
+            const bool row = r < tok_unit * G && tok < w.count;
+            T *dst = static_cast<T *>(p.out) +
+                     (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
+            if (steps == 0) {  // no keys: zero rows
+                if (row)
+                    for (int c = 0; c < D / 8; ++c)
+                        reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+                continue;
+            }
+            for (int si = 0; si < steps && ok; ++si, ++g) {
+                if (warp == kWtOutWarp && w.hidden(si))
+                    ok = zero_hidden(w, si, g & 1);
+                if (si == 0)
+                    store_rows();
+            }
+            const int b = nu & 1;
+            const uint32_t ph = (nu >> 1) & 1;
+            ++nu;
+            ok = ok && wait(lfull(b), ph) && wait(ufull(b), ph);
+            if (!ok)
+                break;
+            tc_fence_after();
+            // O is relative to the last step's reference, which the softmax
+            // warps of that step have; the others' is not above it
+            const int a0 = (2 * b + (int)((g - 1) & 1)) * kWtRows + r;
+            const int a1 = (2 * b + (int)(g & 1)) * kWtRows + r;
+            const float l0 = part_l[a0], l1 = part_l[a1];
+            const float l = l1 == 0.f ? l0 : l0 + l1 * exp2f(part_m[a1] - part_m[a0]);
+            const float inv = l > 0.f ? p.out_scale / l : l;  // (0 for a row without keys)
+            const uint32_t o_at = tmem + lanes + kWtTmemO;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(o_at + c * 32, o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                    v[16 * c + k] = MmaOp<T>::pack(__uint_as_float(o[2 * k]) * inv,
+                                                   __uint_as_float(o[2 * k + 1]) * inv);
+            }
+            // O is read: the next unit's value products may write it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(ufree(b));
+            if (row)
+                pend = dst;
+        }
+        store_rows();
     } else {
         if (warp == kWtKeyWarp || warp == kWtValueWarp) {
             // ===== fetch warps: keys and query tiles (8), values (9) ====================
@@ -727,45 +772,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 mbar_wait_bounded(qfull((nq - 1) & 1), ((nq - 1) >> 1) & 1, kDrainWaitNs);
             if (nq > 1)
                 mbar_wait_bounded(qfull((nq - 2) & 1), ((nq - 2) >> 1) & 1, kDrainWaitNs);
-        } else if (warp == kWtFixWarp) {
-            // ===== hidden value rows: zeroed once landed, before the MMA warp may read ====
-            uint32_t g = 0;
-            uint32_t nland0 = 0, nland1 = 0;
-            bool ok = true;
-            WtUnit w;
-            for (int ku = 0; ok && unit_at(ku, w); ++ku) {
-                const int steps = w.steps();
-                for (int si = 0; si < steps; ++si, ++g) {
-                    if (!w.hidden(si))
-                        continue;
-                    const int st = g & 1;
-                    ok = wait(vland(st), (st ? nland1 : nland0) & 1);
-                    if (!ok)
-                        break;
-                    ++(st ? nland1 : nland0);
-                    const int c0 = si * kWtKeys;
-                    const int rows = w.half(si) ? kWtHalf : kWtKeys;
-                    const uint32_t vb = sbase + L::kV + st * L::kTile;
-                    for (int i = lane; i < rows; i += 32) {
-                        const int c = c0 + i;
-                        if (!(c >= w.kend || (c >= w.hide0 && c < w.hide1)))
-                            continue;
-#pragma unroll
-                        for (int hf = 0; hf < L::kHalves; ++hf)
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                                 vb + hf * L::kHalfBytes + i * 128 +
-                                                 (((k + i) & 7) << 4)),
-                                             "r"(0)
-                                             : "memory");
-                    }
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane == 0)
-                        mbar_arrive(vfull(st));
-                }
-            }
         } else {
             // ===== tensor-core warps: scores (10), value products (11) ======================
             // One elected lane of each issues.  An MMA takes its warp ~60 cycles
