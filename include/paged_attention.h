@@ -487,7 +487,8 @@ PA_API pa_status pa_prefill_attention_fp8(void *out, const void *query, const vo
  *   window         : >= 1;  num_sinks : >= 0 (PA_ERR_INVALID_ARG otherwise)
  *   partition_size : as pa_decode_attention, in visible tokens rounded to
  *                    16-token tiles, so the number of partitions is bounded
- *                    by window and num_sinks, not by the context
+ *                    by window and num_sinks, not by the context; a remainder
+ *                    of less than half a partition joins the one before
  *   workspace      : >= pa_window_workspace_bytes(...) bytes, 256-byte
  *                    aligned, its first bytes (the arrival counters of
  *                    pa_decode_workspace_bytes, the same region) zeroed
