@@ -488,7 +488,8 @@ PA_API pa_status pa_prefill_attention_fp8(void *out, const void *query, const vo
  *   partition_size : as pa_decode_attention, in visible tokens rounded to
  *                    16-token tiles, so the number of partitions is bounded
  *                    by window and num_sinks, not by the context; a remainder
- *                    of less than half a partition joins the one before
+ *                    of less than half a partition joins the one before, and
+ *                    partitions are longer where fewer of them fill the GPU
  *   workspace      : >= pa_window_workspace_bytes(...) bytes, 256-byte
  *                    aligned, its first bytes (the arrival counters of
  *                    pa_decode_workspace_bytes, the same region) zeroed

@@ -778,14 +778,15 @@ static pa_status launch_window_pass(const WindowParams &prm, const CUtensorMap &
 
 template <typename T, typename KV, int D, int NT>
 static pa_status launch_window(const WindowParams &prm, const CUtensorMap &mk,
-                               const CUtensorMap &mv, cudaStream_t stream, long long max_units)
+                               const CUtensorMap &mv, cudaStream_t stream, int max_parts)
 {
+    const long long max_units = (long long)prm.num_seqs * prm.num_kv_heads * max_parts;
     constexpr int kStages = sizeof(KV) == 1 ? kWinStagesFp8 : kWinStages;
     pa_status st = launch_window_pass<T, KV, D, NT, kStages>(prm, mk, mv, stream, max_units);
     // batches whose per-sequence arrays do not fit next to the default rings
     if (st == PA_ERR_UNSUPPORTED)
         st = launch_window_pass<T, KV, D, NT, 1>(prm, mk, mv, stream, max_units);
-    if (st != PA_OK || prm.max_parts <= kMergeMax)
+    if (st != PA_OK || max_parts <= kMergeMax)
         return st;
     DecodeParams reduce = prm;
     reduce.context_lens = prm.len_out;
@@ -795,14 +796,14 @@ static pa_status launch_window(const WindowParams &prm, const CUtensorMap &mk,
 template <typename T, typename KV>
 static pa_status launch_window_as(const WindowParams &prm, const CUtensorMap &mk,
                                   const CUtensorMap &mv, cudaStream_t stream,
-                                  long long max_units, int head_dim)
+                                  int max_parts, int head_dim)
 {
     const bool wide = prm.group > 8;
     if (head_dim == 128)
-        return wide ? launch_window<T, KV, 128, 2>(prm, mk, mv, stream, max_units)
-                    : launch_window<T, KV, 128, 1>(prm, mk, mv, stream, max_units);
-    return wide ? launch_window<T, KV, 64, 2>(prm, mk, mv, stream, max_units)
-                : launch_window<T, KV, 64, 1>(prm, mk, mv, stream, max_units);
+        return wide ? launch_window<T, KV, 128, 2>(prm, mk, mv, stream, max_parts)
+                    : launch_window<T, KV, 128, 1>(prm, mk, mv, stream, max_parts);
+    return wide ? launch_window<T, KV, 64, 2>(prm, mk, mv, stream, max_parts)
+                : launch_window<T, KV, 64, 1>(prm, mk, mv, stream, max_parts);
 }
 
 // Longest compact length of any sequence: the first tokens' tiles, and the
@@ -861,14 +862,40 @@ static pa_status run_window(void *out, const void *query, const void *key_cache,
     // (positions of a whole tile past the last one stay in 32 bits)
     if ((long long)max_blocks_per_seq * block_size > (1ll << 31) - 256)
         return PA_ERR_UNSUPPORTED;
-    if (prm.max_parts > kMergeMax) {
-        size_t len_off = 0;
-        const WorkspaceLayout wl = window_workspace(num_seqs, num_heads, num_kv_heads, head_dim,
-                                                    prm.max_parts, &len_off);
-        if (workspace_bytes < wl.total)
-            return PA_ERR_WORKSPACE;
-        prm.len_out = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + len_off);
+    size_t len_off = 0;
+    if (prm.max_parts > 1 &&
+        workspace_bytes < window_workspace(num_seqs, num_heads, num_kv_heads, head_dim,
+                                           prm.max_parts, &len_off)
+                              .total)
+        return PA_ERR_WORKSPACE;
+    // Partitions are there to give every CTA work.  Where the sequences and KV
+    // heads by themselves give less than one unit a CTA, more partitions than
+    // fill one round of CTAs only add partials and a second, nearly empty round
+    // (16 sequences, 8 KV heads, window 4,096, FP8 pools: partitions of 512
+    // 39.8 us, of 1,376, one round, 29.9; 16-bit pools 50.4 and 43.9).
+    if (prm.max_parts > 1) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess)
+            return record_cuda(e);
+        DeviceInfo info;
+        const pa_status di = device_info(dev, &info);
+        if (di != PA_OK)
+            return di;
+        const long long ctas =
+            (long long)info.sms * (prm.group > 8 ? 1 : fp8 ? kWinMinBlocksFp8 : kWinMinBlocks);
+        const long long per = ctas / ((long long)num_seqs * num_kv_heads);
+        if (per >= 1) {
+            const long long t = kTileTokens;
+            const long long fill = (compact + per * t - 1) / (per * t) * t;
+            prm.part_tokens = (int)std::max<long long>(prm.part_tokens, fill);
+        }
     }
+    const int parts = window_parts(compact, prm.part_tokens) > 1
+                          ? window_parts(compact, prm.part_tokens)
+                          : 1;
+    if (parts > kMergeMax)
+        prm.len_out = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + len_off);
     prm.max_context_len = max_context_len;
     prm.window = window;
     // (first tokens past the tables' reach hide nothing)
@@ -885,16 +912,14 @@ static pa_status run_window(void *out, const void *query, const void *key_cache,
     if (!encode_pool_map(&mk, key_cache, pool, num_blocks, block_size, num_kv_heads, head_dim) ||
         !encode_pool_map(&mv, value_cache, pool, num_blocks, block_size, num_kv_heads, head_dim))
         return PA_ERR_CUDA;
-    const long long max_units = (long long)num_seqs * num_kv_heads * prm.max_parts;
     cudaStream_t st = as_stream(stream);
     using B16 = __nv_bfloat16;
     if (fp8)
         return dtype == PA_BF16
-                   ? launch_window_as<B16, uint8_t>(prm, mk, mv, st, max_units, head_dim)
-                   : launch_window_as<__half, uint8_t>(prm, mk, mv, st, max_units, head_dim);
-    return dtype == PA_BF16 ? launch_window_as<B16, B16>(prm, mk, mv, st, max_units, head_dim)
-                            : launch_window_as<__half, __half>(prm, mk, mv, st, max_units,
-                                                               head_dim);
+                   ? launch_window_as<B16, uint8_t>(prm, mk, mv, st, parts, head_dim)
+                   : launch_window_as<__half, uint8_t>(prm, mk, mv, st, parts, head_dim);
+    return dtype == PA_BF16 ? launch_window_as<B16, B16>(prm, mk, mv, st, parts, head_dim)
+                            : launch_window_as<__half, __half>(prm, mk, mv, st, parts, head_dim);
 }
 
 } // namespace pa
