@@ -2,6 +2,8 @@
 // windowed chunked-attention kernels (16-bit pools, FP8 pools).
 #pragma once
 
+#include <type_traits>
+
 #include "pa_decode_common.cuh"
 #include "pa_tcgen05.cuh"
 
@@ -23,6 +25,7 @@ struct WindowMqParams {
     int sink_tokens;    // num_sinks rounded up to whole boxes
     float scale_log2;   // scale * log2(e) (times the K scale for FP8 pools)
     float out_scale;    // applied to the output (the V scale for FP8 pools)
+    const void *key_cache, *value_cache;  // (for rows computed anew)
     int num_tokens;     // rows of query and out (T)
     int q_tma;          // FP8 kernel: each unit's query tile arrives by TMA
     int ordered;        // 16-bit kernel: units numbered longest first
@@ -113,6 +116,128 @@ __device__ __forceinline__ int window_order_key(const WindowMqParams &p, int s, 
     const unsigned keys = min((unsigned)ctx, (unsigned)min(p.sink_tokens, ctx) +
                                                  (unsigned)min(p.window, ctx));
     return buckets - 1 - (int)min((keys + 63) / 64, (unsigned)buckets - 1);
+}
+
+// ---- rows that a hidden value made non-finite -----------------------------------
+//
+// The tensor cores multiply a key that is hidden from a row by a weight of 0,
+// which is not 0 when its value is infinite or NaN, and a value row that some
+// row of the tile sees cannot be zeroed.  So a row that comes out non-finite is
+// looked at again, by one warp: if the values it sees account for every
+// non-finite element (the newest are read first, so a sequence that has
+// diverged is done at once) it stays; else it is computed anew from what it
+// sees.  Only rows of such tiles pay for this.
+
+template <typename T> __device__ __forceinline__ float window_float(T x)
+{
+    if constexpr (std::is_same<T, __half>::value)
+        return __half2float(x);
+    else
+        return __bfloat162float(x);
+}
+
+// This lane's E = D / 32 elements of a pool row, as numbers.
+template <typename T, int E, bool kFp8>
+__device__ __forceinline__ void window_pool_row(const void *pool, size_t elem, float (&x)[E])
+{
+    if constexpr (kFp8) {
+        const uint8_t *c = static_cast<const uint8_t *>(pool) + elem;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+            const uint32_t w = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t *>(c + e));
+            x[e] = __half2float(__ushort_as_half((unsigned short)(w & 0xffffu)));
+            x[e + 1] = __half2float(__ushort_as_half((unsigned short)(w >> 16)));
+        }
+    } else {
+        const T *v = static_cast<const T *>(pool) + elem;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            x[e] = window_float<T>(v[e]);
+    }
+}
+
+// A finite test that fast-math arithmetic does not fold away.
+__device__ __forceinline__ bool window_finite(float x)
+{
+    return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
+}
+
+// One row (position pos of the sequence with this table, KV head kh), by a
+// warp: out and query are its D elements.
+template <typename T, int D, bool kFp8>
+__device__ __noinline__ void window_mend_row(const WindowMqParams &p, const void *key_cache,
+                                             const void *value_cache, const int32_t *table,
+                                             int kh, int pos, const T *query, T *out)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int low = max(0, pos + 1 - p.window);     // [low, pos] and [0, first) are seen
+    const int first = min(p.num_sinks, low);
+    const int seen = pos + 1 - low + first;
+    // the i-th key seen, newest first; its place in the pools, or -1
+    auto place = [&](int i) -> long long {
+        const int t = i <= pos - low ? pos - i : first - 1 - (i - (pos + 1 - low));
+        const int b = table[t >> p.block_shift];
+        if (b < 0 || b >= p.num_blocks)
+            return -1;
+        return (((long long)b * p.block_size + (t & (p.block_size - 1))) * p.num_kv_heads + kh) *
+                   D + lane * E;
+    };
+    // elements that are non-finite and not yet accounted for
+    unsigned open = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        if (!window_finite(window_float<T>(out[lane * E + e])))
+            open |= 1u << e;
+    for (int i = 0; i < seen; ++i) {
+        if (!__any_sync(kFull, open != 0))
+            return;
+        const long long at = place(i);
+        if (at < 0)
+            return;  // (a bad table entry: flagged, the row is undefined)
+        float v[E];
+        window_pool_row<T, E, kFp8>(value_cache, at, v);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (!window_finite(v[e]))
+                open &= ~(1u << e);
+    }
+    if (!__any_sync(kFull, open != 0))
+        return;
+    float q[E], o[E], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) {
+        q[e] = window_float<T>(query[lane * E + e]);
+        o[e] = 0.f;
+    }
+    for (int i = 0; i < seen; ++i) {
+        const long long at = place(i);
+        if (at < 0)
+            return;
+        float k[E], v[E];
+        window_pool_row<T, E, kFp8>(key_cache, at, k);
+        window_pool_row<T, E, kFp8>(value_cache, at, v);
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            s = fmaf(q[e], k[e], s);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            s += __shfl_xor_sync(kFull, s, off);
+        s *= p.scale_log2;
+        const float mn = fmaxf(m, s);
+        const float a = mn == m ? 1.f : exp2f(m - mn);  // (m: -inf at first)
+        const float w = s == mn ? 1.f : exp2f(s - mn);
+        m = mn;
+        l = l * a + w;
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = o[e] * a + w * v[e];
+    }
+    const float inv = p.out_scale / l;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+        out[lane * E + e] = MmaOp<T>::from_float(o[e] * inv);
 }
 
 // The windowed chunk over 16-bit pools (pa_window_tiles.cu).

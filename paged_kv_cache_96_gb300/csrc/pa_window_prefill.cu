@@ -700,6 +700,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             // epilogue: this thread's row of O / l (TMEM loads are warp-wide)
             const float inv = (w.n > 0 && l_run > 0.f) ? p.out_scale / l_run : 0.f;
             const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
+            bool bad = !window_finite(inv);
 #pragma unroll
             for (int c = 0; c < D / 64; ++c) {
                 uint32_t r[64];
@@ -712,6 +713,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 }
                 if (ooff < 0)
                     continue;
+#pragma unroll
+                for (int i = 0; i < 64; ++i)
+                    bad |= !window_finite(__uint_as_float(r[i]));
                 if (out32) {
                     // 32-byte stores: half the store instructions of 16-byte ones
                     // for the row's 256-byte run (rows sit 256 bytes apart)
@@ -745,6 +749,20 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                              __uint_as_float(r[8 * i + 7]) * inv);
                         dst[i] = v;
                     }
+                }
+            }
+            // rows that came out non-finite, perhaps for a value hidden from them
+            unsigned todo = __ballot_sync(kFull, ooff >= 0 && bad);
+            if (todo != 0) {
+                __syncwarp();
+                for (; todo != 0; todo &= todo - 1) {
+                    const int src = __ffs(todo) - 1;
+                    const long long at = __shfl_sync(kFull, ooff, src);
+                    const int pos = __shfl_sync(kFull, lim, src) - 1;
+                    if (pos >= 0)
+                        window_mend_row<T, D, kFp8>(p, p.key_cache, p.value_cache, w.table, w.kh,
+                                                    pos, static_cast<const T *>(p.query) + at,
+                                                    static_cast<T *>(p.out) + at);
                 }
             }
             g += w.n;
@@ -1245,6 +1263,8 @@ static pa_status run_window_prefill(
     prm.sink_tokens = (prm.num_sinks + kTileTokens - 1) & ~(kTileTokens - 1);
     prm.scale_log2 = scale * (fp8 ? k_scale : 1.f) * kLog2e;
     prm.out_scale = fp8 ? v_scale : 1.f;
+    prm.key_cache = key_cache;
+    prm.value_cache = value_cache;
     prm.num_tokens = num_tokens;
     // row tiles: at most one partial tile per sequence beyond the full ones
     const long long max_units =

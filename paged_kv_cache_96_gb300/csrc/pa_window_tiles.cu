@@ -594,6 +594,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 mbar_arrive(vfull(st));
             return true;
         };
+        auto packed_finite = [](uint32_t w) -> bool {
+            constexpr uint32_t kExp = kBf16 ? 0x7f80u : 0x7c00u;
+            return (w & kExp) != kExp && ((w >> 16) & kExp) != kExp;
+        };
         // A unit's rounded rows are stored after the next unit's first step has
         // its value rows: those are what the tensor cores may be waiting for.
         uint32_t v[D / 2];
@@ -669,6 +673,28 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 mbar_arrive(ufree(b));
             if (row)
                 pend = dst;
+            // rows that came out non-finite, perhaps for a value hidden from them
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < D / 2; ++k)
+                bad |= !packed_finite(v[k]);
+            unsigned todo = __ballot_sync(kFull, row && bad);
+            if (todo != 0) {
+                store_rows();
+                __syncwarp();
+                const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
+                for (; todo != 0; todo &= todo - 1) {
+                    const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
+                    const int tk = rr / G;
+                    const long long at =
+                        (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
+                    if (w.pos0 + tk >= 0)
+                        window_mend_row<T, D, false>(p, p.key_cache, p.value_cache, table, w.kh,
+                                                     w.pos0 + tk,
+                                                     static_cast<const T *>(p.query) + at,
+                                                     static_cast<T *>(p.out) + at);
+                }
+            }
         }
         store_rows();
     } else {

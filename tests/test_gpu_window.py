@@ -276,6 +276,46 @@ def test_context_zero(B):
     assert (c.out[0] == 0).all() and torch.isfinite(c.out[1].float()).all()
 
 
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("H,K,D,window,sinks", [(8, 2, 128, 40, 5), (4, 4, 64, 20, 0),
+                                               (6, 2, 64, 500, 2)])
+def test_chunk_values_hidden_from_some_rows(B, dtype, fp8, H, K, D, window, sinks):
+    """Infinite and NaN values at positions that some rows of a chunk see and
+    others do not: each row has what the definition gives it, element by
+    element."""
+    c = Case([300, 90], [130, 90], H, K, D, 16, dtype, fp8, window, sinks, seed=8)
+    kc, vc = c.kc, c.vc
+    spots = [(0, 200, 0, 3), (0, 290, K - 1, 5), (0, 171, 0, D - 1), (1, 60, 0, 9), (1, 0, 0, 1)]
+    for s, p, h, d in spots:
+        b, r = c.tables[s][p // 16], p % 16
+        if b >= vc.shape[0]:
+            continue  # (no row sees it)
+        if fp8:
+            vc[b, r, h, d] = 0x7F
+        else:
+            vc[b, r, h, d] = float("inf") if d % 2 else float("nan")
+    c.chunk(B)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0
+    got = c.out.double().cpu().numpy()
+    kv, vv = (R.pool_values(x, c.kv) for x in (kc, vc))
+    hot = ~np.isfinite(vv)
+    # the definition: an element is non-finite where a value the row sees is
+    clean = np.where(hot, 0.0, vv)
+    want, tol = R.window_attention(c.q, kv, clean, c.tables, c.start, c.ctx, c.scale, window, sinks,
+                                   dtype, torch.float16 if fp8 else dtype)
+    touched = np.zeros(want.shape, dtype=bool)
+    for s in range(2):
+        for i in range(int(c.rows[s])):
+            pos = int(c.ctx[s] - c.rows[s] + i)
+            p = R.visible(pos, int(c.ctx[s]), window, sinks)
+            bad = hot[c.tables[s][p // 16], p % 16].any(0)        # [K, D]
+            touched[c.start[s] + i] = np.repeat(bad, H // K, axis=0)
+    assert touched.any() and not touched.all()
+    assert np.array_equal(~np.isfinite(got), touched)
+    assert (np.abs(got - want) <= tol)[~touched].all()
+
+
 @pytest.mark.parametrize("call", ["decode", "chunk"])
 def test_large_scores(B, call):
     """Scores in the hundreds: one key takes nearly all the weight."""
