@@ -524,8 +524,10 @@ PA_API pa_status pa_decode_attention_window_fp8(
  * A row at a negative position gets a zero row; rows of out past
  * query_start[num_seqs] are left as they were.  query_start entries outside
  * [0, num_tokens] are clipped and flagged PA_DEVERR_TOKEN_RANGE.
- * num_tokens * num_heads < 2^31 - 128.  Other arguments, limits and errors as
- * pa_prefill_attention(_fp8) (scale positive).  No workspace.
+ * num_tokens * num_heads < 2^31 - 128, num_seqs <= 5,120 and
+ * max_blocks_per_seq * block_size <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).
+ * Other arguments, limits and errors as pa_prefill_attention(_fp8) (scale
+ * positive).  No workspace.
  */
 PA_API pa_status pa_prefill_attention_window(
     void *out, const void *query, const void *key_cache, const void *value_cache,

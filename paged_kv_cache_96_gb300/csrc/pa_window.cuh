@@ -1,5 +1,5 @@
-// pa_window.cuh -- launch parameters and device helpers shared by the two
-// windowed chunked-attention kernels (16-bit pools, FP8 pools).
+// pa_window.cuh -- launch parameters and device helpers of the windowed
+// chunked-attention kernel.
 #pragma once
 
 #include <type_traits>
@@ -27,8 +27,7 @@ struct WindowMqParams {
     float out_scale;    // applied to the output (the V scale for FP8 pools)
     const void *key_cache, *value_cache;  // (for rows computed anew)
     int num_tokens;     // rows of query and out (T)
-    int q_tma;          // FP8 kernel: each unit's query tile arrives by TMA
-    int ordered;        // 16-bit kernel: units numbered longest first
+    int ordered;        // units numbered longest first
 };
 
 // ---- fp32 helpers for the softmax ---------------------------------------------
@@ -240,8 +239,12 @@ __device__ __noinline__ void window_mend_row(const WindowMqParams &p, const void
         out[lane * E + e] = MmaOp<T>::from_float(o[e] * inv);
 }
 
-// The windowed chunk over 16-bit pools (pa_window_tiles.cu).
-pa_status launch_window_tiles(const WindowMqParams &prm, pa_dtype dtype, const void *key_cache,
-                             const void *value_cache, int head_dim, cudaStream_t stream);
+// The windowed chunk (pa_window_tiles.cu).
+// Sequences of one launch (their unit counts are kept in shared memory).
+constexpr int kWindowMaxSeqs = 5120;
+
+// dtype: the query's, the output's and (unless fp8: e4m3 codes) the pools'.
+pa_status launch_window_tiles(const WindowMqParams &prm, pa_dtype dtype, bool fp8, int head_dim,
+                             cudaStream_t stream);
 
 }  // namespace pa

@@ -1,6 +1,6 @@
-// pa_window_tiles.cu -- chunked prefill and mixed batches over 16-bit paged pools
-// with a sliding window and a few first tokens that stay visible, for sm_103a,
-// on the 5th-generation tensor cores.
+// pa_window_tiles.cu -- chunked prefill and mixed batches over paged pools with a
+// sliding window and a few first tokens that stay visible, for sm_103a, on the
+// 5th-generation tensor cores.
 //
 // Row of sequence s at position pos, window W, first tokens N:
 //     seen = { p <= pos : p > pos - W  or  p < N }
@@ -10,38 +10,54 @@
 //
 // What bounds it: the tensor cores (4 d flop a row and key), and beside them
 // the softmax of every score.  A CTA (one an SM, all of its tensor memory) works
-// through 128 query rows of one KV head at a time, in steps of 128 keys:
+// through 128 query rows of one KV head at a time, in steps of 128 keys.  Times
+// below: 8,192 rows of 4 sequences, 32 heads over 8, d 128, window 4,096 and 64
+// first tokens of up to 32,768, blocks of 32 (0.56 TFLOP of rows and keys seen:
+// 400 us, 1.39 PFLOP/s, where the device is within 5 % of its power limit);
+// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (43 us,
+// 0.61 PFLOP/s).
 //  * A score product reads its query rows from shared memory for every step,
-//    so N = 128 keys cost what 64 do (128 bytes a cycle: 8 MMAs take ~480
-//    cycles for either); 64-key steps pay that, and every barrier and commit,
-//    twice.
-//  * Tensor memory: two S buffers (128 fp32 columns each) and two O buffers.  The
-//    scores of step g + 1 are computed while the softmax of step g runs; P
-//    goes over the upper half of its S as 16-bit pairs, in two halves of 64
-//    keys, so the value product starts on the first while the second is
-//    computed.
-//  * A step's softmax takes ~1,500 cycles of four warps, its products ~1,000 of
-//    the tensor cores, so two sets of four warps take the steps in turn.  The
-//    rows' reference maximum goes from one to the other through shared memory
-//    as soon as it is known; the sums are joined at the unit's end, by the set
-//    that did not have the last step, after its first step of the next unit.
+//    so N = 128 keys cost what 64 do (~60 cycles an MMA for either); 64-key
+//    steps pay that, and every barrier and commit, twice (505 us).
+//  * Sixteen warps, each kind with a clock of its own.  0-3 and 4-7: the softmax
+//    of even and odd steps, one thread a row, with a reference maximum that moves
+//    only when a score passes it by 2^8 and goes from one set to the other
+//    through shared memory as soon as it is known.  (A step's softmax takes
+//    ~1,500 cycles of four warps, its products ~1,000 of the tensor cores: one
+//    set alone 430 us.)  8-11: output rows, while the next unit is computed
+//    (left to the softmax warps: 411).  12: key and query fetches, 13: value
+//    fetches, 14: score products, 15: value products (both from one warp: 568,
+//    since a wait for either held up the other).
+//  * Tensor memory: three S buffers of 128 fp32 columns and O.  P goes over the
+//    first half of its S as 16-bit pairs, in two halves of 64 keys, so the value
+//    product starts on the first while the second is computed; the third S
+//    lets the scores run a whole step ahead of the softmax (two: 519).
+//  * The softmax step is a loop over halves, not unrolled over 128 scores: two sets
+//    of warps at different places of a long body missed in the instruction cache.
 //  * Keys are counted without a gap ("compact positions", at the grain of one
 //    TMA box): the first tokens' boxes, then the window's, `skip` tokens further
 //    on; row r sees c with c < lim_r and (c >= low_r or c < N).  Steps past the
 //    window do not exist, and a last step of 64 keys or fewer is done at half
 //    size.
-//  * Twelve warps: 0-3 and 4-7 the softmax (one thread a row, a reference maximum
-//    that moves only when a score passes it by 2^8) and the rows, 8 loads keys
-//    and query tiles, 9 values, 10 issues the MMAs, 11 zeroes value rows
-//    that no row of the unit sees (so that NaN or another sequence's rows never
-//    meet a zero weight) in the few steps that have such rows.  They meet only
-//    at mbarriers; every wait is bounded, the first to run out stops all roles,
-//    and tensor memory is released on every path.
+//  * A TMA box takes ~70 cycles to issue whatever its size: boxes of 32 tokens
+//    where a block holds them (391 us; blocks of 16: 479).
+//  * The roles meet only at mbarriers; every wait is bounded, the first to run
+//    out stops all of them, and tensor memory is released on every path.
 //  * Query tiles hold floor(128 / G) whole tokens, so that any group size
 //    arrives by one TMA box a d-half.
-// P is rounded to the pools' type as an MMA operand, relative error 2^-9
-// (bf16) or 2^-12: about that of the rounded output; the sum keeps the
-// unrounded fp32 weights.
+//  * Value rows that no row of a unit sees are zeroed in shared memory before
+//    the value product, so that NaN or another sequence's rows never meet a zero
+//    weight; a row that still comes out non-finite is computed anew from the
+//    keys it sees alone.
+//  * FP8 pools: codes land where the upper half of their fp16 tile will be (d
+//    128; beside it at d 64) and the output warps widen them, in whatever order
+//    keys, values, query tiles and finished units come.  By count
+//    shared memory bounds it: 32 KB of codes written and read and 64 KB of fp16
+//    written a step, ~1,000 cycles beside the ~1,000 of the operands' reads
+//    (580 us and 65).  The query is rounded to fp16, the K scale joins the
+//    exponent's scale and the V scale the output.
+// P is rounded to the operands' type, relative error 2^-9 (bf16) or 2^-12: about
+// that of the rounded output; the sum keeps the unrounded fp32 weights.
 #include <cuda.h>
 
 #include <algorithm>
@@ -80,7 +96,9 @@ struct WtUnit {
     __device__ int steps() const { return (kend + kWtKeys - 1) / kWtKeys; }
     // a last step of 64 keys or fewer
     __device__ bool half(int si) const { return kend - si * kWtKeys <= kWtHalf; }
-    // value rows of step si that no row sees
+    // a value row (compact position) that no row of the unit sees
+    __device__ bool unseen(int c) const { return c >= kend || (c >= hide0 && c < hide1); }
+    // whether step si has such rows
     __device__ bool hidden(int si) const
     {
         const int c0 = si * kWtKeys;
@@ -104,18 +122,23 @@ struct Slot3 {
     __device__ Slot3 before() const { return i > 0 ? Slot3{i - 1, ph} : Slot3{2, ph ^ 1}; }
 };
 
-template <int D> struct WtLayout {
+template <int D, bool kFp8> struct WtLayout {
     static constexpr int kHalves = D / 64;               // 128-byte rows of 64 elements
     static constexpr int kHalfBytes = 128 * 128;         // 128 rows of one d-half
     static constexpr int kTile = kHalves * kHalfBytes;   // a query tile, or K or V of a step
     static constexpr int kK = 0;                         // 2 stages
     static constexpr int kV = 2 * kTile;                 // 2 stages
     static constexpr int kQ = 4 * kTile;                 // 2 query tiles
-    static constexpr int kRef = 6 * kTile;               // float reference [2 steps][128]
+    // FP8 pools: where a step's codes land, [stage][K, V]: the upper half of
+    // their own 16-bit tile at d 128, a place of their own at d 64
+    static constexpr int kCodeTile = kWtKeys * D;
+    static constexpr int kCodes = 6 * kTile;
+    static constexpr int kRef = kCodes + (kFp8 && D == 64 ? 4 * kCodeTile : 0);
+                                                         // float reference [2 steps][128]
     static constexpr int kPartL = kRef + 2 * 128 * 4;    // float l, m [2 units][2][128]
     static constexpr int kPartM = kPartL + 4 * 128 * 4;
-    static constexpr int kBars = kPartM + 4 * 128 * 4;   // 30 mbarriers
-    static constexpr int kTmemSlot = kBars + 30 * 8;
+    static constexpr int kBars = kPartM + 4 * 128 * 4;   // 34 mbarriers
+    static constexpr int kTmemSlot = kBars + 34 * 8;
     static constexpr int kAbort = kTmemSlot + 8;
     static constexpr int kUnits = kTmemSlot + 16;        // the CTA's first units
     // int unit prefix[n + 1], then (ordered) order[n], units[n], key[n] and
@@ -126,6 +149,9 @@ template <int D> struct WtLayout {
         return 1024 + kSeg + 4 * ((size_t)segments + 1) +
                (ordered ? 4 * (3 * (size_t)segments + kWtOrderBuckets) : 0);
     }
+    static_assert(1024 + kSeg + 4 * (kWindowMaxSeqs + 1) <= 227 * 1024 &&
+                      kWindowMaxSeqs > 4 * kWtOrderSegs + kWtOrderBuckets,
+                  "a CTA's shared memory");
 };
 
 // 16 columns of this warp's 32 lanes, without waiting for the store.
@@ -143,6 +169,37 @@ __device__ __forceinline__ void tmem_wait_st()
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+__device__ __forceinline__ uint4 load_shared(uint32_t a)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(a)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t a, const uint4 &v)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y),
+                 "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// Whether a barrier's phase has completed (never suspends, unlike a try_wait).
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t done;
+    asm volatile("{\n\t"
+                 ".reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t"
+                 "}"
+                 : "=r"(done)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return done != 0;
+}
+
 // The rest of a wait whose phase has not completed yet.  Out of line: it is
 // called from a dozen places, and the roles' loops have to stay short enough
 // for the instruction cache.
@@ -156,15 +213,18 @@ __device__ __noinline__ bool wt_wait_slow(uint32_t b, uint32_t parity, uint64_t 
     return ok;
 }
 
-template <typename T, int D, int kBox>
+// T: the query's and output's type; kFp8: the pools hold e4m3 codes (else T).
+template <typename T, int D, int kBox, bool kFp8>
 __global__ void __launch_bounds__(kWtThreads, 1)
     window_tiles_kernel(const __grid_constant__ WindowMqParams p,
                        const __grid_constant__ CUtensorMap tmap_k,
                        const __grid_constant__ CUtensorMap tmap_v,
                        const __grid_constant__ CUtensorMap tmap_q)
 {
-    using L = WtLayout<D>;
-    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    using L = WtLayout<D, kFp8>;
+    using OT = typename std::conditional<kFp8, __half, T>::type;  // operand type
+    constexpr bool kBf16 = std::is_same<OT, __nv_bfloat16>::value;
+    constexpr bool kConvQ = !std::is_same<OT, T>::value;  // queries rounded to fp16 here
     constexpr uint32_t kIdescS = idesc_f16(kBf16, kWtRows, kWtKeys, false, false);
     constexpr uint32_t kIdescSHalf = idesc_f16(kBf16, kWtRows, kWtHalf, false, false);
     constexpr uint32_t kIdescO = idesc_f16(kBf16, kWtRows, D, false, true);
@@ -199,6 +259,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     auto sfull = [&](int i) { return bar(18 + i); };
     auto pfull = [&](int h, int i) { return bar(21 + 3 * h + i); };
     auto ofull = [&](int i) { return bar(27 + i); };
+    // FP8 pools: the codes of K landed (V's: vland); the bf16 query tile landed
+    auto kland = [&](int st) { return bar(30 + st); };
+    auto qland = [&](int b) { return bar(32 + b); };
     auto mma_drain = [&](int i) { return bar(6 + i); };
     float *ref_s = reinterpret_cast<float *>(smem + L::kRef);
     float *part_l = reinterpret_cast<float *>(smem + L::kPartL);
@@ -211,10 +274,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
     if (tid == 0) {
         for (int st = 0; st < 2; ++st) {
-            mbar_init(kfull(st), 1);
-            mbar_init(vfull(st), 1);
+            mbar_init(kfull(st), kFp8 ? 4 : 1);  // (FP8 pools: widened by 4 warps)
+            mbar_init(vfull(st), kFp8 ? 4 : 1);
             mbar_init(vland(st), 1);
-            mbar_init(qfull(st), 1);
+            mbar_init(kland(st), 1);
+            mbar_init(qfull(st), kConvQ ? 4 : 1);
+            mbar_init(qland(st), 1);
             mbar_init(ufull(st), 1);
             mbar_init(lfull(st), 8);
             mbar_init(mfull(st), 4);
@@ -442,10 +507,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (!ok)
                     break;
                 tc_fence_after();
-                // The loops over halves stay loops: unrolled, the step's code
-                // passes the instruction cache and both sets of warps wait for
-                // it (572 us against 505 for 8,192 rows behind 4,096 tokens).
-                // Reading S twice costs less than holding it.
+                // The loops over halves stay loops: unrolled, the step's code in
+                // two sets of warps passes the instruction cache (85 % of its
+                // throughput measured).  Reading S twice costs less than holding it.
                 float mx = -INFINITY;  // maximum raw score (the scale is positive)
 #pragma unroll 1
                 for (int h = 0; h < halves; ++h) {
@@ -523,7 +587,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                          e1);
                             const float p0 = exp2f(e0), p1 = exp2f(e1);
                             acc[i & 1] = fadd_f32x2(acc[i & 1], pack_f32x2(p0, p1));
-                            pw[i] = MmaOp<T>::pack(p0, p1);
+                            pw[i] = MmaOp<OT>::pack(p0, p1);
                         }
                         // over the first half of S, which both passes have read
                         tmem_st_x16_nowait(s_at + 32 * h + 16 * c, pw);
@@ -561,45 +625,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
     } else if (warp < kWtKeyWarp) {
         // ===== output warps: O / l of a unit, while the next one is computed ==============
-        // Warp 8 also zeroes, once landed, the value rows that no row of a unit
-        // sees, before the value-product warp may read them.
         const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-        uint32_t g = 0, nu = 0;
-        uint32_t nland0 = 0, nland1 = 0;
-        bool ok = true;
-        auto zero_hidden = [&](const WtUnit &w, int si, int st) -> bool {
-            if (!wait(vland(st), (st ? nland1 : nland0) & 1))
-                return false;
-            ++(st ? nland1 : nland0);
-            const int c0 = si * kWtKeys;
-            const int rows = w.half(si) ? kWtHalf : kWtKeys;
-            const uint32_t vb = sbase + L::kV + st * L::kTile;
-#pragma unroll 1
-            for (int i = lane; i < rows; i += 32) {
-                const int c = c0 + i;
-                if (!(c >= w.kend || (c >= w.hide0 && c < w.hide1)))
-                    continue;
-#pragma unroll
-                for (int hf = 0; hf < L::kHalves; ++hf)
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                         vb + hf * L::kHalfBytes + i * 128 + (((k + i) & 7) << 4)),
-                                     "r"(0)
-                                     : "memory");
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(vfull(st));
-            return true;
-        };
         auto packed_finite = [](uint32_t w) -> bool {
-            constexpr uint32_t kExp = kBf16 ? 0x7f80u : 0x7c00u;
+            constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
             return (w & kExp) != kExp && ((w >> 16) & kExp) != kExp;
         };
-        // A unit's rounded rows are stored after the next unit's first step has
-        // its value rows: those are what the tensor cores may be waiting for.
         uint32_t v[D / 2];
         T *pend = nullptr;
         auto store_rows = [&]() {
@@ -624,30 +654,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             }
             pend = nullptr;
         };
-        WtUnit w;
-        for (int ku = 0; ok && unit_at(ku, w); ++ku) {
-            const int steps = w.steps();
-            const bool row = r < tok_unit * G && tok < w.count;
-            T *dst = static_cast<T *>(p.out) +
-                     (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
-            if (steps == 0) {  // no keys: zero rows
-                if (row)
-                    for (int c = 0; c < D / 8; ++c)
-                        reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
-                continue;
-            }
-            for (int si = 0; si < steps && ok; ++si, ++g) {
-                if (warp == kWtOutWarp && w.hidden(si))
-                    ok = zero_hidden(w, si, g & 1);
-                if (si == 0)
-                    store_rows();
-            }
-            const int b = nu & 1;
-            const uint32_t ph = (nu >> 1) & 1;
-            ++nu;
-            ok = ok && wait(lfull(b), ph) && wait(ufull(b), ph);
-            if (!ok)
-                break;
+        // A unit's rows (the CTA's steps up to its end: g) rounded into v, once its
+        // sums and last value product are there; O given back.
+        auto read_rows = [&](uint32_t g, int b) {
             tc_fence_after();
             // O is relative to the last step's reference, which the softmax
             // warps of that step have; the others' is not above it
@@ -671,15 +680,121 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(ufree(b));
-            if (row)
-                pend = dst;
-            // rows that came out non-finite, perhaps for a value hidden from them
-            bool bad = false;
+        };
+        if constexpr (!kFp8) {
+            // Warp 8 also zeroes, once landed, the value rows that no row of a unit
+            // sees, before the value-product warp may read them.
+            uint32_t g = 0, nu = 0;
+            uint32_t nland0 = 0, nland1 = 0;
+            bool ok = true;
+            auto zero_hidden = [&](const WtUnit &w, int si, int st) -> bool {
+                if (!wait(vland(st), (st ? nland1 : nland0) & 1))
+                    return false;
+                ++(st ? nland1 : nland0);
+                const int c0 = si * kWtKeys;
+                const int rows = w.half(si) ? kWtHalf : kWtKeys;
+                const uint32_t vb = sbase + L::kV + st * L::kTile;
+#pragma unroll 1
+                for (int i = lane; i < rows; i += 32) {
+                    const int c = c0 + i;
+                    if (!w.unseen(c))
+                        continue;
 #pragma unroll
-            for (int k = 0; k < D / 2; ++k)
-                bad |= !packed_finite(v[k]);
-            unsigned todo = __ballot_sync(kFull, row && bad);
-            if (todo != 0) {
+                    for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                             vb + hf * L::kHalfBytes + i * 128 + (((k + i) & 7) << 4)),
+                                         "r"(0)
+                                         : "memory");
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(vfull(st));
+                return true;
+            };
+            // A unit's rounded rows are stored after the next unit's first step has
+            // its value rows: those are what the tensor cores may be waiting for.
+            WtUnit w;
+            for (int ku = 0; ok && unit_at(ku, w); ++ku) {
+                const int steps = w.steps();
+                const bool row = r < tok_unit * G && tok < w.count;
+                T *dst = static_cast<T *>(p.out) +
+                         (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
+                if (steps == 0) {  // no keys: zero rows
+                    if (row)
+                        for (int c = 0; c < D / 8; ++c)
+                            reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+                    continue;
+                }
+                for (int si = 0; si < steps && ok; ++si, ++g) {
+                    if (warp == kWtOutWarp && w.hidden(si))
+                        ok = zero_hidden(w, si, g & 1);
+                    if (si == 0)
+                        store_rows();
+                }
+                const int b = nu & 1;
+                const uint32_t ph = (nu >> 1) & 1;
+                ++nu;
+                ok = ok && wait(lfull(b), ph) && wait(ufull(b), ph);
+                if (!ok)
+                    break;
+                read_rows(g, b);
+                if (row)
+                    pend = dst;
+                // rows that came out non-finite, perhaps for a value hidden from them
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < D / 2; ++k)
+                    bad |= !packed_finite(v[k]);
+                unsigned todo = __ballot_sync(kFull, row && bad);
+                if (todo != 0) {
+                    store_rows();
+                    __syncwarp();
+                    const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
+                    for (; todo != 0; todo &= todo - 1) {
+                        const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
+                        const int tk = rr / G;
+                        const long long at =
+                            (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
+                        if (w.pos0 + tk >= 0)
+                            window_mend_row<T, D, false>(p, p.key_cache, p.value_cache, table, w.kh,
+                                                         w.pos0 + tk,
+                                                         static_cast<const T *>(p.query) + at,
+                                                         static_cast<T *>(p.out) + at);
+                    }
+                }
+            }
+            store_rows();
+        } else {
+            // FP8 pools: these warps also widen each step's codes to the fp16
+            // operands (one thread a row; value rows that no row of the unit
+            // sees become zeros) and round bf16 query tiles to fp16.  Each warp
+            // takes whatever is there, its own 32 rows of it, in any order: the
+            // keys of a step, its values, a query tile, a finished unit.
+            struct Walk {  // steps of one kind done so far, at step si of unit ku
+                int ku = -1, si = 0, steps = 0;
+                uint32_t g = 0, nu = 0;
+                bool more = true;
+                WtUnit w;
+            };
+            Walk wk, wv, wq, wo;
+            // this thread's row of a unit
+            auto row_of = [&](const WtUnit &w) -> T * {
+                return r < tok_unit * G && tok < w.count
+                           ? static_cast<T *>(p.out) +
+                                 (((long long)w.row0 + tok) * H + w.kh * G + hg) * D
+                           : nullptr;
+            };
+            // a unit's rows stored, those that came out non-finite computed anew
+            auto keep_rows = [&](const WtUnit &w, T *dst) {
+                pend = dst;
+                bool bad = false;
+#pragma unroll
+                for (int k = 0; k < D / 2; ++k)
+                    bad |= !packed_finite(v[k]);
+                unsigned todo = __ballot_sync(kFull, dst != nullptr && bad);
                 store_rows();
                 __syncwarp();
                 const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
@@ -689,21 +804,159 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     const long long at =
                         (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
                     if (w.pos0 + tk >= 0)
-                        window_mend_row<T, D, false>(p, p.key_cache, p.value_cache, table, w.kh,
-                                                     w.pos0 + tk,
-                                                     static_cast<const T *>(p.query) + at,
-                                                     static_cast<T *>(p.out) + at);
+                        window_mend_row<T, D, true>(p, p.key_cache, p.value_cache, table, w.kh,
+                                                    w.pos0 + tk,
+                                                    static_cast<const T *>(p.query) + at,
+                                                    static_cast<T *>(p.out) + at);
+                }
+            };
+            auto zero_row = [&](const WtUnit &w) {  // a unit without keys
+                uint4 *dst = reinterpret_cast<uint4 *>(row_of(w));
+                if (dst != nullptr)
+                    for (int c = 0; c < D / 8; ++c)
+                        dst[c] = make_uint4(0, 0, 0, 0);
+            };
+            // the next unit with keys (zeros for one without, where asked)
+            auto open = [&](Walk &x, bool zeros) {
+                x.si = 0;
+                x.steps = 0;
+                while (x.more && x.steps == 0) {
+                    x.more = unit_at(++x.ku, x.w);
+                    if (x.more) {
+                        x.steps = x.w.steps();
+                        if (x.steps == 0 && zeros)
+                            zero_row(x.w);
+                    }
+                }
+            };
+            auto step = [&](Walk &x) {
+                ++x.g;
+                if (++x.si == x.steps)
+                    open(x, false);
+            };
+            // this thread's row (keys: of the tile at `tile`) from its codes
+            auto widen = [&](uint32_t tile, uint32_t codes, bool zero) {
+                uint4 src[D / 16];
+#pragma unroll
+                for (int c = 0; c < D / 16; ++c)
+                    src[c] = zero ? make_uint4(0, 0, 0, 0)
+                                  : load_shared(codes + r * D + (D == 128
+                                                                     ? (c ^ (r & 7)) << 4
+                                                                     : (c ^ ((r >> 1) & 3)) << 4));
+#pragma unroll
+                for (int f = 0; f < D / 8; ++f) {  // fp16 chunk f: codes 8f .. 8f + 7
+                    const uint4 s = src[f >> 1];
+                    const uint32_t lo = (f & 1) ? s.z : s.x, hi = (f & 1) ? s.w : s.y;
+                    store_shared(tile + (f >> 3) * L::kHalfBytes + r * 128 +
+                                     (((f & 7) ^ (r & 7)) << 4),
+                                 make_uint4(e4m3x2_to_f16x2((uint16_t)(lo & 0xffffu)),
+                                            e4m3x2_to_f16x2((uint16_t)(lo >> 16)),
+                                            e4m3x2_to_f16x2((uint16_t)(hi & 0xffffu)),
+                                            e4m3x2_to_f16x2((uint16_t)(hi >> 16))));
+                }
+            };
+            auto announce = [&](uint32_t b) {
+                fence_proxy_async_smem();  // (generic stores, read by the tensor cores)
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(b);
+            };
+            auto there = [&](uint32_t b, uint32_t parity) -> bool {
+                return __all_sync(kFull, mbar_test(b, parity));
+            };
+            auto code_base = [&](int st, int vals) -> uint32_t {
+                return D == 128 ? sbase + (vals ? L::kV : L::kK) + st * L::kTile + L::kHalfBytes
+                                : sbase + L::kCodes + (2 * st + vals) * L::kCodeTile;
+            };
+            open(wk, false);
+            open(wv, false);
+            open(wq, false);
+            open(wo, true);
+            if constexpr (!kConvQ)
+                wq.more = false;
+            bool q_over = false;  // a query element past the fp16 range
+            uint64_t idle_since = 0;
+            while (wk.more || wv.more || wq.more || wo.more) {
+                bool did = false;
+                if (wk.more && there(kland(wk.g & 1), (wk.g >> 1) & 1)) {
+                    const int st = wk.g & 1;
+                    if (r < kWtHalf || !wk.w.half(wk.si))
+                        widen(sbase + L::kK + st * L::kTile, code_base(st, 0), false);
+                    announce(kfull(st));
+                    step(wk);
+                    did = true;
+                }
+                if (wv.more && there(vland(wv.g & 1), (wv.g >> 1) & 1)) {
+                    const int st = wv.g & 1;
+                    if (r < kWtHalf || !wv.w.half(wv.si))
+                        widen(sbase + L::kV + st * L::kTile, code_base(st, 1),
+                              wv.w.unseen(wv.si * kWtKeys + r));
+                    announce(vfull(st));
+                    step(wv);
+                    did = true;
+                }
+                if constexpr (kConvQ) {
+                    if (wq.more && there(qland(wq.nu & 1), (wq.nu >> 1) & 1)) {
+                        const uint32_t tile = sbase + L::kQ + (wq.nu & 1) * L::kTile;
+                        const bool row = row_of(wq.w) != nullptr;
+#pragma unroll
+                        for (int c = 0; c < D / 8; ++c) {
+                            const uint32_t a = tile + (c >> 3) * L::kHalfBytes + r * 128 +
+                                               (((c & 7) ^ (r & 7)) << 4);
+                            uint4 x = load_shared(a);
+                            uint32_t *xw = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float lo = __uint_as_float(xw[k] << 16);
+                                const float hi = __uint_as_float(xw[k] & 0xffff0000u);
+                                q_over |= row && fmaxf(fabsf(lo), fabsf(hi)) > 65504.f;
+                                xw[k] = pack_f16x2(lo, hi);
+                            }
+                            store_shared(a, x);
+                        }
+                        announce(qfull(wq.nu & 1));
+                        ++wq.nu;
+                        open(wq, false);
+                        did = true;
+                    }
+                }
+                if (wo.more && there(lfull(wo.nu & 1), (wo.nu >> 1) & 1) &&
+                    there(ufull(wo.nu & 1), (wo.nu >> 1) & 1)) {
+                    wo.g += wo.steps;
+                    T *const dst = row_of(wo.w);
+                    read_rows(wo.g, wo.nu & 1);
+                    keep_rows(wo.w, dst);
+                    ++wo.nu;
+                    open(wo, true);
+                    did = true;
+                }
+                if (did) {
+                    idle_since = 0;
+                    continue;
+                }
+                // nothing there: the bounded wait of this role
+                const uint64_t now = global_timer_ns();
+                if (idle_since == 0)
+                    idle_since = now;
+                const bool give_up = *abort_flag != 0 || now - idle_since > p.wait_ns;
+                if (__any_sync(kFull, give_up)) {
+                    *abort_flag = 1;
+                    break;
                 }
             }
+            if (__any_sync(kFull, q_over) && lane == 0)
+                flag_error(p.error_word, PA_DEVERR_QUERY_RANGE);
         }
-        store_rows();
     } else {
         if (warp == kWtKeyWarp || warp == kWtValueWarp) {
             // ===== fetch warps: keys and query tiles (8), values (9) ====================
             // Lane j owns box j / halves and d-half j % halves of every step: it
             // looks up that box's physical block one step ahead and issues it.
             const bool values = warp == kWtValueWarp;
-            const int my_sb = lane / L::kHalves, my_hf = lane % L::kHalves;
+            // (FP8 pools: a box has whole rows of codes)
+            constexpr int kParts = kFp8 ? 1 : L::kHalves;
+            constexpr int kBoxBytes = kFp8 ? kBox * D : kBox * 128;
+            const int my_sb = lane / kParts, my_hf = lane % kParts;
             uint32_t g = 0;
             Slot3 s2;                     // of step g - 2
             int qk = 0;                   // next unit whose query tile goes out
@@ -745,18 +998,26 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     if (!(p.withhold_fill != 0 && !values && g == 0)) {
                         const int c0 = si * kWtKeys;
                         const int nsub = min(kSubs, (w.kend - c0 + kBox - 1) / kBox);
-                        const bool fix = values && w.hidden(si);
-                        const uint32_t fb = !values ? kfull(st) : fix ? vland(st) : vfull(st);
+                        // (value rows that no row sees are zeroed before the tensor
+                        // cores are told, by the warps that widen FP8 codes too)
+                        const bool fix = !kFp8 && values && w.hidden(si);
+                        const uint32_t fb = kFp8 ? (values ? vland(st) : kland(st))
+                                            : !values ? kfull(st)
+                                            : fix     ? vland(st)
+                                                      : vfull(st);
+                        const uint32_t tile = sbase + (values ? L::kV : L::kK) + st * L::kTile;
+                        const uint32_t dst =
+                            !kFp8      ? tile + my_hf * L::kHalfBytes
+                            : D == 128 ? tile + L::kHalfBytes
+                                       : sbase + L::kCodes + (2 * st + values) * L::kCodeTile;
                         if (lane == 0)
-                            mbar_arrive_expect_tx(fb, (uint32_t)(nsub * L::kHalves * kBox * 128));
+                            mbar_arrive_expect_tx(fb, (uint32_t)(nsub * kParts * kBoxBytes));
                         __syncwarp();
                         if (my_sb < nsub) {
                             const int c = c0 + my_sb * kBox;
                             const int tk = c + (c >= sink_tokens ? w.skip : 0);
-                            tma_load_4d(sbase + (values ? L::kV : L::kK) + st * L::kTile +
-                                            my_hf * L::kHalfBytes + my_sb * kBox * 128,
-                                        values ? &tmap_v : &tmap_k, fb, my_hf * 64, w.kh,
-                                        tk & (p.block_size - 1), ent);
+                            tma_load_4d(dst + my_sb * kBoxBytes, values ? &tmap_v : &tmap_k, fb,
+                                        my_hf * 64, w.kh, tk & (p.block_size - 1), ent);
                         }
                         (st ? last1 : last0) = fb;
                         (st ? last_ph1 : last_ph0) = fix ? (st ? nland1 : nland0) & 1 : ph;
@@ -772,7 +1033,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         WtUnit wq;
                         while (nq < due && unit_at(qk, wq)) {
                             if (wq.kend > 0) {
-                                const uint32_t qb = qfull(nq & 1);
+                                const uint32_t qb = kConvQ ? qland(nq & 1) : qfull(nq & 1);
                                 if (lane == 0)
                                     mbar_arrive_expect_tx(qb, L::kHalves * 128 * tok_unit * G);
                                 __syncwarp();
@@ -795,9 +1056,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (last1 != 0)
                 mbar_wait_bounded(last1, last_ph1, kDrainWaitNs);
             if (nq > 0)
-                mbar_wait_bounded(qfull((nq - 1) & 1), ((nq - 1) >> 1) & 1, kDrainWaitNs);
+                mbar_wait_bounded(kConvQ ? qland((nq - 1) & 1) : qfull((nq - 1) & 1),
+                                  ((nq - 1) >> 1) & 1, kDrainWaitNs);
             if (nq > 1)
-                mbar_wait_bounded(qfull((nq - 2) & 1), ((nq - 2) >> 1) & 1, kDrainWaitNs);
+                mbar_wait_bounded(kConvQ ? qland((nq - 2) & 1) : qfull((nq - 2) & 1),
+                                  ((nq - 2) >> 1) & 1, kDrainWaitNs);
         } else {
             // ===== tensor-core warps: scores (10), value products (11) ======================
             // One elected lane of each issues.  An MMA takes its warp ~60 cycles
@@ -898,15 +1161,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
 // ---- host side -------------------------------------------------------------------
 
-template <typename T, int D, int kBox>
+template <typename T, int D, int kBox, bool kFp8>
 static pa_status launch_tiles_as(const WindowMqParams &prm, const CUtensorMap &mk,
                                 const CUtensorMap &mv, const CUtensorMap &mq,
                                 cudaStream_t stream, int grid, int optin)
 {
-    auto kernel = window_tiles_kernel<T, D, kBox>;
+    auto kernel = window_tiles_kernel<T, D, kBox, kFp8>;
     static size_t enabled[kMaxDevices];
     static std::mutex mu;
-    const size_t smem = WtLayout<D>::bytes(prm.num_segments, prm.ordered != 0);
+    const size_t smem = WtLayout<D, kFp8>::bytes(prm.num_segments, prm.ordered != 0);
     if (smem > (size_t)optin)
         return PA_ERR_UNSUPPORTED;
     int dev = 0;
@@ -927,31 +1190,29 @@ static pa_status launch_tiles_as(const WindowMqParams &prm, const CUtensorMap &m
                       mv, mq);
 }
 
-// A 4-D map of a 16-bit pool [num_blocks][block_size][num_kv_heads][head_dim]
-// with boxes of 64 elements x 1 head x `tokens` x 1 block, and a 3-D map of the
-// query [T][H][D] with boxes of 64 elements x G heads x whole tokens of a tile;
-// 128-byte swizzle, zero fill past the end.
-static bool encode_tiles_map(CUtensorMap *map, const void *base, pa_dtype dtype, int rank,
-                            const cuuint64_t *dims, const cuuint32_t *box)
+// Tensor map of a contiguous array of `rank` dimensions (type: 16-bit or e4m3
+// codes as bytes), the rows of its boxes 64 or 128 bytes, swizzled at that grain.
+static bool encode_tiles_map(CUtensorMap *map, const void *base, CUtensorMapDataType type,
+                            int rank, const cuuint64_t *dims, const cuuint32_t *box)
 {
     EncodeTiledFn fn = get_encode_fn();
     if (!fn)
         return false;
+    const cuuint64_t esize = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
     cuuint64_t strides[3];
-    cuuint64_t bytes = 2;
+    cuuint64_t bytes = esize;
     for (int i = 0; i + 1 < rank; ++i)
         strides[i] = bytes *= dims[i];
     const cuuint32_t estr[4] = {1, 1, 1, 1};
-    return fn(map, dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
-                                    : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
-              (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    return fn(map, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box[0] * esize == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-pa_status launch_window_tiles(const WindowMqParams &prm_in, pa_dtype dtype, const void *key_cache,
-                             const void *value_cache, int head_dim, cudaStream_t stream)
+pa_status launch_window_tiles(const WindowMqParams &prm_in, pa_dtype dtype, bool fp8, int head_dim,
+                             cudaStream_t stream)
 {
     WindowMqParams prm = prm_in;
     int dev = 0;
@@ -975,30 +1236,36 @@ pa_status launch_window_tiles(const WindowMqParams &prm_in, pa_dtype dtype, cons
     CUtensorMap mk, mv, mq;
     const cuuint64_t pool[4] = {(cuuint64_t)head_dim, (cuuint64_t)prm.num_kv_heads,
                                 (cuuint64_t)prm.block_size, (cuuint64_t)prm.num_blocks};
-    const cuuint32_t pool_box[4] = {64, 1, (cuuint32_t)box_tokens, 1};
+    const cuuint32_t pool_box[4] = {fp8 ? (cuuint32_t)head_dim : 64u, 1, (cuuint32_t)box_tokens,
+                                    1};
     const cuuint64_t rows[3] = {(cuuint64_t)head_dim, (cuuint64_t)prm.num_heads,
                                 (cuuint64_t)prm.num_tokens};
     const cuuint32_t rows_box[3] = {64, (cuuint32_t)prm.group, (cuuint32_t)tok_tile};
-    if (!encode_tiles_map(&mk, key_cache, dtype, 4, pool, pool_box) ||
-        !encode_tiles_map(&mv, value_cache, dtype, 4, pool, pool_box) ||
-        !encode_tiles_map(&mq, prm.query, dtype, 3, rows, rows_box))
+    const CUtensorMapDataType type = dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const CUtensorMapDataType pool_type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type;
+    if (!encode_tiles_map(&mk, prm.key_cache, pool_type, 4, pool, pool_box) ||
+        !encode_tiles_map(&mv, prm.value_cache, pool_type, 4, pool, pool_box) ||
+        !encode_tiles_map(&mq, prm.query, type, 3, rows, rows_box))
         return PA_ERR_CUDA;
-    using B16 = __nv_bfloat16;
-    auto run = [&](auto kernel_launch) {
-        return kernel_launch(prm, mk, mv, mq, stream, grid, info.optin);
+    auto run = [&](auto type_tag, auto dim, auto box, auto codes) {
+        return launch_tiles_as<decltype(type_tag), decltype(dim)::value, decltype(box)::value,
+                               decltype(codes)::value>(prm, mk, mv, mq, stream, grid,
+                                                       info.optin);
     };
-    if (dtype == PA_BF16) {
-        if (head_dim == 128)
-            return box_tokens == 32 ? run(launch_tiles_as<B16, 128, 32>)
-                                    : run(launch_tiles_as<B16, 128, 16>);
-        return box_tokens == 32 ? run(launch_tiles_as<B16, 64, 32>)
-                                : run(launch_tiles_as<B16, 64, 16>);
-    }
-    if (head_dim == 128)
-        return box_tokens == 32 ? run(launch_tiles_as<__half, 128, 32>)
-                                : run(launch_tiles_as<__half, 128, 16>);
-    return box_tokens == 32 ? run(launch_tiles_as<__half, 64, 32>)
-                            : run(launch_tiles_as<__half, 64, 16>);
+    auto by_pool = [&](auto type_tag, auto dim, auto box) {
+        return fp8 ? run(type_tag, dim, box, std::true_type{})
+                   : run(type_tag, dim, box, std::false_type{});
+    };
+    auto by_box = [&](auto type_tag, auto dim) {
+        return box_tokens == 32 ? by_pool(type_tag, dim, std::integral_constant<int, 32>{})
+                                : by_pool(type_tag, dim, std::integral_constant<int, 16>{});
+    };
+    auto by_dim = [&](auto type_tag) {
+        return head_dim == 128 ? by_box(type_tag, std::integral_constant<int, 128>{})
+                               : by_box(type_tag, std::integral_constant<int, 64>{});
+    };
+    return dtype == PA_BF16 ? by_dim(__nv_bfloat16{}) : by_dim(__half{});
 }
 
 }  // namespace pa

@@ -127,6 +127,8 @@ def test_chunk_window_needs_a_positive_scale_and_offsets(B):
     assert _chunk(B, T=-1) == B.PA_ERR_INVALID_ARG
     assert _chunk(B, T=0) == B.PA_OK
     assert _chunk(B, T=1 << 28) == B.PA_ERR_UNSUPPORTED
+    assert _chunk(B, S=5121) == B.PA_ERR_UNSUPPORTED
+    assert _chunk(B, True, S=5121) == B.PA_ERR_UNSUPPORTED
 
 
 def test_window_workspace(B):
