@@ -13,9 +13,9 @@
 // through 128 query rows of one KV head at a time, in steps of 128 keys.  Times
 // below: 8,192 rows of 4 sequences, 32 heads over 8, d 128, window 4,096 and 64
 // first tokens of up to 32,768, blocks of 32 (0.56 TFLOP of rows and keys seen:
-// 400 us, 1.39 PFLOP/s, where the device is within 5 % of its power limit);
-// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (43 us,
-// 0.61 PFLOP/s).
+// 389 us, 1.44 PFLOP/s, where the device is within 5 % of its power limit);
+// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (41 us,
+// 0.63 PFLOP/s).
 //  * A score product reads its query rows from shared memory for every step,
 //    so N = 128 keys cost what 64 do (~60 cycles an MMA for either); 64-key
 //    steps pay that, and every barrier and commit, twice (505 us).
@@ -39,8 +39,10 @@
 //    on; row r sees c with c < lim_r and (c >= low_r or c < N).  Steps past the
 //    window do not exist, and a last step of 64 keys or fewer is done at half
 //    size.
-//  * A TMA box takes ~70 cycles to issue whatever its size: boxes of 32 tokens
-//    where a block holds them (391 us; blocks of 16: 479).
+//  * A TMA box takes ~70 cycles to issue whatever its size, so a box brings both
+//    d-halves of its tokens, as atoms of 8 tokens that the descriptors step over
+//    (a box a half: 403 us, and 479 instead of 400 for blocks of 16), and 32
+//    tokens where a block holds them.
 //  * The roles meet only at mbarriers; every wait is bounded, the first to run
 //    out stops all of them, and tensor memory is released on every path.
 //  * Query tiles hold floor(128 / G) whole tokens, so that any group size
@@ -126,6 +128,11 @@ template <int D, bool kFp8> struct WtLayout {
     static constexpr int kHalves = D / 64;               // 128-byte rows of 64 elements
     static constexpr int kHalfBytes = 128 * 128;         // 128 rows of one d-half
     static constexpr int kTile = kHalves * kHalfBytes;   // a query tile, or K or V of a step
+    // K and V of a step are atoms of 8 tokens x 64 elements (1,024 bytes): atom
+    // (token group j, d-half f) at j kGroup + f kPart.  16-bit pools: one TMA
+    // box brings both halves, so they alternate
+    static constexpr int kGroup = kFp8 ? 1024 : kHalves * 1024;
+    static constexpr int kPart = kFp8 ? kHalfBytes : 1024;
     static constexpr int kK = 0;                         // 2 stages
     static constexpr int kV = 2 * kTile;                 // 2 stages
     static constexpr int kQ = 4 * kTile;                 // 2 query tiles
@@ -704,7 +711,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 8; ++k)
                             asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             vb + hf * L::kHalfBytes + i * 128 + (((k + i) & 7) << 4)),
+                                             vb + (i >> 3) * L::kGroup + hf * L::kPart +
+                                             (i & 7) * 128 + (((k + i) & 7) << 4)),
                                          "r"(0)
                                          : "memory");
                 }
@@ -953,10 +961,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             // Lane j owns box j / halves and d-half j % halves of every step: it
             // looks up that box's physical block one step ahead and issues it.
             const bool values = warp == kWtValueWarp;
-            // (FP8 pools: a box has whole rows of codes)
-            constexpr int kParts = kFp8 ? 1 : L::kHalves;
-            constexpr int kBoxBytes = kFp8 ? kBox * D : kBox * 128;
-            const int my_sb = lane / kParts, my_hf = lane % kParts;
+            constexpr int kBoxBytes = kBox * D * (kFp8 ? 1 : 2);
             uint32_t g = 0;
             Slot3 s2;                     // of step g - 2
             int qk = 0;                   // next unit whose query tile goes out
@@ -970,8 +975,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int steps = w.steps();
                 const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
                 auto lookup = [&](int si) -> int {
-                    const int c = si * kWtKeys + my_sb * kBox;
-                    if (my_sb >= kSubs || c >= w.kend)
+                    const int c = si * kWtKeys + lane * kBox;
+                    if (lane >= kSubs || c >= w.kend)
                         return 0;
                     return __ldg(table + ((c + (c >= sink_tokens ? w.skip : 0)) >> p.block_shift));
                 };
@@ -1007,17 +1012,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                                       : vfull(st);
                         const uint32_t tile = sbase + (values ? L::kV : L::kK) + st * L::kTile;
                         const uint32_t dst =
-                            !kFp8      ? tile + my_hf * L::kHalfBytes
+                            !kFp8      ? tile
                             : D == 128 ? tile + L::kHalfBytes
                                        : sbase + L::kCodes + (2 * st + values) * L::kCodeTile;
                         if (lane == 0)
-                            mbar_arrive_expect_tx(fb, (uint32_t)(nsub * kParts * kBoxBytes));
+                            mbar_arrive_expect_tx(fb, (uint32_t)(nsub * kBoxBytes));
                         __syncwarp();
-                        if (my_sb < nsub) {
-                            const int c = c0 + my_sb * kBox;
+                        if (lane < nsub) {
+                            const int c = c0 + lane * kBox;
                             const int tk = c + (c >= sink_tokens ? w.skip : 0);
-                            tma_load_4d(dst + my_sb * kBoxBytes, values ? &tmap_v : &tmap_k, fb,
-                                        my_hf * 64, w.kh, tk & (p.block_size - 1), ent);
+                            const int row = tk & (p.block_size - 1);
+                            if constexpr (kFp8)
+                                tma_load_4d(dst + lane * kBoxBytes, values ? &tmap_v : &tmap_k,
+                                            fb, 0, w.kh, row, ent);
+                            else
+                                tma_load_4d(dst + lane * kBoxBytes, values ? &tmap_v : &tmap_k,
+                                            fb, 0, 0, w.kh * L::kHalves,
+                                            (ent << (p.block_shift - 3)) + (row >> 3));
                         }
                         (st ? last1 : last0) = fb;
                         (st ? last_ph1 : last_ph0) = fix ? (st ? nland1 : nland0) & 1 : ph;
@@ -1068,8 +1079,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             // one warp for both would be what the kernel waits for.
             const bool scores = warp == kWtScoreWarp;
             const uint64_t desc_q0 = smem_desc_sw128(sbase + L::kQ, 16, 1024);
-            const uint64_t desc_k0 = smem_desc_sw128(sbase + L::kK, 16, 1024);
-            const uint64_t desc_v0 = smem_desc_sw128(sbase + L::kV, L::kHalfBytes, 1024);
+            const uint64_t desc_k0 = smem_desc_sw128(sbase + L::kK, 16, L::kGroup);
+            const uint64_t desc_v0 = smem_desc_sw128(sbase + L::kV, L::kPart, L::kGroup);
             uint32_t g = 0, nu = 0;
             Slot3 s3;
             bool ok = true;
@@ -1098,8 +1109,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         if (elect_one()) {
 #pragma unroll
                             for (int kk = 0; kk < KT; ++kk) {
-                                const uint32_t o = ((kk >> 2) * L::kHalfBytes + (kk & 3) * 32) >> 4;
-                                tc_mma_ss(at, dq + o, dk + o, idesc, kk > 0 ? 1u : 0u);
+                                const uint32_t off_q = ((kk >> 2) * L::kHalfBytes + (kk & 3) * 32) >> 4;
+                                const uint32_t off_k = ((kk >> 2) * L::kPart + (kk & 3) * 32) >> 4;
+                                tc_mma_ss(at, dq + off_q, dk + off_k, idesc, kk > 0 ? 1u : 0u);
                             }
                             tc_commit(sfull(s3.i));
                         }
@@ -1125,7 +1137,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 #pragma unroll
                                 for (int ks = 0; ks < kWtHalf / 16; ++ks)
                                     tc_mma_ts(tmem + kWtTmemO, p_at + ks * 8,
-                                              dv + (uint64_t)((ks * 2048) >> 4), kIdescO,
+                                              dv + (uint64_t)((ks * 2 * L::kGroup) >> 4), kIdescO,
                                               (rem < kend || h > 0 || ks > 0) ? 1u : 0u);
                                 if (h == halves - 1) {
                                     tc_commit(ofull(s3.i));
@@ -1133,7 +1145,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                         tc_commit(ufull(b));
                                 }
                             }
-                            dv += (kWtHalf * 128) >> 4;
+                            dv += (kWtHalf / 8 * L::kGroup) >> 4;
                             p_at += 32;
                         }
                     }
@@ -1190,23 +1202,21 @@ static pa_status launch_tiles_as(const WindowMqParams &prm, const CUtensorMap &m
                       mv, mq);
 }
 
-// Tensor map of a contiguous array of `rank` dimensions (type: 16-bit or e4m3
-// codes as bytes), the rows of its boxes 64 or 128 bytes, swizzled at that grain.
+// Tensor map of an array of `rank` dimensions (type: 16-bit or e4m3 codes as
+// bytes; strides in bytes from the second dimension on), the rows of its boxes 64 or
+// 128 bytes, swizzled at that grain.
 static bool encode_tiles_map(CUtensorMap *map, const void *base, CUtensorMapDataType type,
-                            int rank, const cuuint64_t *dims, const cuuint32_t *box)
+                            int rank, const cuuint64_t *dims, const cuuint64_t *strides,
+                            const cuuint32_t *box)
 {
     EncodeTiledFn fn = get_encode_fn();
     if (!fn)
         return false;
-    const cuuint64_t esize = type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2;
-    cuuint64_t strides[3];
-    cuuint64_t bytes = esize;
-    for (int i = 0; i + 1 < rank; ++i)
-        strides[i] = bytes *= dims[i];
+    const cuuint32_t row_bytes = box[0] * (type == CU_TENSOR_MAP_DATA_TYPE_UINT8 ? 1 : 2);
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     return fn(map, type, (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE,
-              box[0] * esize == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              row_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1234,19 +1244,31 @@ pa_status launch_window_tiles(const WindowMqParams &prm_in, pa_dtype dtype, bool
     prm.ordered = units > info.sms && prm.num_segments <= kWtOrderSegs;
 
     CUtensorMap mk, mv, mq;
-    const cuuint64_t pool[4] = {(cuuint64_t)head_dim, (cuuint64_t)prm.num_kv_heads,
-                                (cuuint64_t)prm.block_size, (cuuint64_t)prm.num_blocks};
-    const cuuint32_t pool_box[4] = {fp8 ? (cuuint32_t)head_dim : 64u, 1, (cuuint32_t)box_tokens,
-                                    1};
-    const cuuint64_t rows[3] = {(cuuint64_t)head_dim, (cuuint64_t)prm.num_heads,
-                                (cuuint64_t)prm.num_tokens};
-    const cuuint32_t rows_box[3] = {64, (cuuint32_t)prm.group, (cuuint32_t)tok_tile};
+    // 16-bit pools: [8 tokens][d-halves of all heads][64], tokens in groups of 8
+    // (a whole number of them in a block); codes: [tokens][heads][d] by blocks
+    using U64 = cuuint64_t;
+    using U32 = cuuint32_t;
+    const U64 dim = head_dim, heads = prm.num_kv_heads, tokens = prm.block_size;
+    const U64 row = heads * dim * (fp8 ? 1 : 2);  // bytes of a token
+    const U32 halves = head_dim / 64;
+    const U64 pool16[4] = {64, 8, halves * heads, prm.num_blocks * tokens / 8};
+    const U64 pool16_strides[3] = {row, 128, 8 * row};
+    const U32 pool16_box[4] = {64, 8, halves, (U32)box_tokens / 8};
+    const U64 pool8[4] = {dim, heads, tokens, (U64)prm.num_blocks};
+    const U64 pool8_strides[3] = {dim, row, tokens * row};
+    const U32 pool8_box[4] = {(U32)dim, 1, (U32)box_tokens, 1};
+    const U64 rows[3] = {dim, (U64)prm.num_heads, (U64)prm.num_tokens};
+    const U64 rows_strides[2] = {dim * 2, prm.num_heads * dim * 2};
+    const U32 rows_box[3] = {64, (U32)prm.group, (U32)tok_tile};
     const CUtensorMapDataType type = dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                                       : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    const CUtensorMapDataType pool_type = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type;
-    if (!encode_tiles_map(&mk, prm.key_cache, pool_type, 4, pool, pool_box) ||
-        !encode_tiles_map(&mv, prm.value_cache, pool_type, 4, pool, pool_box) ||
-        !encode_tiles_map(&mq, prm.query, type, 3, rows, rows_box))
+    auto pool_map = [&](CUtensorMap *m, const void *base) {
+        return fp8 ? encode_tiles_map(m, base, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, pool8,
+                                      pool8_strides, pool8_box)
+                   : encode_tiles_map(m, base, type, 4, pool16, pool16_strides, pool16_box);
+    };
+    if (!pool_map(&mk, prm.key_cache) || !pool_map(&mv, prm.value_cache) ||
+        !encode_tiles_map(&mq, prm.query, type, 3, rows, rows_strides, rows_box))
         return PA_ERR_CUDA;
     auto run = [&](auto type_tag, auto dim, auto box, auto codes) {
         return launch_tiles_as<decltype(type_tag), decltype(dim)::value, decltype(box)::value,
