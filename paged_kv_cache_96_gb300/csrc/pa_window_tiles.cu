@@ -13,9 +13,9 @@
 // through 128 query rows of one KV head at a time, in steps of 128 keys.  Times
 // below: 8,192 rows of 4 sequences, 32 heads over 8, d 128, window 4,096 and 64
 // first tokens of up to 32,768, blocks of 32 (0.56 TFLOP of rows and keys seen:
-// 389 us, 1.44 PFLOP/s, where the device is within 5 % of its power limit);
-// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (41 us,
-// 0.63 PFLOP/s).
+// 375 us, 1.49 PFLOP/s, where the device is within 5 % of its power limit);
+// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (38 us,
+// 0.68 PFLOP/s).
 //  * A score product reads its query rows from shared memory for every step,
 //    so N = 128 keys cost what 64 do (~60 cycles an MMA for either); 64-key
 //    steps pay that, and every barrier and commit, twice (505 us).
@@ -47,16 +47,16 @@
 //    out stops all of them, and tensor memory is released on every path.
 //  * Query tiles hold floor(128 / G) whole tokens, so that any group size
 //    arrives by one TMA box a d-half.
-//  * Value rows that no row of a unit sees are zeroed in shared memory before
-//    the value product, so that NaN or another sequence's rows never meet a zero
-//    weight; a row that still comes out non-finite is computed anew from the
-//    keys it sees alone.
+//  * Value rows that no row of a unit sees are zeroed in shared memory by the
+//    value-product warp (an output warp, busy with the unit before: 382 us and
+//    40.7), so that NaN or another sequence's rows never meet a zero weight; a row
+//    that still comes out non-finite is computed anew from the keys it sees alone.
 //  * FP8 pools: codes land where the upper half of their fp16 tile will be (d
 //    128; beside it at d 64) and the output warps widen them, in whatever order
 //    keys, values, query tiles and finished units come.  By count
 //    shared memory bounds it: 32 KB of codes written and read and 64 KB of fp16
 //    written a step, ~1,000 cycles beside the ~1,000 of the operands' reads
-//    (580 us and 65).  The query is rounded to fp16, the K scale joins the
+//    (578 us and 62).  The query is rounded to fp16, the K scale joins the
 //    exponent's scale and the V scale the output.
 // P is rounded to the operands' type, relative error 2^-9 (bf16) or 2^-12: about
 // that of the rounded output; the sum keeps the unrounded fp32 weights.
@@ -638,13 +638,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             return (w & kExp) != kExp && ((w >> 16) & kExp) != kExp;
         };
         uint32_t v[D / 2];
-        T *pend = nullptr;
-        auto store_rows = [&]() {
-            if (pend == nullptr)
-                return;
+        auto store_row = [&](T *dst) {
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
-                T *at = pend + 16 * i;
+                T *at = dst + 16 * i;
                 if (out32) {
                     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
                                      at),
@@ -659,11 +656,23 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
                 }
             }
-            pend = nullptr;
         };
-        // A unit's rows (the CTA's steps up to its end: g) rounded into v, once its
-        // sums and last value product are there; O given back.
-        auto read_rows = [&](uint32_t g, int b) {
+        // this thread's row of a unit
+        auto row_of = [&](const WtUnit &w) -> T * {
+            return r < tok_unit * G && tok < w.count
+                       ? static_cast<T *>(p.out) +
+                             (((long long)w.row0 + tok) * H + w.kh * G + hg) * D
+                       : nullptr;
+        };
+        auto zero_row = [&](const WtUnit &w) {  // a unit without keys
+            uint4 *dst = reinterpret_cast<uint4 *>(row_of(w));
+            if (dst != nullptr)
+                for (int c = 0; c < D / 8; ++c)
+                    dst[c] = make_uint4(0, 0, 0, 0);
+        };
+        // A unit's rows (the CTA's steps up to its end: g), once its sums and last
+        // value product are there: rounded, O given back, stored.
+        auto write_rows = [&](const WtUnit &w, uint32_t g, int b) {
             tc_fence_after();
             // O is relative to the last step's reference, which the softmax
             // warps of that step have; the others' is not above it
@@ -687,94 +696,47 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(ufree(b));
+            T *const dst = row_of(w);
+            if (dst != nullptr)
+                store_row(dst);
+            // rows that came out non-finite, perhaps for a value hidden from them
+            bool bad = false;
+#pragma unroll
+            for (int k = 0; k < D / 2; ++k)
+                bad |= !packed_finite(v[k]);
+            unsigned todo = __ballot_sync(kFull, dst != nullptr && bad);
+            if (todo == 0)
+                return;
+            __syncwarp();
+            const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
+            for (; todo != 0; todo &= todo - 1) {
+                const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
+                const int tk = rr / G;
+                const long long at = (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
+                if (w.pos0 + tk >= 0)
+                    window_mend_row<T, D, kFp8>(p, p.key_cache, p.value_cache, table, w.kh,
+                                                w.pos0 + tk,
+                                                static_cast<const T *>(p.query) + at,
+                                                static_cast<T *>(p.out) + at);
+            }
         };
         if constexpr (!kFp8) {
-            // Warp 8 also zeroes, once landed, the value rows that no row of a unit
-            // sees, before the value-product warp may read them.
             uint32_t g = 0, nu = 0;
-            uint32_t nland0 = 0, nland1 = 0;
-            bool ok = true;
-            auto zero_hidden = [&](const WtUnit &w, int si, int st) -> bool {
-                if (!wait(vland(st), (st ? nland1 : nland0) & 1))
-                    return false;
-                ++(st ? nland1 : nland0);
-                const int c0 = si * kWtKeys;
-                const int rows = w.half(si) ? kWtHalf : kWtKeys;
-                const uint32_t vb = sbase + L::kV + st * L::kTile;
-#pragma unroll 1
-                for (int i = lane; i < rows; i += 32) {
-                    const int c = c0 + i;
-                    if (!w.unseen(c))
-                        continue;
-#pragma unroll
-                    for (int hf = 0; hf < L::kHalves; ++hf)
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
-                                             vb + (i >> 3) * L::kGroup + hf * L::kPart +
-                                             (i & 7) * 128 + (((k + i) & 7) << 4)),
-                                         "r"(0)
-                                         : "memory");
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(vfull(st));
-                return true;
-            };
-            // A unit's rounded rows are stored after the next unit's first step has
-            // its value rows: those are what the tensor cores may be waiting for.
             WtUnit w;
-            for (int ku = 0; ok && unit_at(ku, w); ++ku) {
+            for (int ku = 0; unit_at(ku, w); ++ku) {
                 const int steps = w.steps();
-                const bool row = r < tok_unit * G && tok < w.count;
-                T *dst = static_cast<T *>(p.out) +
-                         (((long long)w.row0 + tok) * H + w.kh * G + hg) * D;
-                if (steps == 0) {  // no keys: zero rows
-                    if (row)
-                        for (int c = 0; c < D / 8; ++c)
-                            reinterpret_cast<uint4 *>(dst)[c] = make_uint4(0, 0, 0, 0);
+                if (steps == 0) {
+                    zero_row(w);
                     continue;
                 }
-                for (int si = 0; si < steps && ok; ++si, ++g) {
-                    if (warp == kWtOutWarp && w.hidden(si))
-                        ok = zero_hidden(w, si, g & 1);
-                    if (si == 0)
-                        store_rows();
-                }
+                g += steps;
                 const int b = nu & 1;
                 const uint32_t ph = (nu >> 1) & 1;
                 ++nu;
-                ok = ok && wait(lfull(b), ph) && wait(ufull(b), ph);
-                if (!ok)
+                if (!wait(lfull(b), ph) || !wait(ufull(b), ph))
                     break;
-                read_rows(g, b);
-                if (row)
-                    pend = dst;
-                // rows that came out non-finite, perhaps for a value hidden from them
-                bool bad = false;
-#pragma unroll
-                for (int k = 0; k < D / 2; ++k)
-                    bad |= !packed_finite(v[k]);
-                unsigned todo = __ballot_sync(kFull, row && bad);
-                if (todo != 0) {
-                    store_rows();
-                    __syncwarp();
-                    const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
-                    for (; todo != 0; todo &= todo - 1) {
-                        const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
-                        const int tk = rr / G;
-                        const long long at =
-                            (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
-                        if (w.pos0 + tk >= 0)
-                            window_mend_row<T, D, false>(p, p.key_cache, p.value_cache, table, w.kh,
-                                                         w.pos0 + tk,
-                                                         static_cast<const T *>(p.query) + at,
-                                                         static_cast<T *>(p.out) + at);
-                    }
-                }
+                write_rows(w, g, b);
             }
-            store_rows();
         } else {
             // FP8 pools: these warps also widen each step's codes to the fp16
             // operands (one thread a row; value rows that no row of the unit
@@ -788,42 +750,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 WtUnit w;
             };
             Walk wk, wv, wq, wo;
-            // this thread's row of a unit
-            auto row_of = [&](const WtUnit &w) -> T * {
-                return r < tok_unit * G && tok < w.count
-                           ? static_cast<T *>(p.out) +
-                                 (((long long)w.row0 + tok) * H + w.kh * G + hg) * D
-                           : nullptr;
-            };
-            // a unit's rows stored, those that came out non-finite computed anew
-            auto keep_rows = [&](const WtUnit &w, T *dst) {
-                pend = dst;
-                bool bad = false;
-#pragma unroll
-                for (int k = 0; k < D / 2; ++k)
-                    bad |= !packed_finite(v[k]);
-                unsigned todo = __ballot_sync(kFull, dst != nullptr && bad);
-                store_rows();
-                __syncwarp();
-                const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
-                for (; todo != 0; todo &= todo - 1) {
-                    const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
-                    const int tk = rr / G;
-                    const long long at =
-                        (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
-                    if (w.pos0 + tk >= 0)
-                        window_mend_row<T, D, true>(p, p.key_cache, p.value_cache, table, w.kh,
-                                                    w.pos0 + tk,
-                                                    static_cast<const T *>(p.query) + at,
-                                                    static_cast<T *>(p.out) + at);
-                }
-            };
-            auto zero_row = [&](const WtUnit &w) {  // a unit without keys
-                uint4 *dst = reinterpret_cast<uint4 *>(row_of(w));
-                if (dst != nullptr)
-                    for (int c = 0; c < D / 8; ++c)
-                        dst[c] = make_uint4(0, 0, 0, 0);
-            };
             // the next unit with keys (zeros for one without, where asked)
             auto open = [&](Walk &x, bool zeros) {
                 x.si = 0;
@@ -931,9 +857,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (wo.more && there(lfull(wo.nu & 1), (wo.nu >> 1) & 1) &&
                     there(ufull(wo.nu & 1), (wo.nu >> 1) & 1)) {
                     wo.g += wo.steps;
-                    T *const dst = row_of(wo.w);
-                    read_rows(wo.g, wo.nu & 1);
-                    keep_rows(wo.w, dst);
+                    write_rows(wo.w, wo.g, wo.nu & 1);
                     ++wo.nu;
                     open(wo, true);
                     did = true;
@@ -966,7 +890,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             Slot3 s2;                     // of step g - 2
             int qk = 0;                   // next unit whose query tile goes out
             uint32_t nq = 0, nu = 0;      // query tiles issued, units with keys begun
-            uint32_t nland0 = 0, nland1 = 0;    // fills of a value stage onto vland
             uint32_t last0 = 0, last1 = 0;      // last fill's barrier per stage (0: none)
             uint32_t last_ph0 = 0, last_ph1 = 0;  // and its phase
             bool ok = true;
@@ -1003,13 +926,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     if (!(p.withhold_fill != 0 && !values && g == 0)) {
                         const int c0 = si * kWtKeys;
                         const int nsub = min(kSubs, (w.kend - c0 + kBox - 1) / kBox);
-                        // (value rows that no row sees are zeroed before the tensor
-                        // cores are told, by the warps that widen FP8 codes too)
-                        const bool fix = !kFp8 && values && w.hidden(si);
                         const uint32_t fb = kFp8 ? (values ? vland(st) : kland(st))
-                                            : !values ? kfull(st)
-                                            : fix     ? vland(st)
-                                                      : vfull(st);
+                                                 : (values ? vfull(st) : kfull(st));
                         const uint32_t tile = sbase + (values ? L::kV : L::kK) + st * L::kTile;
                         const uint32_t dst =
                             !kFp8      ? tile
@@ -1031,9 +949,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                             (ent << (p.block_shift - 3)) + (row >> 3));
                         }
                         (st ? last1 : last0) = fb;
-                        (st ? last_ph1 : last_ph0) = fix ? (st ? nland1 : nland0) & 1 : ph;
-                        if (fix)
-                            ++(st ? nland1 : nland0);
+                        (st ? last_ph1 : last_ph0) = ph;
                     }
                     // Query tiles, two units deep: the tile of unit v goes into the
                     // place of unit v - 2's, whose last S is step g - 2 at the
@@ -1117,13 +1033,35 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                         }
                     }
                 } else {
-                    // a unit's first value product waits until the O of the unit
-                    // before has been read
-                    ok = nu == 0 || wait(ufree(b ^ 1), ((nu - 1) >> 1) & 1);
 #pragma unroll 1
                     for (int rem = kend; rem > 0 && ok; rem -= kWtKeys, ++g, s3.next()) {
                         const int st = g & 1;
                         ok = wait(vfull(st), (g >> 1) & 1);
+                        // (FP8 pools: the warps that widen the codes do this)
+                        if (!kFp8 && ok && w.hidden((kend - rem) / kWtKeys)) {
+#pragma unroll 1
+                            for (int i = lane; i < (rem > kWtHalf ? kWtKeys : kWtHalf); i += 32) {
+                                if (!w.unseen(kend - rem + i))
+                                    continue;
+                                const uint32_t at = sbase + L::kV + st * L::kTile +
+                                                    (i >> 3) * L::kGroup + (i & 7) * 128;
+#pragma unroll
+                                for (int hf = 0; hf < L::kHalves; ++hf)
+#pragma unroll
+                                    for (int k = 0; k < 8; ++k)
+                                        asm volatile(
+                                            "st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                                                at + hf * L::kPart + (((k + i) & 7) << 4)),
+                                            "r"(0)
+                                            : "memory");
+                            }
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                        }
+                        // a unit's first value product waits until the O of the
+                        // unit before has been read
+                        if (rem == kend && nu > 0)
+                            ok = ok && wait(ufree(b ^ 1), ((nu - 1) >> 1) & 1);
                         const int halves = rem > kWtHalf ? 2 : 1;
                         uint64_t dv = desc_v0 + (uint64_t)((st * L::kTile) >> 4);
                         uint32_t p_at = tmem + s3.i * kWtKeys;
