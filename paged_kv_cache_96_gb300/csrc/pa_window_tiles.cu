@@ -192,6 +192,18 @@ __device__ __forceinline__ void store_shared(uint32_t a, const uint4 &v)
                  : "memory");
 }
 
+// x * 0 + acc of two 16-bit values.
+template <typename T>
+__device__ __forceinline__ uint32_t fma_zero_x2(uint32_t x, uint32_t acc)
+{
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(acc));
+    else
+        asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(0), "r"(acc));
+    return r;
+}
+
 // Whether a barrier's phase has completed (never suspends, unlike a try_wait).
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 {
@@ -633,10 +645,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     } else if (warp < kWtKeyWarp) {
         // ===== output warps: O / l of a unit, while the next one is computed ==============
         const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-        auto packed_finite = [](uint32_t w) -> bool {
-            constexpr uint32_t kExp = std::is_same<T, __nv_bfloat16>::value ? 0x7f80u : 0x7c00u;
-            return (w & kExp) != kExp && ((w >> 16) & kExp) != kExp;
-        };
         uint32_t v[D / 2];
         auto store_row = [&](T *dst) {
 #pragma unroll
@@ -681,15 +689,21 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const float l0 = part_l[a0], l1 = part_l[a1];
             const float l = l1 == 0.f ? l0 : l0 + l1 * exp2f(part_m[a1] - part_m[a0]);
             const float inv = l > 0.f ? p.out_scale / l : l;  // (0 for a row without keys)
+            const uint64_t inv2 = pack_f32x2(inv, inv), zero2 = pack_f32x2(0.f, 0.f);
             const uint32_t o_at = tmem + lanes + kWtTmemO;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32];
                 tmem_ld_32x32b_x32(o_at + c * 32, o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    v[16 * c + k] = MmaOp<T>::pack(__uint_as_float(o[2 * k]) * inv,
-                                                   __uint_as_float(o[2 * k + 1]) * inv);
+                for (int k = 0; k < 16; ++k) {
+                    float lo, hi;
+                    unpack_f32x2(ffma_f32x2(pack_f32x2(__uint_as_float(o[2 * k]),
+                                                       __uint_as_float(o[2 * k + 1])),
+                                            inv2, zero2),
+                                 lo, hi);
+                    v[16 * c + k] = MmaOp<T>::pack(lo, hi);
+                }
             }
             // O is read: the next unit's value products may write it
             tc_fence_before();
@@ -700,11 +714,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (dst != nullptr)
                 store_row(dst);
             // rows that came out non-finite, perhaps for a value hidden from them
-            bool bad = false;
+            // (x * 0 + nan: a sum that stays zero while everything is finite)
+            uint32_t nan = 0;
 #pragma unroll
             for (int k = 0; k < D / 2; ++k)
-                bad |= !packed_finite(v[k]);
-            unsigned todo = __ballot_sync(kFull, dst != nullptr && bad);
+                nan = fma_zero_x2<T>(v[k], nan);
+            unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0);
             if (todo == 0)
                 return;
             __syncwarp();
