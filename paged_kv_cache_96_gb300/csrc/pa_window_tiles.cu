@@ -14,8 +14,8 @@
 // below: 8,192 rows of 4 sequences, 32 heads over 8, d 128, window 4,096 and 64
 // first tokens of up to 32,768, blocks of 32 (0.56 TFLOP of rows and keys seen:
 // 375 us, 1.49 PFLOP/s, where the device is within 5 % of its power limit);
-// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (38 us,
-// 0.68 PFLOP/s).
+// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (37.6 us,
+// 0.69 PFLOP/s).
 //  * A score product reads its query rows from shared memory for every step,
 //    so N = 128 keys cost what 64 do (~60 cycles an MMA for either); 64-key
 //    steps pay that, and every barrier and commit, twice (505 us).
@@ -56,7 +56,7 @@
 //    keys, values, query tiles and finished units come.  By count
 //    shared memory bounds it: 32 KB of codes written and read and 64 KB of fp16
 //    written a step, ~1,000 cycles beside the ~1,000 of the operands' reads
-//    (578 us and 62).  The query is rounded to fp16, the K scale joins the
+//    (580 us and 56).  The query is rounded to fp16, the K scale joins the
 //    exponent's scale and the V scale the output.
 // P is rounded to the operands' type, relative error 2^-9 (bf16) or 2^-12: about
 // that of the rounded output; the sum keeps the unrounded fp32 weights.
@@ -645,26 +645,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     } else if (warp < kWtKeyWarp) {
         // ===== output warps: O / l of a unit, while the next one is computed ==============
         const bool out32 = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
-        uint32_t v[D / 2];
-        auto store_row = [&](T *dst) {
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) {
-                T *at = dst + 16 * i;
-                if (out32) {
-                    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(
-                                     at),
-                                 "r"(v[8 * i]), "r"(v[8 * i + 1]), "r"(v[8 * i + 2]),
-                                 "r"(v[8 * i + 3]), "r"(v[8 * i + 4]), "r"(v[8 * i + 5]),
-                                 "r"(v[8 * i + 6]), "r"(v[8 * i + 7])
-                                 : "memory");
-                } else {
-                    reinterpret_cast<uint4 *>(at)[0] =
-                        make_uint4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
-                    reinterpret_cast<uint4 *>(at)[1] =
-                        make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
-                }
-            }
-        };
         // this thread's row of a unit
         auto row_of = [&](const WtUnit &w) -> T * {
             return r < tok_unit * G && tok < w.count
@@ -679,7 +659,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     dst[c] = make_uint4(0, 0, 0, 0);
         };
         // A unit's rows (the CTA's steps up to its end: g), once its sums and last
-        // value product are there: rounded, O given back, stored.
+        // value product are there: rounded and stored, O given back.
         auto write_rows = [&](const WtUnit &w, uint32_t g, int b) {
             tc_fence_after();
             // O is relative to the last step's reference, which the softmax
@@ -691,9 +671,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const float inv = l > 0.f ? p.out_scale / l : l;  // (0 for a row without keys)
             const uint64_t inv2 = pack_f32x2(inv, inv), zero2 = pack_f32x2(0.f, 0.f);
             const uint32_t o_at = tmem + lanes + kWtTmemO;
-#pragma unroll
+            T *const dst = row_of(w);
+            // rows that come out non-finite, perhaps for a value hidden from them:
+            // x * 0 + nan is a sum that stays zero while everything is finite
+            uint32_t nan = 0;
+            // (a loop: unrolled, it took the tensor-core warps' code out of the
+            // instruction cache at the end of every unit)
+#pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
-                uint32_t o[32];
+                uint32_t o[32], v[16];
                 tmem_ld_32x32b_x32(o_at + c * 32, o);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
@@ -702,7 +688,27 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                                        __uint_as_float(o[2 * k + 1])),
                                             inv2, zero2),
                                  lo, hi);
-                    v[16 * c + k] = MmaOp<T>::pack(lo, hi);
+                    v[k] = MmaOp<T>::pack(lo, hi);
+                    nan = fma_zero_x2<T>(v[k], nan);
+                }
+                if (dst == nullptr)
+                    continue;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    T *at = dst + 32 * c + 16 * i;
+                    if (out32) {
+                        asm volatile(
+                            "st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(at),
+                            "r"(v[8 * i]), "r"(v[8 * i + 1]), "r"(v[8 * i + 2]),
+                            "r"(v[8 * i + 3]), "r"(v[8 * i + 4]), "r"(v[8 * i + 5]),
+                            "r"(v[8 * i + 6]), "r"(v[8 * i + 7])
+                            : "memory");
+                    } else {
+                        reinterpret_cast<uint4 *>(at)[0] =
+                            make_uint4(v[8 * i], v[8 * i + 1], v[8 * i + 2], v[8 * i + 3]);
+                        reinterpret_cast<uint4 *>(at)[1] =
+                            make_uint4(v[8 * i + 4], v[8 * i + 5], v[8 * i + 6], v[8 * i + 7]);
+                    }
                 }
             }
             // O is read: the next unit's value products may write it
@@ -710,15 +716,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(ufree(b));
-            T *const dst = row_of(w);
-            if (dst != nullptr)
-                store_row(dst);
-            // rows that came out non-finite, perhaps for a value hidden from them
-            // (x * 0 + nan: a sum that stays zero while everything is finite)
-            uint32_t nan = 0;
-#pragma unroll
-            for (int k = 0; k < D / 2; ++k)
-                nan = fma_zero_x2<T>(v[k], nan);
             unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0);
             if (todo == 0)
                 return;
