@@ -12,10 +12,12 @@
 // x * (1 / scale) for FP8 pools.
 //
 // What bounds it: memory.  Every element of q, k and v is read and written
-// once, and the angles cost nothing next to that if they are computed once a
+// once, and the angles cost little next to that if they are computed once a
 // token: a CTA takes one token, its first threads compute the R / 2 sines and
 // cosines into shared memory while the first rows' loads are in flight, and
-// every head reuses them.  A cosine table over positions would have to be
+// every head reuses them (4 tokens 2.0 us a call in a graph, 128 tokens into FP8
+// pools 2.8).  Long batches stream through persistent warps instead (below:
+// 16,381 tokens of 20 KB 111 us, 6.06 TB/s).  A cosine table over positions would have to be
 // read instead (R * 4 bytes a token and axis, and as long as the longest
 // context); the angle itself costs about 40 instructions a pair.
 //
@@ -28,18 +30,29 @@
 // to 10^-8 below a million.
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "pa_common.cuh"
-#include "pa_ptx.cuh"
+#include "pa_decode_common.cuh"
 
 namespace pa {
 
 constexpr int kRopeMaxPairs = 128;  // head_dim up to 256
 constexpr int kRopeMaxThreads = 256;
 constexpr int kAhead = 3;  // rotary items of a thread whose loads go out first
+// the streaming kernel: warps of a CTA (one an SM), bytes of a unit, units ahead
+constexpr int kRingWarps = 24;
+constexpr int kRingUnit = 2560;
+constexpr int kRingDepth = 3;
+// Batches that stream: rows of 4 KB (query, key and value) and 64 MB of them.  64 + 8
+// + 8 heads of 128: 16,381 tokens 111 us (a CTA a token: 123), 4,096 tokens 33.2
+// (33.7), 2,048 tokens 20.5 (18.0); 16 + 2 + 2 heads: 16,381 tokens 36.8 (51.5),
+// 8,192 tokens 22.1 (26.5), 4,096 tokens 13.7 (13.5); rows of 3 KB, 8 + 8 + 8 heads of
+// 64, 16,381 tokens 29.2 (22.9): a warp's own angles are most of its work there.
+constexpr long long kRingRowBytes = 4096;
+constexpr long long kRingBytes = 64ll << 20;
 
 struct RopeParams {
     void *query_out;
@@ -52,6 +65,8 @@ struct RopeParams {
     long long num_slots;
     int num_tokens, num_heads, num_kv_heads, head_dim, rot_dim;
     float k_inv_scale, v_inv_scale;  // FP8 pools
+    uint64_t wait_ns;                // streaming kernel: limit of one wait
+    int parts, part_heads;           // streaming kernel: units of a token, heads of one
     uint8_t axis[kRopeMaxPairs];     // axis of each rotary pair
 };
 
@@ -108,6 +123,31 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], float inv)
     c.y = (uint32_t)f32x2_to_e4m3x2(x[4] * inv, x[5] * inv) |
           ((uint32_t)f32x2_to_e4m3x2(x[6] * inv, x[7] * inv) << 16);
     return c;
+}
+
+// Eight pairs turned: words wu and wv hold (u, v), or, interleaved, pairs 0-3 and 4-7.
+template <typename T, bool kInterleaved>
+__device__ __forceinline__ void rope_turn(const uint4 &wu, const uint4 &wv, const float (&c)[8],
+                                          const float (&s)[8], float (&x)[8], float (&y)[8])
+{
+    float u[8], w[8];
+    unpack8<T>(wu, u);
+    unpack8<T>(wv, w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        // pair i: interleaved, elements 2i and 2i + 1 of the two words
+        const float a = kInterleaved ? (i < 4 ? u[(2 * i) & 7] : w[(2 * i) & 7]) : u[i];
+        const float b = kInterleaved ? (i < 4 ? u[(2 * i + 1) & 7] : w[(2 * i + 1) & 7]) : w[i];
+        const float r0 = a * c[i] - b * s[i];
+        const float r1 = b * c[i] + a * s[i];
+        if constexpr (kInterleaved) {
+            (i < 4 ? x : y)[(2 * i) & 7] = r0;
+            (i < 4 ? x : y)[(2 * i + 1) & 7] = r1;
+        } else {
+            x[i] = r0;
+            y[i] = r1;
+        }
+    }
 }
 
 // One CTA per token.  The row's work is a list of items: first the rotary
@@ -188,29 +228,12 @@ __global__ void __launch_bounds__(kRopeMaxThreads)
     auto turn = [&](int it, const uint4 &wu, const uint4 &wv) {
         int h, lo, hi;
         const int j = locate(it, h, lo, hi);
-        float u[8], w[8], c[8], s[8];
-        unpack8<T>(wu, u);
-        unpack8<T>(wv, w);
+        float c[8], s[8], x[8], y[8];
         *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(cos_s + 8 * j);
         *reinterpret_cast<float4 *>(c + 4) = *reinterpret_cast<const float4 *>(cos_s + 8 * j + 4);
         *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(sin_s + 8 * j);
         *reinterpret_cast<float4 *>(s + 4) = *reinterpret_cast<const float4 *>(sin_s + 8 * j + 4);
-        float x[8], y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            // pair i of the item: interleaved, elements 2i and 2i + 1 of the two words
-            const float a = kInterleaved ? (i < 4 ? u[(2 * i) & 7] : w[(2 * i) & 7]) : u[i];
-            const float b = kInterleaved ? (i < 4 ? u[(2 * i + 1) & 7] : w[(2 * i + 1) & 7]) : w[i];
-            const float r0 = a * c[i] - b * s[i];
-            const float r1 = b * c[i] + a * s[i];
-            if constexpr (kInterleaved) {
-                (i < 4 ? x : y)[(2 * i) & 7] = r0;
-                (i < 4 ? x : y)[(2 * i + 1) & 7] = r1;
-            } else {
-                x[i] = r0;
-                y[i] = r1;
-            }
-        }
+        rope_turn<T, kInterleaved>(wu, wv, c, s, x, y);
         if (h < H) {
             *reinterpret_cast<uint4 *>(qo + h * D + lo) = pack8<T>(x);
             *reinterpret_cast<uint4 *>(qo + h * D + hi) = pack8<T>(y);
@@ -264,9 +287,267 @@ __global__ void __launch_bounds__(kRopeMaxThreads)
     }
 }
 
-template <typename T, bool kFp8>
-static pa_status launch_rope(const RopeParams &p, bool interleaved, cudaStream_t stream)
+// ---- long batches -----------------------------------------------------------------
+//
+// A warp streams units (some consecutive heads of one token's query, key and
+// value rows, kRingUnit bytes at most) through kRingDepth places of its own in
+// shared memory: one lane asks for a unit as bulk copies, whole rows at a time,
+// the warp turns and stores the unit before it.  No warp waits for another,
+// and loads stay in flight while others compute and store, which a CTA a token
+// lacks between its loads and its end.  A warp's units follow one another, so
+// it has a token's angles once (units dealt round by round: 159 us instead of
+// 111, the angles being longer than a unit).  (16 warps with 2 units of 5,120
+// bytes: 123; 24 with 2 of 4,096: 117.)
+
+// `bytes` (a multiple of 16) from 16-byte aligned global memory.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar)
 {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(src), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+
+template <typename T, bool kFp8, bool kInterleaved>
+__global__ void __launch_bounds__(32 * kRingWarps, 1)
+    rope_stream_kernel(const __grid_constant__ RopeParams p)
+{
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint8_t *own = smem + warp * (kRingDepth * kRingUnit);  // this warp's units
+    float *cos_s = reinterpret_cast<float *>(smem + kRingWarps * kRingDepth * kRingUnit) +
+                   warp * (2 * kRopeMaxPairs);
+    float *sin_s = cos_s + kRopeMaxPairs;
+    const uint32_t bars = smem_addr(smem + kRingWarps * (kRingDepth * kRingUnit +
+                                                         8 * kRopeMaxPairs)) +
+                          warp * (8 * kRingDepth);
+    if (lane == 0) {
+        for (int i = 0; i < kRingDepth; ++i)
+            mbar_init(bars + 8 * i, 1);
+        fence_barrier_init();
+    }
+    __syncwarp();
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    const int H = p.num_heads, K = p.num_kv_heads, D = p.head_dim, R = p.rot_dim;
+    const int pairs = R >> 1, chunks = R >> 4, rest = (D - R) >> 3;
+    const int turned = H + K, heads = H + 2 * K;
+    // this lane's place: chunk j of every head_step-th head
+    const int head_step = 32 / chunks;
+    const int j = lane % chunks, first_head = lane / chunks;
+    const int lo = kInterleaved ? 16 * j : 8 * j;
+    const int hi = kInterleaved ? lo + 8 : pairs + 8 * j;
+
+    const long long units = (long long)p.num_tokens * p.parts;
+    const long long workers = (long long)gridDim.x * kRingWarps;
+    const long long w = (long long)warp * gridDim.x + blockIdx.x;
+    const long long begin = units * w / workers, end = units * (w + 1) / workers;
+    if (begin >= end)
+        return;
+
+    struct Cursor {  // a unit: token, and its first head
+        int t, a;
+    };
+    auto advance = [&](Cursor &c) {
+        c.a += p.part_heads;
+        if (c.a >= heads) {
+            c.a = 0;
+            ++c.t;
+        }
+    };
+    Cursor cur, to_fetch;
+    cur.t = (int)(begin / p.parts);
+    cur.a = (int)(begin - (long long)cur.t * p.parts) * p.part_heads;
+    to_fetch = cur;
+    const int count = (int)(end - begin);
+    auto fetch = [&](const Cursor &c, int place) {  // (one lane)
+        const int t = c.t, a = c.a, b = min(a + p.part_heads, heads);
+        const uint32_t bar = bars + 8 * place;
+        const uint32_t dst = smem_addr(own) + place * kRingUnit;
+        mbar_arrive_expect_tx(bar, (uint32_t)((b - a) * D * 2));
+        auto range = [&](const void *base, long long stride, int from, int to) {
+            const int x = max(a, from), y = min(b, to);
+            if (x < y)
+                bulk_load(dst + (x - a) * D * 2,
+                          static_cast<const T *>(base) + t * stride + (x - from) * D,
+                          (uint32_t)((y - x) * D * 2), bar);
+        };
+        range(p.query, p.q_stride, 0, H);
+        range(p.key, p.k_stride, H, turned);
+        range(p.value, p.v_stride, turned, heads);
+    };
+    // what a token's angles and cache row need, loaded one unit ahead
+    float freq[kRopeMaxPairs / 32];
+#pragma unroll
+    for (int m = 0; m < kRopeMaxPairs / 32; ++m)
+        freq[m] = lane + 32 * m < pairs ? p.inv_freq[lane + 32 * m] : 0.f;
+    int pos[kRopeMaxPairs / 32];
+    long long slot;
+    auto ahead = [&](int t) {
+#pragma unroll
+        for (int m = 0; m < kRopeMaxPairs / 32; ++m)
+            pos[m] = lane + 32 * m < pairs
+                         ? __ldg(p.positions + (long long)p.axis[lane + 32 * m] * p.num_tokens + t)
+                         : 0;
+        slot = __ldg(p.slot_mapping + t);
+    };
+
+    for (int i = 0; i < kRingDepth && i < count; ++i) {
+        if (lane == 0)
+            fetch(to_fetch, i);
+        advance(to_fetch);
+    }
+    ahead(cur.t);
+    int angles_of = -1, place = 0;
+    uint32_t phase = 0;
+    for (int u = 0; u < count; ++u) {
+        const int t = cur.t, a = cur.a, b = min(a + p.part_heads, heads);
+        advance(cur);
+        if (angles_of != t) {
+            __syncwarp();  // (the unit before has read the angles)
+#pragma unroll
+            for (int m = 0; m < kRopeMaxPairs / 32; ++m)
+                if (lane + 32 * m < pairs) {
+                    float s, c;
+                    sincospif(2.f * rope_turns(pos[m], freq[m]), &s, &c);
+                    cos_s[lane + 32 * m] = c;
+                    sin_s[lane + 32 * m] = s;
+                }
+            __syncwarp();
+            angles_of = t;
+        }
+        long long row = slot;
+        if (row >= p.num_slots) {
+            if (lane == 0)
+                flag_error(p.error_word, PA_DEVERR_SLOT_RANGE);
+            row = -1;
+        }
+        row *= (long long)K * D;  // element offset of the token's cache row (negative: none)
+        if (u + 1 < count && cur.t != t)
+            ahead(cur.t);
+        if (!__all_sync(kFull, mbar_wait_bounded(bars + 8 * place, phase, p.wait_ns))) {
+            if (lane == 0)
+                flag_error(p.error_word, PA_DEVERR_TIMEOUT);
+            // (no copy may land after this warp has left)
+            for (int i = 0; i < kRingDepth && u + i < count; ++i) {
+                mbar_wait_bounded(bars + 8 * place, phase, kDrainWaitNs);
+                if (++place == kRingDepth) {
+                    place = 0;
+                    phase ^= 1;
+                }
+            }
+            break;
+        }
+        const T *unit = reinterpret_cast<const T *>(own + place * kRingUnit);
+        T *qo = static_cast<T *>(p.query_out) + (long long)t * p.qo_stride;
+        auto put_cache = [&](void *cache, float inv, long long at, const uint4 &word,
+                             const float (&x)[8]) {
+            if (row < 0)
+                return;
+            if constexpr (kFp8)
+                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(cache) + row + at) =
+                    codes8(x, inv);
+            else
+                *reinterpret_cast<uint4 *>(static_cast<T *>(cache) + row + at) = word;
+        };
+        if (first_head < head_step && a < turned) {
+            float c[8], s[8];
+            *reinterpret_cast<float4 *>(c) = *reinterpret_cast<const float4 *>(cos_s + 8 * j);
+            *reinterpret_cast<float4 *>(c + 4) =
+                *reinterpret_cast<const float4 *>(cos_s + 8 * j + 4);
+            *reinterpret_cast<float4 *>(s) = *reinterpret_cast<const float4 *>(sin_s + 8 * j);
+            *reinterpret_cast<float4 *>(s + 4) =
+                *reinterpret_cast<const float4 *>(sin_s + 8 * j + 4);
+            for (int h = a + first_head; h < min(b, turned); h += head_step) {
+                const T *src = unit + (h - a) * D;
+                float x[8], y[8];
+                rope_turn<T, kInterleaved>(*reinterpret_cast<const uint4 *>(src + lo),
+                                           *reinterpret_cast<const uint4 *>(src + hi), c, s, x,
+                                           y);
+                if (h < H) {
+                    *reinterpret_cast<uint4 *>(qo + h * D + lo) = pack8<T>(x);
+                    *reinterpret_cast<uint4 *>(qo + h * D + hi) = pack8<T>(y);
+                } else {
+                    const long long at = (long long)(h - H) * D;
+                    put_cache(p.key_cache, p.k_inv_scale, at + lo, pack8<T>(x), x);
+                    put_cache(p.key_cache, p.k_inv_scale, at + hi, pack8<T>(y), y);
+                }
+            }
+        }
+        // elements past the rotary ones, and values: words passed on
+        const int rest_items = max(0, min(b, turned) - a) * rest;
+        for (int it = lane; it < rest_items; it += 32) {
+            const int h = a + it / rest, d = R + 8 * (it % rest);
+            const uint4 word = *reinterpret_cast<const uint4 *>(unit + (h - a) * D + d);
+            float x[8];
+            unpack8<T>(word, x);
+            if (h < H)
+                *reinterpret_cast<uint4 *>(qo + h * D + d) = word;
+            else
+                put_cache(p.key_cache, p.k_inv_scale, (long long)(h - H) * D + d, word, x);
+        }
+        const int v0 = max(a, turned);
+        const int v_words = max(0, b - v0) * (D >> 3);
+        for (int it = lane; it < v_words; it += 32) {
+            const uint4 word =
+                *reinterpret_cast<const uint4 *>(unit + (v0 - a) * D + 8 * it);
+            float x[8];
+            unpack8<T>(word, x);
+            put_cache(p.value_cache, p.v_inv_scale, (long long)(v0 - turned) * D + 8 * it, word,
+                      x);
+        }
+        __syncwarp();
+        if (u + kRingDepth < count) {
+            if (lane == 0)
+                fetch(to_fetch, place);
+            advance(to_fetch);
+        }
+        if (++place == kRingDepth) {
+            place = 0;
+            phase ^= 1;
+        }
+    }
+}
+
+template <typename T, bool kFp8>
+static pa_status launch_rope(RopeParams &p, bool interleaved, cudaStream_t stream)
+{
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return record_cuda(e);
+    DeviceInfo info;
+    const pa_status st = device_info(dev, &info);
+    if (st != PA_OK)
+        return st;
+    const int heads = p.num_heads + 2 * p.num_kv_heads;
+    const int most = kRingUnit / (2 * p.head_dim);
+    p.parts = (heads + most - 1) / most;
+    p.part_heads = (heads + p.parts - 1) / p.parts;
+    p.wait_ns = stage_wait_limit_ns();
+    const long long row_bytes = 2ll * heads * p.head_dim;
+    if (row_bytes >= kRingRowBytes && row_bytes * p.num_tokens >= kRingBytes) {
+        auto kernel = interleaved ? rope_stream_kernel<T, kFp8, true>
+                                  : rope_stream_kernel<T, kFp8, false>;
+        constexpr size_t smem = kRingWarps * (kRingDepth * kRingUnit + 8 * kRopeMaxPairs +
+                                              8 * kRingDepth);
+        static bool enabled[2][kMaxDevices];
+        static std::mutex mu;
+        {
+            std::lock_guard<std::mutex> lock(mu);
+            if (!enabled[interleaved][dev]) {
+                const cudaError_t err = cudaFuncSetAttribute(
+                    kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                if (err != cudaSuccess)
+                    return record_cuda(err);
+                enabled[interleaved][dev] = true;
+            }
+        }
+        return launch_pdl(kernel, dim3((unsigned)info.sms), dim3(32 * kRingWarps), smem, stream,
+                          p);
+    }
     auto kernel = interleaved ? rope_and_cache_kernel<T, kFp8, true>
                               : rope_and_cache_kernel<T, kFp8, false>;
     // Threads that share the rotary items evenly, kAhead or fewer each for rows

@@ -88,7 +88,13 @@ def check(s, out, q, k, v, kc0, dtype, fp8, interleaved):
     (7, 3, 1, 256, 256, 1, False, False, 2 ** 24),
     (3, 2, 1, 16, 16, 1, True, True, 100),
     (300, 40, 8, 48, 16, 2, False, True, 50000),
-    (2, 128, 16, 128, 112, 3, False, False, 300)])
+    (2, 128, 16, 128, 112, 3, False, False, 300),
+    # long batches: units of one token and of parts of a token
+    (2101, 100, 14, 128, 128, 3, False, True, 131072),
+    (2101, 96, 16, 128, 96, 2, True, True, 131072),
+    (1401, 80, 8, 256, 192, 1, False, False, 2 ** 20),
+    (16001, 16, 1, 128, 128, 1, False, True, 2 ** 31 - 1),
+    (16011, 40, 2, 48, 16, 2, True, False, 1000)])
 def test_matches_the_definition(B, fp8, dtype, T, H, K, D, rot, axes, interleaved, fused, max_pos):
     s = make(T, H, K, D, rot, dtype, fp8, axes, max_pos, fused, T * 7 + D)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
@@ -201,3 +207,47 @@ def test_captured_and_on_another_stream(B):
     g.replay()
     torch.cuda.synchronize()
     check(s, out, q, k, v, kc0, torch.bfloat16, False, False)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_long_batch_in_place_with_bad_slots(B, fp8):
+    """In place in the fused rows; slots that are negative or past the pool
+    write nothing, and only the latter are flagged."""
+    s = make(2300, 100, 14, 128, 128, torch.bfloat16, fp8, 3, 131072, True, 21)
+    q, k, v, kc0 = s["q"].clone(), s["k"].clone(), s["v"].clone(), s["kc"].clone()
+    N, bs = s["kc"].shape[:2]
+    good = s["slots"].clone()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = dict(k_scale=SCALE, v_scale=SCALE) if fp8 else {}
+    s["slots"][5::7] = -1
+    call(B, s, s["q"], error_word=err, **kw)
+    assert int(err.item()) == 0
+    check(s, s["q"], q, k, v, kc0, torch.bfloat16, fp8, False)
+    for name, x in dict(q=q, kc=kc0, vc=kc0).items():
+        s[name].copy_(x)
+    s["slots"].copy_(good)
+    bad = torch.arange(3, 2300, 11, device="cuda")
+    s["slots"][bad] = N * bs
+    call(B, s, s["q"], error_word=err, **kw)
+    assert int(err.item()) == B.DEVERR_SLOT_RANGE
+    s["slots"][bad] = -1
+    check(s, s["q"], q, k, v, kc0, torch.bfloat16, fp8, False)
+
+
+def test_long_batch_captured_beside_another(B):
+    """Two long batches on two streams at once, one of them a captured graph."""
+    a, b = (make(2300, 100, 14, 128, 128, torch.bfloat16, False, 3, 131072, True, i)
+            for i in (31, 32))
+    outs = [torch.empty_like(x["q"].contiguous()) for x in (a, b)]
+    kept = [(x["q"].clone(), x["k"].clone(), x["v"].clone(), x["kc"].clone()) for x in (a, b)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(B, a, outs[0])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        g.replay()
+        call(B, b, outs[1], stream=side)
+    torch.cuda.synchronize()
+    for x, o, (q, k, v, kc0) in zip((a, b), outs, kept):
+        check(x, o, q, k, v, kc0, torch.bfloat16, False, False)
