@@ -4,8 +4,10 @@
 Argument marshalling only: every function takes torch CUDA tensors, checks
 their dtype, device and contiguity, and passes raw pointers, sizes and the
 current CUDA stream to the library of the same name.  All computation runs
-in the library's kernels.  There is no fallback: if the library has not been
-built, importing this module raises.
+in the library's kernels.  The serving-step calls (step maps, rotary cache write,
+windowed attention) do the same in C++ (``pyext/calls.cpp``), since the host's part
+is most of what a small one takes.  There is no fallback: if the library has
+not been built, importing this module raises.
 """
 from __future__ import annotations
 
@@ -148,6 +150,20 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
+def _load_calls():
+    """The calls of the serving step, which read their tensors in C++."""
+    try:
+        from . import _calls as calls
+    except ImportError as e:
+        raise ImportError("the extension _calls is missing; build it with "
+                          "`python -m paged_kv_cache_96_gb300.build`") from e
+    calls.bind(_LIB_PATH)
+    return calls
+
+
+_calls = _load_calls()
+
+
 def lib() -> ctypes.CDLL:
     """The loaded C library (for callers that pass raw pointers)."""
     return _lib
@@ -208,70 +224,8 @@ def _check(fn: str, status: int) -> None:
         raise PAError(fn, status)
 
 
-# The wrappers below check a tensor and take its address in one step: type,
-# device and layout are three attribute reads on the way to the pointer, which
-# for a call of a dozen small tensors is most of what the host spends.
-
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-
-
-def _device(t: torch.Tensor, name: str) -> int:
-    """The device of a call's tensors, which has to be the current one (whose
-    stream the call is queued on)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name}: torch.Tensor expected")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"{name}: on device {dev}, which is not the current device")
-    return dev
-
-
-def _at(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int) -> int:
-    """Address of a contiguous tensor of `dtype` on device `dev`."""
-    try:
-        if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _dev(t, name, dtype)
-    raise ValueError(f"{name}: tensors of one call must be on one device")
-
-
-def _opt_at(t: Optional[torch.Tensor], name: str, dev: int) -> Optional[int]:
-    return None if t is None else _at(t, name, torch.int32, dev)
-
-
-def _space(t: Optional[torch.Tensor], dev: int):
-    """Address and bytes of a workspace of any type."""
-    if t is None:
-        return None, 0
-    return _at(t, "workspace", t.dtype, dev), t.numel() * t.element_size()
-
-
-def _queue(stream, dev: int) -> int:
-    if stream is not None:
-        if stream.device.index != dev:
-            raise ValueError("the stream is on another device than the tensors")
-        return stream.cuda_stream
-    if _raw_stream is not None:
-        return _raw_stream(dev)
-    return torch.cuda.current_stream().cuda_stream
-
-
-def _rows(t: torch.Tensor, name: str, dtype: torch.dtype, dev: int):
-    """Address and token stride of [T, heads, d] whose token rows are dense
-    (a view into a wider row, as the parts of a fused QKV projection are)."""
-    if t.dtype is not dtype:
-        raise TypeError(f"{name}: {dtype} expected, got {t.dtype}")
-    if t.get_device() != dev:
-        raise ValueError(f"{name}: tensors of one call must be on one device")
-    a, b, c = t.stride()
-    n, h, d = t.shape
-    if (c != 1 and d > 1) or (b != d and h > 1):
-        raise ValueError(f"{name}: heads and elements of a token must be dense")
-    return t.data_ptr(), a if n > 1 else h * d
+def _suffix(pool: torch.Tensor) -> str:
+    return "_fp8" if pool.dtype is torch.uint8 else ""
 
 
 def pa_build_step_maps(block_tables: torch.Tensor, context_lens: torch.Tensor,
@@ -286,25 +240,11 @@ def pa_build_step_maps(block_tables: torch.Tensor, context_lens: torch.Tensor,
     query_start [S + 1] and the token arrays [T] (a capacity; -1 past the
     step's tokens) are outputs.  query_lens: new tokens of each sequence, or
     STEP_FINISHED.  context_lens_out / free_count_out may be the inputs."""
-    S, MB = block_tables.shape
-    T = token_seq.shape[0]
-    if (context_lens.shape[0] != S or query_lens.shape[0] != S or
-            context_lens_out.shape[0] != S or query_start.shape[0] != S + 1):
-        raise ValueError("one length per sequence and num_seqs + 1 offsets expected")
-    if token_pos.shape[0] != T or slot_mapping.shape[0] != T:
-        raise ValueError("token_seq, token_pos and slot_mapping must have one length")
-    if free_blocks.numel() < num_blocks or free_count.numel() < 1 or free_count_out.numel() < 1:
-        raise ValueError("a stack of num_blocks entries and its count expected")
-    dev, i32 = _device(block_tables, "block_tables"), torch.int32
-    _check("pa_build_step_maps", _lib.pa_build_step_maps(
-        _at(query_start, "query_start", i32, dev), _at(token_seq, "token_seq", i32, dev),
-        _at(token_pos, "token_pos", i32, dev), _at(slot_mapping, "slot_mapping", i32, dev),
-        _at(context_lens_out, "context_lens_out", i32, dev),
-        _at(free_count_out, "free_count_out", i32, dev),
-        _at(block_tables, "block_tables", i32, dev), MB,
-        _at(context_lens, "context_lens", i32, dev), _at(query_lens, "query_lens", i32, dev),
-        _at(free_blocks, "free_blocks", i32, dev), _at(free_count, "free_count", i32, dev), S, T,
-        block_size, num_blocks, _opt_at(error_word, "error_word", dev), _queue(stream, dev)))
+    status = _calls.step_maps(block_tables, context_lens, query_lens, free_blocks, free_count,
+                              block_size, num_blocks, query_start, token_seq, token_pos,
+                              slot_mapping, context_lens_out, free_count_out, error_word, stream)
+    if status:
+        raise PAError("pa_build_step_maps", status)
 
 
 def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.Tensor,
@@ -319,37 +259,11 @@ def pa_rope_and_cache(query_out: torch.Tensor, query: torch.Tensor, key: torch.T
     pools at their slots (e4m3 codes with the scales when they are uint8).
     query, key and value may be views into wider token rows.  inv_freq:
     float32 [rot_dim / 2]."""
-    T, H, d = query.shape
-    N, bs, Hkv, d2 = key_cache.shape
-    if (d != d2 or query_out.shape != query.shape or key.shape != (T, Hkv, d) or
-            value.shape != key.shape or value_cache.shape != key_cache.shape):
-        raise ValueError("shape mismatch between new tokens and pools")
-    if slot_mapping.shape[0] != T or positions.shape[-1] != T or positions.dim() > 2:
-        raise ValueError("one slot and, per axis, one position per new token expected")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    half = inv_freq.shape[0]
-    axis_ptr = None
-    if axis_of_pair is not None:
-        if (axis_of_pair.dtype != torch.int32 or axis_of_pair.is_cuda or
-                axis_of_pair.shape != (half,) or not axis_of_pair.is_contiguous()):
-            raise ValueError("axis_of_pair: int32 CPU tensor, one axis per rotary pair")
-        axis_ptr = axis_of_pair.data_ptr()
-    dev = _device(query, "query")
-    dt, fp8 = query.dtype, key_cache.dtype is torch.uint8
-    pool = torch.uint8 if fp8 else dt
-    args = (*_rows(query_out, "query_out", dt, dev), *_rows(query, "query", dt, dev),
-            *_rows(key, "key", dt, dev), *_rows(value, "value", dt, dev),
-            _at(key_cache, "key_cache", pool, dev), _at(value_cache, "value_cache", pool, dev),
-            _at(slot_mapping, "slot_mapping", torch.int32, dev),
-            _at(positions, "positions", torch.int32, dev), axes, axis_ptr,
-            _at(inv_freq, "inv_freq", torch.float32, dev), 2 * half, 1 if interleaved else 0, T,
-            H, Hkv, d, bs, N, _dtype_code(query))
-    tail = (_opt_at(error_word, "error_word", dev), _queue(stream, dev))
-    if fp8:
-        _check("pa_rope_and_cache_fp8", _lib.pa_rope_and_cache_fp8(
-            *args, float(k_scale), float(v_scale), *tail))
-        return
-    _check("pa_rope_and_cache", _lib.pa_rope_and_cache(*args, *tail))
+    status = _calls.rope(query_out, query, key, value, key_cache, value_cache, slot_mapping,
+                         positions, inv_freq, axis_of_pair, interleaved, k_scale, v_scale,
+                         error_word, stream)
+    if status:
+        raise PAError("pa_rope_and_cache" + _suffix(key_cache), status)
 
 
 def pa_slot_mapping(slot_mapping: torch.Tensor, block_tables: torch.Tensor,
@@ -655,26 +569,11 @@ def pa_decode_attention_window(out: torch.Tensor, query: torch.Tensor,
     """Paged decode over the last `window` tokens and the first num_sinks; out
     and query are [S, H, d].  uint8 pools take the e4m3 path with k_scale /
     v_scale."""
-    S, H, d = query.shape
-    N, bs, Hkv, d2 = key_cache.shape
-    if (d != d2 or out.shape != query.shape or value_cache.shape != key_cache.shape or
-            block_tables.shape[0] != S or context_lens.shape[0] != S):
-        raise ValueError("shape mismatch")
-    dev, dt, i32 = _device(query, "query"), query.dtype, torch.int32
-    fp8 = key_cache.dtype is torch.uint8
-    pool = torch.uint8 if fp8 else dt
-    head = (_at(out, "out", dt, dev), _at(query, "query", dt, dev),
-            _at(key_cache, "key_cache", pool, dev), _at(value_cache, "value_cache", pool, dev),
-            _at(block_tables, "block_tables", i32, dev), block_tables.shape[1],
-            _at(context_lens, "context_lens", i32, dev), int(max_context_len),
-            _reach(window), _reach(num_sinks), S, H, Hkv, d, bs, N, scale)
-    tail = (int(partition_size), *_space(workspace, dev), _dtype_code(query),
-            _opt_at(error_word, "error_word", dev), _queue(stream, dev))
-    if fp8:
-        _check("pa_decode_attention_window_fp8", _lib.pa_decode_attention_window_fp8(
-            *head, float(k_scale), float(v_scale), *tail))
-        return
-    _check("pa_decode_attention_window", _lib.pa_decode_attention_window(*head, *tail))
+    status = _calls.decode_window(out, query, key_cache, value_cache, block_tables, context_lens,
+                                  max_context_len, scale, window, num_sinks, partition_size,
+                                  workspace, k_scale, v_scale, error_word, stream)
+    if status:
+        raise PAError("pa_decode_attention_window" + _suffix(key_cache), status)
 
 
 def pa_prefill_attention_window(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
@@ -688,27 +587,11 @@ def pa_prefill_attention_window(out: torch.Tensor, query: torch.Tensor, key_cach
     [T, H, d], sequence s owns rows [query_start[s], query_start[s + 1]), its
     newest tokens; each row sees the last `window` tokens up to its own and the
     first num_sinks.  uint8 pools take the e4m3 path with k_scale / v_scale."""
-    T, H, d = query.shape
-    N, bs, Hkv, d2 = key_cache.shape
-    S = context_lens.shape[0]
-    if (d != d2 or out.shape != query.shape or value_cache.shape != key_cache.shape or
-            query_start.shape[0] != S + 1 or block_tables.shape[0] != S):
-        raise ValueError("shape mismatch")
-    dev, dt, i32 = _device(query, "query"), query.dtype, torch.int32
-    fp8 = key_cache.dtype is torch.uint8
-    pool = torch.uint8 if fp8 else dt
-    head = (_at(out, "out", dt, dev), _at(query, "query", dt, dev),
-            _at(key_cache, "key_cache", pool, dev), _at(value_cache, "value_cache", pool, dev),
-            _at(block_tables, "block_tables", i32, dev), block_tables.shape[1],
-            _at(query_start, "query_start", i32, dev),
-            _at(context_lens, "context_lens", i32, dev), int(max_context_len), _reach(window),
-            _reach(num_sinks), S, T, H, Hkv, d, bs, N, scale)
-    tail = (_dtype_code(query), _opt_at(error_word, "error_word", dev), _queue(stream, dev))
-    if fp8:
-        _check("pa_prefill_attention_window_fp8", _lib.pa_prefill_attention_window_fp8(
-            *head, float(k_scale), float(v_scale), *tail))
-        return
-    _check("pa_prefill_attention_window", _lib.pa_prefill_attention_window(*head, *tail))
+    status = _calls.prefill_window(out, query, key_cache, value_cache, block_tables, query_start,
+                                   context_lens, max_context_len, scale, window, num_sinks,
+                                   k_scale, v_scale, error_word, stream)
+    if status:
+        raise PAError("pa_prefill_attention_window" + _suffix(key_cache), status)
 
 
 def pa_plan_prefix_groups(block_tables, context_lens, block_size: int,

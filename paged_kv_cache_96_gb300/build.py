@@ -4,7 +4,8 @@
 
 compiles every ``csrc/*.cu`` (device code, one ``-gencode`` each) and
 ``csrc/*.cpp`` (host-only runtime code) in parallel, CUDA runtime linked
-statically, and links ``lib/libpaged_attention.so``.
+statically, and links ``lib/libpaged_attention.so``; beside it ``_calls.so``, the Python
+calls that read torch tensors themselves (``pyext/calls.cpp``, host compiler).
 """
 from __future__ import annotations
 
@@ -14,12 +15,15 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(LIBDIR, "libpaged_attention.so")
+CALLS = os.path.join(HERE, "_calls.so")
+CALLS_SRC = os.path.join(HERE, "pyext", "calls.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--use_fast_math", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
@@ -46,16 +50,34 @@ def _compile(src: str, verbose_ptxas: bool, objdir: str = OBJDIR, extra=()) -> s
     return obj
 
 
+def _build_calls() -> None:
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    tmp = CALLS + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(root, "include"),
+           "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I" + cuda,
+           CALLS_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
+           "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compiling {CALLS_SRC} failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, CALLS)
+
+
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(CALLS):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        os.path.join(os.path.dirname(HERE), "include", "paged_attention.h")]
+        CALLS_SRC, os.path.join(os.path.dirname(HERE), "include", "paged_attention.h")]
     return all(os.path.getmtime(d) <= t for d in deps)
 
 
@@ -70,8 +92,11 @@ def build(force: bool = False, verbose_ptxas: bool = False, extra=(),
     os.makedirs(objdir, exist_ok=True)
     os.makedirs(os.path.dirname(lib), exist_ok=True)
     srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
+        calls = ex.submit(_build_calls) if out is None else None
         objs = list(ex.map(lambda s: _compile(s, verbose_ptxas, objdir, extra), srcs))
+        if calls is not None:
+            calls.result()
     tmp = lib + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

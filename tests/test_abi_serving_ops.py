@@ -185,3 +185,16 @@ def test_binding_refuses_host_tensors_and_shapes(B):
     with pytest.raises(ValueError):
         B.pa_build_step_maps(z(4, 2), z(4), z(4), z(7), z(1), 16, 8, z(5), z(9), z(9), z(9), z(4),
                              z(1))
+    # not tensors, and lists of another shape
+    with pytest.raises(TypeError):
+        B.pa_decode_attention_window(q, None, pool, pool, z(4, 2), z(4), 32, 0.1, 16)
+    with pytest.raises(TypeError):
+        B.pa_build_step_maps([[1]], z(1), z(1), z(8), z(1), 16, 8, z(2), z(9), z(9), z(9), z(1),
+                             z(1))
+    with pytest.raises(ValueError):
+        B.pa_decode_attention_window(q[0], q[0], pool, pool, z(4, 2), z(4), 32, 0.1, 16)
+    with pytest.raises(ValueError):
+        B.pa_prefill_attention_window(q, q, pool, pool, z(2, 2), z(3, 1), z(2), 32, 0.1, 16)
+    with pytest.raises(ValueError):
+        B.pa_build_step_maps(z(4), z(4), z(4), z(8), z(1), 16, 8, z(5), z(9), z(9), z(9), z(4),
+                             z(1))

@@ -251,3 +251,27 @@ def test_long_batch_captured_beside_another(B):
     torch.cuda.synchronize()
     for x, o, (q, k, v, kc0) in zip((a, b), outs, kept):
         check(x, o, q, k, v, kc0, torch.bfloat16, False, False)
+
+
+def test_binding_checks_every_tensor(B):
+    s = make(9, 4, 2, 64, 64, torch.float16, False, 1, 50, True, 51)
+    out = torch.full((9, 4, 64), 7.0, dtype=torch.float16, device="cuda")
+    kept = s["kc"].clone()
+    for name, bad, error in (
+            ("q", s["q"].float(), TypeError), ("q", s["q"].cpu(), ValueError),
+            ("q", s["q"][..., ::2], ValueError), ("q", s["q"][:, ::2], ValueError),
+            ("k", s["k"].bfloat16(), TypeError), ("k", s["k"][:8], ValueError),
+            ("v", s["v"].cpu(), ValueError), ("v", s["v"][:, :, ::2], ValueError),
+            ("kc", s["kc"].bfloat16(), TypeError), ("vc", s["vc"][:-1], ValueError),
+            ("slots", s["slots"].long(), TypeError), ("slots", s["slots"][:-1], ValueError),
+            ("pos", s["pos"][:, :-1], ValueError), ("pos", s["pos"].cpu(), ValueError),
+            ("pos", s["pos"][None], ValueError), ("freq", s["freq"].double(), TypeError),
+            ("freq", s["freq"][None], ValueError), ("axis", s["axis"].cuda(), ValueError),
+            ("axis", s["axis"][1:], ValueError), ("axis", s["axis"] + 1, B.PAError)):
+        with pytest.raises(error):
+            call(B, dict(s, **{name: bad}), out)
+    with pytest.raises(TypeError):
+        call(B, s, out, error_word=torch.zeros(1, device="cuda"))
+    torch.cuda.synchronize()
+    assert bool((out == 7).all())
+    assert torch.equal(s["kc"].view(torch.int16), kept.view(torch.int16))

@@ -220,3 +220,31 @@ def test_captured_step_walks_its_own_state(B, S, MB):
         check(m.got(), want)
         state = want
     assert int(m.err.item()) == 0
+
+
+def test_binding_checks_every_tensor(B):
+    rng = np.random.default_rng(5)
+    tables, ctx, new, free, count = make(rng, 6, 16, 8, 20, finished=0.0)
+    m = Maps(tables, ctx, new, free, count, 16, 90)
+    for name in ("tables", "ctx", "new", "free", "count", "start", "seq", "pos", "slot", "ctx_out",
+                 "count_out", "err"):
+        good = getattr(m, name)
+        for bad, error in ((good.long(), TypeError), (good.cpu(), ValueError), (None, TypeError),
+                           (good.repeat_interleave(2, -1)[..., ::2], ValueError)):
+            if name == "err" and bad is None or good.numel() == 1 and bad is not None and \
+                    bad.is_cuda and bad.dtype == good.dtype:
+                continue                    # (no error word is fine; one entry is dense)
+            setattr(m, name, bad)
+            with pytest.raises(error):
+                m.call(B)
+            setattr(m, name, good)
+    for name in ("ctx", "new", "start", "pos", "slot", "ctx_out"):
+        good = getattr(m, name)
+        setattr(m, name, good[1:])
+        with pytest.raises(ValueError):
+            m.call(B)
+        setattr(m, name, good)
+    torch.cuda.synchronize()
+    assert bool((m.seq == 77).all()) and np.array_equal(m.tables.cpu().numpy(), tables)
+    m.call(B)
+    check(m.got(), R.step_maps(tables, ctx, new, free, count, 16, 90))

@@ -371,3 +371,40 @@ def test_far_context(B):
     c = Case([400000, 33], [70, 33], 8, 2, 128, 16, torch.bfloat16, False, 200, 9)
     c.chunk(B)
     c.check()
+
+
+@pytest.mark.parametrize("call", ["decode", "chunk"])
+def test_binding_checks_every_tensor(B, call):
+    """Type, device, layout and range of each argument, and what is taken: NumPy
+    numbers, windows past 32 bits, a stream object, an error word or none."""
+    c = Case([40, 70], [1, 1], 4, 2, 64, 16, torch.float16, False, 9, 2, poison=False)
+    run = getattr(c, call)
+    for name, bad, error in (
+            ("q", c.q.float(), TypeError), ("q", c.q.cpu(), ValueError),
+            ("q", c.q.transpose(0, 1).contiguous().transpose(0, 1), ValueError),
+            ("q", c.q[0], ValueError), ("out", c.out.bfloat16(), TypeError),
+            ("out", c.out.cpu(), ValueError), ("out", c.out[:1], ValueError),
+            ("kc", c.kc.bfloat16(), TypeError), ("kc", c.kc[:, ::2], ValueError),
+            ("vc", c.vc[:-1], ValueError), ("vc", c.vc.cpu(), ValueError),
+            ("d_tables", c.d_tables.long(), TypeError), ("d_tables", c.d_tables[:1], ValueError),
+            ("d_ctx", c.d_ctx.cpu(), ValueError), ("d_ctx", c.d_ctx.float(), TypeError),
+            ("err", c.err.long(), TypeError), ("err", c.err.cpu(), ValueError),
+            ("max_ctx", 1 << 40, ValueError),
+            ("scale", "large", TypeError), ("scale", float("inf"), B.PAError)):
+        good = getattr(c, name)
+        setattr(c, name, bad)
+        with pytest.raises(error):
+            run(B)
+        setattr(c, name, good)
+    with pytest.raises(AttributeError):
+        run(B, stream=3)
+    assert bool((c.out == 7).all())
+    c.window, c.sinks, c.max_ctx = 1 << 40, np.int64(2), np.int32(c.max_ctx)
+    run(B, stream=torch.cuda.current_stream())
+    c.window = 70                       # what a window past every context is
+    c.check()
+    c.err = None
+    c.out.fill_(7)
+    run(B)
+    c.err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.check()
