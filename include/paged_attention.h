@@ -830,7 +830,8 @@ PA_API uint64_t pa_stage_wait_limit_ns(void);
  * pa_debug_withhold_first_fill -- test hook of the time-out path above, no
  * counterpart on the pages.  While enabled (enable != 0; process-wide, read
  * at launch), every CTA of every attention kernel launched leaves its first
- * K/V fill unissued: nothing completes that stage, so the wait for it
+ * K/V fill unissued (and of pa_rope_and_cache's streaming kernel its first
+ * copy): nothing completes that stage, so the wait for it
  * runs out after the stage-wait limit and the kernel returns through its
  * time-out path (PA_DEVERR_TIMEOUT, undefined outputs of that call).  No
  * fault, no hang: every other copy the kernel issued is waited for.  Off by

@@ -66,7 +66,8 @@ struct RopeParams {
     int num_tokens, num_heads, num_kv_heads, head_dim, rot_dim;
     float k_inv_scale, v_inv_scale;  // FP8 pools
     uint64_t wait_ns;                // streaming kernel: limit of one wait
-    int parts, part_heads;           // streaming kernel: units of a token, heads of one
+    int withhold_fill;               // its test hook: warp 0's first unit is never asked for
+    int parts, part_heads;           // its units of a token, heads of one
     uint8_t axis[kRopeMaxPairs];     // axis of each rotary pair
 };
 
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(32 * kRingWarps, 1)
     };
 
     for (int i = 0; i < kRingDepth && i < count; ++i) {
-        if (lane == 0)
+        if (lane == 0 && !(p.withhold_fill != 0 && warp == 0 && i == 0))
             fetch(to_fetch, i);
         advance(to_fetch);
     }
@@ -527,6 +528,7 @@ static pa_status launch_rope(RopeParams &p, bool interleaved, cudaStream_t strea
     p.parts = (heads + most - 1) / most;
     p.part_heads = (heads + p.parts - 1) / p.parts;
     p.wait_ns = stage_wait_limit_ns();
+    p.withhold_fill = withhold_first_fill();
     const long long row_bytes = 2ll * heads * p.head_dim;
     if (row_bytes >= kRingRowBytes && row_bytes * p.num_tokens >= kRingBytes) {
         auto kernel = interleaved ? rope_stream_kernel<T, kFp8, true>

@@ -125,7 +125,8 @@ __device__ __forceinline__ int window_order_key(const WindowMqParams &p, int s, 
 // looked at again, by one warp: if the values it sees account for every
 // non-finite element (the newest are read first, so a sequence that has
 // diverged is done at once) it stays; else it is computed anew from what it
-// sees.  Only rows of such tiles pay for this.
+// sees, 32 keys at a time, 8 pool rows in flight.  Only rows of such tiles pay
+// for this.
 
 template <typename T> __device__ __forceinline__ float window_float(T x)
 {
@@ -168,19 +169,34 @@ __device__ __noinline__ void window_mend_row(const WindowMqParams &p, const void
                                              const void *value_cache, const int32_t *table,
                                              int kh, int pos, const T *query, T *out)
 {
-    constexpr int E = D / 32;
+    constexpr int E = D / 32, kBatch = 8;  // elements a lane, pool rows in flight
     const int lane = threadIdx.x & 31;
     const int low = max(0, pos + 1 - p.window);     // [low, pos] and [0, first) are seen
     const int first = min(p.num_sinks, low);
     const int seen = pos + 1 - low + first;
-    // the i-th key seen, newest first; its place in the pools, or -1
+    // the i-th key seen, newest first: its row in the pools (-1: none, -2: a
+    // table entry outside the pool)
     auto place = [&](int i) -> long long {
+        if (i >= seen)
+            return -1;
         const int t = i <= pos - low ? pos - i : first - 1 - (i - (pos + 1 - low));
         const int b = table[t >> p.block_shift];
         if (b < 0 || b >= p.num_blocks)
-            return -1;
+            return -2;
         return (((long long)b * p.block_size + (t & (p.block_size - 1))) * p.num_kv_heads + kh) *
-                   D + lane * E;
+               D;
+    };
+    // rows u .. u + 7 of the 32 whose places the lanes hold (zeros for none)
+    auto rows = [&](const void *pool, long long at, int u, float (&x)[kBatch][E]) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const long long a = __shfl_sync(kFull, at, u + k);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                x[k][e] = 0.f;
+            if (a >= 0)
+                window_pool_row<T, E, kFp8>(pool, a + lane * E, x[k]);
+        }
     };
     // elements that are non-finite and not yet accounted for
     unsigned open = 0;
@@ -188,58 +204,85 @@ __device__ __noinline__ void window_mend_row(const WindowMqParams &p, const void
     for (int e = 0; e < E; ++e)
         if (!window_finite(window_float<T>(out[lane * E + e])))
             open |= 1u << e;
-    for (int i = 0; i < seen; ++i) {
+    for (int i = 0; i < seen; i += 32) {
+        const long long at = place(i + lane);
+        if (__any_sync(kFull, at == -2))
+            return;  // (flagged; the row is undefined)
+#pragma unroll 1
+        for (int u = 0; u < 32; u += kBatch) {
+            float v[kBatch][E];
+            rows(value_cache, at, u, v);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (!window_finite(v[k][e]))
+                        open &= ~(1u << e);
+        }
         if (!__any_sync(kFull, open != 0))
             return;
-        const long long at = place(i);
-        if (at < 0)
-            return;  // (a bad table entry: flagged, the row is undefined)
-        float v[E];
-        window_pool_row<T, E, kFp8>(value_cache, at, v);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (!window_finite(v[e]))
-                open &= ~(1u << e);
     }
-    if (!__any_sync(kFull, open != 0))
-        return;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
+    float q[E], o[E], m = -INFINITY, l = 0.f;  // (l: of this lane's keys)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
         q[e] = window_float<T>(query[lane * E + e]);
         o[e] = 0.f;
     }
-    for (int i = 0; i < seen; ++i) {
-        const long long at = place(i);
-        if (at < 0)
-            return;
-        float k[E], v[E];
-        window_pool_row<T, E, kFp8>(key_cache, at, k);
-        window_pool_row<T, E, kFp8>(value_cache, at, v);
-        float s = 0.f;
+    for (int i = 0; i < seen; i += 32) {
+        const long long at = place(i + lane);
+        float mine = -INFINITY;  // the score of key i + lane
+#pragma unroll 1
+        for (int u = 0; u < 32; u += kBatch) {
+            float k[kBatch][E];
+            rows(key_cache, at, u, k);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            s = fmaf(q[e], k[e], s);
+            for (int b = 0; b < kBatch; ++b) {
+                float s = 0.f;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    s = fmaf(q[e], k[b][e], s);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1)
+                    s += __shfl_xor_sync(kFull, s, off);
+                if (lane == u + b && at >= 0)
+                    mine = s * p.scale_log2;
+            }
+        }
+        float top = mine;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1)
-            s += __shfl_xor_sync(kFull, s, off);
-        s *= p.scale_log2;
-        const float mn = fmaxf(m, s);
-        const float a = mn == m ? 1.f : exp2f(m - mn);  // (m: -inf at first)
-        const float w = s == mn ? 1.f : exp2f(s - mn);
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, off));
+        const float mn = fmaxf(m, top);
+        const float ref = mn == -INFINITY ? 0.f : mn;
+        const float a = exp2f(m - ref);  // (0 at first)
+        const float w = exp2f(mine - ref);
         m = mn;
         l = l * a + w;
 #pragma unroll
         for (int e = 0; e < E; ++e)
-            o[e] = o[e] * a + w * v[e];
+            o[e] *= a;
+#pragma unroll 1
+        for (int u = 0; u < 32; u += kBatch) {
+            float v[kBatch][E];
+            rows(value_cache, at, u, v);
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                const float wk = __shfl_sync(kFull, w, u + k);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    o[e] += wk * v[k][e];
+            }
+        }
     }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        l += __shfl_xor_sync(kFull, l, off);
     const float inv = p.out_scale / l;
 #pragma unroll
     for (int e = 0; e < E; ++e)
         out[lane * E + e] = MmaOp<T>::from_float(o[e] * inv);
 }
 
-// The windowed chunk (pa_window_tiles.cu).
 // Sequences of one launch (their unit counts are kept in shared memory).
 constexpr int kWindowMaxSeqs = 5120;
 

@@ -50,7 +50,8 @@
 //  * Value rows that no row of a unit sees are zeroed in shared memory by the
 //    value-product warp (an output warp, busy with the unit before: 382 us and
 //    40.7), so that NaN or another sequence's rows never meet a zero weight; a row
-//    that still comes out non-finite is computed anew from the keys it sees alone.
+//    that still comes out non-finite is computed anew from the keys it sees alone,
+//    after the CTA's last unit, when no other role waits.
 //  * FP8 pools: codes land where the upper half of their fp16 tile will be (d
 //    128; beside it at d 64) and the output warps widen them, in whatever order
 //    keys, values, query tiles and finished units come.  By count
@@ -76,10 +77,10 @@ constexpr int kWtRows = 128;      // rows of a tile (M of the MMAs)
 constexpr int kWtKeys = 128;      // keys of a step
 constexpr int kWtHalf = 64;       // keys of a half step
 constexpr int kWtOutWarp = 8;       // warps 0-3 and 4-7: softmax of even and odd steps
-constexpr int kWtKeyWarp = 12;      // 8-11: output rows (8: hidden value rows too)
+constexpr int kWtKeyWarp = 12;      // 8-11: output rows (FP8 pools: codes widened too)
 constexpr int kWtValueWarp = 13;
 constexpr int kWtScoreWarp = 14;
-constexpr int kWtThreads = 512;     // (15: value products)
+constexpr int kWtThreads = 512;     // (15: value products, hidden value rows)
 constexpr uint32_t kWtTmemCols = 512;  // S at 0, 128 and 256 (P over each), O at 384
 constexpr uint32_t kWtTmemO = 384;
 constexpr int kWtOrderBuckets = 64;
@@ -108,7 +109,7 @@ struct WtUnit {
     }
 };
 // units of a CTA kept in shared memory; later ones are worked out by each role
-constexpr int kWtUnits = 192;
+constexpr int kWtUnits = 160;
 
 // Step g's slot g % 3 and the parity of g / 3, counted along.
 struct Slot3 {
@@ -148,9 +149,11 @@ template <int D, bool kFp8> struct WtLayout {
     static constexpr int kTmemSlot = kBars + 34 * 8;
     static constexpr int kAbort = kTmemSlot + 8;
     static constexpr int kUnits = kTmemSlot + 16;        // the CTA's first units
+    // unsigned rows to compute anew [unit][output warp]
     // int unit prefix[n + 1], then (ordered) order[n], units[n], key[n] and
     // the sort's buckets
-    static constexpr int kSeg = kUnits + kWtUnits * (int)sizeof(WtUnit);
+    static constexpr int kMend = kUnits + kWtUnits * (int)sizeof(WtUnit);
+    static constexpr int kSeg = kMend + kWtUnits * 4 * 4;
     static size_t bytes(int segments, bool ordered)
     {
         return 1024 + kSeg + 4 * ((size_t)segments + 1) +
@@ -248,7 +251,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     constexpr uint32_t kIdescSHalf = idesc_f16(kBf16, kWtRows, kWtHalf, false, false);
     constexpr uint32_t kIdescO = idesc_f16(kBf16, kWtRows, D, false, true);
     constexpr int KT = D / 16;
-    constexpr int kSubs = kWtKeys / kBox;  // boxes of a step and d-half
+    constexpr int kSubs = kWtKeys / kBox;  // boxes of a step
 
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
@@ -256,20 +259,19 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const uint32_t sbase = smem_addr(smem);
     int *pref = reinterpret_cast<int *>(smem + L::kSeg);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::kAbort);
-    // mbarriers.  [parity of the step]: K / V of a stage ready; V landed before
-    // its hidden rows are zeroed; the rows' references after the step stored.
+    // mbarriers.  [parity of the step]: K / V of a stage ready; its codes landed
+    // (FP8 pools); the rows' references after the step stored.
     // [step % 3]: S computed (frees the K stage); half h of P stored by the 4
     // softmax warps; value product done (frees S, P and the V stage).  (A wait
     // for a step's phase needs the next step on the same barrier to depend on
     // the waiter: the products of step g + 2 do not depend on a wait for step
     // g's, those of step g + 3 do.)
-    // [parity of the unit]: query tile landed; the unit's last value product
+    // [parity of the unit]: query tile ready; the unit's last value product
     // done; its sums stored by the 8 softmax warps; its O and sums read by 4.
     // Every tensor-core operation done.
     auto bar = [&](int i) { return sbase + L::kBars + 8 * i; };
     auto kfull = [&](int st) { return bar(st); };
     auto vfull = [&](int st) { return bar(2 + st); };
-    auto vland = [&](int st) { return bar(4 + st); };
     auto mfull = [&](int st) { return bar(8 + st); };
     auto qfull = [&](int b) { return bar(10 + b); };
     auto ufull = [&](int b) { return bar(12 + b); };
@@ -278,8 +280,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     auto sfull = [&](int i) { return bar(18 + i); };
     auto pfull = [&](int h, int i) { return bar(21 + 3 * h + i); };
     auto ofull = [&](int i) { return bar(27 + i); };
-    // FP8 pools: the codes of K landed (V's: vland); the bf16 query tile landed
+    // FP8 pools: the codes of K and V landed, a bf16 query tile landed
     auto kland = [&](int st) { return bar(30 + st); };
+    auto vland = [&](int st) { return bar(4 + st); };
     auto qland = [&](int b) { return bar(32 + b); };
     auto mma_drain = [&](int i) { return bar(6 + i); };
     float *ref_s = reinterpret_cast<float *>(smem + L::kRef);
@@ -658,9 +661,27 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 for (int c = 0; c < D / 8; ++c)
                     dst[c] = make_uint4(0, 0, 0, 0);
         };
+        // Rows `todo` of this warp's 32 of a unit, computed anew from what they see.
+        auto mend_rows = [&](const WtUnit &w, unsigned todo) {
+            __syncwarp();
+            const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
+            for (; todo != 0; todo &= todo - 1) {
+                const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
+                const int tk = rr / G;
+                const long long at = (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
+                if (w.pos0 + tk >= 0)
+                    window_mend_row<T, D, kFp8>(p, p.key_cache, p.value_cache, table, w.kh,
+                                                w.pos0 + tk,
+                                                static_cast<const T *>(p.query) + at,
+                                                static_cast<T *>(p.out) + at);
+            }
+        };
+        unsigned *const mend_s = reinterpret_cast<unsigned *>(smem + L::kMend);
+        unsigned mend = 0;  // rows of any unit
+        int units_done = 0;
         // A unit's rows (the CTA's steps up to its end: g), once its sums and last
         // value product are there: rounded and stored, O given back.
-        auto write_rows = [&](const WtUnit &w, uint32_t g, int b) {
+        auto write_rows = [&](const WtUnit &w, int ku, uint32_t g, int b) {
             tc_fence_after();
             // O is relative to the last step's reference, which the softmax
             // warps of that step have; the others' is not above it
@@ -717,19 +738,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (lane == 0)
                 mbar_arrive(ufree(b));
             unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0);
-            if (todo == 0)
-                return;
-            __syncwarp();
-            const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
-            for (; todo != 0; todo &= todo - 1) {
-                const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
-                const int tk = rr / G;
-                const long long at = (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
-                if (w.pos0 + tk >= 0)
-                    window_mend_row<T, D, kFp8>(p, p.key_cache, p.value_cache, table, w.kh,
-                                                w.pos0 + tk,
-                                                static_cast<const T *>(p.query) + at,
-                                                static_cast<T *>(p.out) + at);
+            if (ku < kWtUnits) {  // after the last unit: nobody waits for it then
+                if (lane == 0)
+                    mend_s[4 * ku + (warp & 3)] = todo;
+                mend |= todo;
+            } else if (todo != 0) {
+                mend_rows(w, todo);
             }
         };
         if constexpr (!kFp8) {
@@ -747,7 +761,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 ++nu;
                 if (!wait(lfull(b), ph) || !wait(ufull(b), ph))
                     break;
-                write_rows(w, g, b);
+                write_rows(w, ku, g, b);
+                units_done = ku + 1;
             }
         } else {
             // FP8 pools: these warps also widen each step's codes to the fp16
@@ -869,7 +884,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (wo.more && there(lfull(wo.nu & 1), (wo.nu >> 1) & 1) &&
                     there(ufull(wo.nu & 1), (wo.nu >> 1) & 1)) {
                     wo.g += wo.steps;
-                    write_rows(wo.w, wo.g, wo.nu & 1);
+                    write_rows(wo.w, wo.ku, wo.g, wo.nu & 1);
+                    units_done = wo.ku + 1;
                     ++wo.nu;
                     open(wo, true);
                     did = true;
@@ -891,11 +907,20 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (__any_sync(kFull, q_over) && lane == 0)
                 flag_error(p.error_word, PA_DEVERR_QUERY_RANGE);
         }
+        if (mend != 0) {
+            WtUnit w;
+            __syncwarp();
+            for (int ku = 0; ku < min(units_done, kWtUnits); ++ku) {
+                unit_at(ku, w);
+                if (w.steps() > 0)
+                    mend_rows(w, mend_s[4 * ku + (warp & 3)]);
+            }
+        }
     } else {
         if (warp == kWtKeyWarp || warp == kWtValueWarp) {
-            // ===== fetch warps: keys and query tiles (8), values (9) ====================
-            // Lane j owns box j / halves and d-half j % halves of every step: it
-            // looks up that box's physical block one step ahead and issues it.
+            // ===== fetch warps: keys and query tiles (12), values (13) ==================
+            // Lane j owns box j of every step: it looks up that box's physical
+            // block one step ahead and issues it.
             const bool values = warp == kWtValueWarp;
             constexpr int kBoxBytes = kBox * D * (kFp8 ? 1 : 2);
             uint32_t g = 0;

@@ -253,6 +253,28 @@ def test_long_batch_captured_beside_another(B):
         check(x, o, q, k, v, kc0, torch.bfloat16, False, False)
 
 
+def test_long_batch_wait_limit(B):
+    """A copy that never comes ends in a flag, and the next call is whole."""
+    s = make(2300, 100, 14, 128, 128, torch.bfloat16, False, 3, 131072, True, 41)
+    out = torch.empty((2300, 100, 128), dtype=torch.bfloat16, device="cuda")
+    q, k, v, kc0 = s["q"].clone(), s["k"].clone(), s["v"].clone(), s["kc"].clone()
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.pa_set_stage_wait_limit_ns(2_000_000)
+    B.pa_debug_withhold_first_fill(True)
+    try:
+        call(B, s, out, error_word=err)
+        torch.cuda.synchronize()
+    finally:
+        B.pa_debug_withhold_first_fill(False)
+        B.pa_set_stage_wait_limit_ns(0)
+    assert int(err.item()) == B.DEVERR_TIMEOUT
+    err.zero_()
+    call(B, s, out, error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    check(s, out, q, k, v, kc0, torch.bfloat16, False, False)
+
+
 def test_binding_checks_every_tensor(B):
     s = make(9, 4, 2, 64, 64, torch.float16, False, 1, 50, True, 51)
     out = torch.full((9, 4, 64), 7.0, dtype=torch.float16, device="cuda")

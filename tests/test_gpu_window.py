@@ -316,6 +316,32 @@ def test_chunk_values_hidden_from_some_rows(B, dtype, fp8, H, K, D, window, sink
     assert (np.abs(got - want) <= tol)[~touched].all()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_value_hidden_from_rows_of_a_long_context(B, fp8):
+    """Rows before a NaN value share tiles with rows that see it: they are
+    computed anew from 40,000 keys, which must not run out another role's wait
+    (here 5 ms) nor change the units after them."""
+    c = Case([40000, 70], [64, 70], 4, 1, 128, 64, torch.bfloat16, fp8, 60000, 0, seed=4)
+    pos, d = 40000 - 64 + 16, 7
+    c.vc[c.tables[0][pos // 64], pos % 64, 0, d] = 0x7F if fp8 else float("nan")
+    B.pa_set_stage_wait_limit_ns(5_000_000)
+    try:
+        c.chunk(B)
+        torch.cuda.synchronize()
+    finally:
+        B.pa_set_stage_wait_limit_ns(0)
+    assert int(c.err.item()) == 0
+    kv, vv = (R.pool_values(x, c.kv) for x in (c.kc, c.vc))
+    want, tol = R.window_attention(c.q, kv, np.where(np.isfinite(vv), vv, 0.0), c.tables, c.start,
+                                   c.ctx, c.scale, c.window, c.sinks, torch.bfloat16,
+                                   torch.float16 if fp8 else torch.bfloat16)
+    got = c.out.double().cpu().numpy()
+    sees = np.zeros(got.shape, dtype=bool)
+    sees[16:64, :, d] = True
+    assert np.array_equal(~np.isfinite(got), sees)
+    assert (np.abs(got - want) <= tol)[~sees].all()
+
+
 @pytest.mark.parametrize("call", ["decode", "chunk"])
 def test_large_scores(B, call):
     """Scores in the hundreds: one key takes nearly all the weight."""
@@ -348,6 +374,26 @@ def test_captured_and_on_another_stream(B):
 def test_stage_wait_limit(B, call):
     """A fill that never comes ends in a flag, and the next call is whole."""
     c = Case([500, 77, 300], [1, 1, 1], 8, 2, 128, 16, torch.bfloat16, False, 100, 4)
+    B.pa_set_stage_wait_limit_ns(2_000_000)
+    B.pa_debug_withhold_first_fill(True)
+    try:
+        getattr(c, call)(B)
+        torch.cuda.synchronize()
+    finally:
+        B.pa_debug_withhold_first_fill(False)
+        B.pa_set_stage_wait_limit_ns(0)
+    assert int(c.err.item()) == B.DEVERR_TIMEOUT
+    c.err.zero_()
+    c.out.fill_(7.0)
+    getattr(c, call)(B)
+    c.check()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("call", ["decode", "chunk"])
+def test_stage_wait_limit_over_codes(B, call, D):
+    """The same where the fill that never comes is one of FP8 codes."""
+    c = Case([500, 77, 300], [1, 1, 1], 8, 2, D, 32, torch.bfloat16, True, 100, 4)
     B.pa_set_stage_wait_limit_ns(2_000_000)
     B.pa_debug_withhold_first_fill(True)
     try:
