@@ -98,9 +98,14 @@ struct WtUnit {
     int seq;            // sequence (its table)
     __device__ int steps() const { return (kend + kWtKeys - 1) / kWtKeys; }
     // a last step of 64 keys or fewer
-    __device__ bool half(int si) const { return kend - si * kWtKeys <= kWtHalf; }
+    __device__ bool half(int si) const { return half(kend, si); }
+    __device__ static bool half(int kend, int si) { return kend - si * kWtKeys <= kWtHalf; }
     // a value row (compact position) that no row of the unit sees
-    __device__ bool unseen(int c) const { return c >= kend || (c >= hide0 && c < hide1); }
+    __device__ bool unseen(int c) const { return unseen(kend, hide0, hide1, c); }
+    __device__ static bool unseen(int kend, int hide0, int hide1, int c)
+    {
+        return c >= kend || (c >= hide0 && c < hide1);
+    }
     // whether step si has such rows
     __device__ bool hidden(int si) const
     {
@@ -149,7 +154,8 @@ template <int D, bool kFp8> struct WtLayout {
     static constexpr int kTmemSlot = kBars + 34 * 8;
     static constexpr int kAbort = kTmemSlot + 8;
     static constexpr int kUnits = kTmemSlot + 16;        // the CTA's first units
-    // unsigned rows to compute anew [unit][output warp]
+    // unsigned rows to compute anew [unit][output warp] (the last unit's: of all
+    // from there on)
     // int unit prefix[n + 1], then (ordered) order[n], units[n], key[n] and
     // the sort's buckets
     static constexpr int kMend = kUnits + kWtUnits * (int)sizeof(WtUnit);
@@ -661,7 +667,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 for (int c = 0; c < D / 8; ++c)
                     dst[c] = make_uint4(0, 0, 0, 0);
         };
-        // Rows `todo` of this warp's 32 of a unit, computed anew from what they see.
+        // Rows `todo` of this warp's 32 of a unit (those that it has), computed anew
+        // from what they see.
         auto mend_rows = [&](const WtUnit &w, unsigned todo) {
             __syncwarp();
             const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
@@ -669,7 +676,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
                 const int tk = rr / G;
                 const long long at = (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
-                if (w.pos0 + tk >= 0)
+                if (tk < w.count && w.pos0 + tk >= 0)
                     window_mend_row<T, D, kFp8>(p, p.key_cache, p.value_cache, table, w.kh,
                                                 w.pos0 + tk,
                                                 static_cast<const T *>(p.query) + at,
@@ -738,13 +745,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (lane == 0)
                 mbar_arrive(ufree(b));
             unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0);
-            if (ku < kWtUnits) {  // after the last unit: nobody waits for it then
-                if (lane == 0)
-                    mend_s[4 * ku + (warp & 3)] = todo;
-                mend |= todo;
-            } else if (todo != 0) {
-                mend_rows(w, todo);
+            // (looked at after the last unit, when nobody waits for this warp)
+            if (lane == 0) {
+                unsigned &at = mend_s[4 * min(ku, kWtUnits - 1) + (warp & 3)];
+                at = ku < kWtUnits ? todo : at | todo;
             }
+            mend |= todo;
         };
         if constexpr (!kFp8) {
             uint32_t g = 0, nu = 0;
@@ -774,7 +780,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 int ku = -1, si = 0, steps = 0;
                 uint32_t g = 0, nu = 0;
                 bool more = true;
-                WtUnit w;
+                int kend, hide0, hide1, count;  // of the unit (what is used of it)
             };
             Walk wk, wv, wq, wo;
             // the next unit with keys (zeros for one without, where asked)
@@ -782,14 +788,20 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 x.si = 0;
                 x.steps = 0;
                 while (x.more && x.steps == 0) {
-                    x.more = unit_at(++x.ku, x.w);
+                    WtUnit w;
+                    x.more = unit_at(++x.ku, w);
                     if (x.more) {
-                        x.steps = x.w.steps();
+                        x.steps = w.steps();
+                        x.kend = w.kend;
+                        x.hide0 = w.hide0;
+                        x.hide1 = w.hide1;
+                        x.count = w.count;
                         if (x.steps == 0 && zeros)
-                            zero_row(x.w);
+                            zero_row(w);
                     }
                 }
             };
+            auto half = [&](const Walk &x) { return WtUnit::half(x.kend, x.si); };
             auto step = [&](Walk &x) {
                 ++x.g;
                 if (++x.si == x.steps)
@@ -841,7 +853,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 bool did = false;
                 if (wk.more && there(kland(wk.g & 1), (wk.g >> 1) & 1)) {
                     const int st = wk.g & 1;
-                    if (r < kWtHalf || !wk.w.half(wk.si))
+                    if (r < kWtHalf || !half(wk))
                         widen(sbase + L::kK + st * L::kTile, code_base(st, 0), false);
                     announce(kfull(st));
                     step(wk);
@@ -849,9 +861,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 }
                 if (wv.more && there(vland(wv.g & 1), (wv.g >> 1) & 1)) {
                     const int st = wv.g & 1;
-                    if (r < kWtHalf || !wv.w.half(wv.si))
+                    if (r < kWtHalf || !half(wv))
                         widen(sbase + L::kV + st * L::kTile, code_base(st, 1),
-                              wv.w.unseen(wv.si * kWtKeys + r));
+                              WtUnit::unseen(wv.kend, wv.hide0, wv.hide1,
+                                             wv.si * kWtKeys + r));
                     announce(vfull(st));
                     step(wv);
                     did = true;
@@ -859,7 +872,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if constexpr (kConvQ) {
                     if (wq.more && there(qland(wq.nu & 1), (wq.nu >> 1) & 1)) {
                         const uint32_t tile = sbase + L::kQ + (wq.nu & 1) * L::kTile;
-                        const bool row = row_of(wq.w) != nullptr;
+                        const bool row = r < tok_unit * G && tok < wq.count;
 #pragma unroll
                         for (int c = 0; c < D / 8; ++c) {
                             const uint32_t a = tile + (c >> 3) * L::kHalfBytes + r * 128 +
@@ -884,7 +897,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (wo.more && there(lfull(wo.nu & 1), (wo.nu >> 1) & 1) &&
                     there(ufull(wo.nu & 1), (wo.nu >> 1) & 1)) {
                     wo.g += wo.steps;
-                    write_rows(wo.w, wo.ku, wo.g, wo.nu & 1);
+                    WtUnit w;
+                    unit_at(wo.ku, w);
+                    write_rows(w, wo.ku, wo.g, wo.nu & 1);
                     units_done = wo.ku + 1;
                     ++wo.nu;
                     open(wo, true);
@@ -910,10 +925,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         if (mend != 0) {
             WtUnit w;
             __syncwarp();
-            for (int ku = 0; ku < min(units_done, kWtUnits); ++ku) {
+            for (int ku = 0; ku < units_done; ++ku) {
                 unit_at(ku, w);
                 if (w.steps() > 0)
-                    mend_rows(w, mend_s[4 * ku + (warp & 3)]);
+                    mend_rows(w, mend_s[4 * min(ku, kWtUnits - 1) + (warp & 3)]);
             }
         }
     } else {

@@ -342,6 +342,40 @@ def test_chunk_value_hidden_from_rows_of_a_long_context(B, fp8):
     assert (np.abs(got - want) <= tol)[~sees].all()
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_hidden_values_in_the_last_of_many_units(B, fp8):
+    """More units a CTA than it keeps row masks for; NaN values in the first and
+    last of them."""
+    T, H, D, bs, W, dtype = 210000, 16, 64, 16, 9, torch.float16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.empty((T, H, D), dtype=dtype, device="cuda").normal_(generator=g)
+    n = -(-T // bs)
+    kc, vc = (torch.empty((n, bs, 1, D), device="cuda").normal_(generator=g) for _ in range(2))
+    kc, vc = (x.to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x.to(dtype)
+              for x in (kc, vc))
+    spots = [(5, 3), (70003, 8), (T - 12, 60)]
+    for pos, d in spots:
+        vc[pos // bs, pos % bs, 0, d] = 0x7F if fp8 else float("nan")
+    i = lambda a: torch.as_tensor(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    out, err = torch.full_like(q, 7), i([0])
+    B.pa_prefill_attention_window(out, q, kc, vc, i(np.arange(n))[None], i([0, T]), i([T]), T,
+                                  0.125, W, 0, error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    sees = torch.zeros_like(out, dtype=torch.bool)
+    for pos, d in spots:
+        sees[pos:pos + W, :, d] = True
+    assert torch.equal(~torch.isfinite(out), sees)
+    kv, vv = (R.pool_values(x) for x in (kc, vc))
+    vv = np.where(np.isfinite(vv), vv, 0.0)
+    for pos, _ in spots:  # rows about each of them
+        lo, hi = max(0, pos - 20), min(T, pos + 20)
+        want, tol = R.window_attention(q[lo:hi], kv, vv, np.arange(n)[None], [0, hi - lo], [hi],
+                                       0.125, W, 0, dtype, dtype)
+        far = np.abs(out[lo:hi].double().cpu().numpy() - want)
+        assert (far <= tol)[~sees[lo:hi].cpu().numpy()].all()
+
+
 @pytest.mark.parametrize("call", ["decode", "chunk"])
 def test_large_scores(B, call):
     """Scores in the hundreds: one key takes nearly all the weight."""
