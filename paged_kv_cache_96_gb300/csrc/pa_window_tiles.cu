@@ -57,7 +57,7 @@
 //    keys, values, query tiles and finished units come.  By count
 //    shared memory bounds it: 32 KB of codes written and read and 64 KB of fp16
 //    written a step, ~1,000 cycles beside the ~1,000 of the operands' reads
-//    (580 us and 56).  The query is rounded to fp16, the K scale joins the
+//    (570 us and 57).  The query is rounded to fp16, the K scale joins the
 //    exponent's scale and the V scale the output.
 // P is rounded to the operands' type, relative error 2^-9 (bf16) or 2^-12: about
 // that of the rounded output; the sum keeps the unrounded fp32 weights.
@@ -114,7 +114,7 @@ struct WtUnit {
     }
 };
 // units of a CTA kept in shared memory; later ones are worked out by each role
-constexpr int kWtUnits = 160;
+constexpr int kWtUnits = 192;
 
 // Step g's slot g % 3 and the parity of g / 3, counted along.
 struct Slot3 {
@@ -154,12 +154,9 @@ template <int D, bool kFp8> struct WtLayout {
     static constexpr int kTmemSlot = kBars + 34 * 8;
     static constexpr int kAbort = kTmemSlot + 8;
     static constexpr int kUnits = kTmemSlot + 16;        // the CTA's first units
-    // unsigned rows to compute anew [unit][output warp] (the last unit's: of all
-    // from there on)
     // int unit prefix[n + 1], then (ordered) order[n], units[n], key[n] and
     // the sort's buckets
-    static constexpr int kMend = kUnits + kWtUnits * (int)sizeof(WtUnit);
-    static constexpr int kSeg = kMend + kWtUnits * 4 * 4;
+    static constexpr int kSeg = kUnits + kWtUnits * (int)sizeof(WtUnit);
     static size_t bytes(int segments, bool ordered)
     {
         return 1024 + kSeg + 4 * ((size_t)segments + 1) +
@@ -683,8 +680,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                                                 static_cast<T *>(p.out) + at);
             }
         };
-        unsigned *const mend_s = reinterpret_cast<unsigned *>(smem + L::kMend);
-        unsigned mend = 0;  // rows of any unit
+        constexpr int kOutUnroll = kFp8 ? D / 32 : 1;
+        unsigned mend = 0;  // the mask of unit `lane` (the last lane: all from there on)
         int units_done = 0;
         // A unit's rows (the CTA's steps up to its end: g), once its sums and last
         // value product are there: rounded and stored, O given back.
@@ -703,9 +700,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             // rows that come out non-finite, perhaps for a value hidden from them:
             // x * 0 + nan is a sum that stays zero while everything is finite
             uint32_t nan = 0;
-            // (a loop: unrolled, it took the tensor-core warps' code out of the
-            // instruction cache at the end of every unit)
-#pragma unroll 1
+            // (16-bit pools: a loop; unrolled, it took the tensor-core warps' code
+            // out of the instruction cache at the end of every unit, 38.3 us for
+            // 37.6.  FP8 pools, where these warps' polling loop is the larger part:
+            // unrolled, 569 us for 614 and 57 for 59)
+#pragma unroll kOutUnroll
             for (int c = 0; c < D / 32; ++c) {
                 uint32_t o[32], v[16];
                 tmem_ld_32x32b_x32(o_at + c * 32, o);
@@ -746,11 +745,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 mbar_arrive(ufree(b));
             unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0);
             // (looked at after the last unit, when nobody waits for this warp)
-            if (lane == 0) {
-                unsigned &at = mend_s[4 * min(ku, kWtUnits - 1) + (warp & 3)];
-                at = ku < kWtUnits ? todo : at | todo;
-            }
-            mend |= todo;
+            if (lane == min(ku, 31))
+                mend |= todo;
         };
         if constexpr (!kFp8) {
             uint32_t g = 0, nu = 0;
@@ -922,13 +918,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (__any_sync(kFull, q_over) && lane == 0)
                 flag_error(p.error_word, PA_DEVERR_QUERY_RANGE);
         }
-        if (mend != 0) {
+        if (__any_sync(kFull, mend != 0)) {
             WtUnit w;
-            __syncwarp();
             for (int ku = 0; ku < units_done; ++ku) {
+                const unsigned todo = __shfl_sync(kFull, mend, min(ku, 31));
                 unit_at(ku, w);
                 if (w.steps() > 0)
-                    mend_rows(w, mend_s[4 * min(ku, kWtUnits - 1) + (warp & 3)]);
+                    mend_rows(w, todo);
             }
         }
     } else {

@@ -344,7 +344,7 @@ def test_chunk_value_hidden_from_rows_of_a_long_context(B, fp8):
 
 @pytest.mark.parametrize("fp8", [False, True])
 def test_chunk_hidden_values_in_the_last_of_many_units(B, fp8):
-    """More units a CTA than it keeps row masks for; NaN values in the first and
+    """More units a CTA than it keeps in shared memory; NaN values in the first and
     last of them."""
     T, H, D, bs, W, dtype = 210000, 16, 64, 16, 9, torch.float16
     g = torch.Generator(device="cuda").manual_seed(3)
