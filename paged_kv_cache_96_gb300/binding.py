@@ -157,6 +157,10 @@ def _load_calls():
     except ImportError as e:
         raise ImportError("the extension _calls is missing; build it with "
                           "`python -m paged_kv_cache_96_gb300.build`") from e
+    if calls.torch_version != torch.__version__:
+        raise ImportError(f"the extension _calls was built for torch {calls.torch_version}, this is "
+                          f"{torch.__version__}; build it again with "
+                          "`python -m paged_kv_cache_96_gb300.build --force`")
     calls.bind(_LIB_PATH)
     return calls
 
