@@ -28,7 +28,7 @@
 //    warp independent); softmax is online in fp32; a merge warp combines the
 //    tile warps' records while they stream the next unit.
 //  * Partitions of a sequence are merged by log-sum-exp weights, in the pass
-//    for up to 8 of them, else by the reduce kernel behind it, which then
+//    for up to 3 of them, else by the reduce kernel behind it, which then
 //    takes the compact lengths this pass leaves in the workspace.
 //  * Hidden rows of a border tile get a score of -inf by selection and a zero
 //    value row, so what they hold never reaches the output.
@@ -51,7 +51,17 @@ struct WindowParams : DecodeParams {
     int window, num_sinks;
     int sink_tokens;   // num_sinks rounded up to tiles
     int32_t *len_out;  // compact lengths for the reduce kernel (null: it will not run)
+    int merge_max;     // partials of a sequence that the pass merges itself, at most
 };
+
+// Batches whose sequences have at most this many partials are merged by the
+// pass, others by the reduce kernel: a merge in the pass is a trip to L2 for
+// every partial or two, at the end of the last CTA or in the way of its next
+// unit; the reduce kernel is ~2 us behind the pass.  1 sequence, window 2,048, 8
+// heads of 8, FP8: 8 partials 14.0 us by the pass, 9.8 by the kernel, 4 partials
+// 13.6 and 12.6, 2 partials 18.2 and 18.1; 128 such sequences, window 1,024: 163 and
+// 96, 78 and 76, 62.5 and 65.9 (16-bit pools 183 and 117, 110 and 103, 93 and 98).
+constexpr int kWinMergeMax = 3;
 
 // A sequence's compact length, and how far its window's tiles lie behind
 // their compact positions (a multiple of 16 tokens; 0: no tile is left out).
@@ -691,7 +701,7 @@ __global__ void __launch_bounds__(window_bound_threads(NW + 1, MINB), MINB)
             // from their next unit on
             if (next_u(u) < total_units)
                 named_barrier_arrive(kRecFree, kThreads);
-            if (split && nparts <= kMergeMax)
+            if (split && nparts <= p.merge_max)
                 // records loaded per lane at once: fewer under the FP8 register cap
                 arrive_and_merge<T, D, kHeads, kFp8 ? 2 : 8>(p, s, kh, nparts, lane);
         }
@@ -786,9 +796,10 @@ static pa_status launch_window(const WindowParams &prm, const CUtensorMap &mk,
     // batches whose per-sequence arrays do not fit next to the default rings
     if (st == PA_ERR_UNSUPPORTED)
         st = launch_window_pass<T, KV, D, NT, 1>(prm, mk, mv, stream, max_units);
-    if (st != PA_OK || max_parts <= kMergeMax)
+    if (st != PA_OK || max_parts <= prm.merge_max)
         return st;
     DecodeParams reduce = prm;
+    reduce.counters = nullptr;  // (nothing was merged by the pass)
     reduce.context_lens = prm.len_out;
     return launch_reduce<T, D>(reduce, stream);
 }
@@ -830,7 +841,7 @@ static WorkspaceLayout window_workspace(int S, int H, int Hkv, int D, int parts,
 {
     WorkspaceLayout w = workspace_layout(S, H, Hkv, D, parts);
     *len_off = w.total;
-    if (parts > kMergeMax)
+    if (parts > kWinMergeMax)
         w.total += align256((size_t)S * 4);
     return w;
 }
@@ -894,7 +905,8 @@ static pa_status run_window(void *out, const void *query, const void *key_cache,
     const int parts = window_parts(compact, prm.part_tokens) > 1
                           ? window_parts(compact, prm.part_tokens)
                           : 1;
-    if (parts > kMergeMax)
+    prm.merge_max = parts > kWinMergeMax ? 1 : kWinMergeMax;
+    if (parts > prm.merge_max)
         prm.len_out = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + len_off);
     prm.max_context_len = max_context_len;
     prm.window = window;

@@ -133,7 +133,7 @@ def test_chunk_window_needs_a_positive_scale_and_offsets(B):
 
 def test_window_workspace(B):
     """Partitions are counted in visible tokens, whatever the context, a
-    remainder of less than half of one joining the one before; past 8 of them
+    remainder of less than half of one joining the one before; past 3 of them
     the lengths for the reduce kernel come on top."""
     f = B.pa_window_workspace_bytes
     plain = B.pa_decode_workspace_bytes
@@ -143,7 +143,8 @@ def test_window_workspace(B):
     assert f(2, 8, 2, 128, 50, 64, 4, 32) == plain(2, 8, 2, 128, 50, 32)
     assert f(2, 8, 2, 128, 47, 64, 4, 32) == 0               # 32 + 15
     assert f(2, 8, 2, 128, 100000, 1024, 4, 1024) == 0       # 1056 at most
-    assert f(2, 8, 2, 128, 100000, 4096, 16, 512) == plain(2, 8, 2, 128, 4096, 512)
+    assert f(2, 8, 2, 128, 100000, 4096, 16, 1376) == plain(2, 8, 2, 128, 4128, 1376)
+    assert f(2, 8, 2, 128, 100000, 4096, 16, 512) == plain(2, 8, 2, 128, 4096, 512) + 256
     assert f(3, 8, 2, 128, 100000, 128, 0, 16) == plain(3, 8, 2, 128, 144, 16) + 256
     assert f(2, 8, 2, 128, 1 << 30, 1 << 40, 1 << 40, 1 << 20) == \
         plain(2, 8, 2, 128, 1 << 30, 1 << 20) + 256         # a reach past int32 hides nothing
