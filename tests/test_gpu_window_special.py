@@ -1,0 +1,119 @@
+"""Windowed attention where keys, queries or values are not numbers or infinite, and
+its outputs from call to call.  The definition in 64 bits says for every element
+whether it is a number, which infinity, or not a number."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+import operator_refs as R  # noqa: E402
+from test_gpu_window import IDS, TYPES, Case  # noqa: E402
+
+FLOATS = [(torch.bfloat16, False), (torch.float16, False)]
+
+
+@pytest.fixture(scope="module")
+def B():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from paged_kv_cache_96_gb300 import binding
+    return binding
+
+
+def definition(c):
+    """Outputs and tolerances of a Case as operator_refs.window_attention has them,
+    for pools and queries that may hold infinities and NaN: a key whose score is -inf
+    has weight 0 and no share in the scores' rounding."""
+    q = c.q.double().cpu().numpy()
+    kc, vc = (R.pool_values(x, c.kv) for x in (c.kc, c.vc))
+    T, H, D = q.shape
+    bs, K = kc.shape[1], kc.shape[2]
+    G = H // K
+    p_half = R.HALF_STEP[torch.float16 if c.fp8 else c.dtype]
+    out, tol = np.zeros((T, H, D)), np.zeros((T, H, D))
+    with np.errstate(all="ignore"):
+        for s, n in enumerate(c.ctx):
+            n, lo, hi = int(n), int(c.start[s]), int(c.start[s + 1])
+            for r in range(lo, hi):
+                pos = n - (hi - lo) + (r - lo)
+                if pos < 0:
+                    continue
+                p = R.visible(pos, n, c.window, c.sinks)
+                blk = c.tables[s][p // bs]
+                for h in range(K):
+                    k, v = kc[blk, p % bs, h], vc[blk, p % bs, h]
+                    real = np.isfinite(k).all(-1)
+                    for g in range(h * G, (h + 1) * G):
+                        x = (k * q[r, g]).sum(-1) * c.scale
+                        w = np.exp(x - x.max())
+                        w = (w / w.sum())[:, None]
+                        o = np.where(w == 0, np.where(np.isfinite(v), 0.0, np.nan), w * v).sum(0)
+                        size = c.scale * (np.abs(k[real]) @ np.abs(q[r, g])).max(initial=0)
+                        e = 2 * ((D + 4) * 2.0 ** -22 * size + (len(p) + 8) * 2.0 ** -23)
+                        mass = (w * np.abs(np.where(np.isfinite(v), v, 0))).sum(0)
+                        out[r, g] = o
+                        tol[r, g] = (R.HALF_STEP[c.dtype] * np.abs(o) +
+                                     1.01 * (p_half + e) * mass + 2.0 ** -24)
+    return out, tol
+
+
+def check(c, what=""):
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == 0, what
+    got = c.out.double().cpu().numpy()
+    want, tol = definition(c)
+    wrong = int((np.isnan(got) != np.isnan(want)).sum())
+    assert wrong == 0, f"{what}: {wrong} elements numbers on one side only"
+    for sign in (1, -1):
+        wrong = int(((got == sign * np.inf) != (want == sign * np.inf)).sum())
+        assert wrong == 0, f"{what}: {wrong} infinities on one side only"
+    real = np.isfinite(want)
+    far = np.abs(got - want)[real]
+    assert (far <= tol[real]).all(), f"{what}: worst {np.max(far / tol[real]):.2f}x"
+    return want
+
+
+def place(c, s, p):
+    """Block and row of position p of sequence s."""
+    bs = c.kc.shape[1]
+    return int(c.tables[s][p // bs]), p % bs
+
+
+def put(c, pool, s, positions, d, value):
+    for p in positions:
+        pool[place(c, s, p)][..., d] = value
+
+
+PARTITIONS = (0, 144, 96, 80, 64, 32, 16)  # of 288 tokens: 1, 2, 3, 4, 5, 9 and 18
+
+
+@pytest.mark.parametrize("dtype,fp8", FLOATS, ids=IDS[:2])
+@pytest.mark.parametrize("H,K,D", [(8, 2, 128), (16, 1, 64), (3, 3, 64)])
+@pytest.mark.parametrize("span", [(0, 144), (144, 288), (80, 240)])
+def test_decode_partition_of_keys_without_weight(B, dtype, fp8, H, K, D, span):
+    """Keys whose scores are all -inf, a partition and more of them: they have weight 0
+    whatever the partition size, and the others their own."""
+    c = Case([288, 30, 288], [1] * 3, H, K, D, 16, dtype, fp8, 5000, 0, seed=7)
+    c.q[..., 1] = c.q[..., 1].abs() + 0.5
+    put(c, c.kc, 0, range(*span), 1, float("-inf"))
+    for P in PARTITIONS:
+        c.out.fill_(7.0)
+        c.decode(B, P)
+        check(c, f"P={P}")
+
+
+@pytest.mark.parametrize("dtype,fp8", FLOATS, ids=IDS[:2])
+@pytest.mark.parametrize("window,sinks", [(17, 3), (33, 0), (50, 16)])
+def test_decode_border_tile_without_weight(B, dtype, fp8, window, sinks):
+    """Partitions of one tile, whose few visible keys (the first tokens' or the
+    window's oldest) have a score of -inf."""
+    c = Case(range(100, 117), [1] * 17, 4, 2, 64, 16, dtype, fp8, window, sinks, seed=9)
+    c.q[..., 1] = c.q[..., 1].abs() + 0.5
+    for s, n in enumerate(c.ctx):
+        low = int(n) - window
+        put(c, c.kc, s, [*range(sinks), *range(low, -(-(low + 1) // 16) * 16)], 1, float("-inf"))
+    for P in (0, 16, 32):
+        c.out.fill_(7.0)
+        c.decode(B, P)
+        check(c, f"P={P}")
