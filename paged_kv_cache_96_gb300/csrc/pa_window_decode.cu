@@ -40,6 +40,7 @@
 #include <type_traits>
 
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <mutex>
 
@@ -692,7 +693,9 @@ __global__ void __launch_bounds__(window_bound_threads(NW + 1, MINB), MINB)
                     dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
                     dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
                     if (d0 == 0) {
-                        p.part_m[idx] = mmax * kLn2;
+                        // (finite wherever l is not 0: scores that are all not a number
+                        // leave no maximum, and a merge passes over m = -inf)
+                        p.part_m[idx] = lsum == 0.f ? -INFINITY : fmaxf(mmax * kLn2, -FLT_MAX);
                         p.part_l[idx] = lsum;
                     }
                 }

@@ -117,3 +117,17 @@ def test_decode_border_tile_without_weight(B, dtype, fp8, window, sinks):
         c.out.fill_(7.0)
         c.decode(B, P)
         check(c, f"P={P}")
+
+
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("span", [(0, 144), (144, 288), (80, 240), (100, 101)])
+def test_decode_partition_of_keys_that_are_not_numbers(B, dtype, fp8, span):
+    """A visible key that is not a number makes its row so, also where a whole
+    partition holds nothing else."""
+    c = Case([288, 30, 288], [1] * 3, 8, 2, 128, 16, dtype, fp8, 5000, 0, seed=7)
+    put(c, c.kc, 0, range(*span), 5, 0x7F if fp8 else float("nan"))
+    for P in PARTITIONS:
+        c.out.fill_(7.0)
+        c.decode(B, P)
+        want = check(c, f"P={P}")
+    assert np.isnan(want[0]).all() and np.isfinite(want[1:]).all()
