@@ -693,7 +693,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const int a1 = (2 * b + (int)(g & 1)) * kWtRows + r;
             const float l0 = part_l[a0], l1 = part_l[a1];
             const float l = l1 == 0.f ? l0 : l0 + l1 * exp2f(part_m[a1] - part_m[a0]);
-            const float inv = l > 0.f ? p.out_scale / l : l;  // (0 for a row without keys)
+            // no weight: zeros for a row at a negative position, which sees no key;
+            // of keys that all have a score of -inf the softmax is not a number
+            const float none = w.pos0 + tok < 0 ? 0.f : __uint_as_float(0x7fffffffu);
+            const float inv = l > 0.f ? p.out_scale / l : none;
             const uint64_t inv2 = pack_f32x2(inv, inv), zero2 = pack_f32x2(0.f, 0.f);
             const uint32_t o_at = tmem + lanes + kWtTmemO;
             T *const dst = row_of(w);
@@ -743,7 +746,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(ufree(b));
-            unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0);
+            unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0 &&
+                                                     l != 0.f);
             // (looked at after the last unit, when nobody waits for this warp)
             if (lane == min(ku, 31))
                 mend |= todo;

@@ -131,3 +131,19 @@ def test_decode_partition_of_keys_that_are_not_numbers(B, dtype, fp8, span):
         c.decode(B, P)
         want = check(c, f"P={P}")
     assert np.isnan(want[0]).all() and np.isfinite(want[1:]).all()
+
+
+@pytest.mark.parametrize("dtype,fp8", FLOATS, ids=IDS[:2])
+@pytest.mark.parametrize("call", ["decode", "chunk"])
+def test_rows_whose_scores_are_all_minus_infinity(B, dtype, fp8, call):
+    """Their softmax is not a number; rows that see one key more have their answer."""
+    rows = [1, 1] if call == "decode" else [45, 50]
+    c = Case([200, 50], rows, 8, 2, 128, 16, dtype, fp8, 20, 0, seed=3, poison=False)
+    c.q[..., 1] = c.q[..., 1].abs() + 0.5
+    put(c, c.kc, 0, range(175, 200), 1, float("-inf"))
+    for P in (0, 16) if call == "decode" else (0,):
+        c.out.fill_(7.0)
+        c.decode(B, P) if call == "decode" else c.chunk(B)
+        want = check(c, f"P={P}")
+    bad = np.isnan(want).all((1, 2))
+    assert bad[:rows[0]].sum() == min(rows[0], 6) and not bad[rows[0]:].any()
