@@ -92,6 +92,13 @@ __device__ __forceinline__ int window_context(const WindowMqParams &p, int s)
     return c;
 }
 
+// First position of the window of the row at `pos` (0 for a row before the
+// first position too: pos + 1 - window would pass the 32 bits there).
+__device__ __forceinline__ int window_low(int pos, int window)
+{
+    return pos < window ? 0 : pos + 1 - window;
+}
+
 // First row of sequence s, kept inside the query; offsets that are not are
 // flagged by the caller that passes `flag`.
 __device__ __forceinline__ int window_row0(const WindowMqParams &p, int s, bool flag)
@@ -171,7 +178,7 @@ __device__ __noinline__ void window_mend_row(const WindowMqParams &p, const void
 {
     constexpr int E = D / 32, kBatch = 8;  // elements a lane, pool rows in flight
     const int lane = threadIdx.x & 31;
-    const int low = max(0, pos + 1 - p.window);     // [low, pos] and [0, first) are seen
+    const int low = window_low(pos, p.window);      // [low, pos] and [0, first) are seen
     const int first = min(p.num_sinks, low);
     const int seen = pos + 1 - low + first;
     // the i-th key seen, newest first: its row in the pools (-1: none, -2: a

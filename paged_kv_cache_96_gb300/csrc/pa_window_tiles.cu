@@ -440,7 +440,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         const int ctx = window_context(p, w.seq);
         w.pos0 = ctx - rows + tok0;
         const int end = max(0, w.pos0 + w.count);        // one past the last key
-        const int low = max(0, w.pos0 + 1 - p.window);   // the first row's window
+        const int low = window_low(w.pos0, p.window);    // the first row's window
         w.skip = max(0, (low & ~(kBox - 1)) - sink_tokens);
         w.kend = end - w.skip;
         w.hide0 = sinks;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const bool row = r < tok_unit * G && tok < w.count;
             // compact: one past the row's own position, its window's start
             const int lim = row ? w.pos0 + tok + 1 - w.skip : 0;
-            const int low = max(0, w.pos0 + tok + 1 - p.window) - w.skip;
+            const int low = window_low(w.pos0 + tok, p.window) - w.skip;
             const uint32_t o_at = tmem + lanes + kWtTmemO;
             float m_own = -INFINITY, l_own = 0.f;  // reference, and sum relative to it
             for (int si = 0; si < steps; ++si, ++g, s3.next()) {

@@ -147,3 +147,15 @@ def test_rows_whose_scores_are_all_minus_infinity(B, dtype, fp8, call):
         want = check(c, f"P={P}")
     bad = np.isnan(want).all((1, 2))
     assert bad[:rows[0]].sum() == min(rows[0], 6) and not bad[rows[0]:].any()
+
+
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 20, 1 << 40])
+def test_chunk_longer_than_its_context_behind_a_window_past_every_length(B, dtype, fp8, window):
+    """Rows at negative positions, whose window would start before -2^31."""
+    c = Case([10, 40, 0], [300, 40, 9], 4, 2, 64, 16, dtype, fp8, 5000, 2, poison=False)
+    c.window = window
+    c.chunk(B)
+    c.window = 5000     # what a window past every context is
+    check(c)
+    assert (c.out[:290] == 0).all() and (c.out[340:] == 0).all()
