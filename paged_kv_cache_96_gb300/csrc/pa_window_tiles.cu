@@ -665,7 +665,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     dst[c] = make_uint4(0, 0, 0, 0);
         };
         // Rows `todo` of this warp's 32 of a unit (those that it has), computed anew
-        // from what they see.
+        // from what they see (nothing, at a negative position).
         auto mend_rows = [&](const WtUnit &w, unsigned todo) {
             __syncwarp();
             const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
@@ -673,7 +673,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
                 const int tk = rr / G;
                 const long long at = (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
-                if (tk < w.count && w.pos0 + tk >= 0)
+                if (tk >= w.count)
+                    continue;
+                if (w.pos0 + tk < 0)
+                    for (int e = lane; e < D / 2; e += 32)
+                        reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at)[e] = 0;
+                else
                     window_mend_row<T, D, kFp8>(p, p.key_cache, p.value_cache, table, w.kh,
                                                 w.pos0 + tk,
                                                 static_cast<const T *>(p.query) + at,
@@ -695,7 +700,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const float l = l1 == 0.f ? l0 : l0 + l1 * exp2f(part_m[a1] - part_m[a0]);
             // no weight: zeros for a row at a negative position, which sees no key;
             // of keys that all have a score of -inf the softmax is not a number
-            const float none = w.pos0 + tok < 0 ? 0.f : __uint_as_float(0x7fffffffu);
+            const bool before = w.pos0 + tok < 0;
+            const float none = before ? 0.f : __uint_as_float(0x7fffffffu);
             const float inv = l > 0.f ? p.out_scale / l : none;
             const uint64_t inv2 = pack_f32x2(inv, inv), zero2 = pack_f32x2(0.f, 0.f);
             const uint32_t o_at = tmem + lanes + kWtTmemO;
@@ -747,7 +753,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (lane == 0)
                 mbar_arrive(ufree(b));
             unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0 &&
-                                                     l != 0.f);
+                                                     (l != 0.f || before));
             // (looked at after the last unit, when nobody waits for this warp)
             if (lane == min(ku, 31))
                 mend |= todo;

@@ -69,7 +69,7 @@ def check(c, what=""):
         wrong = int(((got == sign * np.inf) != (want == sign * np.inf)).sum())
         assert wrong == 0, f"{what}: {wrong} infinities on one side only"
     real = np.isfinite(want)
-    far = np.abs(got - want)[real]
+    far = np.abs(got[real] - want[real])
     assert (far <= tol[real]).all(), f"{what}: worst {np.max(far / tol[real]):.2f}x"
     return want
 
@@ -147,6 +147,19 @@ def test_rows_whose_scores_are_all_minus_infinity(B, dtype, fp8, call):
         want = check(c, f"P={P}")
     bad = np.isnan(want).all((1, 2))
     assert bad[:rows[0]].sum() == min(rows[0], 6) and not bad[rows[0]:].any()
+
+
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+def test_chunk_rows_before_the_first_beside_values_that_are_not_numbers(B, dtype, fp8):
+    """Rows at negative positions stay zero beside rows that see such a value."""
+    for window, sinks in ((12, 2), (100, 0)):
+        c = Case([10, 40], [16, 40], 4, 2, 64, 16, dtype, fp8, window, sinks, poison=False)
+        put(c, c.vc, 0, [5], 3, 0x7F if fp8 else float("nan"))
+        if not fp8:
+            put(c, c.vc, 0, [7], 11, float("inf"))
+        c.chunk(B)
+        check(c)
+        assert (c.out[:6] == 0).all()
 
 
 @pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
