@@ -129,11 +129,13 @@ __device__ __forceinline__ int window_order_key(const WindowMqParams &p, int s, 
 // The tensor cores multiply a key that is hidden from a row by a weight of 0,
 // which is not 0 when its value is infinite or NaN, and a value row that some
 // row of the tile sees cannot be zeroed.  So a row that comes out non-finite is
-// looked at again, by one warp: if the values it sees account for every
-// non-finite element (the newest are read first, so a sequence that has
-// diverged is done at once) it stays; else it is computed anew from what it
-// sees, 32 keys at a time, 8 pool rows in flight.  Only rows of such tiles pay
-// for this.
+// looked at again, by one warp.  Only values of keys that are hidden from it and seen
+// by another row of its unit can have done that: the keys after its own position
+// and those that its window has just left, as many of both as the unit has tokens
+// at most.  If one of them is non-finite where the row is, the row is computed anew
+// from what it sees, 32 keys at a time, 8 pool rows in flight (unless it sees a NaN
+// there itself; the newest are read first, so a sequence that has diverged is done
+// at once).  Only rows of such tiles pay for this.
 
 template <typename T> __device__ __forceinline__ float window_float(T x)
 {
@@ -169,48 +171,103 @@ __device__ __forceinline__ bool window_finite(float x)
     return (__float_as_uint(x) & 0x7f800000u) != 0x7f800000u;
 }
 
-// One row (position pos of the sequence with this table, KV head kh), by a
-// warp: out and query are its D elements.
-template <typename T, int D, bool kFp8>
-__device__ __noinline__ void window_mend_row(const WindowMqParams &p, const void *key_cache,
-                                             const void *value_cache, const int32_t *table,
-                                             int kh, int pos, const T *query, T *out)
-{
-    constexpr int E = D / 32, kBatch = 8;  // elements a lane, pool rows in flight
-    const int lane = threadIdx.x & 31;
-    const int low = window_low(pos, p.window);      // [low, pos] and [0, first) are seen
-    const int first = min(p.num_sinks, low);
-    const int seen = pos + 1 - low + first;
-    // the i-th key seen, newest first: its row in the pools (-1: none, -2: a
-    // table entry outside the pool)
-    auto place = [&](int i) -> long long {
-        if (i >= seen)
-            return -1;
-        const int t = i <= pos - low ? pos - i : first - 1 - (i - (pos + 1 - low));
+// The places in the pools of the keys of one sequence and KV head.
+struct WindowKeys {
+    const WindowMqParams &p;
+    const int32_t *table;
+    int kh;
+    // elements before position t's row (-2: a table entry outside the pool)
+    __device__ __forceinline__ long long at(int t, int head_dim) const
+    {
         const int b = table[t >> p.block_shift];
         if (b < 0 || b >= p.num_blocks)
             return -2;
         return (((long long)b * p.block_size + (t & (p.block_size - 1))) * p.num_kv_heads + kh) *
-               D;
-    };
-    // rows u .. u + 7 of the 32 whose places the lanes hold (zeros for none)
-    auto rows = [&](const void *pool, long long at, int u, float (&x)[kBatch][E]) {
+               head_dim;
+    }
+};
+
+constexpr int kWindowBatch = 8;  // pool rows in flight
+
+// This lane's elements of rows u .. u + 7 of the 32 whose places the lanes hold
+// (negative places: none, zeros).
+template <typename T, int E, bool kFp8>
+__device__ __forceinline__ void window_pool_rows(const void *pool, long long at, int u,
+                                                 float (&x)[kWindowBatch][E])
+{
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const long long a = __shfl_sync(kFull, at, u + k);
+    for (int k = 0; k < kWindowBatch; ++k) {
+        const long long a = __shfl_sync(kFull, at, u + k);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[k][e] = 0.f;
-            if (a >= 0)
-                window_pool_row<T, E, kFp8>(pool, a + lane * E, x[k]);
+        for (int e = 0; e < E; ++e)
+            x[k][e] = 0.f;
+        if (a >= 0)
+            window_pool_row<T, E, kFp8>(pool, a + (threadIdx.x & 31) * E, x[k]);
+    }
+}
+
+// This lane's elements (bits) at which one of the values of positions [a0, a1)
+// and [b0, b1) is non-finite, by a warp.
+template <typename T, int D, bool kFp8>
+__device__ __noinline__ unsigned window_non_finite(WindowKeys keys, const void *values,
+                                                   int a0, int a1, int b0, int b1)
+{
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31, na = max(0, a1 - a0), n = na + max(0, b1 - b0);
+    unsigned hot = 0;
+    for (int i = 0; i < n; i += 32) {
+        const int j = i + lane;
+        const long long at = j < n ? keys.at(j < na ? a0 + j : b0 + j - na, D) : -1;
+#pragma unroll 1
+        for (int u = 0; u < min(32, n - i); u += kWindowBatch) {
+            float v[kWindowBatch][E];
+            window_pool_rows<T, E, kFp8>(values, at, u, v);
+#pragma unroll
+            for (int k = 0; k < kWindowBatch; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (!window_finite(v[k][e]))
+                        hot |= 1u << e;
         }
-    };
-    // elements that are non-finite and not yet accounted for
+    }
+    return hot;
+}
+
+// One row (position pos of the sequence with this table, KV head kh), by a
+// warp: out and query are its D elements; unit: the first position that its
+// unit's rows have, and one past the last.
+template <typename T, int D, bool kFp8>
+__device__ __noinline__ void window_mend_row(WindowKeys keys, const void *key_cache,
+                                             const void *value_cache, int pos, int unit0,
+                                             int unit1, const T *query, T *out)
+{
+    constexpr int E = D / 32, kBatch = kWindowBatch;
+    const WindowMqParams &p = keys.p;
+    const int lane = threadIdx.x & 31;
+    const int low = window_low(pos, p.window);      // [low, pos] and [0, first) are seen
+    const int first = min(p.num_sinks, low);
+    const int seen = pos + 1 - low + first;
+    // elements that are non-finite where a hidden value is
     unsigned open = 0;
 #pragma unroll
     for (int e = 0; e < E; ++e)
         if (!window_finite(window_float<T>(out[lane * E + e])))
             open |= 1u << e;
+    if (!__any_sync(kFull, open != 0))
+        return;
+    open &= window_non_finite<T, D, kFp8>(keys, value_cache, pos + 1, unit1,
+                                          max(window_low(unit0, p.window), p.num_sinks), low);
+    if (!__any_sync(kFull, open != 0))
+        return;
+    // the i-th key seen, newest first: its place in the pools (-1: none)
+    auto place = [&](int i) -> long long {
+        return i >= seen ? -1
+                         : keys.at(i <= pos - low ? pos - i : first - 1 - (i - (pos + 1 - low)), D);
+    };
+    auto rows = [&](const void *pool, long long at, int u, float (&x)[kBatch][E]) {
+        window_pool_rows<T, E, kFp8>(pool, at, u, x);
+    };
+    // a NaN that the row sees accounts for its element
     for (int i = 0; i < seen; i += 32) {
         const long long at = place(i + lane);
         if (__any_sync(kFull, at == -2))
@@ -223,7 +280,7 @@ __device__ __noinline__ void window_mend_row(const WindowMqParams &p, const void
             for (int k = 0; k < kBatch; ++k)
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    if (!window_finite(v[k][e]))
+                    if ((__float_as_uint(v[k][e]) & 0x7fffffffu) > 0x7f800000u)
                         open &= ~(1u << e);
         }
         if (!__any_sync(kFull, open != 0))

@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // from what they see (nothing, at a negative position).
         auto mend_rows = [&](const WtUnit &w, unsigned todo) {
             __syncwarp();
-            const int32_t *table = p.block_tables + (size_t)w.seq * p.max_blocks_per_seq;
+            const WindowKeys keys{p, p.block_tables + (size_t)w.seq * p.max_blocks_per_seq, w.kh};
             for (; todo != 0; todo &= todo - 1) {
                 const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
                 const int tk = rr / G;
@@ -679,8 +679,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                     for (int e = lane; e < D / 2; e += 32)
                         reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at)[e] = 0;
                 else
-                    window_mend_row<T, D, kFp8>(p, p.key_cache, p.value_cache, table, w.kh,
-                                                w.pos0 + tk,
+                    window_mend_row<T, D, kFp8>(keys, p.key_cache, p.value_cache, w.pos0 + tk,
+                                                w.pos0, w.pos0 + w.count,
                                                 static_cast<const T *>(p.query) + at,
                                                 static_cast<T *>(p.out) + at);
             }

@@ -162,6 +162,23 @@ def test_chunk_rows_before_the_first_beside_values_that_are_not_numbers(B, dtype
         assert (c.out[:6] == 0).all()
 
 
+@pytest.mark.parametrize("dtype,fp8", FLOATS, ids=IDS[:2])
+@pytest.mark.parametrize("H,K,D,window,sinks", [(8, 2, 128, 40, 5), (4, 4, 64, 20, 0),
+                                               (6, 2, 64, 500, 2)])
+def test_chunk_infinite_values_beside_hidden_ones(B, dtype, fp8, H, K, D, window, sinks):
+    """What a row sees says which infinity an element is; a NaN or another infinity at the
+    same element of a key hidden from the row says nothing."""
+    c = Case([300, 90], [130, 90], H, K, D, 16, dtype, fp8, window, sinks, seed=8, poison=False)
+    inf, nan = float("inf"), float("nan")
+    for s, p, d, x in ((0, 200, 3, inf), (0, 210, 3, nan), (0, 205, 7, -inf), (0, 230, 7, inf),
+                       (0, 260, 9, nan), (0, 263, 9, inf), (0, 171, D - 1, inf),
+                       (0, 173, D - 1, inf), (1, 0, 1, -inf), (1, 60, 1, nan), (1, 33, 2, inf)):
+        put(c, c.vc, s, [p], d, x)
+    c.chunk(B)
+    want = check(c)
+    assert (want == inf).any() and (want == -inf).any() and np.isnan(want).any()
+
+
 @pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 20, 1 << 40])
 def test_chunk_longer_than_its_context_behind_a_window_past_every_length(B, dtype, fp8, window):
