@@ -134,8 +134,11 @@ __device__ __forceinline__ int window_order_key(const WindowMqParams &p, int s, 
 // and those that its window has just left, as many of both as the unit has tokens
 // at most.  If one of them is non-finite where the row is, the row is computed anew
 // from what it sees, 32 keys at a time, 8 pool rows in flight (unless it sees a NaN
-// there itself; the newest are read first, so a sequence that has diverged is done
-// at once).  Only rows of such tiles pay for this.
+// there itself; the newest are read first).  So rows that are not numbers by what
+// they see -- their query, a key, a value -- cost one look at the hidden values of
+// their unit, and none where their sum of weights is NaN (64 rows of a context of
+// 40,000, all NaN by an old key or an old value: 230 and 243 us, clean 230; reading
+// again what each row sees took 472 and 265 ms).
 
 template <typename T> __device__ __forceinline__ float window_float(T x)
 {

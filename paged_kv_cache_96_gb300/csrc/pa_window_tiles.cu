@@ -669,6 +669,14 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         auto mend_rows = [&](const WtUnit &w, unsigned todo) {
             __syncwarp();
             const WindowKeys keys{p, p.block_tables + (size_t)w.seq * p.max_blocks_per_seq, w.kh};
+            // whether a value hidden from one row and seen by another is non-finite
+            const int end = w.pos0 + w.count;
+            const bool hot =
+                todo != 0 &&
+                __any_sync(kFull, window_non_finite<T, D, kFp8>(
+                                      keys, p.value_cache, max(w.pos0, 0) + 1, end,
+                                      max(window_low(w.pos0, p.window), p.num_sinks),
+                                      window_low(end - 1, p.window)) != 0);
             for (; todo != 0; todo &= todo - 1) {
                 const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
                 const int tk = rr / G;
@@ -678,9 +686,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (w.pos0 + tk < 0)
                     for (int e = lane; e < D / 2; e += 32)
                         reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at)[e] = 0;
-                else
+                else if (hot)
                     window_mend_row<T, D, kFp8>(keys, p.key_cache, p.value_cache, w.pos0 + tk,
-                                                w.pos0, w.pos0 + w.count,
+                                                w.pos0, end,
                                                 static_cast<const T *>(p.query) + at,
                                                 static_cast<T *>(p.out) + at);
             }
@@ -752,8 +760,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(ufree(b));
+            // (a sum that is NaN comes from scores that the row sees, and a row without
+            // weight is not a number: both are their softmax)
             unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0 &&
-                                                     (l != 0.f || before));
+                                                     (l > 0.f || before));
             // (looked at after the last unit, when nobody waits for this warp)
             if (lane == min(ku, 31))
                 mend |= todo;

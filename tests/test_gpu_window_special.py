@@ -149,6 +149,47 @@ def test_rows_whose_scores_are_all_minus_infinity(B, dtype, fp8, call):
     assert bad[:rows[0]].sum() == min(rows[0], 6) and not bad[rows[0]:].any()
 
 
+def timed(run):
+    run()
+    a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+    torch.cuda.synchronize()
+    a.record()
+    run()
+    b.record()
+    torch.cuda.synchronize()
+    return a.elapsed_time(b)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_of_a_diverged_sequence_takes_no_longer(B, fp8):
+    """Rows that are not numbers by what they see -- a query, a key, an old value -- are
+    the definition's and need nothing computed anew, however long their context."""
+    def make():
+        return Case([40000, 70], [64, 70], 4, 1, 128, 64, torch.bfloat16, fp8, 60000, 0, seed=4)
+    nan = 0x7F if fp8 else float("nan")
+    c = make()
+    clean = timed(lambda: c.chunk(B))
+    whole = c.out.clone()
+    assert torch.isfinite(whole.float()).all()
+    for what in ("query", "key", "value"):
+        c = make()
+        bad = torch.zeros_like(whole, dtype=torch.bool)
+        if what == "query":
+            c.q[3:50, 1, 7] = float("nan")
+            bad[3:50, 1] = True
+        elif what == "key":
+            put(c, c.kc, 0, [1234], 9, nan)
+            bad[:64] = True
+        else:
+            put(c, c.vc, 0, [1234], 9, nan)
+            bad[:64, :, 9] = True
+        ms = timed(lambda: c.chunk(B))
+        assert int(c.err.item()) == 0
+        assert torch.equal(torch.isnan(c.out), bad), what
+        assert torch.equal(c.out[~bad], whole[~bad]), what
+        assert ms < 3 * clean + 0.5, f"{what}: {ms:.2f} ms, {clean:.2f} ms without"
+
+
 @pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
 def test_chunk_rows_before_the_first_beside_values_that_are_not_numbers(B, dtype, fp8):
     """Rows at negative positions stay zero beside rows that see such a value."""
