@@ -494,6 +494,7 @@ PA_API pa_status pa_prefill_attention_fp8(void *out, const void *query, const vo
  *                    aligned, its first bytes (the arrival counters of
  *                    pa_decode_workspace_bytes, the same region) zeroed
  *                    before first use; may be NULL when that size is 0
+ * scale * k_scale * log2(e) has to be finite in fp32 (PA_ERR_INVALID_ARG).
  * Other arguments, limits and errors as pa_decode_attention(_fp8).
  */
 PA_API size_t pa_window_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
@@ -526,6 +527,7 @@ PA_API pa_status pa_decode_attention_window_fp8(
  * [0, num_tokens] are clipped and flagged PA_DEVERR_TOKEN_RANGE.
  * num_tokens * num_heads < 2^31 - 128, num_seqs <= 5,120 and
  * max_blocks_per_seq * block_size <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).
+ * scale * k_scale * log2(e) has to be finite in fp32 (PA_ERR_INVALID_ARG).
  * Other arguments, limits and errors as pa_prefill_attention(_fp8) (scale
  * positive).  No workspace.
  */

@@ -864,6 +864,8 @@ static pa_status run_window(void *out, const void *query, const void *key_cache,
     if (fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f &&
                  v_scale > 0.f))
         return PA_ERR_INVALID_ARG;
+    if (!std::isfinite(scale * (fp8 ? k_scale : 1.f) * kLog2e))
+        return PA_ERR_INVALID_ARG;
     // lengths in compact tokens here (partitions, workspace)
     const int compact = window_compact_max(max_context_len, window, num_sinks);
     WindowParams prm{};

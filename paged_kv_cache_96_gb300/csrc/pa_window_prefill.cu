@@ -2,6 +2,7 @@
 // a sliding window and a few first tokens that stay visible: checks of the
 // arguments, then the tensor-core kernel.
 #include <algorithm>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 
@@ -25,6 +26,9 @@ static pa_status run_window_prefill(
         return PA_ERR_INVALID_ARG;
     if (fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f &&
                  v_scale > 0.f))
+        return PA_ERR_INVALID_ARG;
+    const float scale_log2 = scale * (fp8 ? k_scale : 1.f) * kLog2e;
+    if (!std::isfinite(scale_log2))
         return PA_ERR_INVALID_ARG;
     if (num_seqs == 0 || num_tokens == 0)
         return PA_OK;
@@ -64,7 +68,10 @@ static pa_status run_window_prefill(
     prm.window = window;
     // (first tokens past the tables' reach hide nothing)
     prm.num_sinks = std::min(num_sinks, max_blocks_per_seq * block_size);
-    prm.scale_log2 = scale * (fp8 ? k_scale : 1.f) * kLog2e;
+    // The kernel flushes a subnormal factor to 0, and a hidden score of -inf times 0
+    // is not a number.  The smallest normal one (2^-126) in its place moves a score
+    // below 2^100 by less than 2^-26.
+    prm.scale_log2 = std::max(scale_log2, FLT_MIN);
     prm.out_scale = fp8 ? v_scale : 1.f;
     prm.key_cache = key_cache;
     prm.value_cache = value_cache;

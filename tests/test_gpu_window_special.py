@@ -230,3 +230,15 @@ def test_chunk_longer_than_its_context_behind_a_window_past_every_length(B, dtyp
     c.window = 5000     # what a window past every context is
     check(c)
     assert (c.out[:290] == 0).all() and (c.out[340:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("call", ["decode", "chunk"])
+@pytest.mark.parametrize("scale", [1e-39, 1e-44, 1.5e-38])
+def test_scales_below_the_normal_range(B, dtype, fp8, call, scale):
+    """Every visible key has the same weight, hidden ones none."""
+    rows = [1, 1] if call == "decode" else [45, 30]
+    c = Case([100, 30], rows, 8, 2, 64, 16, dtype, fp8, 20, 3, seed=6)
+    c.scale = scale
+    getattr(c, call)(B)
+    check(c)
