@@ -524,7 +524,8 @@ PA_API pa_status pa_decode_attention_window_fp8(
  *     p in [0, pos]  with  p > pos - window  or  p < num_sinks.
  * A row at a negative position gets a zero row; rows of out past
  * query_start[num_seqs] are left as they were.  query_start entries outside
- * [0, num_tokens] are clipped and flagged PA_DEVERR_TOKEN_RANGE.
+ * [0, num_tokens] are clipped, a sequence whose entries decrease has no rows, and
+ * both are flagged PA_DEVERR_TOKEN_RANGE (rows of several sequences are undefined).
  * num_tokens * num_heads < 2^31 - 128, num_seqs <= 5,120 and
  * max_blocks_per_seq * block_size <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).
  * scale * k_scale * log2(e) has to be finite in fp32 (PA_ERR_INVALID_ARG).

@@ -28,6 +28,7 @@ struct WindowMqParams {
     const void *key_cache, *value_cache;  // (for rows computed anew)
     int num_tokens;     // rows of query and out (T)
     int ordered;        // units numbered longest first
+    int max_units;      // units of a KV head that query_start in order can give
 };
 
 // ---- fp32 helpers for the softmax ---------------------------------------------
@@ -109,10 +110,13 @@ __device__ __forceinline__ int window_row0(const WindowMqParams &p, int s, bool 
     return min(max(r, 0), p.num_tokens);
 }
 
-// Rows of one sequence's chunk.
+// Rows of one sequence's chunk (none where its offsets decrease).
 __device__ __forceinline__ int window_rows(const WindowMqParams &p, int s, bool flag = false)
 {
-    return max(0, window_row0(p, s + 1, flag) - window_row0(p, s, flag));
+    const int rows = window_row0(p, s + 1, flag) - window_row0(p, s, flag);
+    if (flag && rows < 0)
+        flag_error(p.error_word, PA_DEVERR_TOKEN_RANGE);
+    return max(0, rows);
 }
 
 // Key tiles (of 64) a sequence's last row sees: the order of the deal.

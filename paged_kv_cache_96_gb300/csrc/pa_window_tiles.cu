@@ -391,9 +391,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (lane >= o)
                     x += y;
             }
+            // (about 2^24 units a sequence at most, 2^30 in 32 of them)
             if (k < nseg)
-                pref[k] = carry + x - n;
+                pref[k] = min(carry + x - n, p.max_units);
             carry += __shfl_sync(kFull, x, 31);
+            if (carry > p.max_units) {
+                // more rows than there are: offsets that decrease somewhere
+                carry = p.max_units;
+                flag_error(p.error_word, PA_DEVERR_TOKEN_RANGE);
+            }
         }
         if (lane == 0)
             pref[nseg] = carry;
@@ -1246,6 +1252,9 @@ pa_status launch_window_tiles(const WindowMqParams &prm_in, pa_dtype dtype, bool
     const long long units = ((long long)prm.num_tokens / tok_tile + prm.num_segments) *
                             prm.num_kv_heads;
     const int grid = (int)std::max(1ll, std::min((long long)info.sms, units));
+    if (units > (1ll << 31) - 1 - info.sms)
+        return PA_ERR_UNSUPPORTED;  // (unit numbers stay in 32 bits)
+    prm.max_units = (int)(units / prm.num_kv_heads);
     // more than a round of units: longest first
     prm.ordered = units > info.sms && prm.num_segments <= kWtOrderSegs;
 

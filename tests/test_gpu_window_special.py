@@ -242,3 +242,19 @@ def test_scales_below_the_normal_range(B, dtype, fp8, call, scale):
     c.scale = scale
     getattr(c, call)(B)
     check(c)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("seqs", [3, 300, 600])
+def test_chunk_offsets_that_go_back(B, fp8, seqs):
+    """Offsets that decrease name rows twice: flagged, and no row past the last one is
+    written, however many rows they add up to."""
+    c = Case([90] * seqs, [40] * seqs, 8, 2, 128, 16, torch.bfloat16, fp8, 30, 2, poison=False)
+    T = 60
+    c.q, c.out = c.q[:T], torch.full((T + 50, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    whole, c.out = c.out, c.out[:T]
+    c.d_start.copy_(torch.arange(seqs + 1, dtype=torch.int32) % 2 * T)
+    c.chunk(B)
+    torch.cuda.synchronize()
+    assert int(c.err.item()) == B.DEVERR_TOKEN_RANGE
+    assert (whole[T:] == 7).all() and torch.isfinite(whole.float()).all()
