@@ -233,8 +233,9 @@ PA_API pa_status pa_build_step_maps(int32_t *query_start, int32_t *token_seq,
  *                       to token (a multiple of 8, at most 2^28): the parts of
  *                       a fused QKV row as they are
  *   query_out         : rows like query's; query itself with its stride (in
- *                       place), or rows that share no byte with query, key and
- *                       value (PA_ERR_INVALID_ARG)
+ *                       place) or rows that share no byte with it, and in
+ *                       either case none with key and value
+ *                       (PA_ERR_INVALID_ARG)
  *   positions         : int32 [num_axes][num_tokens] (device): one axis for
  *                       text, three (time, height, width) for images and video
  *   axis_of_pair      : int32 [rot_dim / 2] (HOST; read before the call

@@ -623,13 +623,15 @@ static pa_status run_rope(void *query_out, long long qo_stride, const void *quer
         !stride_ok(k_stride, num_kv_heads, head_dim, num_tokens) ||
         !stride_ok(v_stride, num_kv_heads, head_dim, num_tokens))
         return PA_ERR_INVALID_ARG;
-    if ((query_out != query || qo_stride != q_stride) &&
-        (rows_meet(query_out, qo_stride, num_heads, query, q_stride, num_heads, head_dim,
-                   num_tokens) ||
-         rows_meet(query_out, qo_stride, num_heads, key, k_stride, num_kv_heads, head_dim,
-                   num_tokens) ||
-         rows_meet(query_out, qo_stride, num_heads, value, v_stride, num_kv_heads, head_dim,
-                   num_tokens)))
+    // in place: the query's own rows, never a key's or a value's (they are read while
+    // the query is written)
+    const bool in_place = query_out == query && qo_stride == q_stride;
+    if ((!in_place && rows_meet(query_out, qo_stride, num_heads, query, q_stride, num_heads,
+                                head_dim, num_tokens)) ||
+        rows_meet(query_out, qo_stride, num_heads, key, k_stride, num_kv_heads, head_dim,
+                  num_tokens) ||
+        rows_meet(query_out, qo_stride, num_heads, value, v_stride, num_kv_heads, head_dim,
+                  num_tokens))
         return PA_ERR_INVALID_ARG;
     RopeParams p;
     for (int i = 0; i < rot_dim / 2; ++i) {
