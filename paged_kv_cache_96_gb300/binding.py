@@ -6,16 +6,20 @@ their dtype, device and contiguity, and passes raw pointers, sizes and the
 current CUDA stream to the library of the same name.  All computation runs
 in the library's kernels.  The serving-step calls (step maps, rotary cache write,
 windowed attention) do the same in C++ (``pyext/calls.cpp``), since the host's part
-is most of what a small one takes.  There is no fallback: if the library has
-not been built, importing this module raises.
+is most of what a small one takes; that extension is loaded when one of them is first
+used.  There is no fallback: if the library has not been built, importing this module
+raises, and so do those calls without the extension.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 from typing import Optional
 
 import torch
+
+from . import build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.environ.get("PA_LIBRARY",
@@ -152,20 +156,29 @@ _lib = _load()
 
 def _load_calls():
     """The calls of the serving step, which read their tensors in C++."""
-    try:
-        from . import _calls as calls
-    except ImportError as e:
-        raise ImportError("the extension _calls is missing; build it with "
-                          "`python -m paged_kv_cache_96_gb300.build`") from e
-    if calls.torch_version != torch.__version__:
-        raise ImportError(f"the extension _calls was built for torch {calls.torch_version}, this is "
-                          f"{torch.__version__}; build it again with "
-                          "`python -m paged_kv_cache_96_gb300.build --force`")
+    path = build.calls_path(torch.__version__)
+    if not os.path.exists(path):
+        raise ImportError(f"the serving-step calls are not built for torch {torch.__version__} and "
+                          f"this Python ({path} is missing); build them with "
+                          "`python -m paged_kv_cache_96_gb300.build`")
+    spec = importlib.util.spec_from_file_location(__package__ + "._calls", path)
+    calls = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(calls)
     calls.bind(_LIB_PATH)
     return calls
 
 
-_calls = _load_calls()
+class _CallsOnFirstUse:
+    """Stands for the extension until one of its calls is used: the others here need
+    neither it nor the torch that it was built for."""
+
+    def __getattr__(self, name):
+        global _calls
+        _calls = _load_calls()
+        return getattr(_calls, name)
+
+
+_calls = _CallsOnFirstUse()
 
 
 def lib() -> ctypes.CDLL:

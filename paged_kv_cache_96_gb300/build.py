@@ -4,8 +4,10 @@
 
 compiles every ``csrc/*.cu`` (device code, one ``-gencode`` each) and
 ``csrc/*.cpp`` (host-only runtime code) in parallel, CUDA runtime linked
-statically, and links ``lib/libpaged_attention.so``; beside it ``_calls.so``, the Python
-calls that read torch tensors themselves (``pyext/calls.cpp``, host compiler).
+statically, and links ``lib/libpaged_attention.so``; beside it the Python calls that
+read torch tensors themselves (``pyext/calls.cpp``, host compiler and torch's headers).
+Only the serving-step calls need those: where they do not compile the build warns, and
+the calls raise when they are used.
 """
 from __future__ import annotations
 
@@ -16,14 +18,15 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIBDIR = os.path.join(HERE, "lib")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(LIBDIR, "libpaged_attention.so")
-CALLS = os.path.join(HERE, "_calls.so")
 CALLS_SRC = os.path.join(HERE, "pyext", "calls.cpp")
+HEADER = os.path.join(os.path.dirname(HERE), "include", "paged_attention.h")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--use_fast_math", "-Xcompiler", "-fPIC",
               "-Xcompiler", "-fvisibility=hidden", "--expt-relaxed-constexpr"]
@@ -50,15 +53,22 @@ def _compile(src: str, verbose_ptxas: bool, objdir: str = OBJDIR, extra=()) -> s
     return obj
 
 
+def calls_path(torch_version: str) -> str:
+    """The extension for this Python and a version of torch, whose tensors' layout it
+    is compiled for: both are part of its name, so that another's is never loaded."""
+    return os.path.join(HERE, f"_calls.torch-{torch_version}" +
+                        sysconfig.get_config_var("EXT_SUFFIX"))
+
+
 def _build_calls() -> None:
     import torch
+    calls = calls_path(torch.__version__)
     root = os.path.dirname(torch.__file__)
     cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
-    tmp = CALLS + f".tmp{os.getpid()}"
+    tmp = calls + f".tmp{os.getpid()}"
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
            "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
-           f'-DPA_TORCH_VERSION="{torch.__version__}"',
            "-I" + sysconfig.get_paths()["include"], "-I" + os.path.join(root, "include"),
            "-I" + os.path.join(root, "include", "torch", "csrc", "api", "include"), "-I" + cuda,
            CALLS_SRC, "-o", tmp, "-L" + os.path.join(root, "lib"), "-lc10", "-lc10_cuda",
@@ -66,20 +76,41 @@ def _build_calls() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"compiling {CALLS_SRC} failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, CALLS)
+    os.replace(tmp, calls)
+    for other in set(glob.glob(os.path.join(HERE, "_calls*.so"))) - {calls}:
+        os.remove(other)  # of older sources, for a torch or Python that was here before
 
 
 def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")) + glob.glob(os.path.join(CSRC, "*.cpp")))
 
 
-def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(CALLS):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [
-        CALLS_SRC, os.path.join(os.path.dirname(HERE), "include", "paged_attention.h")]
-    return all(os.path.getmtime(d) <= t for d in deps)
+def _newer(built: str, deps) -> bool:
+    return os.path.exists(built) and \
+        all(os.path.getmtime(d) <= os.path.getmtime(built) for d in deps)
+
+
+def library_up_to_date() -> bool:
+    return _newer(LIB, sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [HEADER])
+
+
+def calls_up_to_date() -> bool:
+    import torch
+    return _newer(calls_path(torch.__version__), [CALLS_SRC, HEADER])
+
+
+def _build_library(lib: str, verbose_ptxas: bool, extra, objdir: str) -> None:
+    os.makedirs(objdir, exist_ok=True)
+    os.makedirs(os.path.dirname(lib), exist_ok=True)
+    srcs = sources()
+    with cf.ThreadPoolExecutor(max_workers=len(srcs)) as ex:
+        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas, objdir, extra), srcs))
+    tmp = lib + f".tmp{os.getpid()}"
+    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, lib)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, extra=(),
@@ -87,23 +118,21 @@ def build(force: bool = False, verbose_ptxas: bool = False, extra=(),
     """Compile and link; `extra` nvcc flags and `out` library path are for
     building tuning variants next to the default library."""
     lib = out or LIB
-    if not force and out is None and not extra and up_to_date():
-        return LIB
-    objdir = OBJDIR if out is None else os.path.join(os.path.dirname(out), "_obj")
-    os.makedirs(objdir, exist_ok=True)
-    os.makedirs(os.path.dirname(lib), exist_ok=True)
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=len(srcs) + 1) as ex:
-        calls = ex.submit(_build_calls) if out is None else None
-        objs = list(ex.map(lambda s: _compile(s, verbose_ptxas, objdir, extra), srcs))
-        if calls is not None:
-            calls.result()
-    tmp = lib + f".tmp{os.getpid()}"
-    cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, lib)
+
+    def build_calls():
+        if force or not calls_up_to_date():
+            _build_calls()
+
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        calls = ex.submit(build_calls) if out is None else None
+        if force or out is not None or extra or not library_up_to_date():
+            _build_library(lib, verbose_ptxas, extra,
+                           OBJDIR if out is None else os.path.join(os.path.dirname(out), "_obj"))
+        try:
+            if calls is not None:
+                calls.result()
+        except Exception as e:
+            warnings.warn(f"the serving-step calls were not built: {e}")
     return lib
 
 

@@ -480,9 +480,5 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,
 
 PyMODINIT_FUNC PyInit__calls(void)
 {
-    PyObject *m = PyModule_Create(&module);
-    // the tensors' layout is that of the torch this was compiled against
-    if (m != nullptr && PyModule_AddStringConstant(m, "torch_version", PA_TORCH_VERSION) != 0)
-        Py_CLEAR(m);
-    return m;
+    return PyModule_Create(&module);
 }
