@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
+import operator
 import os
 from typing import Optional
 
@@ -563,7 +564,7 @@ def pa_prefill_attention(out: torch.Tensor, query: torch.Tensor, key_cache: torc
 def _reach(n: int) -> int:
     """A window or a number of first tokens as a C int: what passes the int32
     range hides as little as its largest value, negative ones are refused."""
-    return max(-1, min(int(n), 0x7FFFFFFF))
+    return max(-1, min(operator.index(n), 0x7FFFFFFF))
 
 
 def pa_window_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,

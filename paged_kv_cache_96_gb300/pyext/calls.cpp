@@ -139,7 +139,10 @@ int size_int(int64_t n, const char *name)
 
 int64_t integer(PyObject *o, const char *name, bool saturate)
 {
-    PyObject *n = PyLong_Check(o) ? Py_NewRef(o) : PyNumber_Long(o);
+    // (Python's integers and what stands for one, as NumPy's; no float, no text)
+    if (!PyIndex_Check(o))
+        fail(PyExc_TypeError, "%s: integer expected, got %s", name, Py_TYPE(o)->tp_name);
+    PyObject *n = PyNumber_Index(o);
     if (n == nullptr)
         throw PythonError{};
     int over = 0;

@@ -258,3 +258,26 @@ def test_chunk_offsets_that_go_back(B, fp8, seqs):
     torch.cuda.synchronize()
     assert int(c.err.item()) == B.DEVERR_TOKEN_RANGE
     assert (whole[T:] == 7).all() and torch.isfinite(whole.float()).all()
+
+
+@pytest.mark.parametrize("call", ["decode", "chunk"])
+def test_integer_arguments(B, call):
+    """Windows, lengths and partitions are integers (Python's or NumPy's): nothing is cut
+    to one or read from a text."""
+    c = Case([40, 70], [1, 1], 4, 2, 64, 16, torch.float16, False, 9, 2, poison=False)
+    if call == "decode":
+        args = [c.max_ctx, c.window, c.sinks, 0]
+        run = lambda m, w, n, P: B.pa_decode_attention_window(  # noqa: E731
+            c.out, c.q, c.kc, c.vc, c.d_tables, c.d_ctx, m, c.scale, w, n, P, error_word=c.err)
+    else:
+        args = [c.max_ctx, c.window, c.sinks]
+        run = lambda m, w, n: B.pa_prefill_attention_window(  # noqa: E731
+            c.out, c.q, c.kc, c.vc, c.d_tables, c.d_start, c.d_ctx, m, c.scale, w, n,
+            error_word=c.err)
+    for k, good in enumerate(args):
+        for bad in (good + 0.7, float(good), str(good), None, np.float64(good)):
+            with pytest.raises(TypeError):
+                run(*args[:k], bad, *args[k + 1:])
+    assert bool((c.out == 7).all())
+    run(*[t(a) for t, a in zip((np.int64, np.uint16, torch.tensor, np.int8), args)])
+    c.check()
