@@ -674,8 +674,8 @@ __global__ void __launch_bounds__(window_bound_threads(NW + 1, MINB), MINB)
                     acc[0] += wgt * x0.x; acc[1] += wgt * x0.y; acc[2] += wgt * x0.z; acc[3] += wgt * x0.w;
                     acc[4] += wgt * x1.x; acc[5] += wgt * x1.y; acc[6] += wgt * x1.z; acc[7] += wgt * x1.w;
                 }
-                // a partial of no weight (scores of -inf alone) is 0 with m = -inf;
-                // a whole row of none is not a number, as its softmax
+                // a partial of no weight (scores of -inf alone) is 0 with l = 0; a whole
+                // row of none is not a number, as its softmax
                 const float inv = split && lsum == 0.f ? 0.f : p.out_scale / lsum;
                 const size_t h = (size_t)kh * G + jh;
                 if (!split) {
@@ -693,9 +693,9 @@ __global__ void __launch_bounds__(window_bound_threads(NW + 1, MINB), MINB)
                     dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
                     dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
                     if (d0 == 0) {
-                        // (finite wherever l is not 0: scores that are all not a number
-                        // leave no maximum, and a merge passes over m = -inf)
-                        p.part_m[idx] = lsum == 0.f ? -INFINITY : fmaxf(mmax * kLn2, -FLT_MAX);
+                        // (never -inf, which a merge passes over: what is not a number
+                        // in a partition without a maximum counts as well)
+                        p.part_m[idx] = fmaxf(mmax * kLn2, -FLT_MAX);
                         p.part_l[idx] = lsum;
                     }
                 }

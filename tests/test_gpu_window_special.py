@@ -281,3 +281,20 @@ def test_integer_arguments(B, call):
     assert bool((c.out == 7).all())
     run(*[t(a) for t, a in zip((np.int64, np.uint16, torch.tensor, np.int8), args)])
     c.check()
+
+
+@pytest.mark.parametrize("dtype,fp8", FLOATS, ids=IDS[:2])
+@pytest.mark.parametrize("span", [(0, 144), (144, 288)])
+def test_decode_values_of_keys_without_weight(B, dtype, fp8, span):
+    """A weight of 0 times an infinite or NaN value is not a number, in whichever
+    partition it comes."""
+    c = Case([288, 30, 288], [1] * 3, 8, 2, 128, 16, dtype, fp8, 5000, 0, seed=7)
+    c.q[..., 1] = c.q[..., 1].abs() + 0.5
+    put(c, c.kc, 0, range(*span), 1, float("-inf"))
+    put(c, c.vc, 0, [span[0] + 70], 3, float("nan"))
+    put(c, c.vc, 0, [span[0] + 100], 5, float("inf"))
+    for P in PARTITIONS:
+        c.out.fill_(7.0)
+        c.decode(B, P)
+        want = check(c, f"P={P}")
+    assert (np.isnan(want[0]).all(0).nonzero()[0] == [3, 5]).all()
