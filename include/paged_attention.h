@@ -527,6 +527,7 @@ PA_API pa_status pa_decode_attention_window_fp8(
  * query_start[num_seqs] are left as they were.  query_start entries outside
  * [0, num_tokens] are clipped, a sequence whose entries decrease has no rows, and
  * both are flagged PA_DEVERR_TOKEN_RANGE (rows of several sequences are undefined).
+ * out may not overlap query (PA_ERR_INVALID_ARG).
  * num_tokens * num_heads < 2^31 - 128, num_seqs <= 5,120 and
  * max_blocks_per_seq * block_size <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).
  * scale * k_scale * log2(e) has to be finite in fp32 (PA_ERR_INVALID_ARG).

@@ -46,6 +46,11 @@ static pa_status run_window_prefill(
         (long long)max_blocks_per_seq * block_size > (1ll << 31) - 256 ||
         (long long)num_tokens * num_heads >= (1ll << 31) - 128)  // (a tile of rows past the last)
         return PA_ERR_UNSUPPORTED;
+    // (a row computed anew reads its query after its output was written)
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), q = reinterpret_cast<uintptr_t>(query);
+    const uintptr_t row_bytes = (uintptr_t)2 * num_tokens * num_heads * head_dim;
+    if (o < q + row_bytes && q < o + row_bytes)
+        return PA_ERR_INVALID_ARG;
 
     WindowMqParams prm{};
     prm.out = out;

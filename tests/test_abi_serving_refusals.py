@@ -46,3 +46,12 @@ def test_binding_takes_integers_only(B, bad):  # noqa: F811
         with pytest.raises(TypeError):
             B.pa_build_step_maps(z(4, 2), z(4), z(4), z(8), z(1), size, blocks, z(5), z(9), z(9),
                                  z(9), z(4), z(1))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_refuses_outputs_over_its_queries(B, fp8):  # noqa: F811
+    q = 0x100000
+    size = 2 * 9 * 8 * 128                                   # of _chunk's 9 rows
+    for out in (q, q + 16, q + size - 16, q - size + 16):
+        assert _chunk(B, fp8, out=ctypes.c_void_p(out), q=ctypes.c_void_p(q)) == \
+            B.PA_ERR_INVALID_ARG
