@@ -221,6 +221,27 @@ def test_chunk_infinite_values_beside_hidden_ones(B, dtype, fp8, H, K, D, window
 
 
 @pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+def test_outputs_repeat_bit_by_bit(B, dtype, fp8):
+    """The same call again has the same bits, whichever CTA merges its partials."""
+    c = Case([3000, 700, 5, 1400], [1] * 4, 8, 2, 128, 16, dtype, fp8, 600, 20)
+    d = Case([900, 100, 641, 300] * 4, [90, 100, 64, 77] * 4, 32, 8, 64, 16, dtype, fp8, 90, 5)
+    for P in (0, 16, 80, 224, 320):
+        c.decode(B, P)
+        first = c.out.clone()
+        for _ in range(8):
+            c.out.fill_(7.0)
+            c.decode(B, P)
+            assert torch.equal(first, c.out), P
+    d.chunk(B)
+    first = d.out.clone()
+    for _ in range(8):
+        d.out.fill_(7.0)
+        d.chunk(B)
+        assert torch.equal(first, d.out)
+    c.check()
+
+
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
 @pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 20, 1 << 40])
 def test_chunk_longer_than_its_context_behind_a_window_past_every_length(B, dtype, fp8, window):
     """Rows at negative positions, whose window would start before -2^31."""
@@ -298,3 +319,13 @@ def test_decode_values_of_keys_without_weight(B, dtype, fp8, span):
         c.decode(B, P)
         want = check(c, f"P={P}")
     assert (np.isnan(want[0]).all(0).nonzero()[0] == [3, 5]).all()
+
+
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("P", [0, 16])
+def test_decode_of_eleven_thousand_sequences(B, dtype, fp8, P):
+    S = 11000
+    ctx = np.random.default_rng(2).integers(1, 60, size=S)
+    c = Case(ctx, [1] * S, 2, 1, 64, 16, dtype, fp8, 20, 3, seed=2)
+    c.decode(B, P)
+    c.check()
