@@ -93,11 +93,11 @@ __device__ __forceinline__ int window_context(const WindowMqParams &p, int s)
     return c;
 }
 
-// First position of the window of the row at `pos` (0 for a row before the
-// first position too: pos + 1 - window would pass the 32 bits there).
+// First position of the window of the row at `pos` (of a row before the first
+// position too, where pos + 1 - window would pass the 32 bits).
 __device__ __forceinline__ int window_low(int pos, int window)
 {
-    return pos < window ? 0 : pos + 1 - window;
+    return max(0, max(pos, -1) + 1 - window);
 }
 
 // First row of sequence s, kept inside the query; offsets that are not are
@@ -352,6 +352,41 @@ __device__ __noinline__ void window_mend_row(WindowKeys keys, const void *key_ca
 #pragma unroll
     for (int e = 0; e < E; ++e)
         out[lane * E + e] = MmaOp<T>::from_float(o[e] * inv);
+}
+
+// Rows `todo` of the calling warp's 32 of a unit (those that it has), computed anew
+// from what they see (nothing, at a negative position).  Out of line, like what it
+// calls: within the output warps' code it slowed their loop down (8,192 rows over FP8
+// pools 606 us for 580).
+template <typename T, int D, bool kFp8>
+__device__ __noinline__ void window_mend_unit(const WindowMqParams &p, int seq, int row0, int kh,
+                                              int count, int pos0, unsigned todo)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = p.group;
+    const WindowKeys keys{p, p.block_tables + (size_t)seq * p.max_blocks_per_seq, kh};
+    __syncwarp();
+    // whether a value hidden from one row and seen by another is non-finite
+    const int end = pos0 + count;
+    const bool hot =
+        __any_sync(kFull, window_non_finite<T, D, kFp8>(
+                              keys, p.value_cache, max(pos0, 0) + 1, end,
+                              max(window_low(pos0, p.window), p.num_sinks),
+                              window_low(end - 1, p.window)) != 0);
+    for (; todo != 0; todo &= todo - 1) {
+        const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
+        const int tk = rr / G;
+        if (tk >= count)
+            continue;
+        const long long at =
+            (((long long)row0 + tk) * p.num_heads + kh * G + rr - tk * G) * D;
+        T *out = static_cast<T *>(p.out) + at;
+        if (pos0 + tk < 0)
+            for (int e = lane; e < D / 2; e += 32)
+                reinterpret_cast<uint32_t *>(out)[e] = 0;
+        else if (hot)
+            window_mend_row<T, D, kFp8>(keys, p.key_cache, p.value_cache, pos0 + tk, pos0, end,
+                                        static_cast<const T *>(p.query) + at, out);
+    }
 }
 
 // Sequences of one launch (their unit counts are kept in shared memory).

@@ -670,35 +670,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 for (int c = 0; c < D / 8; ++c)
                     dst[c] = make_uint4(0, 0, 0, 0);
         };
-        // Rows `todo` of this warp's 32 of a unit (those that it has), computed anew
-        // from what they see (nothing, at a negative position).
-        auto mend_rows = [&](const WtUnit &w, unsigned todo) {
-            __syncwarp();
-            const WindowKeys keys{p, p.block_tables + (size_t)w.seq * p.max_blocks_per_seq, w.kh};
-            // whether a value hidden from one row and seen by another is non-finite
-            const int end = w.pos0 + w.count;
-            const bool hot =
-                todo != 0 &&
-                __any_sync(kFull, window_non_finite<T, D, kFp8>(
-                                      keys, p.value_cache, max(w.pos0, 0) + 1, end,
-                                      max(window_low(w.pos0, p.window), p.num_sinks),
-                                      window_low(end - 1, p.window)) != 0);
-            for (; todo != 0; todo &= todo - 1) {
-                const int rr = 32 * (warp & 3) + __ffs(todo) - 1;
-                const int tk = rr / G;
-                const long long at = (((long long)w.row0 + tk) * H + w.kh * G + rr - tk * G) * D;
-                if (tk >= w.count)
-                    continue;
-                if (w.pos0 + tk < 0)
-                    for (int e = lane; e < D / 2; e += 32)
-                        reinterpret_cast<uint32_t *>(static_cast<T *>(p.out) + at)[e] = 0;
-                else if (hot)
-                    window_mend_row<T, D, kFp8>(keys, p.key_cache, p.value_cache, w.pos0 + tk,
-                                                w.pos0, end,
-                                                static_cast<const T *>(p.query) + at,
-                                                static_cast<T *>(p.out) + at);
-            }
-        };
         constexpr int kOutUnroll = kFp8 ? D / 32 : 1;
         unsigned mend = 0;  // the mask of unit `lane` (the last lane: all from there on)
         int units_done = 0;
@@ -712,11 +683,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             const int a1 = (2 * b + (int)(g & 1)) * kWtRows + r;
             const float l0 = part_l[a0], l1 = part_l[a1];
             const float l = l1 == 0.f ? l0 : l0 + l1 * exp2f(part_m[a1] - part_m[a0]);
-            // no weight: zeros for a row at a negative position, which sees no key;
-            // of keys that all have a score of -inf the softmax is not a number
-            const bool before = w.pos0 + tok < 0;
-            const float none = before ? 0.f : __uint_as_float(0x7fffffffu);
-            const float inv = l > 0.f ? p.out_scale / l : none;
+            // no weight (0 / 0): of keys that all have a score of -inf the softmax is not
+            // a number; a row at a negative position, which sees no key, gets its
+            // zeros below
+            const float inv = p.out_scale / l;
+            // (a sum that is NaN comes from scores that the row sees: it is its softmax)
+            const unsigned real = __ballot_sync(kFull, l >= 0.f);
             const uint64_t inv2 = pack_f32x2(inv, inv), zero2 = pack_f32x2(0.f, 0.f);
             const uint32_t o_at = tmem + lanes + kWtTmemO;
             T *const dst = row_of(w);
@@ -766,10 +738,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(ufree(b));
-            // (a sum that is NaN comes from scores that the row sees, and a row without
-            // weight is not a number: both are their softmax)
-            unsigned todo = __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0 &&
-                                                     (l > 0.f || before));
+            unsigned todo =
+                real & __ballot_sync(kFull, dst != nullptr && (nan & 0x7fff7fffu) != 0);
             // (looked at after the last unit, when nobody waits for this warp)
             if (lane == min(ku, 31))
                 mend |= todo;
@@ -949,8 +919,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             for (int ku = 0; ku < units_done; ++ku) {
                 const unsigned todo = __shfl_sync(kFull, mend, min(ku, 31));
                 unit_at(ku, w);
-                if (w.steps() > 0)
-                    mend_rows(w, todo);
+                if (w.steps() > 0 && todo != 0)
+                    window_mend_unit<T, D, kFp8>(p, w.seq, w.row0, w.kh, w.count, w.pos0, todo);
             }
         }
     } else {
