@@ -203,12 +203,13 @@ __global__ void __launch_bounds__(kReduceThreads, PA_REDUCE_MINB)
                     c_lo[u] = c_hi[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                 }
             }
+            // q = c0 < nparts: the chunk's maximum is finite.  (Of a pass that stores
+            // m = -inf where every score of a partition is -inf it may not be, and
+            // the row is then not a number; the windowed pass stores -FLT_MAX.)
             float mn = mt;
 #pragma unroll
             for (int u = 0; u < kReduceUnroll; ++u)
                 mn = fmaxf(mn, cm[u]);
-            if (mn == -INFINITY)
-                continue;  // only partials without weight so far (every score -inf)
             const float alpha = exp2f((mt - mn) * kLog2e);  // 0 while mt is -inf
             lt *= alpha;
 #pragma unroll
@@ -250,7 +251,7 @@ __global__ void __launch_bounds__(kReduceThreads, PA_REDUCE_MINB)
     __syncthreads();
     if (tid >= items)
         return;
-    // (-inf if no partial has weight: the softmax is not a number, nor is the row)
+    // group 0 holds q = 0 < nparts: the maximum over groups is finite (as above)
     float mx = -INFINITY;
     for (int g2 = 0; g2 < qgroups; ++g2)
         mx = fmaxf(mx, red_m[g2 * items + tid]);
@@ -258,7 +259,7 @@ __global__ void __launch_bounds__(kReduceThreads, PA_REDUCE_MINB)
     float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     for (int g2 = 0; g2 < qgroups; ++g2) {
         const int r = g2 * items + tid;
-        const float w = exp2f((red_m[r] - mx) * kLog2e);  // 0 for a group without weight
+        const float w = exp2f((red_m[r] - mx) * kLog2e);  // 0 for a group with no partition
         lsum += w * red_l[r];
         const float4 *src = reinterpret_cast<const float4 *>(red_o + (size_t)r * 8);
         const float4 x0 = src[0], x1 = src[1];

@@ -33,7 +33,7 @@
 //  * Hidden rows of a border tile get a score of -inf by selection and a zero
 //    value row, so what they hold never reaches the output.
 // Weights are rounded to the pools' type (fp16 for FP8 pools) as the operand of
-// the value product, relative error 2^-9 (bf16) or 2^-12: about that of the
+// the value product, relative error 2^-8 (bf16) or 2^-11: about that of the
 // rounded output; their sum keeps the unrounded fp32 weights.
 #include <cuda.h>
 
@@ -62,6 +62,8 @@ struct WindowParams : DecodeParams {
 // heads of 8, FP8: 8 partials 14.0 us by the pass, 9.8 by the kernel, 4 partials
 // 13.6 and 12.6, 2 partials 18.2 and 18.1; 128 such sequences, window 1,024: 163 and
 // 96, 78 and 76, 62.5 and 65.9 (16-bit pools 183 and 117, 110 and 103, 93 and 98).
+// 3 partials: 128 sequences 67.7 and 70.0 (16-bit pools 98.3 and 99.6), 8 sequences,
+// window 2,048, 18.5 and 20.6, 1 sequence 18.5 and 16.5.
 constexpr int kWinMergeMax = 3;
 
 // A sequence's compact length, and how far its window's tiles lie behind
@@ -693,8 +695,9 @@ __global__ void __launch_bounds__(window_bound_threads(NW + 1, MINB), MINB)
                     dst[0] = make_float4(acc[0] * inv, acc[1] * inv, acc[2] * inv, acc[3] * inv);
                     dst[1] = make_float4(acc[4] * inv, acc[5] * inv, acc[6] * inv, acc[7] * inv);
                     if (d0 == 0) {
-                        // (never -inf, which a merge passes over: what is not a number
-                        // in a partition without a maximum counts as well)
+                        // (never -inf: the reduce kernel takes a finite maximum, and the
+                        // merge in the pass would leave out what is not a number in a
+                        // partition without one)
                         p.part_m[idx] = fmaxf(mmax * kLn2, -FLT_MAX);
                         p.part_l[idx] = lsum;
                     }
