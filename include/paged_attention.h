@@ -524,12 +524,15 @@ PA_API pa_status pa_decode_attention_window_fp8(
  * where the chunk row at position pos sees
  *     p in [0, pos]  with  p > pos - window  or  p < num_sinks.
  * A row at a negative position gets a zero row; rows of out past
- * query_start[num_seqs] are left as they were.  query_start entries outside
+ * query_start[num_seqs] are left as they were.  An element is what the softmax over
+ * the visible positions gives, infinities and NaN among it, whatever the hidden ones
+ * hold; of scores that are all -inf it is NaN (pa_decode_attention_window too).
+ * query_start entries outside
  * [0, num_tokens] are clipped, a sequence whose entries decrease has no rows, and
  * both are flagged PA_DEVERR_TOKEN_RANGE (rows of several sequences are undefined).
  * out may not overlap query (PA_ERR_INVALID_ARG).
- * num_tokens * num_heads < 2^31 - 128, num_seqs <= 5,120 and
- * max_blocks_per_seq * block_size <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).
+ * num_tokens * num_heads < 2^31 - 128, num_seqs <= 5,120, num_seqs * num_kv_heads < 2^30
+ * and max_blocks_per_seq * block_size <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).
  * scale * k_scale * log2(e) has to be finite in fp32 (PA_ERR_INVALID_ARG).
  * Other arguments, limits and errors as pa_prefill_attention(_fp8) (scale
  * positive).  No workspace.

@@ -13,9 +13,9 @@
 // through 128 query rows of one KV head at a time, in steps of 128 keys.  Times
 // below: 8,192 rows of 4 sequences, 32 heads over 8, d 128, window 4,096 and 64
 // first tokens of up to 32,768, blocks of 32 (0.56 TFLOP of rows and keys seen:
-// 375 us, 1.49 PFLOP/s, where the device is within 5 % of its power limit);
-// and 2,048 rows of 4 sequences, 64 heads over 8, window 512, blocks of 16 (37.6 us,
-// 0.69 PFLOP/s).
+// 376 us by itself, 1.49 PFLOP/s; in a run of calls 417, 1.34 PFLOP/s, where the power
+// limit sets the clock: 1,370 of 1,400 W at 1,725 of 2,070 MHz); and 2,048 rows of 4
+// sequences, 64 heads over 8, window 512, blocks of 16 (37.6 us, 0.69 PFLOP/s).
 //  * A score product reads its query rows from shared memory for every step,
 //    so N = 128 keys cost what 64 do (~60 cycles an MMA for either); 64-key
 //    steps pay that, and every barrier and commit, twice (505 us).
@@ -54,12 +54,13 @@
 //    after the CTA's last unit, when no other role waits.
 //  * FP8 pools: codes land where the upper half of their fp16 tile will be (d
 //    128; beside it at d 64) and the output warps widen them, in whatever order
-//    keys, values, query tiles and finished units come.  By count
-//    shared memory bounds it: 32 KB of codes written and read and 64 KB of fp16
-//    written a step, ~1,000 cycles beside the ~1,000 of the operands' reads
-//    (570 us and 57).  The query is rounded to fp16, the K scale joins the
-//    exponent's scale and the V scale the output.
-// P is rounded to the operands' type, relative error 2^-9 (bf16) or 2^-12: about
+//    keys, values, query tiles and finished units come: 32 KB of codes written and
+//    read and 64 KB of fp16 written a step (580 us and 58).  No unit is busy all
+//    the time by its counter: tensor pipe 43 %, the shared-memory pipe of the warps'
+//    loads and stores 49 % (the operands' reads come on top), issue 49 %.  The query
+//    is rounded to fp16, the K scale joins the exponent's scale and the V scale the
+//    output.
+// P is rounded to the operands' type, relative error 2^-8 (bf16) or 2^-11: about
 // that of the rounded output; the sum keeps the unrounded fp32 weights.
 #include <cuda.h>
 
@@ -1033,7 +1034,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 mbar_wait_bounded(kConvQ ? qland((nq - 2) & 1) : qfull((nq - 2) & 1),
                                   ((nq - 2) >> 1) & 1, kDrainWaitNs);
         } else {
-            // ===== tensor-core warps: scores (10), value products (11) ======================
+            // ===== tensor-core warps: scores (14), value products (15) ======================
             // One elected lane of each issues.  An MMA takes its warp ~60 cycles
             // to issue, about what it takes to run, and every wait some tens:
             // one warp for both would be what the kernel waits for.
