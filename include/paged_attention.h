@@ -527,9 +527,9 @@ PA_API pa_status pa_decode_attention_window_fp8(
  * query_start[num_seqs] are left as they were.  An element is what the softmax over
  * the visible positions gives, infinities and NaN among it, whatever the hidden ones
  * hold; of scores that are all -inf it is NaN (pa_decode_attention_window too).
- * query_start entries outside
- * [0, num_tokens] are clipped, a sequence whose entries decrease has no rows, and
- * both are flagged PA_DEVERR_TOKEN_RANGE (rows of several sequences are undefined).
+ * query_start entries outside [0, num_tokens] are clipped, a sequence whose entries
+ * decrease has no rows, and both are flagged PA_DEVERR_TOKEN_RANGE; a row that
+ * offsets give to several sequences is undefined.
  * out may not overlap query (PA_ERR_INVALID_ARG).
  * num_tokens * num_heads < 2^31 - 128, num_seqs <= 5,120, num_seqs * num_kv_heads < 2^30
  * and max_blocks_per_seq * block_size <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).
