@@ -12,6 +12,7 @@ the calls raise when they are used.
 from __future__ import annotations
 
 import concurrent.futures as cf
+import contextlib
 import glob
 import os
 import shutil
@@ -77,8 +78,6 @@ def _build_calls() -> None:
     if r.returncode != 0:
         raise RuntimeError(f"compiling {CALLS_SRC} failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, calls)
-    for other in set(glob.glob(os.path.join(HERE, "_calls*.so"))) - {calls}:
-        os.remove(other)  # of older sources, for a torch or Python that was here before
 
 
 def sources():
@@ -121,6 +120,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, extra=(),
 
     def build_calls():
         if force or not calls_up_to_date():
+            for stale in glob.glob(os.path.join(HERE, "_calls*.so")):
+                with contextlib.suppress(FileNotFoundError):
+                    os.remove(stale)  # of older sources, or for another torch or Python
             _build_calls()
 
     with cf.ThreadPoolExecutor(max_workers=1) as ex:

@@ -88,11 +88,27 @@ def test_name_says_what_it_was_built_for(built):
     assert built.calls_path("1.2.3") != path
 
 
-def test_library_is_built_where_the_extension_does_not_compile(built, monkeypatch):
+def test_library_is_built_where_the_extension_does_not_compile(built, monkeypatch, tmp_path):
     def no_compiler():
         raise RuntimeError("no host compiler")
-    monkeypatch.setattr(built, "calls_up_to_date", lambda: False)
+    monkeypatch.setattr(built, "HERE", str(tmp_path))
     monkeypatch.setattr(built, "_build_calls", no_compiler)
     monkeypatch.setattr(built, "library_up_to_date", lambda: True)
     with pytest.warns(UserWarning, match="no host compiler"):
         assert built.build() == built.LIB
+
+
+def test_extension_of_older_sources_does_not_stay(built, monkeypatch, tmp_path):
+    """Where it is out of date and does not compile there is none, rather than one that
+    passes the library other arguments."""
+    (tmp_path / os.path.basename(built.calls_path("1.2.3"))).touch()
+    (tmp_path / "_calls.so").touch()
+
+    def no_compiler():
+        raise RuntimeError("no host compiler")
+    monkeypatch.setattr(built, "HERE", str(tmp_path))
+    monkeypatch.setattr(built, "_build_calls", no_compiler)
+    monkeypatch.setattr(built, "library_up_to_date", lambda: True)
+    with pytest.warns(UserWarning, match="no host compiler"):
+        built.build()
+    assert not os.listdir(tmp_path)
