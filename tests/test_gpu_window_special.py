@@ -329,3 +329,60 @@ def test_decode_of_eleven_thousand_sequences(B, dtype, fp8, P):
     c = Case(ctx, [1] * S, 2, 1, 64, 16, dtype, fp8, 20, 3, seed=2)
     c.decode(B, P)
     c.check()
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_chunk_special_values_in_more_units_than_masks(B, fp8):
+    """Sequences of more rows than tokens, 65 units a CTA and more, a NaN value at
+    position 5 of each: rows before the first position are zero, rows 0 to 4 numbers, and
+    later ones NaN in that element alone."""
+    S, H, D, bs, rows, ctx = 5000, 4, 64, 16, 40, 20
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.empty((S * rows, H, D), dtype=torch.float16, device="cuda").normal_(generator=g)
+    kc, vc = (torch.empty((2 * S, bs, 1, D), device="cuda").normal_(generator=g)
+              for _ in range(2))
+    kc, vc = (x.to(torch.float8_e4m3fn).view(torch.uint8) if fp8 else x.half() for x in (kc, vc))
+    vc[::2, 5, 0, 9] = 0x7F if fp8 else float("nan")
+    i = lambda a: torch.as_tensor(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    out, err = torch.full_like(q, 7), i([0])
+    B.pa_prefill_attention_window(out, q, kc, vc, i(np.arange(2 * S).reshape(S, 2)),
+                                  i(np.arange(S + 1) * rows), i([ctx] * S), ctx, 0.125, 100, 0,
+                                  error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == 0
+    x = out.view(S, rows, H, D)
+    assert (x[:, :rows - ctx] == 0).all()
+    nan = torch.zeros_like(x[:, rows - ctx:], dtype=torch.bool)
+    nan[:, 5:, :, 9] = True
+    assert torch.equal(torch.isnan(x[:, rows - ctx:]), nan)
+    # row 0 sees its own key alone
+    v = vc[::2, 0, 0].view(torch.float8_e4m3fn).half() if fp8 else vc[::2, 0, 0]
+    assert torch.equal(x[:, rows - ctx], v[:, None].expand(S, H, D))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_decode_and_chunk_at_once(B, fp8):
+    """Windowed decode and prefill on two streams at the same time, one of them a replayed
+    graph, each with a workspace of its own."""
+    d = Case([3000, 700, 5, 1400], [1] * 4, 8, 2, 128, 16, torch.bfloat16, fp8, 600, 20)
+    c = Case([900, 100, 641, 300] * 4, [90, 100, 64, 77] * 4, 32, 8, 64, 16, torch.bfloat16, fp8,
+             90, 5)
+    n = B.pa_window_workspace_bytes(4, 8, 2, 128, 3000, 600, 20, 16)
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    d.decode(B, 16, ws)
+    c.chunk(B)
+    torch.cuda.synchronize()
+    want = d.out.clone(), c.out.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        for _ in range(4):
+            c.chunk(B)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        g.replay()
+        for P in (16, 80, 16):
+            d.decode(B, P, ws, stream=side)
+    torch.cuda.synchronize()
+    assert int(d.err.item()) == 0 and int(c.err.item()) == 0
+    assert torch.equal(d.out, want[0]) and torch.equal(c.out, want[1])
