@@ -553,6 +553,80 @@ PA_API pa_status pa_prefill_attention_window_fp8(
     int32_t *error_word, void *stream);
 
 /*
+ * pa_summarize_blocks -- 8-bit bounds of the keys of every block that a step
+ * wrote to (no counterpart on the pages: with pa_select_blocks and
+ * pa_decode_attention_sparse an addition to [GAO] §1.6 that reads a long
+ * context in part).  For block b, KV head kh and the keys K[p] of its positions
+ * p below the context, with a = max over p and d of |K[p][d]|:
+ *     summaries[b][kh][0][d] = rint(min_p K[p][d] * (127 / a))
+ *     summaries[b][kh][1][d] = rint(max_p K[p][d] * (127 / a))
+ *     summary_scales[b][kh]  = a * (1 / 127)
+ * in fp32, each operation rounded to nearest.  a below 2^-40 counts as 0: codes
+ * and scale are 0.  A block with a key that is not finite has codes 0 and scale
+ * +inf, and no score is larger than its own.  FP8 pools: K[p][d] is e4m3(code),
+ * without the pool's scale (which is one factor of all scores).
+ *   summaries      : int8 [num_blocks][num_kv_heads][2][head_dim], 16-byte aligned
+ *   summary_scales : float [num_blocks][num_kv_heads]
+ *   context_lens   : int32 [num_seqs], counting the step's new tokens
+ *   query_start    : int32 [num_seqs + 1], as pa_prefill_attention takes it: the
+ *                    blocks that hold the last query_start[s + 1] - query_start[s]
+ *                    tokens of sequence s are summarized anew, others left as they
+ *                    were.  NULL: every block of every context (after an
+ *                    eviction, or a cache that was filled elsewhere).
+ * A length outside its table, or more new tokens than the context, is clipped and
+ * sets PA_DEVERR_CONTEXT_RANGE; a table entry outside [0, num_blocks) is skipped and
+ * sets PA_DEVERR_BLOCK_RANGE.  A block of several sequences has to hold as many
+ * tokens of each (else one of their bounds stands).  dtype: of the pool (PA_F16,
+ * PA_BF16, PA_FP8_E4M3).
+ * Supported: head_dim 64 or 128; block_size a power of two from 16 to 256.
+ */
+PA_API pa_status pa_summarize_blocks(int8_t *summaries, float *summary_scales,
+                                     const void *key_cache, const int32_t *block_tables,
+                                     int max_blocks_per_seq, const int32_t *context_lens,
+                                     const int32_t *query_start, int num_seqs, int num_blocks,
+                                     int block_size, int num_kv_heads, int head_dim,
+                                     pa_dtype dtype, int32_t *error_word, void *stream);
+
+/*
+ * pa_select_blocks -- for every query row t and KV head kh the blocks of its
+ * context that it attends: the first num_first, the last num_last (the newest
+ * among them), and of the others those with the largest score, top_k in all; every
+ * block where the context has no more than top_k.  With the row's query heads
+ * coded as pa_summarize_blocks codes keys (c_h and scale s_h, each head by itself;
+ * a head with an element that is not finite has codes and scale 0):
+ *     I_h(b)   = sum_d max(c_h[d] * summaries[b][kh][0][d],
+ *                          c_h[d] * summaries[b][kh][1][d])       (whole numbers)
+ *     score(b) = max over the group's heads of (s_h * I_h(b)) * summary_scales[b][kh]
+ * two fp32 products, each rounded to nearest (+inf where the block's scale is) --
+ * one number, so that a selection does not depend on how it was computed.  Of
+ * equal scores the lower block index is taken.
+ *   selected  : int32 [num_tokens][num_kv_heads][top_k] (output): block indices
+ *               (of the sequence, not the pool) in ascending order, then -1
+ *   query     : dtype, [num_tokens][num_heads][head_dim], rotated
+ *   token_seq, token_pos : int32 [num_tokens], as pa_build_step_maps gives them:
+ *               row t is at position token_pos[t] of sequence token_seq[t] and
+ *               sees the blocks up to its own.  A negative sequence is padding:
+ *               the row's entries are all -1; so are those of a sequence >=
+ *               num_seqs or a position outside the table, which set
+ *               PA_DEVERR_TOKEN_RANGE.
+ *   max_context_len : (host) >= every token_pos[t] + 1 (longer contexts are
+ *               clipped and set PA_DEVERR_CONTEXT_RANGE)
+ * A table entry outside [0, num_blocks) sets PA_DEVERR_BLOCK_RANGE and has the lowest
+ * score.  num_first + num_last <= top_k (PA_ERR_INVALID_ARG otherwise).
+ * Supported: as pa_decode_attention, and at most about 55,000 blocks of
+ * max_context_len (their scores are kept in shared memory).
+ */
+PA_API pa_status pa_select_blocks(int32_t *selected, int top_k, const void *query,
+                                  const int8_t *summaries, const float *summary_scales,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *token_seq, const int32_t *token_pos,
+                                  int max_context_len, int num_first, int num_last,
+                                  int num_tokens, int num_seqs, int num_heads,
+                                  int num_kv_heads, int head_dim, int block_size,
+                                  int num_blocks, pa_dtype dtype, int32_t *error_word,
+                                  void *stream);
+
+/*
  * Prefix plan -- which sequences of a decode batch share leading physical
  * blocks ([FEI] "共享前缀的 Block 复用": block tables that name the same
  * physical blocks for a common prefix, the blocks' reference counts > 1).

@@ -109,6 +109,9 @@ def _load() -> ctypes.CDLL:
         "pa_prefill_attention_window_fp8": (i32, [P, P, P, P, P, i32, P, P, i32, i32, i32, i32,
                                                   i32, i32, i32, i32, i32, i32, f32, f32, f32,
                                                   i32, P, P]),
+        "pa_summarize_blocks": (i32, [P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32, P, P]),
+        "pa_select_blocks": (i32, [P, i32, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32,
+                                   i32, i32, i32, i32, i32, P, P]),
         "pa_prefix_plan_ints": (sz, [i32, i32, i32]),
         "pa_plan_prefix_groups": (i32, [P, i32, P, i32, i32, i32, P, sz, P, P]),
         "pa_cascade_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
@@ -610,6 +613,36 @@ def pa_prefill_attention_window(out: torch.Tensor, query: torch.Tensor, key_cach
                                    k_scale, v_scale, error_word, stream)
     if status:
         raise PAError("pa_prefill_attention_window" + _suffix(key_cache), status)
+
+
+def pa_summarize_blocks(summaries: torch.Tensor, summary_scales: torch.Tensor,
+                        key_cache: torch.Tensor, block_tables: torch.Tensor,
+                        context_lens: torch.Tensor, query_start: Optional[torch.Tensor] = None,
+                        error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """8-bit bounds of the keys of each block that holds one of the last
+    query_start[s + 1] - query_start[s] tokens of sequence s (None: of every
+    block): summaries int8 [N, Hkv, 2, d] (minimum, maximum) and summary_scales
+    float32 [N, Hkv], beside key_cache [N, bs, Hkv, d]."""
+    status = _calls.summarize(summaries, summary_scales, key_cache, block_tables, context_lens,
+                              query_start, error_word, stream)
+    if status:
+        raise PAError("pa_summarize_blocks", status)
+
+
+def pa_select_blocks(selected: torch.Tensor, query: torch.Tensor, summaries: torch.Tensor,
+                     summary_scales: torch.Tensor, block_tables: torch.Tensor,
+                     token_seq: torch.Tensor, token_pos: torch.Tensor, max_context_len: int,
+                     block_size: int, num_first: int = 1, num_last: int = 1,
+                     error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Blocks that each row of query [T, H, d] attends, into selected int32
+    [T, Hkv, top_k]: the first num_first and last num_last of its context and
+    those with the largest score their summaries allow, ascending, then -1.
+    token_seq / token_pos [T]: as pa_build_step_maps gives them (-1: padding)."""
+    status = _calls.select_blocks(selected, query, summaries, summary_scales, block_tables, token_seq,
+                           token_pos, max_context_len, block_size, num_first, num_last,
+                           error_word, stream)
+    if status:
+        raise PAError("pa_select_blocks", status)
 
 
 def pa_plan_prefix_groups(block_tables, context_lens, block_size: int,

@@ -1,0 +1,797 @@
+// pa_blocks.cu -- which blocks of a long context a query row attends: 8-bit bounds
+// of every block's keys, and the blocks whose bounds allow the largest score, for
+// sm_103a.  An addition to paged attention ("PagedAttention & Continuous Batching"
+// §1.4 block table, §1.6, §2.4 decode is memory-bound): a row then reads its selected
+// blocks (pa_list_decode.cu) and, of every other block, 2 d + 4 bytes a KV head.
+//
+// Bounds of block b and KV head kh over its n keys (positions below the context):
+//     lo_d = min_p K[p][d], hi_d = max_p K[p][d], a = max_d max(|lo_d|, |hi_d|)
+//     code(x) = rint(x * (127 / a)), scale = a * (1 / 127)        (fp32, IEEE)
+// a not finite: codes 0, scale +inf; a < 2^-40: codes 0, scale 0.
+//
+// Score of block b for the row's G query heads, their elements coded the same way
+// (codes c_h, scale s_h, each head by itself):
+//     I_h = sum_d max(c_h,d lo_d, c_h,d hi_d) = sum_d min(c, 0) lo_d + max(c, 0) hi_d
+//     score = max_h fl(s_h I_h) * scale
+// the largest q . k that a key within the bounds could have, up to the codes'
+// rounding.  I_h is a whole number of magnitude <= 128 * 127^2 < 2^21, so it is exact
+// in any order, and with the two rounded fp32 products the score is one number however
+// it is computed: what is selected does not depend on tiles or clusters.
+#include <algorithm>
+#include <cmath>
+#include <mutex>
+#include <type_traits>
+
+#include <cooperative_groups.h>
+
+#include "pa_decode_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace pa {
+
+constexpr float kTiny = 0x1p-40f;  // amplitudes below it count as zero
+
+__device__ __forceinline__ bool finite(float x)
+{
+    return (__float_as_uint(x) & 0x7fffffffu) < 0x7f800000u;
+}
+
+// The codes' factor and the scale of values of amplitude `top` (finite).
+struct CodeScale {
+    float inv, scale;
+};
+__device__ __forceinline__ CodeScale code_scale(float top)
+{
+    if (top < kTiny)
+        return {0.f, 0.f};
+    return {__fdiv_rn(127.f, top), __fmul_rn(top, 1.f / 127.f)};
+}
+
+// ---- bounds ---------------------------------------------------------------------
+//
+// What bounds it: HBM, each key of a touched block read once.  A warp takes one
+// (block, KV head): its rows of d keys are runs of 64 to 256 bytes, so a group of
+// lanes has one row and the warp several, 16 bytes a lane, eight loads in flight;
+// minima and maxima are taken on packed pairs in the pools' own type (FP8 codes as
+// the fp16 values they are), which rounds nothing.  Consecutive warps take a block's
+// consecutive heads.  The blocks that the step wrote to are numbered through all
+// sequences by a scan in every CTA, so that one long prompt among decode rows is
+// spread over the device.
+struct SummaryParams {
+    int8_t *codes;   // [num_blocks][num_kv_heads][2][head_dim]
+    float *scales;   // [num_blocks][num_kv_heads]
+    const void *key_cache;
+    const int32_t *block_tables;
+    const int32_t *context_lens;
+    const int32_t *query_start;  // [S + 1], or null: whole contexts
+    int32_t *error_word;
+    int max_blocks_per_seq, num_seqs, num_blocks, block_shift, num_kv_heads;
+};
+
+constexpr int kSumThreads = 256;
+constexpr int kSumSeqs = 2 * kSumThreads;  // sequences numbered at once
+
+// First block and number of blocks that the new tokens of sequence s are in.
+struct Touched {
+    int first, count, ctx;
+};
+__device__ __forceinline__ Touched touched_blocks(const SummaryParams &p, int s, bool flag)
+{
+    const int bs = 1 << p.block_shift;
+    const long long cap = (long long)p.max_blocks_per_seq << p.block_shift;
+    const int limit = (int)min(cap, (long long)INT32_MAX - bs);
+    int c = p.context_lens[s];
+    bool bad = c < 0 || c > limit;
+    c = c < 0 ? 0 : min(c, limit);
+    int n = c;
+    if (p.query_start != nullptr) {
+        const long long rows = (long long)p.query_start[s + 1] - p.query_start[s];
+        bad |= rows < 0 || rows > c;
+        n = (int)min(max(rows, 0ll), (long long)c);
+    }
+    if (bad && flag)
+        flag_error(p.error_word, PA_DEVERR_CONTEXT_RANGE);
+    if (n == 0)
+        return {0, 0, c};
+    const int first = (c - n) >> p.block_shift;
+    return {first, ((c + bs - 1) >> p.block_shift) - first, c};
+}
+
+// Packed minimum and maximum that pass a NaN on.
+__device__ __forceinline__ __half2 pair_min(__half2 a, __half2 b) { return __hmin2_nan(a, b); }
+__device__ __forceinline__ __half2 pair_max(__half2 a, __half2 b) { return __hmax2_nan(a, b); }
+__device__ __forceinline__ __nv_bfloat162 pair_min(__nv_bfloat162 a, __nv_bfloat162 b)
+{
+    return __hmin2_nan(a, b);
+}
+__device__ __forceinline__ __nv_bfloat162 pair_max(__nv_bfloat162 a, __nv_bfloat162 b)
+{
+    return __hmax2_nan(a, b);
+}
+__device__ __forceinline__ float2 pair_float(__half2 x) { return __half22float2(x); }
+__device__ __forceinline__ float2 pair_float(__nv_bfloat162 x) { return __bfloat1622float2(x); }
+
+// KV: __half, __nv_bfloat16, or uint8_t (e4m3 codes).
+template <typename KV, int D>
+__global__ void __launch_bounds__(kSumThreads)
+    summarize_kernel(const __grid_constant__ SummaryParams p)
+{
+    constexpr bool kFp8 = sizeof(KV) == 1;
+    constexpr int kRowBytes = D * (int)sizeof(KV);
+    constexpr int kLanes = kRowBytes / 16;  // lanes of a row
+    constexpr int kRows = 32 / kLanes;      // rows of a warp's load
+    constexpr int kElems = 16 / (int)sizeof(KV);  // elements of a lane
+    constexpr int kPairs = kElems / 2;
+    constexpr int kBatch = kFp8 ? 4 : 8;    // loads in flight
+    using P = typename std::conditional<std::is_same<KV, __nv_bfloat16>::value, __nv_bfloat162,
+                                        __half2>::type;
+    __shared__ int pref[kSumSeqs + 1], first[kSumSeqs], len[kSumSeqs];
+    __shared__ int warp_sum[kSumThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int bs = 1 << p.block_shift;
+    const int part = lane % kLanes, row0 = lane / kLanes;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    for (int s0 = 0; s0 < p.num_seqs; s0 += kSumSeqs) {
+        const int seqs = min(kSumSeqs, p.num_seqs - s0);
+        int carry = 0;
+        for (int c = 0; c < seqs; c += kSumThreads) {
+            const int k = c + tid;
+            int n = 0;
+            if (k < seqs) {
+                const Touched t = touched_blocks(p, s0 + k, blockIdx.x == 0);
+                first[k] = t.first;
+                len[k] = t.ctx;
+                n = t.count;
+            }
+            int x = n;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_up_sync(kFull, x, o);
+                if (lane >= o)
+                    x += y;
+            }
+            if (lane == 31)
+                warp_sum[warp] = x;
+            __syncthreads();
+            int before = carry, all = 0;
+#pragma unroll
+            for (int w = 0; w < kSumThreads / 32; ++w) {
+                before += w < warp ? warp_sum[w] : 0;
+                all += warp_sum[w];
+            }
+            if (k < seqs)
+                pref[k] = before + x - n;
+            carry += all;
+            __syncthreads();
+        }
+        if (tid == 0)
+            pref[seqs] = carry;
+        __syncthreads();
+
+        const long long items = (long long)carry * p.num_kv_heads;
+        const long long step = (long long)gridDim.x * (kSumThreads / 32);
+        for (long long i = (long long)blockIdx.x * (kSumThreads / 32) + warp; i < items;
+             i += step) {
+            const int q = (int)(i / p.num_kv_heads);
+            const int kh = (int)(i - (long long)q * p.num_kv_heads);
+            int lo_s = 0, n_s = seqs;  // the last sequence with pref <= q
+            while (n_s > 1) {
+                const int half = n_s >> 1;
+                if (pref[lo_s + half] <= q) {
+                    lo_s += half;
+                    n_s -= half;
+                } else {
+                    n_s = half;
+                }
+            }
+            const int blk = first[lo_s] + q - pref[lo_s];
+            const int phys = p.block_tables[(size_t)(s0 + lo_s) * p.max_blocks_per_seq + blk];
+            if (phys < 0 || phys >= p.num_blocks) {
+                if (lane == 0)
+                    flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
+                continue;
+            }
+            const int live = min(bs, len[lo_s] - (blk << p.block_shift));
+            const size_t pitch = (size_t)p.num_kv_heads * kRowBytes;  // token to token
+            const uint8_t *at = static_cast<const uint8_t *>(p.key_cache) +
+                                ((size_t)phys << p.block_shift) * pitch +
+                                (size_t)kh * kRowBytes + part * 16;
+            P lo[kPairs], hi[kPairs];
+            for (int r = row0; r < live + row0; r += kBatch * kRows) {
+                uint4 w[kBatch];
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u)  // (rows past the end repeat the last one)
+                    w[u] = *reinterpret_cast<const uint4 *>(
+                        at + (size_t)min(r + u * kRows, live - 1) * pitch);
+                if (r == row0) {
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        const uint32_t *x = reinterpret_cast<const uint32_t *>(&w[0]);
+                        uint32_t v;
+                        if constexpr (kFp8)
+                            v = e4m3x2_to_f16x2((uint16_t)(x[e / 2] >> (16 * (e & 1))));
+                        else
+                            v = x[e];
+                        lo[e] = hi[e] = *reinterpret_cast<const P *>(&v);
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < kBatch; ++u) {
+                    const uint32_t *x = reinterpret_cast<const uint32_t *>(&w[u]);
+#pragma unroll
+                    for (int e = 0; e < kPairs; ++e) {
+                        uint32_t v;
+                        if constexpr (kFp8)
+                            v = e4m3x2_to_f16x2((uint16_t)(x[e / 2] >> (16 * (e & 1))));
+                        else
+                            v = x[e];
+                        const P y = *reinterpret_cast<const P *>(&v);
+                        lo[e] = pair_min(lo[e], y);
+                        hi[e] = pair_max(hi[e], y);
+                    }
+                }
+            }
+            float top = 0.f;
+            bool ok = true;
+#pragma unroll
+            for (int e = 0; e < kPairs; ++e) {
+#pragma unroll
+                for (int o = kLanes; o < 32; o <<= 1) {
+                    lo[e] = pair_min(lo[e], __shfl_xor_sync(kFull, lo[e], o));
+                    hi[e] = pair_max(hi[e], __shfl_xor_sync(kFull, hi[e], o));
+                }
+                const float2 a = pair_float(lo[e]), b = pair_float(hi[e]);
+                ok &= finite(a.x) && finite(a.y) && finite(b.x) && finite(b.y);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)),
+                                       fmaxf(fabsf(b.x), fabsf(b.y))));
+            }
+            ok = __all_sync(kFull, ok);
+#pragma unroll
+            for (int o = 1; o < kLanes; o <<= 1)
+                top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            const CodeScale cs = ok ? code_scale(top) : CodeScale{0.f, INFINITY};
+            const size_t unit = (size_t)phys * p.num_kv_heads + kh;
+            if (lane == 0)
+                p.scales[unit] = cs.scale;
+            if (row0 < 2) {  // the first rows' lanes write lo, the second's hi
+                uint32_t out[kElems / 4];
+#pragma unroll
+                for (int e = 0; e < kPairs; e += 2) {
+                    const float2 a0 = pair_float(lo[e]), a1 = pair_float(hi[e]);
+                    const float2 b0 = pair_float(lo[e + 1]), b1 = pair_float(hi[e + 1]);
+                    const float v[4] = {row0 ? a1.x : a0.x, row0 ? a1.y : a0.y,
+                                        row0 ? b1.x : b0.x, row0 ? b1.y : b0.y};
+                    uint32_t bytes = 0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int code = ok ? __float2int_rn(__fmul_rn(v[j], cs.inv)) : 0;
+                        bytes |= ((uint32_t)code & 0xffu) << (8 * j);
+                    }
+                    out[e / 2] = bytes;
+                }
+                int8_t *dst = p.codes + (unit * 2 + row0) * D + part * kElems;
+                if constexpr (kFp8)
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(out[0], out[1], out[2], out[3]);
+                else
+                    *reinterpret_cast<uint2 *>(dst) = make_uint2(out[0], out[1]);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// ---- selection ------------------------------------------------------------------
+//
+// One CTA, or a cluster of them, per (row, KV head).  What bounds it: HBM where
+// contexts are long (2 d + 4 bytes a block), else the chain of dependent loads and
+// barriers.  The score product runs on the tensor cores as blocks x heads: a warp
+// takes 16 blocks, whose codes a lane loads 16 bytes at a time straight into the
+// order that the product needs (the sum over d is taken in a permuted order, which
+// whole numbers allow), widens to fp16 (exact) and multiplies with the coded heads,
+// which stay in registers.  fp16 products of codes are exact, and so are their sums
+// in fp32.  Keys that order the scores go to the first CTA's shared memory, where
+// the smallest selected key is found digit by digit, over the bits in which the
+// keys differ at all.
+struct SelectParams {
+    int32_t *selected;  // [T][Hkv][top_k]
+    const void *query;
+    const int8_t *codes;
+    const float *scales;
+    const int32_t *block_tables;
+    const int32_t *token_seq, *token_pos;
+    int32_t *error_word;
+    int max_blocks_per_seq, num_seqs, num_blocks, block_shift, max_context_len;
+    int num_heads, num_kv_heads, group, top_k, num_first, num_last;
+};
+
+constexpr int kSelThreads = 256;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 256;
+
+// Keys in the scores' order.
+__device__ __forceinline__ uint32_t score_key(float x)
+{
+    const uint32_t u = __float_as_uint(x);
+    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+
+// Four signed bytes to two fp16 pairs: u = code + 128 below fp16 1024 + u, less 1152.
+__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t &a, uint32_t &b)
+{
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
+    uint32_t x = byte_perm(u, 0x64646464u, 0x4140u), y = byte_perm(u, 0x64646464u, 0x4342u);
+    const __half2 hx = __hsub2(*reinterpret_cast<__half2 *>(&x), bias);
+    const __half2 hy = __hsub2(*reinterpret_cast<__half2 *>(&y), bias);
+    a = *reinterpret_cast<const uint32_t *>(&hx);
+    b = *reinterpret_cast<const uint32_t *>(&hy);
+}
+
+struct SelectShared {
+    float q_scale[16];
+    int hist[kSelBins];
+    uint32_t lo[kSelWarps], hi[kSelWarps];
+    int above[kSelWarps], ties[kSelWarps];
+    int bin, rest, last_bin;
+};
+
+// T: the query's type; NT: heads of a KV head in eights.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kSelThreads)
+    select_kernel(const __grid_constant__ SelectParams p)
+{
+    constexpr int kSegs = 2 * D / 64;  // 64-byte runs of a block's codes
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    __shared__ SelectShared sh;
+    __shared__ __align__(16) __half qs[8 * NT][2 * D];
+    extern __shared__ uint32_t keys[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, t4 = lane & 3;
+    const int unit = (int)blockIdx.x / ctas;
+    const int t = unit / p.num_kv_heads, kh = unit - t * p.num_kv_heads;
+    const int G = p.group, top_k = p.top_k;
+    if (ctas > 1)
+        cluster.sync();  // the first CTA's shared memory is there to be written
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    // ---- the row's context ----------------------------------------------------------
+    const int s = p.token_seq[t], pos = p.token_pos[t];
+    const bool whole = rank == 0 && tid == 0 && kh == 0;  // reports for the row
+    int ctx = 0;
+    if (s >= 0) {
+        const long long cap = (long long)p.max_blocks_per_seq << p.block_shift;
+        if (s >= p.num_seqs || pos < 0 || pos >= cap) {
+            if (whole)
+                flag_error(p.error_word, PA_DEVERR_TOKEN_RANGE);
+        } else {
+            if (pos >= p.max_context_len && whole)
+                flag_error(p.error_word, PA_DEVERR_CONTEXT_RANGE);
+            ctx = min(pos, p.max_context_len - 1) + 1;
+        }
+    }
+    const int nb = (int)(((long long)ctx + (1 << p.block_shift) - 1) >> p.block_shift);
+    int32_t *out = p.selected + (size_t)unit * top_k;
+    if (nb <= top_k) {
+        if (rank == 0)
+            for (int i = tid; i < top_k; i += kSelThreads)
+                out[i] = i < nb ? i : -1;
+        return;
+    }
+    const int first = p.num_first, tail = nb - p.num_last;
+    const int want = top_k - p.num_first - p.num_last;
+    const int n = tail - first;  // candidates, more than are wanted
+
+    // ---- the query heads' codes ------------------------------------------------------
+    for (int h = warp; h < 8 * NT; h += kSelWarps) {
+        float x[D / 32];
+        float top = 0.f;
+        bool ok = true;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            const T *row = static_cast<const T *>(p.query) +
+                           ((size_t)t * p.num_heads + (size_t)kh * G + (h < G ? h : 0)) * D;
+            x[e] = h < G ? (float)row[e * 32 + lane] : 0.f;
+            ok &= finite(x[e]);
+            top = fmaxf(top, fabsf(x[e]));
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+        ok = __all_sync(kFull, ok);
+        const CodeScale cs = ok ? code_scale(top) : CodeScale{0.f, 0.f};
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e) {
+            const int code = ok ? __float2int_rn(__fmul_rn(x[e], cs.inv)) : 0;
+            qs[h][e * 32 + lane] = __int2half_rn(min(code, 0));
+            qs[h][D + e * 32 + lane] = __int2half_rn(max(code, 0));
+        }
+        if (lane == 0)
+            sh.q_scale[h] = cs.scale;
+    }
+    __syncthreads();
+    // B fragments: head 8 nt + g; product step (seg, j) of lane t4 stands for codes
+    // 64 seg + 16 t4 + 4 j .. + 3 of the block's 2 D
+    uint32_t qf[NT][kSegs][4][2];
+    float q_scale[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int sg = 0; sg < kSegs; ++sg)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(
+                    &qs[nt * 8 + g][sg * 64 + t4 * 16 + j * 4]);
+                qf[nt][sg][j][0] = w.x;
+                qf[nt][sg][j][1] = w.y;
+            }
+        q_scale[nt][0] = sh.q_scale[nt * 8 + 2 * t4];
+        q_scale[nt][1] = sh.q_scale[nt * 8 + 2 * t4 + 1];
+    }
+
+    // ---- scores, 16 blocks a warp ----------------------------------------------------
+    uint32_t *dst = ctas > 1 ? cluster.map_shared_rank(keys, 0) : keys;
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq + first;
+    const int tiles = (n + 15) / 16;
+    for (int tile = rank * kSelWarps + warp; tile < tiles; tile += ctas * kSelWarps) {
+        uint4 w[2][kSegs];
+        float scale[2];
+        bool ok[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int i = tile * 16 + g + 8 * r;
+            int phys = i < n ? __ldg(table + i) : 0;
+            ok[r] = phys >= 0 && phys < p.num_blocks;
+            if (!ok[r] && t4 == 0)
+                flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
+            phys = ok[r] ? phys : 0;
+            const size_t at = (size_t)phys * p.num_kv_heads + kh;
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.codes + at * 2 * D) + t4;
+#pragma unroll
+            for (int sg = 0; sg < kSegs; ++sg)
+                w[r][sg] = __ldg(src + sg * 4);
+            scale[r] = __ldg(p.scales + at);
+        }
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+            acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+#pragma unroll
+        for (int sg = 0; sg < kSegs; ++sg) {
+            const uint32_t x[4] = {w[0][sg].x, w[0][sg].y, w[0][sg].z, w[0][sg].w};
+            const uint32_t y[4] = {w[1][sg].x, w[1][sg].y, w[1][sg].z, w[1][sg].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a[4];
+                widen_codes(x[j], a[0], a[2]);
+                widen_codes(y[j], a[1], a[3]);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    MmaOp<__half>::run(acc[nt], a, qf[nt][sg][j][0], qf[nt][sg][j][1]);
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float best = -INFINITY;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    if (nt * 8 + 2 * t4 + e < G)
+                        best = fmaxf(best, __fmul_rn(acc[nt][2 * r + e], q_scale[nt][e]));
+            best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
+            best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
+            const int i = tile * 16 + g + 8 * r;
+            if (t4 == 0 && i < n) {
+                const float x = __float_as_uint(scale[r]) == 0x7f800000u
+                                    ? scale[r] : __fmul_rn(best, scale[r]);
+                dst[i] = ok[r] ? score_key(x) : 0u;
+            }
+        }
+    }
+    if (ctas > 1)
+        cluster.sync();
+    else
+        __syncthreads();
+    if (rank != 0)
+        return;
+
+    // ---- the smallest selected key, digit by digit -----------------------------------
+    uint32_t lo = 0xffffffffu, hi = 0u;
+    for (int i = tid; i < n; i += kSelThreads) {
+        lo = min(lo, keys[i]);
+        hi = max(hi, keys[i]);
+    }
+    lo = __reduce_min_sync(kFull, lo);
+    hi = __reduce_max_sync(kFull, hi);
+    if (lane == 0) {
+        sh.lo[warp] = lo;
+        sh.hi[warp] = hi;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kSelWarps; ++w) {
+        lo = min(lo, sh.lo[w]);
+        hi = max(hi, sh.hi[w]);
+    }
+    // keys less lo have `bits` bits; those at or above `from` << shift are looked at
+    // further while more of them are wanted than of the digits above
+    int shift = 32 - __clz((int)(hi - lo));
+    uint32_t prefix = 0;  // of the keys still looked at
+    int rest = want;      // of them, how many are selected
+    while (shift > 0 && rest > 0) {
+        const int width = min(8, shift);
+        shift -= width;
+        for (int b = tid; b < kSelBins; b += kSelThreads)
+            sh.hist[b] = 0;
+        __syncthreads();
+        for (int i = tid; i < n; i += kSelThreads) {
+            const uint32_t v = keys[i] - lo;
+            if (((unsigned long long)v >> (shift + width)) == prefix)
+                atomicAdd(&sh.hist[(v >> shift) & ((1u << width) - 1)], 1);
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // lane l has bins 8 l .. 8 l + 7; counts from the top bin down
+            int own[8], sum = 0;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                own[b] = sh.hist[lane * 8 + b];
+                sum += own[b];
+            }
+            int above = sum;  // of this lane's bins and those of higher lanes
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int y = __shfl_down_sync(kFull, above, o);
+                if (lane + o < 32)
+                    above += y;
+            }
+            int over = above - sum;  // of higher lanes' bins
+#pragma unroll
+            for (int b = 7; b >= 0; --b) {
+                if (over < rest && over + own[b] >= rest) {
+                    sh.bin = lane * 8 + b;
+                    sh.rest = rest - over;
+                    sh.last_bin = own[b] == rest - over;
+                }
+                over += own[b];
+            }
+        }
+        __syncthreads();
+        prefix = (prefix << width) | (uint32_t)sh.bin;
+        rest = sh.rest;
+        const bool all = sh.last_bin != 0;  // the whole bin is selected
+        __syncthreads();
+        if (all)
+            break;
+    }
+    // selected: key digits above the prefix, and the first `rest` at it
+    // ---- the list, in ascending order ------------------------------------------------
+    const int run = (n + kSelThreads - 1) / kSelThreads * 32;  // candidates of a warp
+    const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
+    int above = 0, ties = 0;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const uint32_t v = (uint32_t)((unsigned long long)(keys[i] - lo) >> shift);
+        above += v > prefix;
+        ties += v == prefix;
+    }
+    above = __reduce_add_sync(kFull, above);
+    ties = __reduce_add_sync(kFull, ties);
+    if (lane == 0) {
+        sh.above[warp] = above;
+        sh.ties[warp] = ties;
+    }
+    __syncthreads();
+    above = ties = 0;
+    for (int w = 0; w < warp; ++w) {
+        above += sh.above[w];
+        ties += sh.ties[w];
+    }
+    for (int b = i0; b < i1; b += 32) {
+        const int i = b + lane;
+        const uint32_t v = i < i1 ? (uint32_t)((unsigned long long)(keys[i] - lo) >> shift) : 0u;
+        const bool over = i < i1 && v > prefix, tie = i < i1 && v == prefix;
+        const uint32_t over_m = __ballot_sync(kFull, over), tie_m = __ballot_sync(kFull, tie);
+        const uint32_t below = (1u << lane) - 1;
+        const int my_ties = ties + __popc(tie_m & below);
+        if (over || (tie && my_ties < rest))
+            out[first + above + __popc(over_m & below) + min(my_ties, rest)] = first + i;
+        above += __popc(over_m);
+        ties += __popc(tie_m);
+    }
+    for (int i = tid; i < first; i += kSelThreads)
+        out[i] = i;
+    for (int i = tid; i < p.num_last; i += kSelThreads)
+        out[top_k - p.num_last + i] = tail + i;
+}
+
+// ---- host side -------------------------------------------------------------------
+
+static bool pool_block(int block_size, int head_dim)
+{
+    return (head_dim == 64 || head_dim == 128) && block_size >= kTileTokens &&
+           block_size <= 256 && (block_size & (block_size - 1)) == 0;
+}
+
+static pa_status current_device(int *dev, DeviceInfo *info)
+{
+    const cudaError_t e = cudaGetDevice(dev);
+    return e != cudaSuccess ? record_cuda(e) : device_info(*dev, info);
+}
+
+template <typename KV>
+static pa_status launch_summary(const SummaryParams &p, int head_dim, int sms,
+                                cudaStream_t stream)
+{
+    // CTAs that the device holds at once, or a warp for every block that there can be
+    const long long most = (long long)p.num_seqs * p.max_blocks_per_seq * p.num_kv_heads;
+    const long long warps = kSumThreads / 32;
+    const int grid = (int)std::min<long long>(8ll * sms, (most + warps - 1) / warps);
+    return head_dim == 128
+               ? launch_pdl(summarize_kernel<KV, 128>, dim3(grid), dim3(kSumThreads), 0, stream, p)
+               : launch_pdl(summarize_kernel<KV, 64>, dim3(grid), dim3(kSumThreads), 0, stream, p);
+}
+
+template <typename T, int D, int NT>
+static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream_t stream)
+{
+    auto kernel = select_kernel<T, D, NT>;
+    static size_t enabled[kMaxDevices];
+    static std::mutex mu;
+    int dev = 0;
+    DeviceInfo info;
+    const pa_status st = current_device(&dev, &info);
+    if (st != PA_OK)
+        return st;
+    const int bs = 1 << p.block_shift;
+    const int most = std::min<long long>(p.max_blocks_per_seq,
+                                         ((long long)p.max_context_len + bs - 1) / bs);
+    const size_t smem = std::max<size_t>(16, (size_t)most * 4);
+    if (smem + sizeof(SelectShared) + sizeof(__half) * 16 * NT * D + 1024 > (size_t)info.optin)
+        return PA_ERR_UNSUPPORTED;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (smem > enabled[dev]) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess)
+                return record_cuda(e);
+            enabled[dev] = smem;
+        }
+    }
+    const long long units = (long long)num_tokens * p.num_kv_heads;
+    int ctas = 1;
+    while (ctas < 8 && units * ctas * 2 <= 2 * info.sms && most >= 256 * ctas)
+        ctas *= 2;
+    if (units * ctas > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(units * ctas));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = ctas;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return record_cuda(cudaLaunchKernelEx(&cfg, kernel, p));
+}
+
+template <typename T>
+static pa_status select_as(const SelectParams &p, int head_dim, int num_tokens,
+                           cudaStream_t stream)
+{
+    const bool wide = p.group > 8;
+    if (head_dim == 128)
+        return wide ? launch_select<T, 128, 2>(p, num_tokens, stream)
+                    : launch_select<T, 128, 1>(p, num_tokens, stream);
+    return wide ? launch_select<T, 64, 2>(p, num_tokens, stream)
+                : launch_select<T, 64, 1>(p, num_tokens, stream);
+}
+
+} // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_summarize_blocks(int8_t *summaries, float *summary_scales,
+                                         const void *key_cache, const int32_t *block_tables,
+                                         int max_blocks_per_seq, const int32_t *context_lens,
+                                         const int32_t *query_start, int num_seqs,
+                                         int num_blocks, int block_size, int num_kv_heads,
+                                         int head_dim, pa_dtype dtype, int32_t *error_word,
+                                         void *stream)
+{
+    if (num_seqs < 0 || num_blocks <= 0 || block_size <= 0 || max_blocks_per_seq <= 0 ||
+        num_kv_heads <= 0 || head_dim <= 0 ||
+        (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_FP8_E4M3))
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs == 0)
+        return PA_OK;
+    if (!summaries || !summary_scales || !key_cache || !block_tables || !context_lens ||
+        !aligned16(summaries) || !aligned16(key_cache))
+        return PA_ERR_INVALID_ARG;
+    if (!pool_block(block_size, head_dim) || (long long)num_blocks * block_size >= (1ll << 31) ||
+        (long long)num_seqs * max_blocks_per_seq >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
+    SummaryParams p{};
+    p.codes = summaries;
+    p.scales = summary_scales;
+    p.key_cache = key_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.query_start = query_start;
+    p.error_word = error_word;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.num_blocks = num_blocks;
+    p.block_shift = __builtin_ctz((unsigned)block_size);
+    p.num_kv_heads = num_kv_heads;
+    int dev = 0;
+    DeviceInfo info;
+    const pa_status st = current_device(&dev, &info);
+    if (st != PA_OK)
+        return st;
+    cudaStream_t q = as_stream(stream);
+    return dtype == PA_FP8_E4M3 ? launch_summary<uint8_t>(p, head_dim, info.sms, q)
+           : dtype == PA_BF16   ? launch_summary<__nv_bfloat16>(p, head_dim, info.sms, q)
+                                : launch_summary<__half>(p, head_dim, info.sms, q);
+}
+
+extern "C" pa_status pa_select_blocks(int32_t *selected, int top_k, const void *query,
+                                      const int8_t *summaries, const float *summary_scales,
+                                      const int32_t *block_tables, int max_blocks_per_seq,
+                                      const int32_t *token_seq, const int32_t *token_pos,
+                                      int max_context_len, int num_first, int num_last,
+                                      int num_tokens, int num_seqs, int num_heads,
+                                      int num_kv_heads, int head_dim, int block_size,
+                                      int num_blocks, pa_dtype dtype, int32_t *error_word,
+                                      void *stream)
+{
+    if (num_tokens < 0 || num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 ||
+        head_dim <= 0 || block_size <= 0 || num_blocks <= 0 || max_blocks_per_seq <= 0 ||
+        max_context_len < 0 || top_k <= 0 || num_first < 0 || num_last < 0 ||
+        num_first > top_k || num_last > top_k - num_first ||
+        (dtype != PA_F16 && dtype != PA_BF16) || num_heads % num_kv_heads != 0)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0)
+        return PA_OK;
+    if (!selected || !query || !summaries || !summary_scales || !block_tables || !token_seq ||
+        !token_pos || !aligned16(query) || !aligned16(summaries))
+        return PA_ERR_INVALID_ARG;
+    if (!pool_block(block_size, head_dim) || num_heads / num_kv_heads > 16 ||
+        (long long)num_blocks * block_size >= (1ll << 31) ||
+        (long long)max_blocks_per_seq * block_size >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
+    SelectParams p{};
+    p.selected = selected;
+    p.query = query;
+    p.codes = summaries;
+    p.scales = summary_scales;
+    p.block_tables = block_tables;
+    p.token_seq = token_seq;
+    p.token_pos = token_pos;
+    p.error_word = error_word;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.num_blocks = num_blocks;
+    p.block_shift = __builtin_ctz((unsigned)block_size);
+    p.max_context_len = max_context_len;
+    p.num_heads = num_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.group = num_heads / num_kv_heads;
+    p.top_k = top_k;
+    p.num_first = num_first;
+    p.num_last = num_last;
+    return dtype == PA_BF16
+               ? select_as<__nv_bfloat16>(p, head_dim, num_tokens, as_stream(stream))
+               : select_as<__half>(p, head_dim, num_tokens, as_stream(stream));
+}

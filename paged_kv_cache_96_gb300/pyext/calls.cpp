@@ -46,6 +46,8 @@ struct Library {
     decltype(&pa_decode_attention_window_fp8) decode_fp8;
     decltype(&pa_prefill_attention_window) prefill;
     decltype(&pa_prefill_attention_window_fp8) prefill_fp8;
+    decltype(&pa_summarize_blocks) summarize;
+    decltype(&pa_select_blocks) select;
 };
 Library lib;
 
@@ -424,6 +426,89 @@ pa_status prefill_window(PyObject *const *a)
                        x.dim, x.block_size, x.num_blocks, scale, x.dtype, err, stream);
 }
 
+// The 8-bit bounds [num_blocks, num_kv_heads, 2, head_dim] of a pool's blocks.
+struct Summaries {
+    int8_t *codes;
+    float *scales;
+    int num_blocks, kv_heads, dim;
+};
+
+Summaries summaries(PyObject *codes, PyObject *scales, int dev)
+{
+    const at::Tensor &c = tensor(codes, "summaries"), &s = tensor(scales, "summary_scales");
+    dimensions(c, "summaries", 4);
+    dimensions(s, "summary_scales", 2);
+    need(c.size(2) == 2 && s.size(0) == c.size(0) && s.size(1) == c.size(1),
+         "summaries [num_blocks, num_kv_heads, 2, head_dim] and one scale per block and KV head "
+         "expected");
+    return {static_cast<int8_t *>(address(c, "summaries", at::kChar, dev)),
+            static_cast<float *>(address(s, "summary_scales", at::kFloat, dev)),
+            size_int(c.size(0), "summaries"), size_int(c.size(1), "summaries"),
+            size_int(c.size(3), "summaries")};
+}
+
+pa_status summarize(PyObject *const *a)
+{
+    const at::Tensor &kc = tensor(a[2], "key_cache"), &tables = tensor(a[3], "block_tables"),
+                     &ctx = tensor(a[4], "context_lens");
+    dimensions(kc, "key_cache", 4);
+    dimensions(tables, "block_tables", 2);
+    dimensions(ctx, "context_lens", 1);
+    const int64_t S = ctx.size(0);
+    const int dev = device_of(kc, "key_cache");
+    const pa_dtype dtype = kc.scalar_type() == at::kByte ? PA_FP8_E4M3 : dtype_of(kc, "key_cache");
+    const Summaries x = summaries(a[0], a[1], dev);
+    need(tables.size(0) == S && kc.size(0) == x.num_blocks && kc.size(2) == x.kv_heads &&
+             kc.size(3) == x.dim,
+         "shape mismatch between summaries, pool and tables");
+    const int32_t *start = nullptr;
+    if (a[5] != Py_None) {
+        const at::Tensor &q = tensor(a[5], "query_start");
+        need(q.dim() == 1 && q.size(0) == S + 1, "query_start: num_seqs + 1 offsets expected");
+        start = ints(q, "query_start", dev);
+    }
+    const void *pool = address(kc, "key_cache", kc.scalar_type(), dev);
+    const int32_t *pt = ints(tables, "block_tables", dev), *pc = ints(ctx, "context_lens", dev);
+    const int mb = size_int(tables.size(1), "block_tables"), seqs = size_int(S, "context_lens"),
+              bs = size_int(kc.size(1), "key_cache");
+    int32_t *err = optional_ints(a[6], "error_word", dev);
+    void *stream = queue(a[7], dev);
+    const Unlocked unlocked;
+    return lib.summarize(x.codes, x.scales, pool, pt, mb, pc, start, seqs, x.num_blocks, bs,
+                         x.kv_heads, x.dim, dtype, err, stream);
+}
+
+pa_status select_blocks(PyObject *const *a)
+{
+    const at::Tensor &sel = tensor(a[0], "selected"), &q = tensor(a[1], "query"),
+                     &tables = tensor(a[4], "block_tables"), &seq = tensor(a[5], "token_seq"),
+                     &pos = tensor(a[6], "token_pos");
+    dimensions(sel, "selected", 3);
+    dimensions(q, "query", 3);
+    dimensions(tables, "block_tables", 2);
+    const int64_t T = q.size(0);
+    const int dev = device_of(q, "query");
+    const pa_dtype dtype = dtype_of(q, "query");
+    const Summaries x = summaries(a[2], a[3], dev);
+    need(q.size(2) == x.dim && sel.size(0) == T && sel.size(1) == x.kv_heads &&
+             seq.dim() == 1 && seq.size(0) == T && pos.dim() == 1 && pos.size(0) == T,
+         "shape mismatch between query, selected, summaries and tokens");
+    const void *pq = address(q, "query", q.scalar_type(), dev);
+    int32_t *ps = ints(sel, "selected", dev);
+    const int32_t *pt = ints(tables, "block_tables", dev), *pn = ints(seq, "token_seq", dev),
+                  *pp = ints(pos, "token_pos", dev);
+    const int max_ctx = to_int(a[7], "max_context_len"), bs = to_int(a[8], "block_size"),
+              first = to_int(a[9], "num_first"), last = to_int(a[10], "num_last");
+    const int top_k = size_int(sel.size(2), "selected"), mb = size_int(tables.size(1), "block_tables"),
+              rows = size_int(T, "query"), seqs = size_int(tables.size(0), "block_tables"),
+              heads = size_int(q.size(1), "query");
+    int32_t *err = optional_ints(a[11], "error_word", dev);
+    void *stream = queue(a[12], dev);
+    const Unlocked unlocked;
+    return lib.select(ps, top_k, pq, x.codes, x.scales, pt, mb, pn, pp, max_ctx, first, last, rows,
+                      seqs, heads, x.kv_heads, x.dim, bs, x.num_blocks, dtype, err, stream);
+}
+
 template <pa_status (*call)(PyObject *const *), int count>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -458,6 +543,8 @@ PyObject *bind(PyObject *, PyObject *path)
         find(h, "pa_decode_attention_window_fp8", found.decode_fp8);
         find(h, "pa_prefill_attention_window", found.prefill);
         find(h, "pa_prefill_attention_window_fp8", found.prefill_fp8);
+        find(h, "pa_summarize_blocks", found.summarize);
+        find(h, "pa_select_blocks", found.select);
         lib = found;
         Py_RETURN_NONE;
     } catch (const PythonError &) {
@@ -474,6 +561,8 @@ PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
                          PA_ENTRY(rope, 15),
                          PA_ENTRY(decode_window, 16),
                          PA_ENTRY(prefill_window, 15),
+                         PA_ENTRY(summarize, 8),
+                         PA_ENTRY(select_blocks, 13),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,

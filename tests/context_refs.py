@@ -1,0 +1,85 @@
+"""Plain definitions of the operators that read or keep a long context in part, one
+block and one token at a time.  Nothing here uses the library.
+
+Bounds and scores are whole numbers and single fp32 operations, so they are computed
+exactly and compared for equality."""
+import numpy as np
+import torch
+
+F = np.float32
+
+
+def values(pool):
+    """Keys as the values their codes stand for, without a pool's scale."""
+    if pool.dtype == torch.uint8:
+        pool = pool.cpu().view(torch.float8_e4m3fn)
+    return pool.float().cpu().numpy()
+
+
+def code(x):
+    """(int codes, fp32 scale) of one vector set with a common amplitude."""
+    with np.errstate(invalid="ignore", over="ignore"):
+        top = np.abs(x).max() if x.size else F(0)
+    if not np.isfinite(x).all():
+        return np.zeros(x.shape, dtype=np.int64), F(np.inf)
+    if top < F(2.0 ** -40):
+        return np.zeros(x.shape, dtype=np.int64), F(0)
+    inv = F(127) / F(top)
+    return np.rint(x.astype(F) * inv).astype(np.int64), F(top) * (F(1) / F(127))
+
+
+def summarize(codes, scales, keys, tables, ctx, start=None):
+    """codes int8 [N, K, 2, D] and scales [N, K] (numpy, changed in place)."""
+    bs = keys.shape[1]
+    for s, c in enumerate(ctx):
+        n = c if start is None else start[s + 1] - start[s]
+        for j in range((c - n) // bs, -(-c // bs)) if n > 0 else ():
+            b = tables[s][j]
+            for h in range(keys.shape[2]):
+                k = keys[b, :min(bs, c - j * bs), h]
+                bad = not np.isfinite(k).all()
+                lo_hi = np.stack([k.min(0), k.max(0)]) if not bad else np.full((2, k.shape[1]),
+                                                                              np.nan)
+                codes[b, h], scales[b, h] = code(lo_hi)
+
+
+def scores(query, codes, scales, table, have, kh, group):
+    """fp32 scores of the `have` blocks of a table row for one KV head."""
+    out = np.zeros(have, dtype=F)
+    q = [code(query[h].astype(F)) for h in range(kh * group, (kh + 1) * group)]
+    for j in range(have):
+        b = table[j]
+        if np.isposinf(scales[b, kh]):
+            out[j] = np.inf
+            continue
+        best = None
+        for c, s in q:
+            s = F(0) if np.isinf(s) else s
+            total = np.maximum(c * codes[b, kh, 0].astype(np.int64),
+                               c * codes[b, kh, 1].astype(np.int64)).sum()
+            with np.errstate(over="ignore"):
+                x = F(s) * F(total)
+            best = x if best is None else max(best, x)
+        with np.errstate(over="ignore"):
+            out[j] = best * F(scales[b, kh])
+    return out
+
+
+def select(query, codes, scales, tables, seq, pos, bs, top_k, first, last, kv_heads):
+    """int32 [T, K, top_k]; query a float numpy array [T, H, D]."""
+    T, H, _ = query.shape
+    out = np.full((T, kv_heads, top_k), -1, dtype=np.int32)
+    for t in range(T):
+        if seq[t] < 0:
+            continue
+        have = pos[t] // bs + 1
+        for h in range(kv_heads):
+            if have <= top_k:
+                out[t, h, :have] = np.arange(have)
+                continue
+            x = scores(query[t], codes, scales, tables[seq[t]], have, h, H // kv_heads)
+            mid = np.arange(first, have - last)
+            best = mid[np.lexsort((mid, -x[mid].astype(np.float64)))][:top_k - first - last]
+            out[t, h] = np.sort(np.concatenate([np.arange(first), best,
+                                                np.arange(have - last, have)]))
+    return out
