@@ -627,6 +627,95 @@ PA_API pa_status pa_select_blocks(int32_t *selected, int top_k, const void *quer
                                   void *stream);
 
 /*
+ * pa_decode_attention_sparse, pa_decode_attention_sparse_fp8 -- paged attention of
+ * single query rows over a list of blocks for each row and KV head:
+ *     out[t][h][:] = sum_p softmax(scale * q[t][h] . K[p][kh])_p V[p][kh][:]
+ * over the positions p <= token_pos[t] of sequence token_seq[t] that are in one of
+ * the blocks selected[t][kh][0 .. n), n = min(top_k, blocks of the row's context);
+ * negative entries are left out, a block that is listed twice counts twice, and the
+ * order has no influence but on rounding.  A row that sees nothing (padding, an empty
+ * list) is zero.
+ *   token_seq, token_pos, selected : as pa_select_blocks takes and gives them; an
+ *                    entry past the row's own block is left out and sets
+ *                    PA_DEVERR_CONTEXT_RANGE
+ *   partition_size : as pa_decode_attention, in tokens of the list (top_k * block_size
+ *                    of them at most); a remainder of less than half a partition joins
+ *                    the one before, and partitions are longer where fewer of them fill
+ *                    the GPU
+ *   workspace      : >= pa_sparse_workspace_bytes(...) bytes, 256-byte aligned, its
+ *                    first bytes (the arrival counters of pa_decode_workspace_bytes, the
+ *                    same region) zeroed before first use; may be NULL when that size
+ *                    is 0
+ * scale * k_scale * log2(e) has to be finite in fp32 (PA_ERR_INVALID_ARG); num_tokens *
+ * num_kv_heads times the partitions of a list <= 2^30 and max_blocks_per_seq * block_size
+ * <= 2^31 - 256 (PA_ERR_UNSUPPORTED otherwise).  Other arguments, limits and errors as
+ * pa_decode_attention(_fp8); PA_DEVERR_TOKEN_RANGE as pa_select_blocks.
+ */
+PA_API size_t pa_sparse_workspace_bytes(int num_tokens, int num_heads, int num_kv_heads,
+                                        int head_dim, int top_k, int block_size,
+                                        int partition_size);
+
+PA_API pa_status pa_decode_attention_sparse(
+    void *out, const void *query, const void *key_cache, const void *value_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *token_seq,
+    const int32_t *token_pos, const int32_t *selected, int top_k, int num_tokens, int num_seqs,
+    int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    int partition_size, void *workspace, size_t workspace_bytes, pa_dtype dtype,
+    int32_t *error_word, void *stream);
+
+PA_API pa_status pa_decode_attention_sparse_fp8(
+    void *out, const void *query, const void *key_cache, const void *value_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *token_seq,
+    const int32_t *token_pos, const int32_t *selected, int top_k, int num_tokens, int num_seqs,
+    int num_heads, int num_kv_heads, int head_dim, int block_size, int num_blocks, float scale,
+    float k_scale, float v_scale, int partition_size, void *workspace, size_t workspace_bytes,
+    pa_dtype dtype, int32_t *error_word, void *stream);
+
+/*
+ * pa_decode_attention_weights, pa_decode_attention_weights_fp8 -- decode attention
+ * (out, query and the cache as pa_decode_attention(_fp8)) that also adds up what each
+ * cached token is attended with, from which pa_plan_eviction chooses:  for every
+ * position p of sequence s, at its slot (block block_tables[s][p / block_size], row
+ * p % block_size),
+ *     weights_out[slot] = (p < weighted_lens[s] ? weights[slot] : 0)
+ *                         + sum over all query heads h of softmax(score[s][h])_p
+ * in fp32, in one order: the same call again gives the same bits.
+ *   weights, weights_out : float [num_blocks][block_size], which may be the same
+ *                    array; slots of no position of the batch are left as they were.
+ *                    A block in several sequences' contexts is undefined.
+ *   weighted_lens  : int32 [num_seqs]: positions whose weights hold earlier steps'
+ *                    sums (the context before the step's token; 0 for a context that
+ *                    no such step has attended yet)
+ *   workspace      : >= pa_weights_workspace_bytes(...) bytes (the scores of every
+ *                    head and position among them), 256-byte aligned, its first bytes
+ *                    zeroed before first use as pa_decode_attention's
+ *   partition_size : as pa_decode_attention; a remainder of less than half a
+ *                    partition joins the one before
+ * num_heads <= 4,096, and the limits of pa_decode_attention_sparse.  Other arguments
+ * and errors as pa_decode_attention(_fp8).
+ */
+PA_API size_t pa_weights_workspace_bytes(int num_seqs, int num_heads, int num_kv_heads,
+                                         int head_dim, int max_context_len,
+                                         int partition_size);
+
+PA_API pa_status pa_decode_attention_weights(
+    void *out, float *weights_out, const void *query, const void *key_cache,
+    const void *value_cache, const float *weights, const int32_t *block_tables,
+    int max_blocks_per_seq, const int32_t *context_lens, const int32_t *weighted_lens,
+    int max_context_len, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, int partition_size, void *workspace,
+    size_t workspace_bytes, pa_dtype dtype, int32_t *error_word, void *stream);
+
+PA_API pa_status pa_decode_attention_weights_fp8(
+    void *out, float *weights_out, const void *query, const void *key_cache,
+    const void *value_cache, const float *weights, const int32_t *block_tables,
+    int max_blocks_per_seq, const int32_t *context_lens, const int32_t *weighted_lens,
+    int max_context_len, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+    int block_size, int num_blocks, float scale, float k_scale, float v_scale,
+    int partition_size, void *workspace, size_t workspace_bytes, pa_dtype dtype,
+    int32_t *error_word, void *stream);
+
+/*
  * Prefix plan -- which sequences of a decode batch share leading physical
  * blocks ([FEI] "共享前缀的 Block 复用": block tables that name the same
  * physical blocks for a common prefix, the blocks' reference counts > 1).

@@ -112,6 +112,18 @@ def _load() -> ctypes.CDLL:
         "pa_summarize_blocks": (i32, [P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32, P, P]),
         "pa_select_blocks": (i32, [P, i32, P, P, P, P, i32, P, P, i32, i32, i32, i32, i32, i32,
                                    i32, i32, i32, i32, i32, P, P]),
+        "pa_sparse_workspace_bytes": (sz, [i32] * 7),
+        "pa_decode_attention_sparse": (i32, [P, P, P, P, P, i32, P, P, P, i32, i32, i32, i32, i32,
+                                             i32, i32, i32, f32, i32, P, sz, i32, P, P]),
+        "pa_decode_attention_sparse_fp8": (i32, [P, P, P, P, P, i32, P, P, P, i32, i32, i32, i32,
+                                                 i32, i32, i32, i32, f32, f32, f32, i32, P, sz,
+                                                 i32, P, P]),
+        "pa_weights_workspace_bytes": (sz, [i32] * 6),
+        "pa_decode_attention_weights": (i32, [P, P, P, P, P, P, P, i32, P, P, i32, i32, i32, i32,
+                                              i32, i32, i32, f32, i32, P, sz, i32, P, P]),
+        "pa_decode_attention_weights_fp8": (i32, [P, P, P, P, P, P, P, i32, P, P, i32, i32, i32,
+                                                  i32, i32, i32, i32, f32, f32, f32, i32, P, sz,
+                                                  i32, P, P]),
         "pa_prefix_plan_ints": (sz, [i32, i32, i32]),
         "pa_plan_prefix_groups": (i32, [P, i32, P, i32, i32, i32, P, sz, P, P]),
         "pa_cascade_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
@@ -643,6 +655,59 @@ def pa_select_blocks(selected: torch.Tensor, query: torch.Tensor, summaries: tor
                            error_word, stream)
     if status:
         raise PAError("pa_select_blocks", status)
+
+
+def pa_sparse_workspace_bytes(num_tokens: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                              top_k: int, block_size: int, partition_size: int) -> int:
+    return int(_lib.pa_sparse_workspace_bytes(num_tokens, num_heads, num_kv_heads, head_dim,
+                                              top_k, block_size, partition_size))
+
+
+def pa_decode_attention_sparse(out: torch.Tensor, query: torch.Tensor, key_cache: torch.Tensor,
+                               value_cache: torch.Tensor, block_tables: torch.Tensor,
+                               token_seq: torch.Tensor, token_pos: torch.Tensor,
+                               selected: torch.Tensor, scale: float, partition_size: int = 0,
+                               workspace: Optional[torch.Tensor] = None, k_scale: float = 1.0,
+                               v_scale: float = 1.0,
+                               error_word: Optional[torch.Tensor] = None,
+                               stream=None) -> None:
+    """Attention of single rows over the blocks that pa_select_blocks (or the
+    caller) lists for each row and KV head: out and query are [T, H, d], selected
+    is int32 [T, Hkv, top_k].  uint8 pools take the e4m3 path with k_scale /
+    v_scale."""
+    status = _calls.decode_sparse(out, query, key_cache, value_cache, block_tables, token_seq,
+                                  token_pos, selected, scale, partition_size, workspace, k_scale,
+                                  v_scale, error_word, stream)
+    if status:
+        raise PAError("pa_decode_attention_sparse" + _suffix(key_cache), status)
+
+
+def pa_weights_workspace_bytes(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                               max_context_len: int, partition_size: int) -> int:
+    return int(_lib.pa_weights_workspace_bytes(num_seqs, num_heads, num_kv_heads, head_dim,
+                                               max_context_len, partition_size))
+
+
+def pa_decode_attention_weights(out: torch.Tensor, weights_out: torch.Tensor,
+                                query: torch.Tensor, key_cache: torch.Tensor,
+                                value_cache: torch.Tensor, weights: torch.Tensor,
+                                block_tables: torch.Tensor, context_lens: torch.Tensor,
+                                weighted_lens: torch.Tensor, max_context_len: int, scale: float,
+                                workspace: Optional[torch.Tensor], partition_size: int = 0,
+                                k_scale: float = 1.0, v_scale: float = 1.0,
+                                error_word: Optional[torch.Tensor] = None,
+                                stream=None) -> None:
+    """Paged decode attention (out and query [S, H, d]) that adds what each cached
+    token is attended with, over all query heads, to its weight: weights and
+    weights_out (which may be one) are float32 [N, bs], weighted_lens [S] the
+    positions that have a weight so far.  workspace:
+    pa_weights_workspace_bytes(...) bytes, zeroed once."""
+    status = _calls.decode_weights(out, query, key_cache, value_cache, block_tables, weights_out,
+                                   weights, context_lens, weighted_lens, max_context_len, scale,
+                                   workspace, partition_size, k_scale, v_scale, error_word,
+                                   stream)
+    if status:
+        raise PAError("pa_decode_attention_weights" + _suffix(key_cache), status)
 
 
 def pa_plan_prefix_groups(block_tables, context_lens, block_size: int,

@@ -48,6 +48,10 @@ struct Library {
     decltype(&pa_prefill_attention_window_fp8) prefill_fp8;
     decltype(&pa_summarize_blocks) summarize;
     decltype(&pa_select_blocks) select;
+    decltype(&pa_decode_attention_sparse) sparse;
+    decltype(&pa_decode_attention_sparse_fp8) sparse_fp8;
+    decltype(&pa_decode_attention_weights) weights;
+    decltype(&pa_decode_attention_weights_fp8) weights_fp8;
 };
 Library lib;
 
@@ -368,6 +372,19 @@ Attention attention(PyObject *const *a, int64_t seqs, bool one_row)
     return x;
 }
 
+struct Space {
+    void *at;
+    size_t bytes;
+};
+
+Space workspace(PyObject *o, int dev)
+{
+    if (o == Py_None)
+        return {nullptr, 0};
+    const at::Tensor &w = tensor(o, "workspace");
+    return {address(w, "workspace", w.scalar_type(), dev), w.nbytes()};
+}
+
 pa_status decode_window(PyObject *const *a)
 {
     const at::Tensor &ctx = tensor(a[5], "context_lens");
@@ -378,13 +395,7 @@ pa_status decode_window(PyObject *const *a)
     const float scale = to_float(a[7]);
     const int window = reach(a[8], "window"), sinks = reach(a[9], "num_sinks");
     const int partition = to_int(a[10], "partition_size");
-    void *space = nullptr;
-    size_t bytes = 0;
-    if (a[11] != Py_None) {
-        const at::Tensor &w = tensor(a[11], "workspace");
-        space = address(w, "workspace", w.scalar_type(), x.dev);
-        bytes = w.nbytes();
-    }
+    const Space w = workspace(a[11], x.dev);
     const float ks = to_float(a[12]), vs = to_float(a[13]);
     int32_t *err = optional_ints(a[14], "error_word", x.dev);
     void *stream = queue(a[15], x.dev);
@@ -392,11 +403,11 @@ pa_status decode_window(PyObject *const *a)
     if (x.fp8)
         return lib.decode_fp8(x.out, x.query, x.key_cache, x.value_cache, x.tables, x.max_blocks,
                               lens, max_ctx, window, sinks, x.rows, x.heads, x.kv_heads, x.dim,
-                              x.block_size, x.num_blocks, scale, ks, vs, partition, space, bytes,
+                              x.block_size, x.num_blocks, scale, ks, vs, partition, w.at, w.bytes,
                               x.dtype, err, stream);
     return lib.decode(x.out, x.query, x.key_cache, x.value_cache, x.tables, x.max_blocks, lens,
                       max_ctx, window, sinks, x.rows, x.heads, x.kv_heads, x.dim, x.block_size,
-                      x.num_blocks, scale, partition, space, bytes, x.dtype, err, stream);
+                      x.num_blocks, scale, partition, w.at, w.bytes, x.dtype, err, stream);
 }
 
 pa_status prefill_window(PyObject *const *a)
@@ -509,6 +520,74 @@ pa_status select_blocks(PyObject *const *a)
                       seqs, heads, x.kv_heads, x.dim, bs, x.num_blocks, dtype, err, stream);
 }
 
+pa_status decode_sparse(PyObject *const *a)
+{
+    const at::Tensor &tables = tensor(a[4], "block_tables"), &seq = tensor(a[5], "token_seq"),
+                     &pos = tensor(a[6], "token_pos"), &sel = tensor(a[7], "selected");
+    dimensions(tables, "block_tables", 2);
+    dimensions(sel, "selected", 3);
+    const int64_t S = tables.size(0);
+    const Attention x = attention(a, S, false);
+    need(seq.dim() == 1 && seq.size(0) == x.rows && pos.dim() == 1 && pos.size(0) == x.rows &&
+             sel.size(0) == x.rows && sel.size(1) == x.kv_heads,
+         "one sequence, position and list of blocks per KV head for every row expected");
+    const int32_t *pn = ints(seq, "token_seq", x.dev), *pp = ints(pos, "token_pos", x.dev),
+                  *ps = ints(sel, "selected", x.dev);
+    const float scale = to_float(a[8]);
+    const int partition = to_int(a[9], "partition_size");
+    const Space w = workspace(a[10], x.dev);
+    const float ks = to_float(a[11]), vs = to_float(a[12]);
+    int32_t *err = optional_ints(a[13], "error_word", x.dev);
+    void *stream = queue(a[14], x.dev);
+    const int top_k = size_int(sel.size(2), "selected"), seqs = size_int(S, "block_tables");
+    const Unlocked unlocked;
+    if (x.fp8)
+        return lib.sparse_fp8(x.out, x.query, x.key_cache, x.value_cache, x.tables, x.max_blocks,
+                              pn, pp, ps, top_k, x.rows, seqs, x.heads, x.kv_heads, x.dim,
+                              x.block_size, x.num_blocks, scale, ks, vs, partition, w.at, w.bytes,
+                              x.dtype, err, stream);
+    return lib.sparse(x.out, x.query, x.key_cache, x.value_cache, x.tables, x.max_blocks, pn, pp,
+                      ps, top_k, x.rows, seqs, x.heads, x.kv_heads, x.dim, x.block_size,
+                      x.num_blocks, scale, partition, w.at, w.bytes, x.dtype, err, stream);
+}
+
+// A pool of one weight a slot, [num_blocks, block_size].
+float *weight_pool(PyObject *o, const char *name, int num_blocks, int block_size, int dev)
+{
+    const at::Tensor &w = tensor(o, name);
+    need(w.dim() == 2 && w.size(0) == num_blocks && w.size(1) == block_size,
+         "weights: [num_blocks, block_size] expected");
+    return static_cast<float *>(address(w, name, at::kFloat, dev));
+}
+
+pa_status decode_weights(PyObject *const *a)
+{
+    const at::Tensor &ctx = tensor(a[7], "context_lens"), &old = tensor(a[8], "weighted_lens");
+    dimensions(ctx, "context_lens", 1);
+    const Attention x = attention(a, ctx.size(0), true);
+    need(old.dim() == 1 && old.size(0) == ctx.size(0), "one weighted length per sequence expected");
+    float *pw_out = weight_pool(a[5], "weights_out", x.num_blocks, x.block_size, x.dev);
+    const float *pw = weight_pool(a[6], "weights", x.num_blocks, x.block_size, x.dev);
+    const int32_t *pc = ints(ctx, "context_lens", x.dev), *po = ints(old, "weighted_lens", x.dev);
+    const int max_ctx = to_int(a[9], "max_context_len");
+    const float scale = to_float(a[10]);
+    const Space w = workspace(a[11], x.dev);
+    const int partition = to_int(a[12], "partition_size");
+    const float ks = to_float(a[13]), vs = to_float(a[14]);
+    int32_t *err = optional_ints(a[15], "error_word", x.dev);
+    void *stream = queue(a[16], x.dev);
+    const Unlocked unlocked;
+    if (x.fp8)
+        return lib.weights_fp8(x.out, pw_out, x.query, x.key_cache, x.value_cache, pw, x.tables,
+                               x.max_blocks, pc, po, max_ctx, x.rows, x.heads, x.kv_heads, x.dim,
+                               x.block_size, x.num_blocks, scale, ks, vs, partition, w.at, w.bytes,
+                               x.dtype, err, stream);
+    return lib.weights(x.out, pw_out, x.query, x.key_cache, x.value_cache, pw, x.tables,
+                       x.max_blocks, pc, po, max_ctx, x.rows, x.heads, x.kv_heads, x.dim,
+                       x.block_size, x.num_blocks, scale, partition, w.at, w.bytes, x.dtype, err,
+                       stream);
+}
+
 template <pa_status (*call)(PyObject *const *), int count>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -545,6 +624,10 @@ PyObject *bind(PyObject *, PyObject *path)
         find(h, "pa_prefill_attention_window_fp8", found.prefill_fp8);
         find(h, "pa_summarize_blocks", found.summarize);
         find(h, "pa_select_blocks", found.select);
+        find(h, "pa_decode_attention_sparse", found.sparse);
+        find(h, "pa_decode_attention_sparse_fp8", found.sparse_fp8);
+        find(h, "pa_decode_attention_weights", found.weights);
+        find(h, "pa_decode_attention_weights_fp8", found.weights_fp8);
         lib = found;
         Py_RETURN_NONE;
     } catch (const PythonError &) {
@@ -563,6 +646,8 @@ PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
                          PA_ENTRY(prefill_window, 15),
                          PA_ENTRY(summarize, 8),
                          PA_ENTRY(select_blocks, 13),
+                         PA_ENTRY(decode_sparse, 15),
+                         PA_ENTRY(decode_weights, 17),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,

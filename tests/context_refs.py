@@ -83,3 +83,78 @@ def select(query, codes, scales, tables, seq, pos, bs, top_k, first, last, kv_he
             out[t, h] = np.sort(np.concatenate([np.arange(first), best,
                                                 np.arange(have - last, have)]))
     return out
+
+
+HALF_STEP = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}  # eps / 2
+
+
+def attend(q, k, v, scale, out_dtype, p_dtype):
+    """One query vector over keys and values [n, D] in 64 bits: (output, its tolerance,
+    weights, theirs).  Counted: the output's half step; the weights' half step as a
+    matrix operand, which moves the output by at most that times sum w |v|; a score's
+    fp32 error, which moves its own weight and the sum of weights; the sums' own."""
+    x = k @ q * scale
+    with np.errstate(invalid="ignore"):
+        w = np.exp(x - x.max())
+    w /= w.sum()
+    o = w @ v
+    size = scale * (np.abs(k) @ np.abs(q)).max()
+    e = 2 * ((len(q) + 4) * 2.0 ** -22 * size + (len(x) + 8) * 2.0 ** -23)
+    tol = HALF_STEP[out_dtype] * np.abs(o) + \
+        1.01 * (HALF_STEP[p_dtype] + e) * (w @ np.abs(v)) + 2.0 ** -24
+    return o, tol, w, w * e
+
+
+def pool_values(pool, scale):
+    if pool.dtype == torch.uint8:
+        return pool.cpu().view(torch.float8_e4m3fn).double().numpy() * scale
+    return pool.double().cpu().numpy()
+
+
+def sparse_attention(q, kc, vc, tables, seq, pos, chosen, scale, out_dtype, p_dtype):
+    """(output, tolerance) of every row over the blocks of its lists (int arrays, negative
+    entries left out); kc and vc are pools of values in 64 bits."""
+    q = q.double().cpu().numpy()
+    T, H, D = q.shape
+    bs, K = kc.shape[1:3]
+    out, tol = np.zeros((T, H, D)), np.zeros((T, H, D))
+    for t in range(T):
+        if seq[t] < 0:
+            continue
+        for h in range(K):
+            blk = chosen[t][h][:min(len(chosen[t][h]), pos[t] // bs + 1)]
+            p = np.concatenate([np.arange(b * bs, b * bs + bs) for b in blk if b >= 0] +
+                               [np.zeros(0, dtype=int)]).astype(int)
+            p = p[p <= pos[t]]
+            if not len(p):
+                continue
+            at = tables[seq[t]][p // bs]
+            for g in range(h * H // K, (h + 1) * H // K):
+                out[t, g], tol[t, g], _, _ = attend(q[t, g], kc[at, p % bs, h], vc[at, p % bs, h],
+                                                    scale, out_dtype, p_dtype)
+    return out, tol
+
+
+def weights_attention(q, kc, vc, weights, tables, ctx, weighted, scale, out_dtype, p_dtype):
+    """(output, tolerance, weights_out, tolerance) of a decode step; entries of weights
+    that no context reaches come back as they are, with a tolerance of 0."""
+    q = q.double().cpu().numpy()
+    S, H, D = q.shape
+    bs, K = kc.shape[1:3]
+    out, tol = np.zeros((S, H, D)), np.zeros((S, H, D))
+    new, new_tol = weights.astype(np.float64).copy(), np.zeros(weights.shape)
+    for s in range(S):
+        p = np.arange(ctx[s])
+        at, row = tables[s][p // bs], p % bs
+        total, err = np.zeros(len(p)), np.zeros(len(p))
+        for h in range(K):
+            for g in range(h * H // K, (h + 1) * H // K) if len(p) else ():
+                out[s, g], tol[s, g], w, e = attend(q[s, g], kc[at, row, h], vc[at, row, h],
+                                                    scale, out_dtype, p_dtype)
+                total, err = total + w, err + e
+        before = np.where(p < weighted[s], new[at, row], 0.0) if len(p) else total
+        new[at, row] = before + total
+        # H terms added one by one, then the sum so far
+        new_tol[at, row] = err + (H + 8) * 2.0 ** -24 * total + \
+            2.0 ** -24 * (before + total) + 2.0 ** -40
+    return out, tol, new, new_tol
