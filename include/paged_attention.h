@@ -716,6 +716,61 @@ PA_API pa_status pa_decode_attention_weights_fp8(
     int32_t *error_word, void *stream);
 
 /*
+ * pa_plan_eviction -- which cached tokens of sequences that have passed a limit are
+ * kept (no counterpart on the pages, whose block manager frees whole sequences).  A
+ * sequence of c = context_lens[s] > limit tokens is cut down to budget of them: its
+ * first num_sinks, its last num_recent, and of the others those with the largest weight
+ * (pa_decode_attention_weights; a weight that is not above 0, NaN among them, counts as
+ * 0; of equal ones the lower position is kept).  Kept tokens below position budget stay
+ * where they are, and the i-th kept one from there on takes the place of the i-th evicted
+ * one before it (both in order of position): attention does not go by the order of
+ * cached tokens, whose keys hold their positions.  Blocks that hold no position below
+ * budget go back on the free stack (sequences in batch order, blocks in logical order).
+ * Sequences of at most limit tokens are left as they are.
+ *   moves          : int32 [num_seqs][max_moves][2] (output): (slot from, slot to) of
+ *                    each moved token, for pa_move_tokens on the pools of every layer
+ *                    that has these tables, then -1 pairs; max_moves >=
+ *                    min(budget, max_context_len - budget)
+ *   context_lens_out : int32 [num_seqs], which may be context_lens
+ *   free_blocks, free_count, free_count_out : the stack of pa_build_step_maps; the
+ *                    counts may be the same
+ *   weights, weights_out : float [num_blocks][block_size]; weights_out gets the
+ *                    weights of positions below context_lens_out[s] in their new
+ *                    places, and may be weights
+ *   max_context_len : (host) >= every context_lens[s]
+ * budget >= 1, limit >= budget >= num_sinks + num_recent (PA_ERR_INVALID_ARG
+ * otherwise).  A table entry outside [0, num_blocks) sets PA_DEVERR_BLOCK_RANGE; its
+ * tokens have weight 0 and their moves are -1.  The plan is refused as a whole, with the
+ * lengths, stack and weights as they were and every move -1, when a length is negative,
+ * past max_context_len or past its table (PA_DEVERR_CONTEXT_RANGE), or the stack would
+ * pass num_blocks or its count is negative (PA_DEVERR_BLOCK_RANGE).  Blocks are taken to
+ * have one owner.  block_size: a power of two; max_moves <= 2^29.
+ * Bounds of the changed blocks: pa_summarize_blocks over whole contexts.
+ */
+PA_API pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *context_lens_out,
+                                  int32_t *free_count_out, float *weights_out,
+                                  const int32_t *block_tables, int max_blocks_per_seq,
+                                  const int32_t *context_lens, const float *weights,
+                                  int32_t *free_blocks, const int32_t *free_count,
+                                  int max_context_len, int limit, int budget, int num_sinks,
+                                  int num_recent, int num_seqs, int block_size, int num_blocks,
+                                  int32_t *error_word, void *stream);
+
+/*
+ * pa_move_tokens -- pa_copy_blocks for single tokens: for every pair (from, to) of
+ * moves, int32 [num_moves][2], the K and V rows of slot `to` become those of slot `from`
+ * (num_kv_heads * head_dim elements each, verbatim).  A pair with a negative slot is
+ * skipped; one with a slot >= num_blocks * block_size is skipped and sets
+ * PA_DEVERR_SLOT_RANGE.  No slot may be both a source and a destination, and
+ * destinations must be distinct; otherwise the result is unspecified.  moves is 8-byte
+ * aligned; rows of at most 16 MB.  dtype: of the pools, as pa_copy_blocks.
+ */
+PA_API pa_status pa_move_tokens(void *key_cache, void *value_cache, const int32_t *moves,
+                                int64_t num_moves, int num_blocks, int block_size,
+                                int num_kv_heads, int head_dim, pa_dtype dtype,
+                                int32_t *error_word, void *stream);
+
+/*
  * Prefix plan -- which sequences of a decode batch share leading physical
  * blocks ([FEI] "共享前缀的 Block 复用": block tables that name the same
  * physical blocks for a common prefix, the blocks' reference counts > 1).

@@ -17,7 +17,10 @@ __all__ = [
     "pa_decode_attention", "pa_decode_workspace_bytes", "PAError",
     "pa_reshape_and_cache_fp8", "pa_decode_attention_fp8", "pa_decode_attention_noalloc",
     "pa_build_step_maps", "pa_rope_and_cache", "pa_decode_attention_window",
-    "pa_prefill_attention_window", "pa_window_workspace_bytes", "library_path",
+    "pa_prefill_attention_window", "pa_window_workspace_bytes", "pa_summarize_blocks",
+    "pa_select_blocks", "pa_decode_attention_sparse", "pa_sparse_workspace_bytes",
+    "pa_decode_attention_weights", "pa_weights_workspace_bytes", "pa_plan_eviction",
+    "pa_move_tokens", "library_path",
 ]
 
 

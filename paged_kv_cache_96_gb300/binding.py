@@ -124,6 +124,9 @@ def _load() -> ctypes.CDLL:
         "pa_decode_attention_weights_fp8": (i32, [P, P, P, P, P, P, P, i32, P, P, i32, i32, i32,
                                                   i32, i32, i32, i32, f32, f32, f32, i32, P, sz,
                                                   i32, P, P]),
+        "pa_plan_eviction": (i32, [P, i32, P, P, P, P, i32, P, P, P, P, i32, i32, i32, i32, i32,
+                                   i32, i32, i32, P, P]),
+        "pa_move_tokens": (i32, [P, P, P, i64, i32, i32, i32, i32, i32, P, P]),
         "pa_prefix_plan_ints": (sz, [i32, i32, i32]),
         "pa_plan_prefix_groups": (i32, [P, i32, P, i32, i32, i32, P, sz, P, P]),
         "pa_cascade_workspace_bytes": (sz, [i32, i32, i32, i32, i32, i32]),
@@ -708,6 +711,35 @@ def pa_decode_attention_weights(out: torch.Tensor, weights_out: torch.Tensor,
                                    stream)
     if status:
         raise PAError("pa_decode_attention_weights" + _suffix(key_cache), status)
+
+
+def pa_plan_eviction(moves: torch.Tensor, context_lens_out: torch.Tensor,
+                     free_count_out: torch.Tensor, weights_out: torch.Tensor,
+                     block_tables: torch.Tensor, context_lens: torch.Tensor,
+                     weights: torch.Tensor, free_blocks: torch.Tensor, free_count: torch.Tensor,
+                     max_context_len: int, limit: int, budget: int, num_sinks: int = 0,
+                     num_recent: int = 0, error_word: Optional[torch.Tensor] = None,
+                     stream=None) -> None:
+    """Cut sequences of more than `limit` cached tokens down to `budget`: the first
+    num_sinks, the last num_recent and those of the largest weights [N, bs].
+    moves int32 [S, M, 2] gets the (from, to) slots for pa_move_tokens (then -1),
+    free_blocks the blocks given back; context_lens_out, free_count_out and
+    weights_out may be the inputs."""
+    status = _calls.plan_eviction(moves, context_lens_out, free_count_out, weights_out,
+                                  block_tables, context_lens, weights, free_blocks, free_count,
+                                  max_context_len, limit, budget, num_sinks, num_recent,
+                                  error_word, stream)
+    if status:
+        raise PAError("pa_plan_eviction", status)
+
+
+def pa_move_tokens(key_cache: torch.Tensor, value_cache: torch.Tensor, moves: torch.Tensor,
+                   error_word: Optional[torch.Tensor] = None, stream=None) -> None:
+    """For each (from, to) pair of slots in moves [..., 2]: the K and V rows of `to`
+    become those of `from`; pairs with a negative slot are skipped."""
+    status = _calls.move_tokens(key_cache, value_cache, moves, error_word, stream)
+    if status:
+        raise PAError("pa_move_tokens", status)
 
 
 def pa_plan_prefix_groups(block_tables, context_lens, block_size: int,

@@ -25,6 +25,7 @@
 #include <cooperative_groups.h>
 
 #include "pa_decode_common.cuh"
+#include "pa_topk.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -309,7 +310,6 @@ struct SelectParams {
 
 constexpr int kSelThreads = 256;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kSelBins = 256;
 
 // Keys in the scores' order.
 __device__ __forceinline__ uint32_t score_key(float x)
@@ -332,10 +332,8 @@ __device__ __forceinline__ void widen_codes(uint32_t w, uint32_t &a, uint32_t &b
 
 struct SelectShared {
     float q_scale[16];
-    int hist[kSelBins];
-    uint32_t lo[kSelWarps], hi[kSelWarps];
+    TopkShared topk;
     int above[kSelWarps], ties[kSelWarps];
-    int bin, rest, last_bin;
 };
 
 // T: the query's type; NT: heads of a KV head in eights.
@@ -500,84 +498,16 @@ __global__ void __launch_bounds__(kSelThreads)
     if (rank != 0)
         return;
 
-    // ---- the smallest selected key, digit by digit -----------------------------------
-    uint32_t lo = 0xffffffffu, hi = 0u;
-    for (int i = tid; i < n; i += kSelThreads) {
-        lo = min(lo, keys[i]);
-        hi = max(hi, keys[i]);
-    }
-    lo = __reduce_min_sync(kFull, lo);
-    hi = __reduce_max_sync(kFull, hi);
-    if (lane == 0) {
-        sh.lo[warp] = lo;
-        sh.hi[warp] = hi;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
-        lo = min(lo, sh.lo[w]);
-        hi = max(hi, sh.hi[w]);
-    }
-    // keys less lo have `bits` bits; those at or above `from` << shift are looked at
-    // further while more of them are wanted than of the digits above
-    int shift = 32 - __clz((int)(hi - lo));
-    uint32_t prefix = 0;  // of the keys still looked at
-    int rest = want;      // of them, how many are selected
-    while (shift > 0 && rest > 0) {
-        const int width = min(8, shift);
-        shift -= width;
-        for (int b = tid; b < kSelBins; b += kSelThreads)
-            sh.hist[b] = 0;
-        __syncthreads();
-        for (int i = tid; i < n; i += kSelThreads) {
-            const uint32_t v = keys[i] - lo;
-            if (((unsigned long long)v >> (shift + width)) == prefix)
-                atomicAdd(&sh.hist[(v >> shift) & ((1u << width) - 1)], 1);
-        }
-        __syncthreads();
-        if (warp == 0) {
-            // lane l has bins 8 l .. 8 l + 7; counts from the top bin down
-            int own[8], sum = 0;
-#pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                own[b] = sh.hist[lane * 8 + b];
-                sum += own[b];
-            }
-            int above = sum;  // of this lane's bins and those of higher lanes
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_down_sync(kFull, above, o);
-                if (lane + o < 32)
-                    above += y;
-            }
-            int over = above - sum;  // of higher lanes' bins
-#pragma unroll
-            for (int b = 7; b >= 0; --b) {
-                if (over < rest && over + own[b] >= rest) {
-                    sh.bin = lane * 8 + b;
-                    sh.rest = rest - over;
-                    sh.last_bin = own[b] == rest - over;
-                }
-                over += own[b];
-            }
-        }
-        __syncthreads();
-        prefix = (prefix << width) | (uint32_t)sh.bin;
-        rest = sh.rest;
-        const bool all = sh.last_bin != 0;  // the whole bin is selected
-        __syncthreads();
-        if (all)
-            break;
-    }
-    // selected: key digits above the prefix, and the first `rest` at it
     // ---- the list, in ascending order ------------------------------------------------
+    const Threshold cut =
+        top_threshold<kSelThreads>(sh.topk, [&](int i) { return keys[i]; }, n, want);
     const int run = (n + kSelThreads - 1) / kSelThreads * 32;  // candidates of a warp
     const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
     int above = 0, ties = 0;
     for (int i = i0 + lane; i < i1; i += 32) {
-        const uint32_t v = (uint32_t)((unsigned long long)(keys[i] - lo) >> shift);
-        above += v > prefix;
-        ties += v == prefix;
+        const uint32_t v = cut.level(keys[i]);
+        above += v > cut.prefix;
+        ties += v == cut.prefix;
     }
     above = __reduce_add_sync(kFull, above);
     ties = __reduce_add_sync(kFull, ties);
@@ -593,13 +523,13 @@ __global__ void __launch_bounds__(kSelThreads)
     }
     for (int b = i0; b < i1; b += 32) {
         const int i = b + lane;
-        const uint32_t v = i < i1 ? (uint32_t)((unsigned long long)(keys[i] - lo) >> shift) : 0u;
-        const bool over = i < i1 && v > prefix, tie = i < i1 && v == prefix;
+        const uint32_t v = i < i1 ? cut.level(keys[i]) : 0u;
+        const bool over = i < i1 && v > cut.prefix, tie = i < i1 && v == cut.prefix;
         const uint32_t over_m = __ballot_sync(kFull, over), tie_m = __ballot_sync(kFull, tie);
         const uint32_t below = (1u << lane) - 1;
         const int my_ties = ties + __popc(tie_m & below);
-        if (over || (tie && my_ties < rest))
-            out[first + above + __popc(over_m & below) + min(my_ties, rest)] = first + i;
+        if (over || (tie && my_ties < cut.rest))
+            out[first + above + __popc(over_m & below) + min(my_ties, cut.rest)] = first + i;
         above += __popc(over_m);
         ties += __popc(tie_m);
     }

@@ -1,0 +1,466 @@
+// pa_evict.cu -- sequences that have passed a limit cut down to the cached tokens that
+// were attended most, for sm_103a: the plan from the weights that
+// pa_decode_attention_weights accumulates, and the K and V rows that it moves.  An
+// addition to the pages, whose block manager frees whole sequences ("vLLM 架构详解",
+// "Block Table 实现").
+//
+// For a sequence of c > limit tokens, of which `budget` stay: the first num_sinks, the
+// last num_recent, and of the others those with the largest weight (weights that are
+// not above 0 count as 0; of equal ones the lower position stays).  Attention does not
+// go by the order of cached tokens (their positions are in the rotated keys), so rows
+// below `budget` that stay are not moved: the i-th row that stays at or past it takes
+// the place of the i-th evicted one before it.  A sequence one step past its limit
+// costs a handful of rows, not a copy of the context.  Blocks behind the budget go back
+// on the free stack, sequences in batch order, blocks in logical order.
+//
+// What bounds it: the plan, latency (a sequence's weights are 4 bytes a token, and
+// selection is a chain of passes over them); the moves, HBM: 4 rows of num_kv_heads *
+// head_dim elements read or written a move.
+#include <algorithm>
+#include <mutex>
+
+#include "pa_decode_common.cuh"
+#include "pa_topk.cuh"
+
+namespace pa {
+
+struct PlanParams {
+    int32_t *moves;  // [S][max_moves][2]
+    int32_t *context_out, *free_count_out, *free_blocks;
+    float *weights_out;
+    const int32_t *block_tables, *context_lens, *free_count;
+    const float *weights;
+    int32_t *error_word;
+    int max_moves, max_blocks_per_seq, max_context_len, limit, budget, num_sinks, num_recent;
+    int num_seqs, block_shift, num_blocks;
+};
+
+// What a sequence's length asks for.
+struct PlanSeq {
+    int c, end;       // tokens before and after
+    int keep, have;   // blocks after and before
+    bool bad;
+};
+__device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s)
+{
+    PlanSeq q;
+    q.c = p.context_lens[s];
+    const long long cap = (long long)p.max_blocks_per_seq << p.block_shift;
+    q.bad = q.c < 0 || q.c > min(cap, (long long)p.max_context_len);
+    q.end = !q.bad && q.c > p.limit ? p.budget : q.c;
+    const unsigned round = (1u << p.block_shift) - 1;
+    q.have = q.bad ? 0 : (int)(((unsigned)q.c + round) >> p.block_shift);
+    q.keep = q.bad ? 0 : (int)(((unsigned)q.end + round) >> p.block_shift);
+    return q;
+}
+
+// The plan is taken or refused as a whole; every CTA finds out for itself.
+__device__ __forceinline__ int plan_refusal(const PlanParams &p, long long given, bool bad)
+{
+    const int count = p.free_count[0];
+    return bad ? PA_DEVERR_CONTEXT_RANGE
+           : count < 0 || count + given > p.num_blocks ? PA_DEVERR_BLOCK_RANGE : 0;
+}
+
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWarps = kPlanThreads / 32;
+
+struct PlanShared {
+    TopkShared topk;
+    int above[kPlanWarps], ties[kPlanWarps];
+    long long given[kPlanWarps];
+    int low_kept;  // tokens between the first and the last ones that stay below the budget
+};
+
+// Sum and OR over the CTA.
+__device__ __forceinline__ long long plan_total(PlanShared &sh, const PlanParams &p, bool &bad)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    long long n = 0;
+    bad = false;
+    for (int s = tid; s < p.num_seqs; s += kPlanThreads) {
+        const PlanSeq q = plan_seq(p, s);
+        n += q.have - q.keep;
+        bad |= q.bad;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        n += __shfl_xor_sync(kFull, n, o);
+    if (lane == 0)
+        sh.given[warp] = n;
+    bad = __syncthreads_or(bad);
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kPlanWarps; ++w)
+        n += sh.given[w];
+    return n;
+}
+
+// One CTA per sequence.  kKept: the keys of the whole context fit in shared memory;
+// else each pass reads the weights again, through L2.
+template <bool kKept>
+__global__ void __launch_bounds__(kPlanThreads)
+    plan_eviction_kernel(const __grid_constant__ PlanParams p)
+{
+    __shared__ PlanShared sh;
+    extern __shared__ uint32_t keys[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s = blockIdx.x;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+
+    bool bad;
+    const long long given = plan_total(sh, p, bad);
+    const int refuse = plan_refusal(p, given, bad);
+    int32_t *moves = p.moves + (size_t)s * p.max_moves * 2;
+    const PlanSeq q = plan_seq(p, s);
+    const int bs = 1 << p.block_shift;
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
+    const int slots = p.num_blocks << p.block_shift;
+    auto slot_of = [&](int pos) {
+        const int b = __ldg(table + (pos >> p.block_shift));
+        if (b < 0 || b >= p.num_blocks) {
+            flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
+            return -1;
+        }
+        return (b << p.block_shift) + (pos & (bs - 1));
+    };
+    int count = 0;  // moves
+    if (refuse == 0) {
+        // what stays where it is
+        if (p.weights_out != p.weights)
+            for (int i = tid; i < q.end; i += kPlanThreads) {
+                const int at = slot_of(i);
+                if (at >= 0)
+                    p.weights_out[at] = p.weights[at];
+            }
+        if (q.end != q.c) {
+            const int first = p.num_sinks, tail = q.c - p.num_recent;  // chosen from [first, tail)
+            const int n = tail - first, want = p.budget - p.num_sinks - p.num_recent;
+            auto fetch = [&](int i) {
+                const int at = slot_of(first + i);
+                // (by its bits: a comparison would take subnormal weights for 0)
+                const int w = at >= 0 ? __float_as_int(p.weights[at]) : 0;
+                return w > 0 && w <= 0x7f800000 ? (uint32_t)w : 0u;
+            };
+            auto key = [&](int i) { return kKept ? keys[i] : fetch(i); };
+            if (kKept) {
+                for (int i = tid; i < n; i += kPlanThreads)
+                    keys[i] = fetch(i);
+                __syncthreads();
+            }
+            const Threshold cut = top_threshold<kPlanThreads>(sh.topk, key, n, want);
+            // a warp's run of them; the tokens that stay before each run
+            const int run = (n + kPlanThreads - 1) / kPlanThreads * 32;
+            const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
+            int above = 0, ties = 0;
+            for (int i = i0 + lane; i < i1; i += 32) {
+                const uint32_t v = cut.level(key(i));
+                above += v > cut.prefix;
+                ties += v == cut.prefix;
+            }
+            above = __reduce_add_sync(kFull, above);
+            ties = __reduce_add_sync(kFull, ties);
+            if (lane == 0) {
+                sh.above[warp] = above;
+                sh.ties[warp] = ties;
+            }
+            __syncthreads();
+            above = ties = 0;
+            for (int w = 0; w < warp; ++w) {
+                above += sh.above[w];
+                ties += sh.ties[w];
+            }
+            const int low = p.budget - first;  // candidates below the budget
+            // visit(i, stays, how many before it do) for every candidate of the run
+            auto walk = [&](auto &&visit) {
+                int a = above, t = ties;
+                for (int b = i0; b < i1; b += 32) {
+                    const int i = b + lane;
+                    const uint32_t v = i < i1 ? cut.level(key(i)) : 0u;
+                    const uint32_t over = __ballot_sync(kFull, i < i1 && v > cut.prefix);
+                    const uint32_t tie = __ballot_sync(kFull, i < i1 && v == cut.prefix);
+                    const uint32_t below = (1u << lane) - 1;
+                    const int my_ties = t + __popc(tie & below);
+                    const bool stays = (over >> lane & 1) || ((tie >> lane & 1) && my_ties < cut.rest);
+                    if (i < i1)
+                        visit(i, stays, a + __popc(over & below) + min(my_ties, cut.rest));
+                    a += __popc(over);
+                    t += __popc(tie);
+                }
+            };
+            if (tid == 0 && low >= n)
+                sh.low_kept = want;
+            if (low >= i0 && low < i1)
+                walk([&](int i, bool, int before) {
+                    if (i == low)
+                        sh.low_kept = before;
+                });
+            __syncthreads();
+            const int low_kept = sh.low_kept;
+            walk([&](int i, bool stays, int before) {
+                if (i < low && !stays)
+                    moves[2 * (i - before) + 1] = slot_of(first + i);
+                if (i >= low && stays)
+                    moves[2 * (before - low_kept)] = slot_of(first + i);
+            });
+            // the last tokens, from the budget on
+            const int late = max(tail, p.budget);
+            const int done = want - low_kept;  // rows before them
+            for (int i = late + tid; i < q.c; i += kPlanThreads)
+                moves[2 * (done + i - late)] = slot_of(i);
+            count = done + q.c - late;
+            __syncthreads();
+            for (int i = tid; i < count; i += kPlanThreads) {
+                const int src = moves[2 * i], dst = moves[2 * i + 1];
+                if (src >= 0 && src < slots && dst >= 0 && dst < slots)
+                    p.weights_out[dst] = p.weights[src];
+            }
+        }
+    }
+    for (int i = 2 * count + tid; i < 2 * p.max_moves; i += kPlanThreads)
+        moves[i] = -1;
+}
+
+// Lengths, the stack and its count, which may be the inputs: by one CTA behind the
+// plan, whose CTAs read every length.
+__global__ void __launch_bounds__(kPlanThreads)
+    apply_eviction_kernel(const __grid_constant__ PlanParams p)
+{
+    __shared__ PlanShared sh;
+    __shared__ int pushed[kPlanThreads + 1], keep_s[kPlanThreads];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    bool bad;
+    const long long given = plan_total(sh, p, bad);
+    const int refuse = plan_refusal(p, given, bad);
+    const int count = p.free_count[0];
+    __syncthreads();  // (the count and the lengths have been read)
+    int base = count;
+    for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
+        const int s = s0 + tid;
+        int n = 0;
+        if (s < p.num_seqs) {
+            const PlanSeq q = plan_seq(p, s);
+            p.context_out[s] = refuse ? q.c : q.end;
+            n = refuse ? 0 : q.have - q.keep;
+            keep_s[tid] = q.keep;
+        }
+        int x = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(kFull, x, o);
+            if (lane >= o)
+                x += y;
+        }
+        if (lane == 31)
+            sh.above[warp] = x;
+        __syncthreads();
+        int before = 0, all = 0;
+        for (int w = 0; w < kPlanWarps; ++w) {
+            before += w < warp ? sh.above[w] : 0;
+            all += sh.above[w];
+        }
+        pushed[tid] = before + x - n;
+        __syncthreads();
+        for (int i = tid; i < all; i += kPlanThreads) {
+            int lo = 0, len = kPlanThreads;  // the last sequence with pushed <= i
+            while (len > 1) {
+                const int half = len >> 1;
+                if (pushed[lo + half] <= i) {
+                    lo += half;
+                    len -= half;
+                } else {
+                    len = half;
+                }
+            }
+            const int id = p.block_tables[(size_t)(s0 + lo) * p.max_blocks_per_seq + keep_s[lo] +
+                                          i - pushed[lo]];
+            if (id < 0 || id >= p.num_blocks)
+                flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
+            p.free_blocks[base + i] = id;
+        }
+        base += all;
+        __syncthreads();
+    }
+    if (tid == 0) {
+        p.free_count_out[0] = base;
+        if (refuse)
+            flag_error(p.error_word, refuse);
+    }
+}
+
+// ---- moves --------------------------------------------------------------------------
+//
+// A warp takes kMoveRun entries of the list at a time (padding entries cost their
+// eight bytes) and copies each move's K and V rows, all of a lane's loads before its
+// stores, 16 bytes a lane.
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRun = 8;
+constexpr int kMoveWords = 8;  // of a lane at once
+
+__global__ void __launch_bounds__(kMoveThreads)
+    move_tokens_kernel(uint4 *__restrict__ key_cache, uint4 *__restrict__ value_cache,
+                       const int2 *__restrict__ moves, long long num_moves, long long num_slots,
+                       int words, int32_t *error_word)
+{
+    const int lane = threadIdx.x & 31;
+    const long long warps = (long long)gridDim.x * (kMoveThreads / 32);
+    long long run = (long long)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
+    pdl_wait_primary();
+    pdl_launch_dependents();
+    for (; run * kMoveRun < num_moves; run += warps) {
+        const long long at = run * kMoveRun + lane;
+        int2 move = make_int2(-1, -1);
+        if (lane < kMoveRun && at < num_moves)
+            move = __ldg(moves + at);
+        const bool real = move.x >= 0 && move.y >= 0;
+        const bool good = real && move.x < num_slots && move.y < num_slots;
+        if (real && !good)
+            flag_error(error_word, PA_DEVERR_SLOT_RANGE);
+        uint32_t todo = __ballot_sync(kFull, good);
+        while (todo != 0) {
+            const int k = __ffs((int)todo) - 1;
+            todo &= todo - 1;
+            const size_t src = (size_t)__shfl_sync(kFull, move.x, k) * words;
+            const size_t dst = (size_t)__shfl_sync(kFull, move.y, k) * words;
+            // words of the key row, then of the value row
+            for (int i0 = lane; i0 < 2 * words; i0 += 32 * kMoveWords) {
+                uint4 w[kMoveWords];
+#pragma unroll
+                for (int u = 0; u < kMoveWords; ++u) {
+                    const int i = i0 + 32 * u;
+                    if (i < 2 * words)
+                        w[u] = i < words ? key_cache[src + i] : value_cache[src + i - words];
+                }
+#pragma unroll
+                for (int u = 0; u < kMoveWords; ++u) {
+                    const int i = i0 + 32 * u;
+                    if (i < words)
+                        key_cache[dst + i] = w[u];
+                    else if (i < 2 * words)
+                        value_cache[dst + i - words] = w[u];
+                }
+            }
+        }
+    }
+}
+
+} // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *context_lens_out,
+                                      int32_t *free_count_out, float *weights_out,
+                                      const int32_t *block_tables, int max_blocks_per_seq,
+                                      const int32_t *context_lens, const float *weights,
+                                      int32_t *free_blocks, const int32_t *free_count,
+                                      int max_context_len, int limit, int budget, int num_sinks,
+                                      int num_recent, int num_seqs, int block_size,
+                                      int num_blocks, int32_t *error_word, void *stream)
+{
+    if (num_seqs < 0 || max_moves < 0 || max_blocks_per_seq <= 0 || block_size <= 0 ||
+        num_blocks <= 0 || max_context_len < 0 || budget <= 0 || limit < budget ||
+        num_sinks < 0 || num_recent < 0 || num_sinks > budget ||
+        num_recent > budget - num_sinks ||
+        max_moves < std::min(budget, std::max(0, max_context_len - budget)))
+        return PA_ERR_INVALID_ARG;
+    if (!free_blocks || !free_count || !free_count_out)
+        return PA_ERR_INVALID_ARG;
+    if (num_seqs > 0 && (!context_lens_out || !block_tables || !context_lens || !weights ||
+                         !weights_out || (max_moves > 0 && !moves)))
+        return PA_ERR_INVALID_ARG;
+    if ((block_size & (block_size - 1)) != 0 || (long long)num_blocks * block_size > INT32_MAX ||
+        (long long)max_blocks_per_seq * block_size > INT32_MAX || max_moves > (1 << 29))
+        return PA_ERR_UNSUPPORTED;
+    PlanParams p{};
+    p.moves = moves;
+    p.context_out = context_lens_out;
+    p.free_count_out = free_count_out;
+    p.free_blocks = free_blocks;
+    p.weights_out = weights_out;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.free_count = free_count;
+    p.weights = weights;
+    p.error_word = error_word;
+    p.max_moves = max_moves;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
+    p.limit = limit;
+    p.budget = budget;
+    p.num_sinks = num_sinks;
+    p.num_recent = num_recent;
+    p.num_seqs = num_seqs;
+    p.block_shift = __builtin_ctz((unsigned)block_size);
+    p.num_blocks = num_blocks;
+    cudaStream_t q = as_stream(stream);
+    if (num_seqs > 0) {
+        int dev = 0;
+        const cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess)
+            return record_cuda(e);
+        DeviceInfo info;
+        pa_status st = device_info(dev, &info);
+        if (st != PA_OK)
+            return st;
+        const size_t smem = (size_t)max_context_len * 4;
+        if (smem + sizeof(PlanShared) + 1024 <= (size_t)info.optin) {
+            static size_t enabled[kMaxDevices];
+            static std::mutex mu;
+            {
+                std::lock_guard<std::mutex> lock(mu);
+                if (smem > enabled[dev]) {
+                    const cudaError_t a = cudaFuncSetAttribute(
+                        plan_eviction_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                        (int)smem);
+                    if (a != cudaSuccess)
+                        return record_cuda(a);
+                    enabled[dev] = smem;
+                }
+            }
+            st = launch_pdl(plan_eviction_kernel<true>, dim3(num_seqs), dim3(kPlanThreads), smem,
+                            q, p);
+        } else {
+            st = launch_pdl(plan_eviction_kernel<false>, dim3(num_seqs), dim3(kPlanThreads), 0, q,
+                            p);
+        }
+        if (st != PA_OK)
+            return st;
+    }
+    return launch_pdl(apply_eviction_kernel, dim3(1), dim3(kPlanThreads), 0, q, p);
+}
+
+extern "C" pa_status pa_move_tokens(void *key_cache, void *value_cache, const int32_t *moves,
+                                    int64_t num_moves, int num_blocks, int block_size,
+                                    int num_kv_heads, int head_dim, pa_dtype dtype,
+                                    int32_t *error_word, void *stream)
+{
+    if (num_moves < 0 || num_blocks <= 0 || block_size <= 0 || num_kv_heads <= 0 ||
+        head_dim <= 0 || (dtype != PA_F16 && dtype != PA_BF16 && dtype != PA_FP8_E4M3))
+        return PA_ERR_INVALID_ARG;
+    if (num_moves == 0)
+        return PA_OK;
+    if (!key_cache || !value_cache || !moves || !aligned16(key_cache) ||
+        !aligned16(value_cache) || (reinterpret_cast<uintptr_t>(moves) & 7u) != 0)
+        return PA_ERR_INVALID_ARG;
+    const long long row_bytes = (long long)num_kv_heads * head_dim * (dtype == PA_FP8_E4M3 ? 1 : 2);
+    if (row_bytes % 16 != 0 || row_bytes > (1 << 24) || num_moves > (1ll << 40) ||
+        (long long)num_blocks * block_size > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return record_cuda(e);
+    DeviceInfo info;
+    const pa_status st = device_info(dev, &info);
+    if (st != PA_OK)
+        return st;
+    const long long runs = (num_moves + kMoveRun - 1) / kMoveRun, warps = kMoveThreads / 32;
+    const int grid = (int)std::min<long long>(4ll * info.sms, (runs + warps - 1) / warps);
+    return launch_pdl(move_tokens_kernel, dim3(grid), dim3(kMoveThreads), 0, as_stream(stream),
+                      static_cast<uint4 *>(key_cache), static_cast<uint4 *>(value_cache),
+                      reinterpret_cast<const int2 *>(moves), (long long)num_moves,
+                      (long long)num_blocks * block_size, (int)(row_bytes / 16), error_word);
+}

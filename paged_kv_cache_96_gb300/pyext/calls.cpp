@@ -52,6 +52,8 @@ struct Library {
     decltype(&pa_decode_attention_sparse_fp8) sparse_fp8;
     decltype(&pa_decode_attention_weights) weights;
     decltype(&pa_decode_attention_weights_fp8) weights_fp8;
+    decltype(&pa_plan_eviction) plan;
+    decltype(&pa_move_tokens) move;
 };
 Library lib;
 
@@ -588,6 +590,61 @@ pa_status decode_weights(PyObject *const *a)
                        stream);
 }
 
+pa_status plan_eviction(PyObject *const *a)
+{
+    const at::Tensor &moves = tensor(a[0], "moves"), &ctx_out = tensor(a[1], "context_lens_out"),
+                     &count_out = tensor(a[2], "free_count_out"), &pool = tensor(a[6], "weights"),
+                     &tables = tensor(a[4], "block_tables"), &ctx = tensor(a[5], "context_lens"),
+                     &stack = tensor(a[7], "free_blocks"), &count = tensor(a[8], "free_count");
+    dimensions(tables, "block_tables", 2);
+    dimensions(pool, "weights", 2);
+    dimensions(moves, "moves", 3);
+    const int64_t S = tables.size(0);
+    need(moves.size(0) == S && moves.size(2) == 2, "moves: [num_seqs, max_moves, 2] expected");
+    need(ctx.numel() == S && ctx_out.numel() == S, "one length per sequence expected");
+    const int dev = device_of(tables, "block_tables");
+    const int N = size_int(pool.size(0), "weights"), bs = size_int(pool.size(1), "weights");
+    need(stack.numel() >= N && count.numel() >= 1 && count_out.numel() >= 1,
+         "a stack of num_blocks entries and its count expected");
+    float *pw_out = weight_pool(a[3], "weights_out", N, bs, dev);
+    const float *pw = weight_pool(a[6], "weights", N, bs, dev);
+    int32_t *pm = ints(moves, "moves", dev), *pco = ints(ctx_out, "context_lens_out", dev),
+            *pno = ints(count_out, "free_count_out", dev), *ps = ints(stack, "free_blocks", dev);
+    const int32_t *pt = ints(tables, "block_tables", dev), *pc = ints(ctx, "context_lens", dev),
+                  *pn = ints(count, "free_count", dev);
+    const int max_ctx = to_int(a[9], "max_context_len"), limit = to_int(a[10], "limit"),
+              budget = to_int(a[11], "budget"), sinks = to_int(a[12], "num_sinks"),
+              recent = to_int(a[13], "num_recent");
+    const int most = size_int(moves.size(1), "moves"), mb = size_int(tables.size(1), "block_tables"),
+              seqs = size_int(S, "block_tables");
+    int32_t *err = optional_ints(a[14], "error_word", dev);
+    void *stream = queue(a[15], dev);
+    const Unlocked unlocked;
+    return lib.plan(pm, most, pco, pno, pw_out, pt, mb, pc, pw, ps, pn, max_ctx, limit, budget,
+                    sinks, recent, seqs, bs, N, err, stream);
+}
+
+pa_status move_tokens(PyObject *const *a)
+{
+    const at::Tensor &kc = tensor(a[0], "key_cache"), &vc = tensor(a[1], "value_cache"),
+                     &moves = tensor(a[2], "moves");
+    dimensions(kc, "key_cache", 4);
+    need(vc.sizes() == kc.sizes() && moves.dim() >= 1 && moves.size(-1) == 2,
+         "two pools of one shape and moves [..., 2] expected");
+    const int dev = device_of(kc, "key_cache");
+    const pa_dtype dtype = kc.scalar_type() == at::kByte ? PA_FP8_E4M3 : dtype_of(kc, "key_cache");
+    void *pk = address(kc, "key_cache", kc.scalar_type(), dev),
+         *pv = address(vc, "value_cache", kc.scalar_type(), dev);
+    const int32_t *pm = ints(moves, "moves", dev);
+    const int N = size_int(kc.size(0), "key_cache"), bs = size_int(kc.size(1), "key_cache"),
+              K = size_int(kc.size(2), "key_cache"), d = size_int(kc.size(3), "key_cache");
+    const int64_t n = moves.numel() / 2;
+    int32_t *err = optional_ints(a[3], "error_word", dev);
+    void *stream = queue(a[4], dev);
+    const Unlocked unlocked;
+    return lib.move(pk, pv, pm, n, N, bs, K, d, dtype, err, stream);
+}
+
 template <pa_status (*call)(PyObject *const *), int count>
 PyObject *entry(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -628,6 +685,8 @@ PyObject *bind(PyObject *, PyObject *path)
         find(h, "pa_decode_attention_sparse_fp8", found.sparse_fp8);
         find(h, "pa_decode_attention_weights", found.weights);
         find(h, "pa_decode_attention_weights_fp8", found.weights_fp8);
+        find(h, "pa_plan_eviction", found.plan);
+        find(h, "pa_move_tokens", found.move);
         lib = found;
         Py_RETURN_NONE;
     } catch (const PythonError &) {
@@ -648,6 +707,8 @@ PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
                          PA_ENTRY(select_blocks, 13),
                          PA_ENTRY(decode_sparse, 15),
                          PA_ENTRY(decode_weights, 17),
+                         PA_ENTRY(plan_eviction, 16),
+                         PA_ENTRY(move_tokens, 5),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, methods,

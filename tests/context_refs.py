@@ -158,3 +158,33 @@ def weights_attention(q, kc, vc, weights, tables, ctx, weighted, scale, out_dtyp
         new_tol[at, row] = err + (H + 8) * 2.0 ** -24 * total + \
             2.0 ** -24 * (before + total) + 2.0 ** -40
     return out, tol, new, new_tol
+
+
+def plan_eviction(tables, ctx, weights, free, count, bs, limit, budget, sinks, recent, capacity):
+    """(moves [S, capacity, 2], lengths, free, count, weights) by the definition; None for
+    a plan that is refused.  numpy arrays, none of them changed."""
+    free, out = free.copy(), weights.copy()
+    N = len(free)
+    moves = np.full((len(ctx), capacity, 2), -1, dtype=np.int32)
+    end = np.asarray(ctx).copy()
+    for s, c in enumerate(ctx):
+        if c <= limit:
+            continue
+        end[s] = budget
+        slot = np.array([int(tables[s][p // bs]) * bs + p % bs for p in range(c)])
+        ranked = sorted(range(sinks, c - recent),
+                        key=lambda p: (-(weights.flat[slot[p]] if weights.flat[slot[p]] > 0
+                                         else 0.0), p))
+        gone = set(ranked[budget - sinks - recent:])
+        late = [p for p in range(budget, c) if p not in gone]
+        holes = [p for p in range(budget) if p in gone]
+        assert len(late) == len(holes)
+        for i, (a, b) in enumerate(zip(late, holes)):
+            moves[s, i] = slot[a], slot[b]
+            out.flat[slot[b]] = weights.flat[slot[a]]
+        for j in range(-(-budget // bs), -(-c // bs)):
+            if count >= N:
+                return None
+            free[count] = tables[s][j]
+            count += 1
+    return moves, end, free, count, out
