@@ -292,8 +292,10 @@ __global__ void __launch_bounds__(kSumThreads)
 // takes 16 blocks, whose codes a lane loads 16 bytes at a time straight into the
 // order that the product needs (the sum over d is taken in a permuted order, which
 // whole numbers allow), widens to fp16 (exact) and multiplies with the coded heads,
-// which stay in registers.  fp16 products of codes are exact, and so are their sums
-// in fp32.  Keys that order the scores go to the first CTA's shared memory, where
+// kept in shared memory in the order of the lanes.  fp16 products of codes are exact,
+// and so are their sums in fp32.  The candidates' pool blocks are looked up all at
+// once, while the query is coded, so that a tile's loads wait for nothing but their
+// own trip.  Keys that order the scores go to the first CTA's shared memory, where
 // the smallest selected key is found digit by digit, over the bits in which the
 // keys differ at all.
 struct SelectParams {
@@ -332,21 +334,24 @@ __device__ __forceinline__ void widen_codes(uint32_t w, uint32_t &a, uint32_t &b
 
 struct SelectShared {
     float q_scale[16];
-    TopkShared topk;
+    TopkShared<8> topk;
     int above[kSelWarps], ties[kSelWarps];
 };
 
 // T: the query's type; NT: heads of a KV head in eights.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kSelThreads)
+__global__ void __launch_bounds__(kSelThreads, NT == 1 ? 4 : 2)
     select_kernel(const __grid_constant__ SelectParams p)
 {
     constexpr int kSegs = 2 * D / 64;  // 64-byte runs of a block's codes
+    static_assert(kSelWarps == 8, "a warp codes every eighth head");
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     __shared__ SelectShared sh;
-    __shared__ __align__(16) __half qs[8 * NT][2 * D];
-    extern __shared__ uint32_t keys[];
+    // B fragments of the coded heads: head 8 nt + g; product step (seg, k) of lane t4
+    // stands for codes 64 seg + 16 t4 + 4 k .. + 3 of a block's 2 D
+    __shared__ __align__(16) uint2 qf[NT][kSegs][4][32];
+    extern __shared__ uint32_t keys[];  // of all candidates; first, pool blocks
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     const int unit = (int)blockIdx.x / ctas;
@@ -359,6 +364,17 @@ __global__ void __launch_bounds__(kSelThreads)
 
     // ---- the row's context ----------------------------------------------------------
     const int s = p.token_seq[t], pos = p.token_pos[t];
+    constexpr int kHeadsPerWarp = NT;  // 8 NT heads, 8 warps
+    float x[kHeadsPerWarp][D / 32];
+#pragma unroll
+    for (int r = 0; r < kHeadsPerWarp; ++r) {
+        const int h = r * kSelWarps + warp;
+        const T *row = static_cast<const T *>(p.query) +
+                       ((size_t)t * p.num_heads + (size_t)kh * G + (h < G ? h : 0)) * D;
+#pragma unroll
+        for (int e = 0; e < D / 32; ++e)
+            x[r][e] = h < G ? (float)row[e * 32 + lane] : 0.f;
+    }
     const bool whole = rank == 0 && tid == 0 && kh == 0;  // reports for the row
     int ctx = 0;
     if (s >= 0) {
@@ -383,66 +399,61 @@ __global__ void __launch_bounds__(kSelThreads)
     const int first = p.num_first, tail = nb - p.num_last;
     const int want = top_k - p.num_first - p.num_last;
     const int n = tail - first;  // candidates, more than are wanted
+    // this CTA's tiles of 16 of them
+    const int tiles = (n + 15) / 16, share = (tiles + ctas - 1) / ctas;
+    const int tile0 = min(tiles, rank * share), tile1 = min(tiles, tile0 + share);
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq + first;
+    for (int i = tile0 * 16 + tid; i < min(n, tile1 * 16); i += kSelThreads)
+        keys[i] = (uint32_t)__ldg(table + i);
 
     // ---- the query heads' codes ------------------------------------------------------
-    for (int h = warp; h < 8 * NT; h += kSelWarps) {
-        float x[D / 32];
+#pragma unroll
+    for (int r = 0; r < kHeadsPerWarp; ++r) {
+        const int h = r * kSelWarps + warp;
         float top = 0.f;
         bool ok = true;
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
-            const T *row = static_cast<const T *>(p.query) +
-                           ((size_t)t * p.num_heads + (size_t)kh * G + (h < G ? h : 0)) * D;
-            x[e] = h < G ? (float)row[e * 32 + lane] : 0.f;
-            ok &= finite(x[e]);
-            top = fmaxf(top, fabsf(x[e]));
+            ok &= finite(x[r][e]);
+            top = fmaxf(top, fabsf(x[r][e]));
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         ok = __all_sync(kFull, ok);
         const CodeScale cs = ok ? code_scale(top) : CodeScale{0.f, 0.f};
+        __half *frag = reinterpret_cast<__half *>(&qf[h / 8][0][0][0]);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
-            const int code = ok ? __float2int_rn(__fmul_rn(x[e], cs.inv)) : 0;
-            qs[h][e * 32 + lane] = __int2half_rn(min(code, 0));
-            qs[h][D + e * 32 + lane] = __int2half_rn(max(code, 0));
+            const int code = ok ? __float2int_rn(__fmul_rn(x[r][e], cs.inv)) : 0;
+#pragma unroll
+            for (int side = 0; side < 2; ++side) {
+                const int k = side * D + e * 32 + lane;  // among a block's 2 D codes
+                const int at = ((k / 64) * 4 + k % 16 / 4) * 32 + (h % 8) * 4 + k % 64 / 16;
+                frag[at * 4 + k % 4] = __int2half_rn(side ? max(code, 0) : min(code, 0));
+            }
         }
         if (lane == 0)
             sh.q_scale[h] = cs.scale;
     }
     __syncthreads();
-    // B fragments: head 8 nt + g; product step (seg, j) of lane t4 stands for codes
-    // 64 seg + 16 t4 + 4 j .. + 3 of the block's 2 D
-    uint32_t qf[NT][kSegs][4][2];
     float q_scale[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-        for (int sg = 0; sg < kSegs; ++sg)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(
-                    &qs[nt * 8 + g][sg * 64 + t4 * 16 + j * 4]);
-                qf[nt][sg][j][0] = w.x;
-                qf[nt][sg][j][1] = w.y;
-            }
         q_scale[nt][0] = sh.q_scale[nt * 8 + 2 * t4];
         q_scale[nt][1] = sh.q_scale[nt * 8 + 2 * t4 + 1];
     }
 
     // ---- scores, 16 blocks a warp ----------------------------------------------------
     uint32_t *dst = ctas > 1 ? cluster.map_shared_rank(keys, 0) : keys;
-    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq + first;
-    const int tiles = (n + 15) / 16;
-    for (int tile = rank * kSelWarps + warp; tile < tiles; tile += ctas * kSelWarps) {
+    for (int tile = tile0 + warp; tile < tile1; tile += kSelWarps) {
         uint4 w[2][kSegs];
         float scale[2];
         bool ok[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int i = tile * 16 + g + 8 * r;
-            int phys = i < n ? __ldg(table + i) : 0;
+            int phys = i < n ? (int)keys[i] : 0;
             ok[r] = phys >= 0 && phys < p.num_blocks;
             if (!ok[r] && t4 == 0)
                 flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
@@ -468,8 +479,10 @@ __global__ void __launch_bounds__(kSelThreads)
                 widen_codes(x[j], a[0], a[2]);
                 widen_codes(y[j], a[1], a[3]);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    MmaOp<__half>::run(acc[nt], a, qf[nt][sg][j][0], qf[nt][sg][j][1]);
+                for (int nt = 0; nt < NT; ++nt) {
+                    const uint2 b = qf[nt][sg][j][lane];
+                    MmaOp<__half>::run(acc[nt], a, b.x, b.y);
+                }
             }
         }
 #pragma unroll
@@ -500,7 +513,7 @@ __global__ void __launch_bounds__(kSelThreads)
 
     // ---- the list, in ascending order ------------------------------------------------
     const Threshold cut =
-        top_threshold<kSelThreads>(sh.topk, [&](int i) { return keys[i]; }, n, want);
+        top_threshold<kSelThreads, 8>(sh.topk, [&](int i) { return keys[i]; }, n, want);
     const int run = (n + kSelThreads - 1) / kSelThreads * 32;  // candidates of a warp
     const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
     int above = 0, ties = 0;
@@ -581,7 +594,7 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     const int most = std::min<long long>(p.max_blocks_per_seq,
                                          ((long long)p.max_context_len + bs - 1) / bs);
     const size_t smem = std::max<size_t>(16, (size_t)most * 4);
-    if (smem + sizeof(SelectShared) + sizeof(__half) * 16 * NT * D + 1024 > (size_t)info.optin)
+    if (smem + sizeof(SelectShared) + 32 * NT * D + 1024 > (size_t)info.optin)
         return PA_ERR_UNSUPPORTED;
     {
         std::lock_guard<std::mutex> lock(mu);
@@ -595,7 +608,7 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     }
     const long long units = (long long)num_tokens * p.num_kv_heads;
     int ctas = 1;
-    while (ctas < 8 && units * ctas * 2 <= 2 * info.sms && most >= 256 * ctas)
+    while (ctas < 8 && units * ctas < 4 * info.sms && most >= 256 * ctas)
         ctas *= 2;
     if (units * ctas > INT32_MAX)
         return PA_ERR_UNSUPPORTED;

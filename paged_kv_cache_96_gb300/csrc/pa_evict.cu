@@ -33,6 +33,7 @@ struct PlanParams {
     int32_t *error_word;
     int max_moves, max_blocks_per_seq, max_context_len, limit, budget, num_sinks, num_recent;
     int num_seqs, block_shift, num_blocks;
+    int apply_later;  // the outputs are the inputs: they are written behind the plan
 };
 
 // What a sequence's length asks for.
@@ -54,46 +55,57 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s)
     return q;
 }
 
-// The plan is taken or refused as a whole; every CTA finds out for itself.
-__device__ __forceinline__ int plan_refusal(const PlanParams &p, long long given, bool bad)
-{
-    const int count = p.free_count[0];
-    return bad ? PA_DEVERR_CONTEXT_RANGE
-           : count < 0 || count + given > p.num_blocks ? PA_DEVERR_BLOCK_RANGE : 0;
-}
-
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
 
 struct PlanShared {
-    TopkShared topk;
+    TopkShared<11> topk;
     int above[kPlanWarps], ties[kPlanWarps];
-    long long given[kPlanWarps];
+    long long given[kPlanWarps], before[kPlanWarps];
     int low_kept;  // tokens between the first and the last ones that stay below the budget
 };
 
-// Sum and OR over the CTA.
-__device__ __forceinline__ long long plan_total(PlanShared &sh, const PlanParams &p, bool &bad)
+// Blocks that all sequences give back, and those of sequences below s; whether a
+// length is out of range.  By the whole CTA.
+struct PlanTotal {
+    long long given, before;
+    bool bad;
+};
+__device__ __forceinline__ PlanTotal plan_total(PlanShared &sh, const PlanParams &p, int s)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    long long n = 0;
-    bad = false;
-    for (int s = tid; s < p.num_seqs; s += kPlanThreads) {
-        const PlanSeq q = plan_seq(p, s);
-        n += q.have - q.keep;
-        bad |= q.bad;
+    PlanTotal t{0, 0, false};
+    for (int k = tid; k < p.num_seqs; k += kPlanThreads) {
+        const PlanSeq q = plan_seq(p, k);
+        t.given += q.have - q.keep;
+        t.before += k < s ? q.have - q.keep : 0;
+        t.bad |= q.bad;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        n += __shfl_xor_sync(kFull, n, o);
-    if (lane == 0)
-        sh.given[warp] = n;
-    bad = __syncthreads_or(bad);
-    n = 0;
+    for (int o = 16; o > 0; o >>= 1) {
+        t.given += __shfl_xor_sync(kFull, t.given, o);
+        t.before += __shfl_xor_sync(kFull, t.before, o);
+    }
+    if (lane == 0) {
+        sh.given[warp] = t.given;
+        sh.before[warp] = t.before;
+    }
+    t.bad = __syncthreads_or(t.bad);
+    t.given = t.before = 0;
 #pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w)
-        n += sh.given[w];
-    return n;
+    for (int w = 0; w < kPlanWarps; ++w) {
+        t.given += sh.given[w];
+        t.before += sh.before[w];
+    }
+    return t;
+}
+
+// The plan is taken or refused as a whole; every CTA finds out for itself.
+__device__ __forceinline__ int plan_refusal(const PlanParams &p, const PlanTotal &t)
+{
+    const int count = p.free_count[0];
+    return t.bad ? PA_DEVERR_CONTEXT_RANGE
+           : count < 0 || count + t.given > p.num_blocks ? PA_DEVERR_BLOCK_RANGE : 0;
 }
 
 // One CTA per sequence.  kKept: the keys of the whole context fit in shared memory;
@@ -109,9 +121,8 @@ __global__ void __launch_bounds__(kPlanThreads)
     pdl_wait_primary();
     pdl_launch_dependents();
 
-    bool bad;
-    const long long given = plan_total(sh, p, bad);
-    const int refuse = plan_refusal(p, given, bad);
+    const PlanTotal sum = plan_total(sh, p, s);
+    const int refuse = plan_refusal(p, sum);
     int32_t *moves = p.moves + (size_t)s * p.max_moves * 2;
     const PlanSeq q = plan_seq(p, s);
     const int bs = 1 << p.block_shift;
@@ -125,8 +136,24 @@ __global__ void __launch_bounds__(kPlanThreads)
         }
         return (b << p.block_shift) + (pos & (bs - 1));
     };
+    if (!p.apply_later && tid == 0) {
+        p.context_out[s] = refuse ? q.c : q.end;
+        if (s == 0) {
+            p.free_count_out[0] = p.free_count[0] + (refuse ? 0 : (int)sum.given);
+            if (refuse)
+                flag_error(p.error_word, refuse);
+        }
+    }
     int count = 0;  // moves
     if (refuse == 0) {
+        // blocks behind the budget onto the stack
+        int32_t *top = p.free_blocks + p.free_count[0] + sum.before;
+        for (int i = tid; i < q.have - q.keep; i += kPlanThreads) {
+            const int id = __ldg(table + q.keep + i);
+            if (id < 0 || id >= p.num_blocks)
+                flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
+            top[i] = id;
+        }
         // what stays where it is
         if (p.weights_out != p.weights)
             for (int i = tid; i < q.end; i += kPlanThreads) {
@@ -137,19 +164,31 @@ __global__ void __launch_bounds__(kPlanThreads)
         if (q.end != q.c) {
             const int first = p.num_sinks, tail = q.c - p.num_recent;  // chosen from [first, tail)
             const int n = tail - first, want = p.budget - p.num_sinks - p.num_recent;
-            auto fetch = [&](int i) {
-                const int at = slot_of(first + i);
+            auto weight_key = [&](int at) {
                 // (by its bits: a comparison would take subnormal weights for 0)
                 const int w = at >= 0 ? __float_as_int(p.weights[at]) : 0;
                 return w > 0 && w <= 0x7f800000 ? (uint32_t)w : 0u;
             };
-            auto key = [&](int i) { return kKept ? keys[i] : fetch(i); };
+            auto key = [&](int i) { return kKept ? keys[i] : weight_key(slot_of(first + i)); };
             if (kKept) {
-                for (int i = tid; i < n; i += kPlanThreads)
-                    keys[i] = fetch(i);
+                // four tokens at a time: table entries, then weights
+                for (int i0 = tid; i0 < n; i0 += 4 * kPlanThreads) {
+                    int at[4];
+                    uint32_t k[4];
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        at[u] = slot_of(first + min(i0 + u * kPlanThreads, n - 1));
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        k[u] = weight_key(at[u]);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u)
+                        if (i0 + u * kPlanThreads < n)
+                            keys[i0 + u * kPlanThreads] = k[u];
+                }
                 __syncthreads();
             }
-            const Threshold cut = top_threshold<kPlanThreads>(sh.topk, key, n, want);
+            const Threshold cut = top_threshold<kPlanThreads, 11>(sh.topk, key, n, want);
             // a warp's run of them; the tokens that stay before each run
             const int run = (n + kPlanThreads - 1) / kPlanThreads * 32;
             const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
@@ -222,70 +261,25 @@ __global__ void __launch_bounds__(kPlanThreads)
         moves[i] = -1;
 }
 
-// Lengths, the stack and its count, which may be the inputs: by one CTA behind the
-// plan, whose CTAs read every length.
+// Lengths and the stack's count where they replace the inputs, which every CTA of the
+// plan reads: one CTA behind it.  (With arrays of their own for the outputs the plan
+// writes them, and this launch, about 2 us behind it, is left out.)
 __global__ void __launch_bounds__(kPlanThreads)
     apply_eviction_kernel(const __grid_constant__ PlanParams p)
 {
     __shared__ PlanShared sh;
-    __shared__ int pushed[kPlanThreads + 1], keep_s[kPlanThreads];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait_primary();
     pdl_launch_dependents();
-    bool bad;
-    const long long given = plan_total(sh, p, bad);
-    const int refuse = plan_refusal(p, given, bad);
+    const PlanTotal t = plan_total(sh, p, 0);
+    const int refuse = plan_refusal(p, t);
     const int count = p.free_count[0];
-    __syncthreads();  // (the count and the lengths have been read)
-    int base = count;
-    for (int s0 = 0; s0 < p.num_seqs; s0 += kPlanThreads) {
-        const int s = s0 + tid;
-        int n = 0;
-        if (s < p.num_seqs) {
-            const PlanSeq q = plan_seq(p, s);
-            p.context_out[s] = refuse ? q.c : q.end;
-            n = refuse ? 0 : q.have - q.keep;
-            keep_s[tid] = q.keep;
-        }
-        int x = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int y = __shfl_up_sync(kFull, x, o);
-            if (lane >= o)
-                x += y;
-        }
-        if (lane == 31)
-            sh.above[warp] = x;
-        __syncthreads();
-        int before = 0, all = 0;
-        for (int w = 0; w < kPlanWarps; ++w) {
-            before += w < warp ? sh.above[w] : 0;
-            all += sh.above[w];
-        }
-        pushed[tid] = before + x - n;
-        __syncthreads();
-        for (int i = tid; i < all; i += kPlanThreads) {
-            int lo = 0, len = kPlanThreads;  // the last sequence with pushed <= i
-            while (len > 1) {
-                const int half = len >> 1;
-                if (pushed[lo + half] <= i) {
-                    lo += half;
-                    len -= half;
-                } else {
-                    len = half;
-                }
-            }
-            const int id = p.block_tables[(size_t)(s0 + lo) * p.max_blocks_per_seq + keep_s[lo] +
-                                          i - pushed[lo]];
-            if (id < 0 || id >= p.num_blocks)
-                flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
-            p.free_blocks[base + i] = id;
-        }
-        base += all;
-        __syncthreads();
+    __syncthreads();  // (the count has been read)
+    for (int s = threadIdx.x; s < p.num_seqs; s += kPlanThreads) {
+        const PlanSeq q = plan_seq(p, s);
+        p.context_out[s] = refuse ? q.c : q.end;
     }
-    if (tid == 0) {
-        p.free_count_out[0] = base;
+    if (threadIdx.x == 0) {
+        p.free_count_out[0] = refuse ? count : count + (int)t.given;
         if (refuse)
             flag_error(p.error_word, refuse);
     }
@@ -395,6 +389,14 @@ extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *co
     p.num_seqs = num_seqs;
     p.block_shift = __builtin_ctz((unsigned)block_size);
     p.num_blocks = num_blocks;
+    const auto apart = [](const int32_t *a, long long n, const int32_t *b, long long m) {
+        const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+        return x + 4 * n <= y || y + 4 * m <= x;
+    };
+    p.apply_later = num_seqs == 0 || !apart(context_lens_out, num_seqs, context_lens, num_seqs) ||
+                    !apart(context_lens_out, num_seqs, free_count, 1) ||
+                    !apart(free_count_out, 1, free_count, 1) ||
+                    !apart(free_count_out, 1, context_lens, num_seqs);
     cudaStream_t q = as_stream(stream);
     if (num_seqs > 0) {
         int dev = 0;
@@ -429,6 +431,8 @@ extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *co
         if (st != PA_OK)
             return st;
     }
+    if (!p.apply_later)
+        return PA_OK;
     return launch_pdl(apply_eviction_kernel, dim3(1), dim3(kPlanThreads), 0, q, p);
 }
 

@@ -845,7 +845,7 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
 // up head by head, the KV heads' sums then in order.  What bounds it: the scores, 4
 // bytes a query head and token, a KV head's being one run of memory for a warp's
 // tokens.  The sums over the context are taken anew in each CTA from the partials'
-// (m, l), a thread a query head.
+// (m, l), which are few beside the scores.
 constexpr int kWeightThreads = 256;
 constexpr int kWeightRun = 512;
 
@@ -867,23 +867,69 @@ __global__ void __launch_bounds__(kWeightThreads)
     const int ctx = clamp_context(p, s, false);
     if (first >= ctx)
         return;
+    const int seen = p.weighted_lens[s];
     float *m = sums, *inv = sums + H;
     const int parts = list_partitions(ctx, p.part_tokens);
-    for (int h = tid; h < H; h += kWeightThreads) {
-        const float *pm = p.part_m + ((size_t)s * H + h) * p.max_parts;
-        const float *pl = p.part_l + ((size_t)s * H + h) * p.max_parts;
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll 4
-        for (int j = 0; j < parts; ++j)
-            top = fmaxf(top, pm[j] * kLog2e);
-#pragma unroll 4
-        for (int j = 0; j < parts; ++j)
-            sum += pl[j] * exp2f(pm[j] * kLog2e - top);
-        m[h] = top;
-        inv[h] = __fdiv_rn(1.f, sum);
+    const float *pm = p.part_m + (size_t)s * H * p.max_parts;
+    const float *pl = p.part_l + (size_t)s * H * p.max_parts;
+    if (parts <= 4) {  // a thread a query head
+        for (int h = tid; h < H; h += kWeightThreads) {
+            float mj[4], lj[4], top = -FLT_MAX, sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mj[j] = j < parts ? pm[(size_t)h * p.max_parts + j] * kLog2e : -FLT_MAX;
+                lj[j] = j < parts ? pl[(size_t)h * p.max_parts + j] : 0.f;
+                top = fmaxf(top, mj[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                sum += lj[j] * exp2f(mj[j] - top);
+            m[h] = top;
+            inv[h] = __fdiv_rn(1.f, sum);
+        }
+    } else {  // a warp four query heads at a time, a lane a partial
+        constexpr int kWarps = kWeightThreads / 32;
+        const int lane = tid & 31;
+        for (int h0 = tid >> 5; h0 < H; h0 += 4 * kWarps) {
+            float top[4], sum[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                top[u] = -FLT_MAX;
+                sum[u] = 0.f;
+            }
+            for (int j = lane; j < parts; j += 32) {
+                float mj[4], lj[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const size_t at = (size_t)min(h0 + u * kWarps, H - 1) * p.max_parts + j;
+                    mj[u] = pm[at] * kLog2e;
+                    lj[u] = pl[at];
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float n = fmaxf(top[u], mj[u]);
+                    sum[u] = sum[u] * exp2f(top[u] - n) + lj[u] * exp2f(mj[u] - n);
+                    top[u] = n;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                float n = top[u];
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    n = fmaxf(n, __shfl_xor_sync(kFull, n, o));
+                float l = sum[u] * exp2f(top[u] - n);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1)
+                    l += __shfl_xor_sync(kFull, l, o);
+                if (lane == 0 && h0 + u * kWarps < H) {
+                    m[h0 + u * kWarps] = n;
+                    inv[h0 + u * kWarps] = __fdiv_rn(1.f, l);
+                }
+            }
+        }
     }
     __syncthreads();
-    const int seen = p.weighted_lens[s];
     const int end = min(ctx, first + kWeightRun);
     for (int pos = first + tid; pos < end; pos += kWeightThreads) {
         const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq +

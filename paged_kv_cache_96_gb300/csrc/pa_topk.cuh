@@ -6,11 +6,13 @@
 
 namespace pa {
 
-constexpr int kTopkBins = 256;
-
-struct TopkShared {
-    int hist[kTopkBins];
+// Digits of BITS bits: a histogram of 2^BITS counters.  8 bits keep a small CTA's passes
+// short; 11 spread keys that differ in their exponents most over more counters, whose
+// additions queue up otherwise.
+template <int BITS> struct TopkShared {
+    int hist[1 << BITS];
     uint32_t lo[32], hi[32];
+    int sums[32];
     int bin, rest, whole;
 };
 
@@ -26,12 +28,15 @@ struct Threshold {
 };
 
 // key(i): the key of i in [0, n), 0 <= want <= n, n > 0.  All of the CTA's THREADS
-// threads call it, with the keys visible to them; digits of 8 bits at a time, each a
-// histogram in shared memory, so that a pass over the keys is all that a digit costs.
-template <int THREADS, typename Key>
-__device__ __forceinline__ Threshold top_threshold(TopkShared &sh, const Key &key, int n, int want)
+// threads call it, with the keys visible to them; a digit costs a pass over the keys,
+// into a histogram in shared memory, and a scan of its bins.
+template <int THREADS, int BITS, typename Key>
+__device__ __forceinline__ Threshold top_threshold(TopkShared<BITS> &sh, const Key &key, int n,
+                                                   int want)
 {
     constexpr int kWarps = THREADS / 32;
+    constexpr int kBins = 1 << BITS, kOwn = kBins / THREADS;
+    static_assert(kBins % THREADS == 0, "whole bins per thread");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint32_t lo = 0xffffffffu, hi = 0u;
     for (int i = tid; i < n; i += THREADS) {
@@ -53,10 +58,11 @@ __device__ __forceinline__ Threshold top_threshold(TopkShared &sh, const Key &ke
     }
     Threshold t{lo, 0u, 32 - __clz((int)(hi - lo)), want};
     while (t.shift > 0 && t.rest > 0) {
-        const int width = min(8, t.shift);
+        const int width = min(BITS, t.shift);
         t.shift -= width;
-        for (int b = tid; b < kTopkBins; b += THREADS)
-            sh.hist[b] = 0;
+#pragma unroll
+        for (int b = 0; b < kOwn; ++b)
+            sh.hist[b * THREADS + tid] = 0;
         __syncthreads();
         for (int i = tid; i < n; i += THREADS) {
             const uint32_t v = t.level(key(i));
@@ -64,31 +70,35 @@ __device__ __forceinline__ Threshold top_threshold(TopkShared &sh, const Key &ke
                 atomicAdd(&sh.hist[v & ((1u << width) - 1)], 1);
         }
         __syncthreads();
-        if (warp == 0) {
-            // lane l has bins 8 l .. 8 l + 7; counts from the top bin down
-            int own[8], sum = 0;
+        // thread t has bins kOwn t and on; counts from the top bin down
+        int own[kOwn], sum = 0;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                own[b] = sh.hist[lane * 8 + b];
-                sum += own[b];
-            }
-            int above = sum;  // of this lane's bins and those of higher lanes
+        for (int b = 0; b < kOwn; ++b) {
+            own[b] = sh.hist[tid * kOwn + b];
+            sum += own[b];
+        }
+        int above = sum;  // of this thread's bins and those of higher lanes
 #pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int y = __shfl_down_sync(0xffffffffu, above, o);
-                if (lane + o < 32)
-                    above += y;
-            }
-            int over = above - sum;  // of higher lanes' bins
+        for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_down_sync(0xffffffffu, above, o);
+            if (lane + o < 32)
+                above += y;
+        }
+        if (lane == 0)
+            sh.sums[warp] = above;
+        __syncthreads();
+        int over = above - sum;  // of higher threads' bins
 #pragma unroll
-            for (int b = 7; b >= 0; --b) {
-                if (over < t.rest && over + own[b] >= t.rest) {
-                    sh.bin = lane * 8 + b;
-                    sh.rest = t.rest - over;
-                    sh.whole = own[b] == t.rest - over;
-                }
-                over += own[b];
+        for (int w = 1; w < kWarps; ++w)
+            over += w > warp ? sh.sums[w] : 0;
+#pragma unroll
+        for (int b = kOwn - 1; b >= 0; --b) {
+            if (over < t.rest && over + own[b] >= t.rest) {
+                sh.bin = tid * kOwn + b;
+                sh.rest = t.rest - over;
+                sh.whole = own[b] == t.rest - over;
             }
+            over += own[b];
         }
         __syncthreads();
         t.prefix = (t.prefix << width) | (uint32_t)sh.bin;
