@@ -71,6 +71,7 @@ struct SummaryParams {
 };
 
 constexpr int kSumThreads = 256;
+constexpr int kSumCtas = 5;  // resident on an SM, which the grid fills once
 constexpr int kSumSeqs = 2 * kSumThreads;  // sequences numbered at once
 
 // First block and number of blocks that the new tokens of sequence s are in.
@@ -115,7 +116,7 @@ __device__ __forceinline__ float2 pair_float(__nv_bfloat162 x) { return __bfloat
 
 // KV: __half, __nv_bfloat16, or uint8_t (e4m3 codes).
 template <typename KV, int D>
-__global__ void __launch_bounds__(kSumThreads)
+__global__ void __launch_bounds__(kSumThreads, kSumCtas)
     summarize_kernel(const __grid_constant__ SummaryParams p)
 {
     constexpr bool kFp8 = sizeof(KV) == 1;
@@ -172,30 +173,53 @@ __global__ void __launch_bounds__(kSumThreads)
             pref[seqs] = carry;
         __syncthreads();
 
-        const long long items = (long long)carry * p.num_kv_heads;
-        const long long step = (long long)gridDim.x * (kSumThreads / 32);
-        for (long long i = (long long)blockIdx.x * (kSumThreads / 32) + warp; i < items;
-             i += step) {
-            const int q = (int)(i / p.num_kv_heads);
-            const int kh = (int)(i - (long long)q * p.num_kv_heads);
+        // this warp's blocks and heads, in turn: the q-th block of all, KV head kh; the next
+        // one's pool block is on its way while one is read
+        struct Item {
+            int q, kh, live, phys;
+        };
+        const int K = p.num_kv_heads;
+        const int warps = gridDim.x * (kSumThreads / 32);
+        const int step_q = warps / K, step_kh = warps - step_q * K;
+        auto look_up = [&](Item &x) {
+            if (x.q >= carry)
+                return;
             int lo_s = 0, n_s = seqs;  // the last sequence with pref <= q
             while (n_s > 1) {
                 const int half = n_s >> 1;
-                if (pref[lo_s + half] <= q) {
+                if (pref[lo_s + half] <= x.q) {
                     lo_s += half;
                     n_s -= half;
                 } else {
                     n_s = half;
                 }
             }
-            const int blk = first[lo_s] + q - pref[lo_s];
-            const int phys = p.block_tables[(size_t)(s0 + lo_s) * p.max_blocks_per_seq + blk];
+            const int blk = first[lo_s] + x.q - pref[lo_s];
+            x.phys = p.block_tables[(size_t)(s0 + lo_s) * p.max_blocks_per_seq + blk];
+            x.live = min(bs, len[lo_s] - (blk << p.block_shift));
+        };
+        auto after = [&](Item x) {
+            x.q += step_q;
+            x.kh += step_kh;
+            if (x.kh >= K) {
+                x.kh -= K;
+                ++x.q;
+            }
+            look_up(x);
+            return x;
+        };
+        const int w0 = blockIdx.x * (kSumThreads / 32) + warp;
+        Item next{w0 / K, w0 % K, 0, 0};
+        look_up(next);
+        while (next.q < carry) {
+            const Item it = next;
+            next = after(it);
+            const int kh = it.kh, live = it.live, phys = it.phys;
             if (phys < 0 || phys >= p.num_blocks) {
                 if (lane == 0)
                     flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
                 continue;
             }
-            const int live = min(bs, len[lo_s] - (blk << p.block_shift));
             const size_t pitch = (size_t)p.num_kv_heads * kRowBytes;  // token to token
             const uint8_t *at = static_cast<const uint8_t *>(p.key_cache) +
                                 ((size_t)phys << p.block_shift) * pitch +
@@ -235,8 +259,9 @@ __global__ void __launch_bounds__(kSumThreads)
                     }
                 }
             }
-            float top = 0.f;
-            bool ok = true;
+            // the amplitude as 16 bits without a sign, which order finite values, infinities
+            // and NaN in this order, in pairs
+            uint32_t top2 = 0;
 #pragma unroll
             for (int e = 0; e < kPairs; ++e) {
 #pragma unroll
@@ -244,15 +269,17 @@ __global__ void __launch_bounds__(kSumThreads)
                     lo[e] = pair_min(lo[e], __shfl_xor_sync(kFull, lo[e], o));
                     hi[e] = pair_max(hi[e], __shfl_xor_sync(kFull, hi[e], o));
                 }
-                const float2 a = pair_float(lo[e]), b = pair_float(hi[e]);
-                ok &= finite(a.x) && finite(a.y) && finite(b.x) && finite(b.y);
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)),
-                                       fmaxf(fabsf(b.x), fabsf(b.y))));
+                const uint32_t a = *reinterpret_cast<const uint32_t *>(&lo[e]) & 0x7fff7fffu;
+                const uint32_t b = *reinterpret_cast<const uint32_t *>(&hi[e]) & 0x7fff7fffu;
+                top2 = __vmaxu2(top2, __vmaxu2(a, b));
             }
-            ok = __all_sync(kFull, ok);
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1)
-                top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+                top2 = __vmaxu2(top2, __shfl_xor_sync(kFull, top2, o));
+            const uint32_t bits = max(top2 & 0xffffu, top2 >> 16);
+            const uint32_t both = bits | bits << 16;
+            const float top = pair_float(*reinterpret_cast<const P *>(&both)).x;
+            const bool ok = finite(top);
             const CodeScale cs = ok ? code_scale(top) : CodeScale{0.f, INFINITY};
             const size_t unit = (size_t)phys * p.num_kv_heads + kh;
             if (lane == 0)
@@ -310,8 +337,12 @@ struct SelectParams {
     int num_heads, num_kv_heads, group, top_k, num_first, num_last;
 };
 
-constexpr int kSelThreads = 256;
-constexpr int kSelWarps = kSelThreads / 32;
+// Threads of a CTA: 128 where a CTA takes a whole context of at most kSelShort blocks
+// (eight CTAs an SM, so that one's selection hides behind the others' loads), 256 in
+// clusters, whose first CTA selects from more.
+constexpr int kSelShort = 1024;
+// Candidates of which one warp selects by itself.
+constexpr int kSelWarp = 512;
 
 // Keys in the scores' order.
 __device__ __forceinline__ uint32_t score_key(float x)
@@ -335,16 +366,43 @@ __device__ __forceinline__ void widen_codes(uint32_t w, uint32_t &a, uint32_t &b
 struct SelectShared {
     float q_scale[16];
     TopkShared<8> topk;
-    int above[kSelWarps], ties[kSelWarps];
+    int above[8], ties[8];
 };
 
+// A warp's list from the candidates' keys in its registers.
+template <int PER>
+__device__ __forceinline__ void warp_list(const uint32_t *keys, int n, int want, int first,
+                                          int32_t *out)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t key[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        key[j] = 32 * j + lane < n ? keys[32 * j + lane] : 0u;
+    const Threshold cut = warp_threshold(key, n, want);
+    const uint32_t below = (1u << lane) - 1;
+    int above = 0, ties = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int i = 32 * j + lane;
+        const uint32_t v = cut.level(key[j]);
+        const bool over = i < n && v > cut.prefix, tie = i < n && v == cut.prefix;
+        const uint32_t over_m = __ballot_sync(kFull, over), tie_m = __ballot_sync(kFull, tie);
+        const int my_ties = ties + __popc(tie_m & below);
+        if (over || (tie && my_ties < cut.rest))
+            out[first + above + __popc(over_m & below) + min(my_ties, cut.rest)] = first + i;
+        above += __popc(over_m);
+        ties += __popc(tie_m);
+    }
+}
+
 // T: the query's type; NT: heads of a KV head in eights.
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kSelThreads, NT == 1 ? 4 : 2)
+template <typename T, int D, int NT, int kSelThreads>
+__global__ void __launch_bounds__(kSelThreads, (NT == 1 ? 1024 : 512) / kSelThreads)
     select_kernel(const __grid_constant__ SelectParams p)
 {
     constexpr int kSegs = 2 * D / 64;  // 64-byte runs of a block's codes
-    static_assert(kSelWarps == 8, "a warp codes every eighth head");
+    constexpr int kSelWarps = kSelThreads / 32;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
     __shared__ SelectShared sh;
@@ -364,7 +422,7 @@ __global__ void __launch_bounds__(kSelThreads, NT == 1 ? 4 : 2)
 
     // ---- the row's context ----------------------------------------------------------
     const int s = p.token_seq[t], pos = p.token_pos[t];
-    constexpr int kHeadsPerWarp = NT;  // 8 NT heads, 8 warps
+    constexpr int kHeadsPerWarp = 8 * NT / kSelWarps;
     float x[kHeadsPerWarp][D / 32];
 #pragma unroll
     for (int r = 0; r < kHeadsPerWarp; ++r) {
@@ -422,16 +480,17 @@ __global__ void __launch_bounds__(kSelThreads, NT == 1 ? 4 : 2)
             top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         ok = __all_sync(kFull, ok);
         const CodeScale cs = ok ? code_scale(top) : CodeScale{0.f, 0.f};
-        __half *frag = reinterpret_cast<__half *>(&qf[h / 8][0][0][0]);
+        // element k = 32 e + lane of a side: product step k % 16 / 4 of run k / 64, lane
+        // 4 (h % 8) + k % 64 / 16 of the fragment, half k % 4 of its four
+        __half *frag = reinterpret_cast<__half *>(&qf[h / 8][0][(lane & 15) >> 2][0]) +
+                       4 * (4 * (h & 7) + (lane >> 4)) + (lane & 3);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
             const int code = ok ? __float2int_rn(__fmul_rn(x[r][e], cs.inv)) : 0;
-#pragma unroll
-            for (int side = 0; side < 2; ++side) {
-                const int k = side * D + e * 32 + lane;  // among a block's 2 D codes
-                const int at = ((k / 64) * 4 + k % 16 / 4) * 32 + (h % 8) * 4 + k % 64 / 16;
-                frag[at * 4 + k % 4] = __int2half_rn(side ? max(code, 0) : min(code, 0));
-            }
+            // (a run is 4 x 32 fragments of four halves)
+            __half *at = frag + e / 2 * 512 + e % 2 * 8;
+            at[0] = __int2half_rn(min(code, 0));
+            at[D / 64 * 512] = __int2half_rn(max(code, 0));
         }
         if (lane == 0)
             sh.q_scale[h] = cs.scale;
@@ -512,6 +571,17 @@ __global__ void __launch_bounds__(kSelThreads, NT == 1 ? 4 : 2)
         return;
 
     // ---- the list, in ascending order ------------------------------------------------
+    for (int i = tid; i < first; i += kSelThreads)
+        out[i] = i;
+    for (int i = tid; i < p.num_last; i += kSelThreads)
+        out[top_k - p.num_last + i] = tail + i;
+    if (n <= kSelWarp) {
+        if (warp == 0 && n <= kSelWarp / 2)
+            warp_list<kSelWarp / 64>(keys, n, want, first, out);
+        else if (warp == 0)
+            warp_list<kSelWarp / 32>(keys, n, want, first, out);
+        return;
+    }
     const Threshold cut =
         top_threshold<kSelThreads, 8>(sh.topk, [&](int i) { return keys[i]; }, n, want);
     const int run = (n + kSelThreads - 1) / kSelThreads * 32;  // candidates of a warp
@@ -546,10 +616,6 @@ __global__ void __launch_bounds__(kSelThreads, NT == 1 ? 4 : 2)
         above += __popc(over_m);
         ties += __popc(tie_m);
     }
-    for (int i = tid; i < first; i += kSelThreads)
-        out[i] = i;
-    for (int i = tid; i < p.num_last; i += kSelThreads)
-        out[top_k - p.num_last + i] = tail + i;
 }
 
 // ---- host side -------------------------------------------------------------------
@@ -573,16 +639,24 @@ static pa_status launch_summary(const SummaryParams &p, int head_dim, int sms,
     // CTAs that the device holds at once, or a warp for every block that there can be
     const long long most = (long long)p.num_seqs * p.max_blocks_per_seq * p.num_kv_heads;
     const long long warps = kSumThreads / 32;
-    const int grid = (int)std::min<long long>(8ll * sms, (most + warps - 1) / warps);
+    const int grid = (int)std::min<long long>(kSumCtas * (long long)sms, (most + warps - 1) / warps);
     return head_dim == 128
                ? launch_pdl(summarize_kernel<KV, 128>, dim3(grid), dim3(kSumThreads), 0, stream, p)
                : launch_pdl(summarize_kernel<KV, 64>, dim3(grid), dim3(kSumThreads), 0, stream, p);
 }
 
-template <typename T, int D, int NT>
+// Blocks that a context can have, at most.
+static int select_blocks_max(const SelectParams &p)
+{
+    const int bs = 1 << p.block_shift;
+    return (int)std::min<long long>(p.max_blocks_per_seq,
+                                    ((long long)p.max_context_len + bs - 1) / bs);
+}
+
+template <typename T, int D, int NT, int THREADS>
 static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream_t stream)
 {
-    auto kernel = select_kernel<T, D, NT>;
+    auto kernel = select_kernel<T, D, NT, THREADS>;
     static size_t enabled[kMaxDevices];
     static std::mutex mu;
     int dev = 0;
@@ -590,9 +664,7 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     const pa_status st = current_device(&dev, &info);
     if (st != PA_OK)
         return st;
-    const int bs = 1 << p.block_shift;
-    const int most = std::min<long long>(p.max_blocks_per_seq,
-                                         ((long long)p.max_context_len + bs - 1) / bs);
+    const int most = select_blocks_max(p);
     const size_t smem = std::max<size_t>(16, (size_t)most * 4);
     if (smem + sizeof(SelectShared) + 32 * NT * D + 1024 > (size_t)info.optin)
         return PA_ERR_UNSUPPORTED;
@@ -608,13 +680,13 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     }
     const long long units = (long long)num_tokens * p.num_kv_heads;
     int ctas = 1;
-    while (ctas < 8 && units * ctas < 4 * info.sms && most >= 256 * ctas)
+    while (ctas < 8 && units * ctas < 1024 / THREADS * info.sms && most >= 256 * ctas)
         ctas *= 2;
     if (units * ctas > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * ctas));
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -629,16 +701,24 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     return record_cuda(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
+template <typename T, int D, int NT>
+static pa_status select_sized(const SelectParams &p, int num_tokens, cudaStream_t stream)
+{
+    return select_blocks_max(p) <= kSelShort
+               ? launch_select<T, D, NT, 128>(p, num_tokens, stream)
+               : launch_select<T, D, NT, 256>(p, num_tokens, stream);
+}
+
 template <typename T>
 static pa_status select_as(const SelectParams &p, int head_dim, int num_tokens,
                            cudaStream_t stream)
 {
     const bool wide = p.group > 8;
     if (head_dim == 128)
-        return wide ? launch_select<T, 128, 2>(p, num_tokens, stream)
-                    : launch_select<T, 128, 1>(p, num_tokens, stream);
-    return wide ? launch_select<T, 64, 2>(p, num_tokens, stream)
-                : launch_select<T, 64, 1>(p, num_tokens, stream);
+        return wide ? select_sized<T, 128, 2>(p, num_tokens, stream)
+                    : select_sized<T, 128, 1>(p, num_tokens, stream);
+    return wide ? select_sized<T, 64, 2>(p, num_tokens, stream)
+                : select_sized<T, 64, 1>(p, num_tokens, stream);
 }
 
 } // namespace pa

@@ -57,6 +57,7 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s)
 
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWarps = kPlanThreads / 32;
+constexpr int kPlanBatch = 4;
 
 struct PlanShared {
     TopkShared<11> topk;
@@ -108,33 +109,42 @@ __device__ __forceinline__ int plan_refusal(const PlanParams &p, const PlanTotal
            : count < 0 || count + t.given > p.num_blocks ? PA_DEVERR_BLOCK_RANGE : 0;
 }
 
-// One CTA per sequence.  kKept: the keys of the whole context fit in shared memory;
-// else each pass reads the weights again, through L2.
+// One CTA per sequence.  kKept: the keys of the whole context, and its table row, fit in
+// shared memory; else each pass reads the weights again, through L2.
 template <bool kKept>
 __global__ void __launch_bounds__(kPlanThreads)
     plan_eviction_kernel(const __grid_constant__ PlanParams p)
 {
     __shared__ PlanShared sh;
-    extern __shared__ uint32_t keys[];
+    extern __shared__ uint32_t keys[];  // then the table row
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int s = blockIdx.x;
     pdl_wait_primary();
     pdl_launch_dependents();
 
-    const PlanTotal sum = plan_total(sh, p, s);
-    const int refuse = plan_refusal(p, sum);
     int32_t *moves = p.moves + (size_t)s * p.max_moves * 2;
     const PlanSeq q = plan_seq(p, s);
     const int bs = 1 << p.block_shift;
     const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq;
-    const int slots = p.num_blocks << p.block_shift;
-    auto slot_of = [&](int pos) {
-        const int b = __ldg(table + (pos >> p.block_shift));
-        if (b < 0 || b >= p.num_blocks) {
+    int *row = reinterpret_cast<int *>(keys) + p.max_context_len;
+    // a pool block, -1 (flagged) for one that is not in the pool
+    auto block_of = [&](int b) {
+        const int id = __ldg(table + b);
+        if (id < 0 || id >= p.num_blocks) {
             flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
             return -1;
         }
-        return (b << p.block_shift) + (pos & (bs - 1));
+        return id;
+    };
+    if (kKept)
+        for (int b = tid; b < q.have; b += kPlanThreads)
+            row[b] = block_of(b);
+    const PlanTotal sum = plan_total(sh, p, s);  // (with a barrier)
+    const int refuse = plan_refusal(p, sum);
+    const int slots = p.num_blocks << p.block_shift;
+    auto slot_of = [&](int pos) {
+        const int b = kKept ? row[pos >> p.block_shift] : block_of(pos >> p.block_shift);
+        return b < 0 ? -1 : (b << p.block_shift) + (pos & (bs - 1));
     };
     if (!p.apply_later && tid == 0) {
         p.context_out[s] = refuse ? q.c : q.end;
@@ -154,40 +164,46 @@ __global__ void __launch_bounds__(kPlanThreads)
                 flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
             top[i] = id;
         }
-        // what stays where it is
-        if (p.weights_out != p.weights)
-            for (int i = tid; i < q.end; i += kPlanThreads) {
-                const int at = slot_of(i);
-                if (at >= 0)
-                    p.weights_out[at] = p.weights[at];
+        const int first = p.num_sinks, tail = q.c - p.num_recent;  // chosen from [first, tail)
+        const int n = q.end != q.c ? tail - first : 0;
+        // (by its bits: a comparison would take subnormal weights for 0)
+        auto weight_key = [](float weight) {
+            const int w = __float_as_int(weight);
+            return w > 0 && w <= 0x7f800000 ? (uint32_t)w : 0u;
+        };
+        // keys of the candidates, and the weights below the new length in their places;
+        // kPlanBatch tokens of a thread at a time
+        const bool apart = p.weights_out != p.weights;
+        const int reach = kKept && n > 0 ? max(tail, q.end) : apart ? q.end : 0;
+        for (int i0 = tid; i0 < reach; i0 += kPlanBatch * kPlanThreads) {
+            int at[kPlanBatch];
+            float w[kPlanBatch];
+#pragma unroll
+            for (int u = 0; u < kPlanBatch; ++u)
+                at[u] = slot_of(min(i0 + u * kPlanThreads, reach - 1));
+#pragma unroll
+            for (int u = 0; u < kPlanBatch; ++u)
+                w[u] = at[u] >= 0 ? p.weights[at[u]] : 0.f;
+#pragma unroll
+            for (int u = 0; u < kPlanBatch; ++u) {
+                const int i = i0 + u * kPlanThreads;
+                if (i >= reach)
+                    continue;
+                if (apart && i < q.end && at[u] >= 0)
+                    p.weights_out[at[u]] = w[u];
+                if (kKept && i >= first && i < first + n)
+                    keys[i - first] = weight_key(w[u]);
             }
-        if (q.end != q.c) {
-            const int first = p.num_sinks, tail = q.c - p.num_recent;  // chosen from [first, tail)
-            const int n = tail - first, want = p.budget - p.num_sinks - p.num_recent;
-            auto weight_key = [&](int at) {
-                // (by its bits: a comparison would take subnormal weights for 0)
-                const int w = at >= 0 ? __float_as_int(p.weights[at]) : 0;
-                return w > 0 && w <= 0x7f800000 ? (uint32_t)w : 0u;
+        }
+        __syncthreads();
+        if (n > 0) {
+            const int want = p.budget - p.num_sinks - p.num_recent;
+            auto key = [&](int i) {
+                if (kKept)
+                    return keys[i];
+                const int at = slot_of(first + i);
+                return at >= 0 ? weight_key(p.weights[at]) : 0u;
             };
-            auto key = [&](int i) { return kKept ? keys[i] : weight_key(slot_of(first + i)); };
-            if (kKept) {
-                // four tokens at a time: table entries, then weights
-                for (int i0 = tid; i0 < n; i0 += 4 * kPlanThreads) {
-                    int at[4];
-                    uint32_t k[4];
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        at[u] = slot_of(first + min(i0 + u * kPlanThreads, n - 1));
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        k[u] = weight_key(at[u]);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        if (i0 + u * kPlanThreads < n)
-                            keys[i0 + u * kPlanThreads] = k[u];
-                }
-                __syncthreads();
-            }
             const Threshold cut = top_threshold<kPlanThreads, 11>(sh.topk, key, n, want);
             // a warp's run of them; the tokens that stay before each run
             const int run = (n + kPlanThreads - 1) / kPlanThreads * 32;
@@ -291,10 +307,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 // eight bytes) and copies each move's K and V rows, all of a lane's loads before its
 // stores, 16 bytes a lane.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRun = 8;
+constexpr int kMoveRun = 4;
 constexpr int kMoveWords = 8;  // of a lane at once
+constexpr int kMoveCtas = 4;   // resident on an SM, which the grid fills once
 
-__global__ void __launch_bounds__(kMoveThreads)
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas)
     move_tokens_kernel(uint4 *__restrict__ key_cache, uint4 *__restrict__ value_cache,
                        const int2 *__restrict__ moves, long long num_moves, long long num_slots,
                        int words, int32_t *error_word)
@@ -407,7 +424,10 @@ extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *co
         pa_status st = device_info(dev, &info);
         if (st != PA_OK)
             return st;
-        const size_t smem = (size_t)max_context_len * 4;
+        const size_t smem = ((size_t)max_context_len +
+                             std::min<size_t>((size_t)max_blocks_per_seq,
+                                              ((size_t)max_context_len + block_size - 1) /
+                                                  block_size)) * 4;
         if (smem + sizeof(PlanShared) + 1024 <= (size_t)info.optin) {
             static size_t enabled[kMaxDevices];
             static std::mutex mu;
@@ -462,7 +482,7 @@ extern "C" pa_status pa_move_tokens(void *key_cache, void *value_cache, const in
     if (st != PA_OK)
         return st;
     const long long runs = (num_moves + kMoveRun - 1) / kMoveRun, warps = kMoveThreads / 32;
-    const int grid = (int)std::min<long long>(4ll * info.sms, (runs + warps - 1) / warps);
+    const int grid = (int)std::min<long long>(kMoveCtas * (long long)info.sms, (runs + warps - 1) / warps);
     return launch_pdl(move_tokens_kernel, dim3(grid), dim3(kMoveThreads), 0, as_stream(stream),
                       static_cast<uint4 *>(key_cache), static_cast<uint4 *>(value_cache),
                       reinterpret_cast<const int2 *>(moves), (long long)num_moves,

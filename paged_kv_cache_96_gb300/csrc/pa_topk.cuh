@@ -111,4 +111,45 @@ __device__ __forceinline__ Threshold top_threshold(TopkShared<BITS> &sh, const K
     return t;
 }
 
+// The same for at most 32 PER keys, by one warp with the keys in registers: key j of
+// lane l is that of 32 j + l.  One bit of the threshold at a time, with a count over
+// the warp, and no barrier of the CTA.
+template <int PER>
+__device__ __forceinline__ Threshold warp_threshold(const uint32_t (&key)[PER], int n, int want)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t lo = 0xffffffffu, hi = 0u;
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        if (32 * j + lane < n) {
+            lo = min(lo, key[j]);
+            hi = max(hi, key[j]);
+        }
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    // (the keys that are not there are as low as any, and no bit counts them)
+    uint32_t v[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j)
+        v[j] = 32 * j + lane < n ? key[j] - lo : 0u;
+    auto count = [&](uint32_t least) {
+        int c = 0;
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            c += v[j] >= least;
+        return __reduce_add_sync(0xffffffffu, c);
+    };
+    Threshold t{lo, 0u, 0, want};
+    for (int b = 31 - __clz((int)(hi - lo)); b >= 0; --b) {
+        const uint32_t least = t.prefix | (1u << b);
+        const int c = count(least);
+        if (c >= want)
+            t.prefix = least;
+        if (c == want)
+            break;
+    }
+    t.rest = want - (t.prefix == 0xffffffffu ? 0 : count(t.prefix + 1));
+    return t;
+}
+
 } // namespace pa
