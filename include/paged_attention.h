@@ -613,8 +613,8 @@ PA_API pa_status pa_summarize_blocks(int8_t *summaries, float *summary_scales,
  *               clipped and set PA_DEVERR_CONTEXT_RANGE)
  * A table entry outside [0, num_blocks) sets PA_DEVERR_BLOCK_RANGE and has the lowest
  * score.  num_first + num_last <= top_k (PA_ERR_INVALID_ARG otherwise).
- * Supported: as pa_decode_attention, and at most about 55,000 blocks of
- * max_context_len (their scores are kept in shared memory).
+ * Supported: as pa_decode_attention, where the scores of max_context_len's blocks
+ * and a few lists fit the shared memory of eight CTAs (300,000 blocks at top_k 128).
  */
 PA_API pa_status pa_select_blocks(int32_t *selected, int top_k, const void *query,
                                   const int8_t *summaries, const float *summary_scales,

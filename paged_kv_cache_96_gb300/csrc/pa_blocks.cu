@@ -313,18 +313,21 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas)
 
 // ---- selection ------------------------------------------------------------------
 //
-// One CTA, or a cluster of them, per (row, KV head).  What bounds it: HBM where
-// contexts are long (2 d + 4 bytes a block), else the chain of dependent loads and
-// barriers.  The score product runs on the tensor cores as blocks x heads: a warp
-// takes 16 blocks, whose codes a lane loads 16 bytes at a time straight into the
-// order that the product needs (the sum over d is taken in a permuted order, which
-// whole numbers allow), widens to fp16 (exact) and multiplies with the coded heads,
-// kept in shared memory in the order of the lanes.  fp16 products of codes are exact,
-// and so are their sums in fp32.  The candidates' pool blocks are looked up all at
-// once, while the query is coded, so that a tile's loads wait for nothing but their
-// own trip.  Keys that order the scores go to the first CTA's shared memory, where
-// the smallest selected key is found digit by digit, over the bits in which the
-// keys differ at all.
+// One CTA, or a cluster of them, per (row, KV head).  What bounds it: the chain of
+// dependent trips to memory -- the row's position, its table row, the blocks' codes -- and
+// the selection behind it; with many long contexts HBM (2 d + 4 bytes a block).
+//  * The candidates' pool blocks are looked up all at once, while the query is coded.  CTAs
+//    are small, several on an SM, so that one's selection hides behind the others' loads
+//    (copies into rings of shared memory in place of loads to registers leave room for
+//    fewer, and a second tile's registers cost what they bring).
+//  * The score product runs on the tensor cores as blocks x heads.  A lane's 16 bytes are
+//    taken in the order in which they lie (the sum over d is in a permuted order, which
+//    whole numbers allow), widened to fp16 (exact) and multiplied with the coded heads,
+//    kept in shared memory in the lanes' order.  fp16 products of codes are exact, and so
+//    are their sums in fp32.
+//  * Each CTA selects from its own candidates as many as are wanted of all, by one warp
+//    from its registers where they are few; the first CTA of a cluster selects from those
+//    lists, which come to its shared memory.
 struct SelectParams {
     int32_t *selected;  // [T][Hkv][top_k]
     const void *query;
@@ -337,12 +340,18 @@ struct SelectParams {
     int num_heads, num_kv_heads, group, top_k, num_first, num_last;
 };
 
-// Threads of a CTA: 128 where a CTA takes a whole context of at most kSelShort blocks
-// (eight CTAs an SM, so that one's selection hides behind the others' loads), 256 in
-// clusters, whose first CTA selects from more.
-constexpr int kSelShort = 1024;
-// Candidates of which one warp selects by itself.
-constexpr int kSelWarp = 512;
+// Threads of a CTA and CTAs that an SM holds.  Without clusters: 6 of 128 threads 21.2 us
+// for 128 decode rows, 4 of 256 22.1, 8 of 128 (which spill) 23.5; in clusters, whose
+// first CTA selects from more: 4 of 256 33 us for 24 rows of up to 4,096 blocks, 6 of
+// 128 39.
+__host__ __device__ constexpr int sel_threads(bool clusters) { return clusters ? 256 : 128; }
+__host__ __device__ constexpr int sel_resident(bool clusters) { return clusters ? 4 : 6; }
+// Shared memory of an SM in percent: the L1 takes the loads under way, and a larger share
+// than the CTAs need cuts them short (128 decode rows 35 us with all of it).
+constexpr int kSelCarveout = 50;
+constexpr int kSelWarp = 512;    // candidates of which one warp selects by itself
+constexpr int kSelCluster = 8;   // CTAs of a row and KV head, at most
+constexpr int kSelShare = 256;   // candidates of a CTA in a cluster, at least
 
 // Keys in the scores' order.
 __device__ __forceinline__ uint32_t score_key(float x)
@@ -369,10 +378,27 @@ struct SelectShared {
     int above[8], ties[8];
 };
 
-// A warp's list from the candidates' keys in its registers.
-template <int PER>
-__device__ __forceinline__ void warp_list(const uint32_t *keys, int n, int want, int first,
-                                          int32_t *out)
+// emit(i, place) for each of a warp's 32 keys from i = base on that is selected, in order;
+// `above` and `ties` count the ones before.
+template <typename Emit>
+__device__ __forceinline__ void emit_run(const Threshold &cut, uint32_t key, int base, int end,
+                                         int &above, int &ties, const Emit &emit)
+{
+    const int lane = threadIdx.x & 31, i = base + lane;
+    const uint32_t below = (1u << lane) - 1, v = cut.level(key);
+    const bool over = i < end && v > cut.prefix, tie = i < end && v == cut.prefix;
+    const uint32_t over_m = __ballot_sync(kFull, over), tie_m = __ballot_sync(kFull, tie);
+    const int my_ties = ties + __popc(tie_m & below);
+    if (over || (tie && my_ties < cut.rest))
+        emit(i, above + __popc(over_m & below) + min(my_ties, cut.rest));
+    above += __popc(over_m);
+    ties += __popc(tie_m);
+}
+
+// A warp's selection from at most 32 PER keys.
+template <int PER, typename Emit>
+__device__ __forceinline__ void warp_select(const uint32_t *keys, int n, int want,
+                                            const Emit &emit)
 {
     const int lane = threadIdx.x & 31;
     uint32_t key[PER];
@@ -380,53 +406,94 @@ __device__ __forceinline__ void warp_list(const uint32_t *keys, int n, int want,
     for (int j = 0; j < PER; ++j)
         key[j] = 32 * j + lane < n ? keys[32 * j + lane] : 0u;
     const Threshold cut = warp_threshold(key, n, want);
-    const uint32_t below = (1u << lane) - 1;
     int above = 0, ties = 0;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-        const int i = 32 * j + lane;
-        const uint32_t v = cut.level(key[j]);
-        const bool over = i < n && v > cut.prefix, tie = i < n && v == cut.prefix;
-        const uint32_t over_m = __ballot_sync(kFull, over), tie_m = __ballot_sync(kFull, tie);
-        const int my_ties = ties + __popc(tie_m & below);
-        if (over || (tie && my_ties < cut.rest))
-            out[first + above + __popc(over_m & below) + min(my_ties, cut.rest)] = first + i;
-        above += __popc(over_m);
-        ties += __popc(tie_m);
-    }
+    for (int j = 0; j < PER; ++j)
+        emit_run(cut, key[j], 32 * j, n, above, ties, emit);
 }
 
-// T: the query's type; NT: heads of a KV head in eights.
-template <typename T, int D, int NT, int kSelThreads>
-__global__ void __launch_bounds__(kSelThreads, (NT == 1 ? 1024 : 512) / kSelThreads)
+// emit(i, place) for the `want` largest of keys [0, n), the lower of equal ones, in order
+// of i.  By the whole CTA, behind a barrier; its threads come back at their own time.
+template <int THREADS, typename Emit>
+__device__ __forceinline__ void cta_select(SelectShared &sh, const uint32_t *keys, int n, int want,
+                                           const Emit &emit)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (n <= kSelWarp) {
+        if (warp == 0 && n <= kSelWarp / 2)
+            warp_select<kSelWarp / 64>(keys, n, want, emit);
+        else if (warp == 0)
+            warp_select<kSelWarp / 32>(keys, n, want, emit);
+        return;
+    }
+    const Threshold cut =
+        top_threshold<THREADS, 8>(sh.topk, [&](int i) { return keys[i]; }, n, want);
+    const int run = (n + THREADS - 1) / THREADS * 32;  // keys of a warp
+    const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
+    int above = 0, ties = 0;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const uint32_t v = cut.level(keys[i]);
+        above += v > cut.prefix;
+        ties += v == cut.prefix;
+    }
+    above = __reduce_add_sync(kFull, above);
+    ties = __reduce_add_sync(kFull, ties);
+    if (lane == 0) {
+        sh.above[warp] = above;
+        sh.ties[warp] = ties;
+    }
+    __syncthreads();
+    above = ties = 0;
+    for (int w = 0; w < warp; ++w) {
+        above += sh.above[w];
+        ties += sh.ties[w];
+    }
+    for (int b = i0; b < i1; b += 32)
+        emit_run(cut, b + lane < i1 ? keys[b + lane] : 0u, b, i1, above, ties, emit);
+}
+
+// Shared memory of a CTA: the keys of its candidates and, in a cluster's first CTA, the
+// lists of all of them.
+static size_t select_bytes(int share, int ctas, int want)
+{
+    return 4 * (size_t)share + (ctas > 1 ? 8 * (size_t)ctas * want : 0);
+}
+
+// T: the query's type; NT: heads of a KV head in eights.  kClusters: for clusters of
+// several CTAs.
+template <typename T, int D, int NT, bool kClusters>
+__global__ void __launch_bounds__(sel_threads(kClusters), sel_resident(kClusters) / NT)
     select_kernel(const __grid_constant__ SelectParams p)
 {
     constexpr int kSegs = 2 * D / 64;  // 64-byte runs of a block's codes
-    constexpr int kSelWarps = kSelThreads / 32;
-    cg::cluster_group cluster = cg::this_cluster();
-    const int rank = (int)cluster.block_rank(), ctas = (int)cluster.num_blocks();
+    constexpr int kThreads = sel_threads(kClusters), kWarps = kThreads / 32;
+    int rank = 0, ctas = 1;
+    if constexpr (kClusters) {
+        rank = (int)cg::this_cluster().block_rank();
+        ctas = (int)cg::this_cluster().num_blocks();
+    }
     __shared__ SelectShared sh;
     // B fragments of the coded heads: head 8 nt + g; product step (seg, k) of lane t4
     // stands for codes 64 seg + 16 t4 + 4 k .. + 3 of a block's 2 D
     __shared__ __align__(16) uint2 qf[NT][kSegs][4][32];
-    extern __shared__ uint32_t keys[];  // of all candidates; first, pool blocks
+    extern __shared__ uint32_t keys[];  // of this CTA's candidates; first, pool blocks
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
     const int unit = (int)blockIdx.x / ctas;
     const int t = unit / p.num_kv_heads, kh = unit - t * p.num_kv_heads;
     const int G = p.group, top_k = p.top_k;
-    if (ctas > 1)
-        cluster.sync();  // the first CTA's shared memory is there to be written
+    if constexpr (kClusters)
+        cg::this_cluster().sync();  // the first CTA's shared memory is there to be written
     pdl_wait_primary();
     pdl_launch_dependents();
 
     // ---- the row's context ----------------------------------------------------------
     const int s = p.token_seq[t], pos = p.token_pos[t];
-    constexpr int kHeadsPerWarp = 8 * NT / kSelWarps;
+    constexpr int kHeadsPerWarp = 8 * NT / kWarps;
     float x[kHeadsPerWarp][D / 32];
 #pragma unroll
     for (int r = 0; r < kHeadsPerWarp; ++r) {
-        const int h = r * kSelWarps + warp;
+        const int h = r * kWarps + warp;
         const T *row = static_cast<const T *>(p.query) +
                        ((size_t)t * p.num_heads + (size_t)kh * G + (h < G ? h : 0)) * D;
 #pragma unroll
@@ -450,24 +517,25 @@ __global__ void __launch_bounds__(kSelThreads, (NT == 1 ? 1024 : 512) / kSelThre
     int32_t *out = p.selected + (size_t)unit * top_k;
     if (nb <= top_k) {
         if (rank == 0)
-            for (int i = tid; i < top_k; i += kSelThreads)
+            for (int i = tid; i < top_k; i += kThreads)
                 out[i] = i < nb ? i : -1;
         return;
     }
     const int first = p.num_first, tail = nb - p.num_last;
     const int want = top_k - p.num_first - p.num_last;
     const int n = tail - first;  // candidates, more than are wanted
-    // this CTA's tiles of 16 of them
-    const int tiles = (n + 15) / 16, share = (tiles + ctas - 1) / ctas;
-    const int tile0 = min(tiles, rank * share), tile1 = min(tiles, tile0 + share);
-    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq + first;
-    for (int i = tile0 * 16 + tid; i < min(n, tile1 * 16); i += kSelThreads)
+    // this CTA's candidates [c0, c0 + own), in tiles of 16
+    const int share = ((n + 15) / 16 + ctas - 1) / ctas * 16;
+    const int c0 = min(n, rank * share), own = min(n, c0 + share) - c0;
+    const int tiles = (own + 15) / 16;
+    const int32_t *table = p.block_tables + (size_t)s * p.max_blocks_per_seq + first + c0;
+    for (int i = tid; i < own; i += kThreads)
         keys[i] = (uint32_t)__ldg(table + i);
 
     // ---- the query heads' codes ------------------------------------------------------
 #pragma unroll
     for (int r = 0; r < kHeadsPerWarp; ++r) {
-        const int h = r * kSelWarps + warp;
+        const int h = r * kWarps + warp;
         float top = 0.f;
         bool ok = true;
 #pragma unroll
@@ -496,26 +564,23 @@ __global__ void __launch_bounds__(kSelThreads, (NT == 1 ? 1024 : 512) / kSelThre
             sh.q_scale[h] = cs.scale;
     }
     __syncthreads();
+
+    // ---- scores, 16 blocks a warp ----------------------------------------------------
     float q_scale[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
         q_scale[nt][0] = sh.q_scale[nt * 8 + 2 * t4];
         q_scale[nt][1] = sh.q_scale[nt * 8 + 2 * t4 + 1];
     }
-
-    // ---- scores, 16 blocks a warp ----------------------------------------------------
-    uint32_t *dst = ctas > 1 ? cluster.map_shared_rank(keys, 0) : keys;
-    for (int tile = tile0 + warp; tile < tile1; tile += kSelWarps) {
+    for (int tile = warp; tile < tiles; tile += kWarps) {
         uint4 w[2][kSegs];
         float scale[2];
         bool ok[2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int i = tile * 16 + g + 8 * r;
-            int phys = i < n ? (int)keys[i] : 0;
+            int phys = i < own ? (int)keys[i] : 0;
             ok[r] = phys >= 0 && phys < p.num_blocks;
-            if (!ok[r] && t4 == 0)
-                flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
             phys = ok[r] ? phys : 0;
             const size_t at = (size_t)phys * p.num_kv_heads + kh;
             const uint4 *src = reinterpret_cast<const uint4 *>(p.codes + at * 2 * D) + t4;
@@ -530,13 +595,13 @@ __global__ void __launch_bounds__(kSelThreads, (NT == 1 ? 1024 : 512) / kSelThre
             acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
 #pragma unroll
         for (int sg = 0; sg < kSegs; ++sg) {
-            const uint32_t x[4] = {w[0][sg].x, w[0][sg].y, w[0][sg].z, w[0][sg].w};
-            const uint32_t y[4] = {w[1][sg].x, w[1][sg].y, w[1][sg].z, w[1][sg].w};
+            const uint32_t a_lo[4] = {w[0][sg].x, w[0][sg].y, w[0][sg].z, w[0][sg].w};
+            const uint32_t a_hi[4] = {w[1][sg].x, w[1][sg].y, w[1][sg].z, w[1][sg].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t a[4];
-                widen_codes(x[j], a[0], a[2]);
-                widen_codes(y[j], a[1], a[3]);
+                widen_codes(a_lo[j], a[0], a[2]);
+                widen_codes(a_hi[j], a[1], a[3]);
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     const uint2 b = qf[nt][sg][j][lane];
@@ -556,65 +621,54 @@ __global__ void __launch_bounds__(kSelThreads, (NT == 1 ? 1024 : 512) / kSelThre
             best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
             best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
             const int i = tile * 16 + g + 8 * r;
-            if (t4 == 0 && i < n) {
-                const float x = __float_as_uint(scale[r]) == 0x7f800000u
-                                    ? scale[r] : __fmul_rn(best, scale[r]);
-                dst[i] = ok[r] ? score_key(x) : 0u;
+            if (t4 == 0 && i < own) {
+                if (!ok[r])
+                    flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
+                const float score = __float_as_uint(scale[r]) == 0x7f800000u
+                                        ? scale[r] : __fmul_rn(best, scale[r]);
+                keys[i] = ok[r] ? score_key(score) : 0u;
             }
         }
     }
-    if (ctas > 1)
-        cluster.sync();
-    else
-        __syncthreads();
-    if (rank != 0)
-        return;
+    __syncthreads();
 
     // ---- the list, in ascending order ------------------------------------------------
-    for (int i = tid; i < first; i += kSelThreads)
-        out[i] = i;
-    for (int i = tid; i < p.num_last; i += kSelThreads)
-        out[top_k - p.num_last + i] = tail + i;
-    if (n <= kSelWarp) {
-        if (warp == 0 && n <= kSelWarp / 2)
-            warp_list<kSelWarp / 64>(keys, n, want, first, out);
-        else if (warp == 0)
-            warp_list<kSelWarp / 32>(keys, n, want, first, out);
-        return;
+    if (rank == 0) {
+        for (int i = tid; i < first; i += kThreads)
+            out[i] = i;
+        for (int i = tid; i < p.num_last; i += kThreads)
+            out[top_k - p.num_last + i] = tail + i;
     }
-    const Threshold cut =
-        top_threshold<kSelThreads, 8>(sh.topk, [&](int i) { return keys[i]; }, n, want);
-    const int run = (n + kSelThreads - 1) / kSelThreads * 32;  // candidates of a warp
-    const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
-    int above = 0, ties = 0;
-    for (int i = i0 + lane; i < i1; i += 32) {
-        const uint32_t v = cut.level(keys[i]);
-        above += v > cut.prefix;
-        ties += v == cut.prefix;
-    }
-    above = __reduce_add_sync(kFull, above);
-    ties = __reduce_add_sync(kFull, ties);
-    if (lane == 0) {
-        sh.above[warp] = above;
-        sh.ties[warp] = ties;
-    }
-    __syncthreads();
-    above = ties = 0;
-    for (int w = 0; w < warp; ++w) {
-        above += sh.above[w];
-        ties += sh.ties[w];
-    }
-    for (int b = i0; b < i1; b += 32) {
-        const int i = b + lane;
-        const uint32_t v = i < i1 ? cut.level(keys[i]) : 0u;
-        const bool over = i < i1 && v > cut.prefix, tie = i < i1 && v == cut.prefix;
-        const uint32_t over_m = __ballot_sync(kFull, over), tie_m = __ballot_sync(kFull, tie);
-        const uint32_t below = (1u << lane) - 1;
-        const int my_ties = ties + __popc(tie_m & below);
-        if (over || (tie && my_ties < cut.rest))
-            out[first + above + __popc(over_m & below) + min(my_ties, cut.rest)] = first + i;
-        above += __popc(over_m);
-        ties += __popc(tie_m);
+    if constexpr (!kClusters) {
+        cta_select<kThreads>(sh, keys, n, want, [&](int i, int at) { out[first + at] = first + i; });
+    } else {
+        // the CTAs' lists come behind one another, keys and candidates
+        cg::cluster_group cluster = cg::this_cluster();
+        const int list0 = rank * min(want, share);  // (all CTAs before this one have `share`)
+        uint32_t *all_keys = keys + share;          // in the first CTA
+        uint32_t *all_ids = all_keys + (size_t)ctas * want;
+        uint32_t *to_keys = cluster.map_shared_rank(all_keys, 0) + list0;
+        uint32_t *to_ids = cluster.map_shared_rank(all_ids, 0) + list0;
+        const int mine = min(want, own);
+        if (mine == own) {
+            for (int i = tid; i < own; i += kThreads) {
+                to_keys[i] = keys[i];
+                to_ids[i] = (uint32_t)(c0 + i);
+            }
+        } else {
+            cta_select<kThreads>(sh, keys, own, mine, [&](int i, int at) {
+                to_keys[at] = keys[i];
+                to_ids[at] = (uint32_t)(c0 + i);
+            });
+        }
+        cluster.sync();
+        if (rank != 0)
+            return;
+        int total = 0;
+        for (int r = 0; r < ctas; ++r)
+            total += min(want, min(n, (r + 1) * share) - min(n, r * share));
+        cta_select<kThreads>(sh, all_keys, total, want,
+                   [&](int i, int at) { out[first + at] = first + (int)all_ids[i]; });
     }
 }
 
@@ -645,48 +699,54 @@ static pa_status launch_summary(const SummaryParams &p, int head_dim, int sms,
                : launch_pdl(summarize_kernel<KV, 64>, dim3(grid), dim3(kSumThreads), 0, stream, p);
 }
 
-// Blocks that a context can have, at most.
-static int select_blocks_max(const SelectParams &p)
-{
-    const int bs = 1 << p.block_shift;
-    return (int)std::min<long long>(p.max_blocks_per_seq,
-                                    ((long long)p.max_context_len + bs - 1) / bs);
-}
-
-template <typename T, int D, int NT, int THREADS>
+template <typename T, int D, int NT>
 static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream_t stream)
 {
-    auto kernel = select_kernel<T, D, NT, THREADS>;
-    static size_t enabled[kMaxDevices];
+    static size_t enabled_for[2][kMaxDevices];
     static std::mutex mu;
     int dev = 0;
     DeviceInfo info;
     const pa_status st = current_device(&dev, &info);
     if (st != PA_OK)
         return st;
-    const int most = select_blocks_max(p);
-    const size_t smem = std::max<size_t>(16, (size_t)most * 4);
-    if (smem + sizeof(SelectShared) + 32 * NT * D + 1024 > (size_t)info.optin)
+    const size_t room = (size_t)info.optin - (sizeof(SelectShared) + 32 * NT * D + 1024);
+    const int bs = 1 << p.block_shift;
+    // candidates of a row, at most
+    const int most = (int)std::min<long long>(p.max_blocks_per_seq,
+                                              ((long long)p.max_context_len + bs - 1) / bs);
+    const int want = p.top_k - p.num_first - p.num_last;
+    auto bytes = [&](int ctas) {
+        return select_bytes(((most + 15) / 16 + ctas - 1) / ctas * 16, ctas, want);
+    };
+    // Clusters where the rows and KV heads leave SMs with fewer CTAs than they hold and contexts are long, or where one CTA's memory does not hold their keys.
+    const long long units = (long long)num_tokens * p.num_kv_heads;
+    int ctas = 1;
+    while (ctas < kSelCluster && units * ctas < sel_resident(true) * info.sms && most >= 2 * ctas * kSelShare &&
+           bytes(2 * ctas) <= room)
+        ctas *= 2;
+    while (ctas < kSelCluster && bytes(ctas) > room)
+        ctas *= 2;
+    const size_t smem = bytes(ctas);
+    if (smem > room || units * ctas > INT32_MAX)
         return PA_ERR_UNSUPPORTED;
+    auto kernel = ctas > 1 ? select_kernel<T, D, NT, true> : select_kernel<T, D, NT, false>;
     {
         std::lock_guard<std::mutex> lock(mu);
+        size_t *enabled = enabled_for[ctas > 1];
         if (smem > enabled[dev]) {
-            const cudaError_t e = cudaFuncSetAttribute(
+            cudaError_t e = cudaFuncSetAttribute(
                 kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e == cudaSuccess)
+                e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         kSelCarveout);
             if (e != cudaSuccess)
                 return record_cuda(e);
             enabled[dev] = smem;
         }
     }
-    const long long units = (long long)num_tokens * p.num_kv_heads;
-    int ctas = 1;
-    while (ctas < 8 && units * ctas < 1024 / THREADS * info.sms && most >= 256 * ctas)
-        ctas *= 2;
-    if (units * ctas > INT32_MAX)
-        return PA_ERR_UNSUPPORTED;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(units * ctas));
-    cfg.blockDim = dim3(THREADS);
+    cfg.blockDim = dim3(sel_threads(ctas > 1));
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
@@ -697,16 +757,8 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = ctas > 1 ? 2 : 1;
     return record_cuda(cudaLaunchKernelEx(&cfg, kernel, p));
-}
-
-template <typename T, int D, int NT>
-static pa_status select_sized(const SelectParams &p, int num_tokens, cudaStream_t stream)
-{
-    return select_blocks_max(p) <= kSelShort
-               ? launch_select<T, D, NT, 128>(p, num_tokens, stream)
-               : launch_select<T, D, NT, 256>(p, num_tokens, stream);
 }
 
 template <typename T>
@@ -715,10 +767,10 @@ static pa_status select_as(const SelectParams &p, int head_dim, int num_tokens,
 {
     const bool wide = p.group > 8;
     if (head_dim == 128)
-        return wide ? select_sized<T, 128, 2>(p, num_tokens, stream)
-                    : select_sized<T, 128, 1>(p, num_tokens, stream);
-    return wide ? select_sized<T, 64, 2>(p, num_tokens, stream)
-                : select_sized<T, 64, 1>(p, num_tokens, stream);
+        return wide ? launch_select<T, 128, 2>(p, num_tokens, stream)
+                    : launch_select<T, 128, 1>(p, num_tokens, stream);
+    return wide ? launch_select<T, 64, 2>(p, num_tokens, stream)
+                : launch_select<T, 64, 1>(p, num_tokens, stream);
 }
 
 } // namespace pa

@@ -120,7 +120,6 @@ __global__ void __launch_bounds__(kPlanThreads)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int s = blockIdx.x;
     pdl_wait_primary();
-    pdl_launch_dependents();
 
     int32_t *moves = p.moves + (size_t)s * p.max_moves * 2;
     const PlanSeq q = plan_seq(p, s);
@@ -275,6 +274,9 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     for (int i = 2 * count + tid; i < 2 * p.max_moves; i += kPlanThreads)
         moves[i] = -1;
+    // (from its start, the moves' CTAs would take the SMs that later CTAs of the plan need:
+    // 128 sequences 126 us, 110 from here)
+    pdl_launch_dependents();
 }
 
 // Lengths and the stack's count where they replace the inputs, which every CTA of the
