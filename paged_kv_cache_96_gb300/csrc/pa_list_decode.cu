@@ -12,13 +12,13 @@
 //
 // What bounds both: HBM, each K and V row of a list or a context read once for the G
 // query heads of its KV head.  So both are one pass over 16-token tiles, built as
-// windowed decode is (pa_window_decode.cu): work units = (row, KV head, partition of
-// the list or the context) dealt to a persistent grid; every tile warp runs its own
-// ring of shared-memory stages ahead by TMA, across unit borders; scores and value
-// products are mma.sync m16n8k16 tiles with the G heads as the narrow side (tcgen05
-// wants 64 rows or more); softmax is online in fp32; a merge warp combines the tile
-// warps' records while they stream the next unit; partitions of a row are merged by
-// log-sum-exp weights, in the pass for a few of them, else by the reduce kernel.
+// windowed decode is (pa_window_decode.cu): a persistent grid takes rows and KV heads
+// or equal shares of all their tiles; every tile warp runs its own ring of
+// shared-memory stages ahead by TMA, across unit borders; scores and value products are
+// mma.sync m16n8k16 tiles with the G heads as the narrow side (tcgen05 wants 64 rows or
+// more); softmax is online in fp32; a merge warp combines the tile warps' records while
+// they stream the next unit; a row's partials are merged by log-sum-exp weights, in the
+// pass for a few of them, else by the reduce kernel.
 // What is different:
 //  * Pool blocks of 32 of a warp's tiles are looked up at once, one a lane, and the
 //    next 32 (of the same unit or the next one) before they are needed: a list's entry
@@ -48,9 +48,11 @@ struct ListParams : DecodeParams {
     // sparse: rows in place of sequences (num_seqs of them)
     const int32_t *selected;  // [rows][num_kv_heads][top_k]
     const int32_t *token_seq, *token_pos;
-    int32_t *len_out;         // list lengths for the reduce kernel (null: it will not run)
+    int32_t *len_out;         // partials for the reduce kernel (null: it will not run)
     int top_k, table_rows;    // entries of a list; sequences in block_tables
-    int list_parts;           // partitions that a list has, at most
+    int share_min;            // split rows: least tiles of a CTA's share (0: whole rows)
+    int aligned;              // shares do not go past a row's end
+    int32_t *part_count;      // weights: partials of each row
     // weights
     const float *weights;     // [num_blocks][block_size]
     float *weights_out;
@@ -60,18 +62,22 @@ struct ListParams : DecodeParams {
     int merge_max;            // partials of a row that the pass merges itself, at most
 };
 
-// Batches whose rows have at most this many partials are merged by the pass, others
-// by the reduce kernel, as in windowed decode.
-constexpr int kListMergeMax = 3;
+// Rows of at most this many partials are merged by the pass, others by the reduce
+// kernel behind it.
+constexpr int kListMergeMax = 4;
+
+// Rows whose tiles are numbered for shares, at most: 4 bytes each in every CTA's shared
+// memory (as many CTAs fit an SM as without them up to about 1,900).
+constexpr int kListShareRows = 8192;
 
 // m of a partial without a visible token, and of one whose scores are all -inf: the
 // first has no say (weight 0 beside any other partial, and an output of 0 by itself),
 // the second makes a row of nothing else NaN, as its softmax.
 constexpr float kNoToken = -FLT_MAX, kNoWeight = -1e38f;
 
-// Partitions of `len` tokens: every P of them, a remainder of less than half a
-// partition joining the one before.
-__host__ __device__ inline int list_partitions(int len, int part_tokens)
+// Partitions that the workspace has room for: every P tokens, a remainder of less than
+// half a partition joining the one before.
+static int list_partitions(int len, int part_tokens)
 {
     const int n = (int)(((long long)len + part_tokens / 2) / part_tokens);
     return len <= 0 ? 0 : n > 0 ? n : 1;
@@ -92,8 +98,8 @@ template <int D, int NT, int NW, int NST, int EB> struct ListLayout {
     static constexpr int kMergeAny = kMergeL + NW * kHeads * 4;  // a warp saw a token
     static constexpr int kBars = (kMergeAny + NW * 4 + 7) / 8 * 8;  // NW * NST stage barriers
     static constexpr int kFirst = kBars + NW * NST * 8;  // a stage's first position, -1: none
-    static constexpr int kSeq = kFirst + NW * NST * 4;   // weights: int len[S], prefix[S + 1]
-    static size_t bytes(int num_seqs) { return 1024 + kSeq + 4 * (2 * (size_t)num_seqs + 1); }
+    static constexpr int kSeq = kFirst + NW * NST * 4;   // shares: int prefix[S + 1]
+    static size_t bytes(int num_seqs) { return 1024 + kSeq + 4 * ((size_t)num_seqs + 1); }
     static_assert(kStageBytes % 1024 == 0, "stages must keep 1024-byte alignment");
 };
 
@@ -135,9 +141,7 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
     const int S = p.num_seqs;
     const int Hkv = p.num_kv_heads;
     const int G = p.group;
-    const int P = p.part_tokens;
-    int *len_s = reinterpret_cast<int *>(smem + L::kSeq);
-    int *pref = len_s + S;    // pref[s] = partitions of sequences [0 .. s)
+    int *pref = reinterpret_cast<int *>(smem + L::kSeq);  // tiles of rows [0 .. r)
     volatile int *stage_pos = reinterpret_cast<volatile int *>(smem + L::kFirst);
     float *merge_o = reinterpret_cast<float *>(smem + L::kMergeO);
     float *merge_m = reinterpret_cast<float *>(smem + L::kMergeM);
@@ -178,34 +182,43 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
         len = min(nb, p.top_k) << p.block_shift;
     };
 
-    int total_units;
-    if constexpr (kSparse) {
-        total_units = S * Hkv * p.list_parts;
-        // checks, list lengths for the reduce kernel, rows with nothing to attend
-        for (int t = blockIdx.x; t < S; t += gridDim.x) {
-            int s, ctx, len;
-            row_of(t, s, ctx, len, tid == 0);
-            if (tid == 0 && p.len_out != nullptr)
-                p.len_out[t] = (int)min((long long)list_partitions(len, P) * P,
-                                        (long long)INT32_MAX);
-            if (len != 0)
-                continue;
-            uint4 *row = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
-                                                   (size_t)t * p.num_heads * D);
-            for (int i = tid; i < p.num_heads * D / 8; i += kThreads)
-                row[i] = make_uint4(0, 0, 0, 0);
-        }
-        __syncthreads();  // (the stage barriers are there)
-    } else {
-        // ---- context lengths and partition prefix sums ----------------------------
-        for (int s = tid; s < S; s += kThreads)
-            len_s[s] = clamp_context(p, s, blockIdx.x == 0);
+    // tokens of a row's list or context
+    auto len_of = [&](int r, bool flag) {
+        int s, ctx, len;
+        if constexpr (kSparse)
+            row_of(r, s, ctx, len, flag);
+        else
+            len = clamp_context(p, r, flag);
+        return len;
+    };
+
+    // ---- the CTA's work -------------------------------------------------------------
+    // Whole rows in turn (a unit: a row and KV head), or, where rows are split, equal
+    // shares of all tiles, numbered through the rows: as many CTAs as there are KV heads
+    // take one share, a head each, so that a token's heads, which lie side by side, are
+    // read at about the same time (shares numbered through the heads as well: long
+    // contexts over FP8 pools 191 us, so 150).  A unit is what one row has in the share.
+    const bool share = p.share_min > 0;
+    int W = 0;                          // tiles of a share
+    int u_first = blockIdx.x, u_end = S * Hkv;
+    // whether the reduce kernel merges a row of that many partials
+    auto by_kernel = [&](int parts) { return p.len_out != nullptr && parts > p.merge_max; };
+    auto tiles_in = [&](int len) { return (len + kTileTokens - 1) / kTileTokens; };
+    // aligned: rows begin with a share of their own (share_min tiles)
+    auto whole_shares = [&](int n) {
+        return p.aligned ? (n + p.share_min - 1) / p.share_min * p.share_min : n;
+    };
+    // shares that the n tiles from tile t on are in
+    auto parts_of = [&](int t, int n) { return n > 0 ? (t + n - 1) / W - t / W + 1 : 0; };
+    if (share) {
+        for (int r = tid; r < S; r += kThreads)
+            pref[r] = whole_shares(tiles_in(len_of(r, blockIdx.x == 0)));
         __syncthreads();
         if (warp == 0) {
             int carry = 0;
             for (int base = 0; base < S; base += 32) {
                 const int k = base + lane;
-                const int n = k < S ? list_partitions(len_s[k], P) : 0;
+                const int n = k < S ? pref[k] : 0;
                 int x = n;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -220,76 +233,93 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
             if (lane == 0)
                 pref[S] = carry;
         }
-        __syncthreads();
-        total_units = pref[S] * Hkv;
-        for (int s = blockIdx.x; s < S; s += gridDim.x) {
-            if (tid == 0 && p.len_out != nullptr)
-                p.len_out[s] = (int)min((long long)(pref[s + 1] - pref[s]) * P,
-                                        (long long)INT32_MAX);
-            if (len_s[s] != 0)
-                continue;
-            uint4 *row = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
-                                                   (size_t)s * p.num_heads * D);
-            for (int i = tid; i < p.num_heads * D / 8; i += kThreads)
-                row[i] = make_uint4(0, 0, 0, 0);
+    }
+    __syncthreads();
+    if (share) {
+        const int groups = (int)gridDim.x / Hkv, group = (int)blockIdx.x / Hkv;
+        const int total = pref[S];
+        // (aligned shares are taken in turn, if there are more of them than groups)
+        W = p.aligned ? p.share_min : max(p.share_min, (total + groups - 1) / groups);
+        u_first = group < groups ? (int)min((long long)total, (long long)group * W) : total;
+        u_end = p.aligned ? total : (int)min((long long)total, (long long)u_first + W);
+    }
+    // rows with nothing to attend, lengths for the reduce kernel (in partials)
+    for (int r = blockIdx.x; r < S; r += gridDim.x) {
+        const int len = len_of(r, !share && tid == 0);
+        if (tid == 0) {
+            const int n = share ? parts_of(pref[r], tiles_in(len)) : len > 0;
+            if (p.part_count != nullptr)
+                p.part_count[r] = n;
+            if (p.len_out != nullptr)
+                p.len_out[r] = by_kernel(n) ? n : 0;
         }
+        if (len != 0)
+            continue;
+        uint4 *row = reinterpret_cast<uint4 *>(static_cast<T *>(p.out) +
+                                               (size_t)r * p.num_heads * D);
+        for (int i = tid; i < p.num_heads * D / 8; i += kThreads)
+            row[i] = make_uint4(0, 0, 0, 0);
     }
 
-    // A unit: partition j of nparts of row r (sparse) or sequence r, KV head kh,
-    // sequence s, tokens [tok0, tok0 + 16 ntiles) of its list or context, context ctx.
+    // A unit: partial j of nparts of row r and KV head kh, sequence s, ntiles tiles from
+    // token tok0 of the list or context on; the row's context is ctx.
     struct Unit {
         int r, s, kh, j, nparts, tok0, ntiles, ctx;
     };
     auto unit_of = [&](int u) {
         Unit x;
-        int len;
-        if constexpr (kSparse) {
-            // first partitions of all rows, then second ones: rows with fewer leave
-            // their units empty
-            x.j = u / (S * Hkv);
-            const int q = u - x.j * (S * Hkv);
-            x.r = q / Hkv;
-            x.kh = q - x.r * Hkv;
-            row_of(x.r, x.s, x.ctx, len, false);
-            x.nparts = list_partitions(len, P);
-        } else {
-            const int q = u / Hkv;
-            x.kh = u - q * Hkv;
-            int lo = 0, hi = S - 1;
+        x.j = x.tok0 = 0;
+        x.nparts = 1;
+        int len = 0;
+        if (share) {
+            int lo = 0, hi = S - 1;  // the last row that starts at or before u
             while (lo < hi) {
                 const int mid = (lo + hi + 1) >> 1;
-                if (pref[mid] <= q)
+                if (pref[mid] <= u)
                     lo = mid;
                 else
                     hi = mid - 1;
             }
-            x.r = x.s = lo;
-            x.j = q - pref[lo];
-            x.nparts = pref[lo + 1] - pref[lo];
-            x.ctx = len = len_s[lo];
+            x.r = lo;
+            x.kh = (int)blockIdx.x % Hkv;
+        } else {
+            x.r = u / Hkv;
+            x.kh = u - x.r * Hkv;
         }
-        x.tok0 = x.j * P;
-        // (the last partition ends with the row)
-        const int end = x.j + 1 == x.nparts ? len : x.tok0 + P;
-        x.ntiles = x.j < x.nparts ? (end - x.tok0 + kTileTokens - 1) / kTileTokens : 0;
+        if constexpr (kSparse) {
+            row_of(x.r, x.s, x.ctx, len, false);
+        } else {
+            x.s = x.r;
+            x.ctx = len = clamp_context(p, x.r, false);
+        }
+        x.ntiles = tiles_in(len);
+        if (share) {
+            const int from = pref[x.r];
+            x.j = u / W - from / W;
+            x.nparts = parts_of(from, x.ntiles);
+            x.tok0 = (u - from) * kTileTokens;
+            x.ntiles = min(x.ntiles - (u - from), (u / W + 1) * W - u);
+        }
         return x;
     };
-    // this CTA's units with tiles, in turn
-    auto next_unit = [&](int u) {
-        for (u += (int)gridDim.x; u < total_units; u += (int)gridDim.x) {
-            if (!kSparse || unit_of(u).ntiles > 0)
+    // this CTA's units with tiles, in turn: the one after u, which is x
+    auto next_unit = [&](int u, const Unit &x) {
+        if (share)
+            return p.aligned ? (u / W + (int)gridDim.x / Hkv) * W : u + x.ntiles;
+        for (u += (int)gridDim.x; u < u_end; u += (int)gridDim.x)
+            if (unit_of(u).ntiles > 0)
                 break;
-        }
         return u;
     };
-    const int u_first = next_unit((int)blockIdx.x - (int)gridDim.x);
+    if (!share)
+        u_first = next_unit(u_first - (int)gridDim.x, Unit{});
 
     // ---- this warp's fetch cursor -----------------------------------------------------
     // Tiles of a unit are taken in chunks of 32 a warp: lane l looks up tile
     // (32 k + l) NW + warp of chunk k.  The next chunk's list entries are loaded as a
     // chunk is entered and its table entries at the fetch after that.
     struct Chunk {
-        int u, k, left;     // unit (>= total_units: none), chunk, this warp's tiles in it
+        int u, k, left;     // unit (>= u_end: none), chunk, this warp's tiles in it
         int pos, phys;      // this lane's tile: first position, pool block (-1: no fetch)
         int row, kh;        // this lane's row in the block; the unit's KV head
         const int32_t *at;  // its table entry, or null
@@ -306,11 +336,13 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
         c.left = 0;
         c.kh = 0;
         c.k = k;
-        for (; u < total_units; u = next_unit(u), c.k = 0) {
+        for (; u < u_end; c.k = 0) {
             const Unit x = unit_of(u);
             const int mine = tiles_of(x) - c.k * 32;
-            if (mine <= 0)
+            if (mine <= 0) {
+                u = next_unit(u, x);
                 continue;
+            }
             c.left = min(mine, 32);
             c.kh = x.kh;
             if (lane < c.left) {
@@ -350,7 +382,7 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
     if (!pdone) {
         cur = enter(u_first, 0);
         look_up(cur);
-        pdone = cur.u >= total_units;
+        pdone = cur.u >= u_end;
         if (!pdone)
             nxt = enter(cur.u, cur.k + 1);
     }
@@ -397,7 +429,7 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
             look_up(nxt);
             cur = nxt;
             at_lane = 0;
-            pdone = cur.u >= total_units;
+            pdone = cur.u >= u_end;
             if (!pdone)
                 nxt = enter(cur.u, cur.k + 1);
         } else if (at_lane == 1) {
@@ -466,7 +498,7 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
             }
         }
     };
-    if (u_first < total_units && warp < NW) {
+    if (u_first < u_end && warp < NW) {
         const Unit x = unit_of(u_first);
         load_query(x.r, x.kh);
     }
@@ -481,9 +513,9 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
     constexpr int kRecFull = 1, kRecFree = 2;  // named barrier ids (0 is __syncthreads)
     if (warp < NW) {
         int k_unit = 0;          // units of this CTA so far
-        for (int u = u_first; u < total_units; ++k_unit) {
+        for (int u = u_first; u < u_end; ++k_unit) {
             const Unit x = unit_of(u);
-            const int un = next_unit(u);
+            const int un = next_unit(u, x);
             const int ctx = x.ctx;
             float *score_row = nullptr;  // this head group's scores of the sequence
             if constexpr (!kSparse)
@@ -706,7 +738,7 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
             }
 
             // Next unit's query: its loads land while this unit's records go out.
-            if (un < total_units) {
+            if (un < u_end) {
                 const Unit y = unit_of(un);
                 load_query(y.r, y.kh);
             }
@@ -753,9 +785,9 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
         }
     } else {
         // ===== the merge warp ======================================================
-        for (int u = u_first; u < total_units;) {
+        for (int u = u_first; u < u_end;) {
             const Unit x = unit_of(u);
-            const int un = next_unit(u);
+            const int un = next_unit(u, x);
             const bool split = x.nparts > 1;
             named_barrier_sync(kRecFull, kThreads);  // every tile warp's records are in
             int any = 0;
@@ -813,9 +845,9 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
             }
             // the records may be rewritten; the tile warps wait for this only
             // from their next unit on
-            if (un < total_units)
+            if (un < u_end)
                 named_barrier_arrive(kRecFree, kThreads);
-            if (split && x.nparts <= p.merge_max)
+            if (split && !by_kernel(x.nparts))
                 // records loaded per lane at once: fewer under the FP8 register cap
                 arrive_and_merge<T, D, kHeads, kFp8 ? 2 : 8>(p, x.r, x.kh, x.nparts, lane);
             u = un;
@@ -840,14 +872,13 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
 
 // ---- accumulated weights -----------------------------------------------------------
 //
-// One CTA per (sequence, run of kWeightRun tokens), a thread a token at a time: the
+// One CTA per (sequence, run of kWeightThreads tokens), a thread a token: the
 // scores of all heads, turned into weights with the sums over the context, are added
 // up head by head, the KV heads' sums then in order.  What bounds it: the scores, 4
 // bytes a query head and token, a KV head's being one run of memory for a warp's
 // tokens.  The sums over the context are taken anew in each CTA from the partials'
 // (m, l), which are few beside the scores.
 constexpr int kWeightThreads = 256;
-constexpr int kWeightRun = 512;
 
 // V: heads loaded at once; GV: loads of a KV head (0: group / V of them, in a loop).
 template <int V, int GV>
@@ -859,17 +890,21 @@ __global__ void __launch_bounds__(kWeightThreads)
     extern __shared__ __align__(16) float sums[];  // m (log2 units) and 1 / l of each head
     const int tid = threadIdx.x;
     const int H = p.num_heads, G = p.group, Hkv = p.num_kv_heads;
-    const int runs = (p.pitch + kWeightRun - 1) / kWeightRun;
+    const int runs = (p.pitch + kWeightThreads - 1) / kWeightThreads;
     const int s = blockIdx.x / runs;
-    const int first = (blockIdx.x - s * runs) * kWeightRun;
+    const int first = (blockIdx.x - s * runs) * kWeightThreads;
     pdl_wait_primary();
     pdl_launch_dependents();
     const int ctx = clamp_context(p, s, false);
     if (first >= ctx)
         return;
+    // this thread's token: its block is on its way while the sums are taken
+    const int pos = first + tid;
+    const int phys = pos < ctx ? p.block_tables[(size_t)s * p.max_blocks_per_seq +
+                                                (pos >> p.block_shift)] : -1;
     const int seen = p.weighted_lens[s];
     float *m = sums, *inv = sums + H;
-    const int parts = list_partitions(ctx, p.part_tokens);
+    const int parts = p.part_count[s];  // of each head, as the pass counted them
     const float *pm = p.part_m + (size_t)s * H * p.max_parts;
     const float *pl = p.part_l + (size_t)s * H * p.max_parts;
     if (parts <= 4) {  // a thread a query head
@@ -930,42 +965,37 @@ __global__ void __launch_bounds__(kWeightThreads)
         }
     }
     __syncthreads();
-    const int end = min(ctx, first + kWeightRun);
-    for (int pos = first + tid; pos < end; pos += kWeightThreads) {
-        const int phys = p.block_tables[(size_t)s * p.max_blocks_per_seq +
-                                        (pos >> p.block_shift)];
-        if (phys < 0 || phys >= p.num_blocks)
-            continue;  // (flagged by the pass)
-        const size_t slot = ((size_t)phys << p.block_shift) + (pos & (p.block_size - 1));
-        const float before = pos < seen ? p.weights[slot] : 0.f;
-        const float *row = p.scores + ((size_t)s * Hkv * p.pitch + pos) * G;
-        float total = 0.f;
+    if (phys < 0 || phys >= p.num_blocks)
+        return;  // (flagged by the pass)
+    const size_t slot = ((size_t)phys << p.block_shift) + (pos & (p.block_size - 1));
+    const float before = pos < seen ? p.weights[slot] : 0.f;
+    const float *row = p.scores + ((size_t)s * Hkv * p.pitch + pos) * G;
+    float total = 0.f;
 #pragma unroll 4
-        for (int kh = 0; kh < Hkv; ++kh) {
-            const Vec *src = reinterpret_cast<const Vec *>(row + (size_t)kh * p.pitch * G);
-            float part = 0.f;
+    for (int kh = 0; kh < Hkv; ++kh) {
+        const Vec *src = reinterpret_cast<const Vec *>(row + (size_t)kh * p.pitch * G);
+        float part = 0.f;
 #pragma unroll
-            for (int i = 0; i < (GV ? GV : G / V); ++i) {
-                const Vec x = __ldcs(src + i);
-                const float *e = reinterpret_cast<const float *>(&x);
+        for (int i = 0; i < (GV ? GV : G / V); ++i) {
+            const Vec x = __ldcs(src + i);
+            const float *e = reinterpret_cast<const float *>(&x);
 #pragma unroll
-                for (int k = 0; k < V; ++k) {
-                    const int h = kh * G + i * V + k;
-                    part += exp2f(e[k] - m[h]) * inv[h];
-                }
+            for (int k = 0; k < V; ++k) {
+                const int h = kh * G + i * V + k;
+                part += exp2f(e[k] - m[h]) * inv[h];
             }
-            total += part;
         }
-        p.weights_out[slot] = before + total;
+        total += part;
     }
+    p.weights_out[slot] = before + total;
 }
 
 // ---- host side -------------------------------------------------------------------
 
 // Tile warps per CTA (the merge warp comes on top), ring stages per warp and CTAs per
 // SM the register budget is sized for, as in windowed decode: 16-bit pools, FP8 pools.
-constexpr int kListWarps = 5, kListStages = 2, kListMinBlocks = 2;
-constexpr int kListWarpsFp8 = 4, kListStagesFp8 = 3, kListMinBlocksFp8 = 3;
+constexpr int kListWarps = 4, kListStages = 2, kListMinBlocks = 2;
+constexpr int kListWarpsFp8 = 3, kListStagesFp8 = 3, kListMinBlocksFp8 = 4;
 
 template <typename T, typename KV, int D, int NT, int NST, bool kSparse>
 static pa_status launch_list_pass(const ListParams &prm, const CUtensorMap &mk,
@@ -981,7 +1011,7 @@ static pa_status launch_list_pass(const ListParams &prm, const CUtensorMap &mk,
     constexpr int kThreads = (NW + 1) * 32;
     static KernelSetting setting[kMaxDevices];
     static std::mutex mu;
-    const size_t smem = L::bytes(kSparse ? 0 : prm.num_seqs);
+    const size_t smem = L::bytes(prm.share_min > 0 ? prm.num_seqs : 0);
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
@@ -1018,12 +1048,14 @@ static pa_status launch_list_pass(const ListParams &prm, const CUtensorMap &mk,
         return PA_ERR_UNSUPPORTED;
     const long long grid =
         std::max(1ll, std::min((long long)info.sms * per_sm, max_units));
+    if (prm.share_min > 0 && grid < prm.num_kv_heads)
+        return PA_ERR_UNSUPPORTED;  // (the caller takes whole rows)
     return launch_pdl(kernel, dim3((unsigned)grid), dim3(kThreads), smem, stream, prm, mk, mv);
 }
 
 static pa_status launch_add_weights(const ListParams &prm, cudaStream_t stream)
 {
-    const long long runs = ((long long)prm.pitch + kWeightRun - 1) / kWeightRun;
+    const long long runs = ((long long)prm.pitch + kWeightThreads - 1) / kWeightThreads;
     const size_t smem = (size_t)prm.num_heads * 8;
     auto kernel = prm.group == 4    ? add_weights_kernel<4, 1>
                   : prm.group == 8  ? add_weights_kernel<4, 2>
@@ -1035,29 +1067,28 @@ static pa_status launch_add_weights(const ListParams &prm, cudaStream_t stream)
 }
 
 template <typename T, typename KV, int D, int NT, bool kSparse>
-static pa_status launch_list(const ListParams &prm, const CUtensorMap &mk,
-                             const CUtensorMap &mv, cudaStream_t stream, int max_parts)
+static pa_status launch_list(ListParams prm, const CUtensorMap &mk, const CUtensorMap &mv,
+                             cudaStream_t stream, int max_parts)
 {
     const long long max_units = (long long)prm.num_seqs * prm.num_kv_heads * max_parts;
     constexpr int kStages = sizeof(KV) == 1 ? kListStagesFp8 : kListStages;
     pa_status st =
         launch_list_pass<T, KV, D, NT, kStages, kSparse>(prm, mk, mv, stream, max_units);
-    if constexpr (!kSparse) {
-        // batches whose per-sequence arrays do not fit next to the default rings
-        if (st == PA_ERR_UNSUPPORTED)
-            st = launch_list_pass<T, KV, D, NT, 1, kSparse>(prm, mk, mv, stream, max_units);
+    if (st == PA_ERR_UNSUPPORTED && prm.share_min > 0) {
+        prm.share_min = 0;
+        prm.len_out = nullptr;
+        st = launch_list_pass<T, KV, D, NT, kStages, kSparse>(prm, mk, mv, stream, max_units);
+    }
+    if constexpr (!kSparse)
         if (st == PA_OK)
             st = launch_add_weights(prm, stream);
-    }
-    if (st != PA_OK || max_parts <= prm.merge_max)
+    if (st != PA_OK || prm.len_out == nullptr)
         return st;
     DecodeParams reduce = prm;
-    reduce.counters = nullptr;  // (nothing was merged by the pass)
-    reduce.context_lens = prm.len_out;
-    if (kSparse) {  // lengths of lists
-        reduce.max_blocks_per_seq = prm.top_k;
-        reduce.max_context_len = prm.top_k * prm.block_size;
-    }
+    reduce.counters = nullptr;  // (what it merges was not merged by the pass)
+    reduce.context_lens = prm.len_out;  // in partials
+    reduce.part_tokens = reduce.block_size = 1;
+    reduce.max_blocks_per_seq = reduce.max_context_len = prm.max_parts;
     return launch_reduce<T, D>(reduce, stream);
 }
 
@@ -1102,9 +1133,9 @@ static ListWorkspace list_workspace(int rows, int H, int Hkv, int D, int parts, 
         w.l_off = align256((size_t)rows * H * 4);
         w.total = 2 * w.l_off;
     }
-    w.len_off = w.total;
-    if (parts > kListMergeMax)
-        w.total += align256((size_t)rows * 4);
+    w.len_off = w.total;  // partials of each row: for the reduce kernel, and of all
+    if (parts > 1 || pitch > 0)
+        w.total += align256((size_t)rows * 8);
     w.scores_off = w.total;
     w.total += align256((size_t)rows * H * (size_t)pitch * 4);
     return w;
@@ -1148,9 +1179,6 @@ static pa_status run_list(ListParams &prm, void *out, const void *query, const v
     if ((long long)max_blocks_per_seq * block_size > (1ll << 31) - 256 ||
         (long long)rows * num_kv_heads * prm.max_parts > (1ll << 30))
         return PA_ERR_UNSUPPORTED;
-    if (partition_size == 0)  // one partition of a whole row
-        prm.part_tokens = (int)std::max<long long>(
-            kTileTokens, (most + kTileTokens - 1) / kTileTokens * kTileTokens);
     prm.pitch = kSparse ? 0 : (int)score_pitch((int)most);
     const ListWorkspace w = list_workspace(rows, num_heads, num_kv_heads, head_dim,
                                            prm.max_parts, prm.pitch);
@@ -1163,31 +1191,42 @@ static pa_status run_list(ListParams &prm, void *out, const void *query, const v
         prm.part_l = reinterpret_cast<float *>(ws + w.l_off);
         prm.scores = reinterpret_cast<float *>(ws + w.scores_off);
     }
-    // A list's rows are of one length: partitions are there to give every CTA work, and
-    // more than fill a round of CTAs only add partials, as in windowed decode.
-    if (kSparse && prm.max_parts > 1) {
-        int dev = 0;
-        const cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess)
-            return record_cuda(e);
-        DeviceInfo info;
-        const pa_status di = device_info(dev, &info);
-        if (di != PA_OK)
-            return di;
-        const long long ctas =
-            (long long)info.sms * (prm.group > 8 ? 1 : fp8 ? kListMinBlocksFp8 : kListMinBlocks);
-        const long long per = ctas / ((long long)rows * num_kv_heads);
-        if (per >= 1) {
-            const long long t = kTileTokens;
-            const long long fill = (most + per * t - 1) / (per * t) * t;
-            prm.part_tokens = (int)std::max<long long>(prm.part_tokens, fill);
+    // Split rows: shares of a partition or more, and of so many tiles that no row has more
+    // partials than there is room for; whole rows where their tiles cannot be numbered in
+    // 32 bits, or their numbers do not fit in shared memory.
+    const long long tiles =
+        (std::min<long long>(most, (long long)max_blocks_per_seq * block_size) + kTileTokens - 1) /
+        kTileTokens;
+    const int parts = prm.max_parts;
+    int32_t *counts = reinterpret_cast<int32_t *>(ws + w.len_off);
+    prm.merge_max = kListMergeMax;
+    if (!kSparse)
+        prm.part_count = counts + rows;
+    if (parts > 1 && tiles * rows < (1ll << 29) && rows <= kListShareRows) {
+        prm.share_min = (int)std::max<long long>(partition_size / kTileTokens,
+                                                 (tiles - 2) / (parts - 1) + 1);
+        if (kSparse) {
+            // Lists are of one length, or shorter: with fewer of them than CTAs for a KV
+            // head, each is cut into as many shares of its own as fill these (16 rows of
+            // 4,096 tokens, FP8: 38.7 us; shares across rows have a few partials more to
+            // merge, 42.3).
+            DeviceInfo info;
+            int dev = 0;
+            const cudaError_t e = cudaGetDevice(&dev);
+            const pa_status di = e != cudaSuccess ? record_cuda(e) : device_info(dev, &info);
+            if (di != PA_OK)
+                return di;
+            const long long ctas = (long long)info.sms *
+                                   (prm.group > 8 ? 1 : fp8 ? kListMinBlocksFp8 : kListMinBlocks);
+            const long long per = ctas / ((long long)num_kv_heads * rows);
+            if (per >= 1) {
+                prm.aligned = 1;
+                prm.share_min = (int)std::max<long long>(prm.share_min, (tiles + per - 1) / per);
+            }
         }
+        if ((tiles + prm.share_min - 2) / prm.share_min + !prm.aligned > prm.merge_max)
+            prm.len_out = counts;
     }
-    const int parts = std::max(1, list_partitions((int)most, prm.part_tokens));
-    prm.list_parts = parts;
-    prm.merge_max = parts > kListMergeMax ? 1 : kListMergeMax;
-    if (parts > prm.merge_max)
-        prm.len_out = reinterpret_cast<int32_t *>(ws + w.len_off);
     prm.max_context_len = (int)most;
     if (fp8) {
         // scores of the K codes: the K scale in the exponent's, the V scale on

@@ -126,7 +126,7 @@ def test_sparse_refuses(B):
     assert B.pa_sparse_workspace_bytes(3, 8, 2, 128, 8, 16, 0) == 0
     assert B.pa_sparse_workspace_bytes(3, 8, 2, 128, 8, 16, 96) == 0       # a short rest joins
     assert B.pa_sparse_workspace_bytes(3, 8, 2, 128, 8, 16, 64) == \
-        B.pa_decode_workspace_bytes(3, 8, 2, 128, 128, 64)
+        B.pa_decode_workspace_bytes(3, 8, 2, 128, 128, 64) + 256           # and partials
     refuses(f, B.PA_ERR_WORKSPACE, dict(), dict(ws=BIG, wsb=need - 1),
             dict(ws=ctypes.c_void_p(0x40000010), wsb=need), P=16)
     for bad in ((-1, 8, 2, 128, 8, 16, 16), (3, 8, 2, 128, 0, 16, 16), (3, 8, 2, 128, 8, 16, -1),
@@ -141,7 +141,7 @@ def test_weights_refuses(B):
     refuses(f, B.PA_ERR_UNSUPPORTED, dict(H=8192, K=512), dict(maxctx=(1 << 31) - 1))
     assert f(S=0) == B.PA_OK
     need = B.pa_weights_workspace_bytes(2, 8, 2, 128, 128, 0)
-    assert need == 2 * 256 + 2 * 8 * 128 * 4                # sums and scores
+    assert need == 3 * 256 + 2 * 8 * 128 * 4                # sums, partials, scores
     refuses(f, B.PA_ERR_WORKSPACE, dict(ws=None), dict(wsb=need - 1),
             dict(ws=ctypes.c_void_p(0x40000010)))
     need = B.pa_weights_workspace_bytes(2, 8, 2, 128, 128, 16)
