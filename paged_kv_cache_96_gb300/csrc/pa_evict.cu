@@ -55,14 +55,15 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s)
     return q;
 }
 
-constexpr int kPlanThreads = 1024;
-constexpr int kPlanWarps = kPlanThreads / 32;
+// Threads of a CTA: 256 for contexts of at most kPlanShort tokens, whose passes are
+// short and barriers most of the time, else 1,024.
+constexpr int kPlanShort = 2048;
 constexpr int kPlanBatch = 4;
 
 struct PlanShared {
     TopkShared<11> topk;
-    int above[kPlanWarps], ties[kPlanWarps];
-    long long given[kPlanWarps], before[kPlanWarps];
+    int above[32], ties[32];
+    long long given[32], before[32];
     int low_kept;  // tokens between the first and the last ones that stay below the budget
 };
 
@@ -72,11 +73,12 @@ struct PlanTotal {
     long long given, before;
     bool bad;
 };
+template <int THREADS>
 __device__ __forceinline__ PlanTotal plan_total(PlanShared &sh, const PlanParams &p, int s)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     PlanTotal t{0, 0, false};
-    for (int k = tid; k < p.num_seqs; k += kPlanThreads) {
+    for (int k = tid; k < p.num_seqs; k += THREADS) {
         const PlanSeq q = plan_seq(p, k);
         t.given += q.have - q.keep;
         t.before += k < s ? q.have - q.keep : 0;
@@ -94,7 +96,7 @@ __device__ __forceinline__ PlanTotal plan_total(PlanShared &sh, const PlanParams
     t.bad = __syncthreads_or(t.bad);
     t.given = t.before = 0;
 #pragma unroll
-    for (int w = 0; w < kPlanWarps; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         t.given += sh.given[w];
         t.before += sh.before[w];
     }
@@ -111,8 +113,8 @@ __device__ __forceinline__ int plan_refusal(const PlanParams &p, const PlanTotal
 
 // One CTA per sequence.  kKept: the keys of the whole context, and its table row, fit in
 // shared memory; else each pass reads the weights again, through L2.
-template <bool kKept>
-__global__ void __launch_bounds__(kPlanThreads)
+template <int THREADS, bool kKept>
+__global__ void __launch_bounds__(THREADS)
     plan_eviction_kernel(const __grid_constant__ PlanParams p)
 {
     __shared__ PlanShared sh;
@@ -136,9 +138,9 @@ __global__ void __launch_bounds__(kPlanThreads)
         return id;
     };
     if (kKept)
-        for (int b = tid; b < q.have; b += kPlanThreads)
+        for (int b = tid; b < q.have; b += THREADS)
             row[b] = block_of(b);
-    const PlanTotal sum = plan_total(sh, p, s);  // (with a barrier)
+    const PlanTotal sum = plan_total<THREADS>(sh, p, s);  // (with a barrier)
     const int refuse = plan_refusal(p, sum);
     const int slots = p.num_blocks << p.block_shift;
     auto slot_of = [&](int pos) {
@@ -157,7 +159,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (refuse == 0) {
         // blocks behind the budget onto the stack
         int32_t *top = p.free_blocks + p.free_count[0] + sum.before;
-        for (int i = tid; i < q.have - q.keep; i += kPlanThreads) {
+        for (int i = tid; i < q.have - q.keep; i += THREADS) {
             const int id = __ldg(table + q.keep + i);
             if (id < 0 || id >= p.num_blocks)
                 flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
@@ -174,18 +176,18 @@ __global__ void __launch_bounds__(kPlanThreads)
         // kPlanBatch tokens of a thread at a time
         const bool apart = p.weights_out != p.weights;
         const int reach = kKept && n > 0 ? max(tail, q.end) : apart ? q.end : 0;
-        for (int i0 = tid; i0 < reach; i0 += kPlanBatch * kPlanThreads) {
+        for (int i0 = tid; i0 < reach; i0 += kPlanBatch * THREADS) {
             int at[kPlanBatch];
             float w[kPlanBatch];
 #pragma unroll
             for (int u = 0; u < kPlanBatch; ++u)
-                at[u] = slot_of(min(i0 + u * kPlanThreads, reach - 1));
+                at[u] = slot_of(min(i0 + u * THREADS, reach - 1));
 #pragma unroll
             for (int u = 0; u < kPlanBatch; ++u)
                 w[u] = at[u] >= 0 ? p.weights[at[u]] : 0.f;
 #pragma unroll
             for (int u = 0; u < kPlanBatch; ++u) {
-                const int i = i0 + u * kPlanThreads;
+                const int i = i0 + u * THREADS;
                 if (i >= reach)
                     continue;
                 if (apart && i < q.end && at[u] >= 0)
@@ -203,9 +205,9 @@ __global__ void __launch_bounds__(kPlanThreads)
                 const int at = slot_of(first + i);
                 return at >= 0 ? weight_key(p.weights[at]) : 0u;
             };
-            const Threshold cut = top_threshold<kPlanThreads, 11>(sh.topk, key, n, want);
+            const Threshold cut = top_threshold<THREADS, 11>(sh.topk, key, n, want);
             // a warp's run of them; the tokens that stay before each run
-            const int run = (n + kPlanThreads - 1) / kPlanThreads * 32;
+            const int run = (n + THREADS - 1) / THREADS * 32;
             const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
             int above = 0, ties = 0;
             for (int i = i0 + lane; i < i1; i += 32) {
@@ -261,18 +263,18 @@ __global__ void __launch_bounds__(kPlanThreads)
             // the last tokens, from the budget on
             const int late = max(tail, p.budget);
             const int done = want - low_kept;  // rows before them
-            for (int i = late + tid; i < q.c; i += kPlanThreads)
+            for (int i = late + tid; i < q.c; i += THREADS)
                 moves[2 * (done + i - late)] = slot_of(i);
             count = done + q.c - late;
             __syncthreads();
-            for (int i = tid; i < count; i += kPlanThreads) {
+            for (int i = tid; i < count; i += THREADS) {
                 const int src = moves[2 * i], dst = moves[2 * i + 1];
                 if (src >= 0 && src < slots && dst >= 0 && dst < slots)
                     p.weights_out[dst] = p.weights[src];
             }
         }
     }
-    for (int i = 2 * count + tid; i < 2 * p.max_moves; i += kPlanThreads)
+    for (int i = 2 * count + tid; i < 2 * p.max_moves; i += THREADS)
         moves[i] = -1;
     // (from its start, the moves' CTAs would take the SMs that later CTAs of the plan need:
     // 128 sequences 126 us, 110 from here)
@@ -282,17 +284,18 @@ __global__ void __launch_bounds__(kPlanThreads)
 // Lengths and the stack's count where they replace the inputs, which every CTA of the
 // plan reads: one CTA behind it.  (With arrays of their own for the outputs the plan
 // writes them, and this launch, about 2 us behind it, is left out.)
-__global__ void __launch_bounds__(kPlanThreads)
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS)
     apply_eviction_kernel(const __grid_constant__ PlanParams p)
 {
     __shared__ PlanShared sh;
     pdl_wait_primary();
     pdl_launch_dependents();
-    const PlanTotal t = plan_total(sh, p, 0);
+    const PlanTotal t = plan_total<THREADS>(sh, p, 0);
     const int refuse = plan_refusal(p, t);
     const int count = p.free_count[0];
     __syncthreads();  // (the count has been read)
-    for (int s = threadIdx.x; s < p.num_seqs; s += kPlanThreads) {
+    for (int s = threadIdx.x; s < p.num_seqs; s += THREADS) {
         const PlanSeq q = plan_seq(p, s);
         p.context_out[s] = refuse ? q.c : q.end;
     }
@@ -305,11 +308,11 @@ __global__ void __launch_bounds__(kPlanThreads)
 
 // ---- moves --------------------------------------------------------------------------
 //
-// A warp takes kMoveRun entries of the list at a time (padding entries cost their
-// eight bytes) and copies each move's K and V rows, all of a lane's loads before its
-// stores, 16 bytes a lane.
+// A warp takes an entry of the list at a time, with the next one on its way (a padding
+// entry costs its eight bytes), and copies the K and V rows of a move together, all of a
+// lane's loads before its stores, 16 bytes a lane.  60,000 moves of 4 KB among 262,000
+// entries, with their plan: 101 us; runs of two or four entries a warp 102 and 112.
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRun = 4;
 constexpr int kMoveWords = 8;  // of a lane at once
 constexpr int kMoveCtas = 4;   // resident on an SM, which the grid fills once
 
@@ -320,41 +323,38 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas)
 {
     const int lane = threadIdx.x & 31;
     const long long warps = (long long)gridDim.x * (kMoveThreads / 32);
-    long long run = (long long)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
+    long long at = (long long)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
     pdl_wait_primary();
     pdl_launch_dependents();
-    for (; run * kMoveRun < num_moves; run += warps) {
-        const long long at = run * kMoveRun + lane;
-        int2 move = make_int2(-1, -1);
-        if (lane < kMoveRun && at < num_moves)
-            move = __ldg(moves + at);
-        const bool real = move.x >= 0 && move.y >= 0;
-        const bool good = real && move.x < num_slots && move.y < num_slots;
-        if (real && !good)
-            flag_error(error_word, PA_DEVERR_SLOT_RANGE);
-        uint32_t todo = __ballot_sync(kFull, good);
-        while (todo != 0) {
-            const int k = __ffs((int)todo) - 1;
-            todo &= todo - 1;
-            const size_t src = (size_t)__shfl_sync(kFull, move.x, k) * words;
-            const size_t dst = (size_t)__shfl_sync(kFull, move.y, k) * words;
-            // words of the key row, then of the value row
-            for (int i0 = lane; i0 < 2 * words; i0 += 32 * kMoveWords) {
-                uint4 w[kMoveWords];
+    auto entry = [&](long long i) { return i < num_moves ? __ldg(moves + i) : make_int2(-1, -1); };
+    int2 next = entry(at);
+    for (; at < num_moves; at += warps) {
+        const int2 move = next;
+        next = entry(at + warps);
+        if (move.x < 0 || move.y < 0)
+            continue;
+        if (move.x >= num_slots || move.y >= num_slots) {
+            if (lane == 0)
+                flag_error(error_word, PA_DEVERR_SLOT_RANGE);
+            continue;
+        }
+        const size_t src = (size_t)move.x * words, dst = (size_t)move.y * words;
+        // words of the key row, then of the value row
+        for (int i0 = lane; i0 < 2 * words; i0 += 32 * kMoveWords) {
+            uint4 w[kMoveWords];
 #pragma unroll
-                for (int u = 0; u < kMoveWords; ++u) {
-                    const int i = i0 + 32 * u;
-                    if (i < 2 * words)
-                        w[u] = i < words ? key_cache[src + i] : value_cache[src + i - words];
-                }
+            for (int u = 0; u < kMoveWords; ++u) {
+                const int i = i0 + 32 * u;
+                if (i < 2 * words)
+                    w[u] = __ldcs(i < words ? key_cache + src + i : value_cache + src + i - words);
+            }
 #pragma unroll
-                for (int u = 0; u < kMoveWords; ++u) {
-                    const int i = i0 + 32 * u;
-                    if (i < words)
-                        key_cache[dst + i] = w[u];
-                    else if (i < 2 * words)
-                        value_cache[dst + i - words] = w[u];
-                }
+            for (int u = 0; u < kMoveWords; ++u) {
+                const int i = i0 + 32 * u;
+                if (i < words)
+                    __stcs(key_cache + dst + i, w[u]);
+                else if (i < 2 * words)
+                    __stcs(value_cache + dst + i - words, w[u]);
             }
         }
     }
@@ -431,31 +431,30 @@ extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *co
                                               ((size_t)max_context_len + block_size - 1) /
                                                   block_size)) * 4;
         if (smem + sizeof(PlanShared) + 1024 <= (size_t)info.optin) {
-            static size_t enabled[kMaxDevices];
+            const bool small = max_context_len <= kPlanShort;
+            auto kernel = small ? plan_eviction_kernel<256, true> : plan_eviction_kernel<1024, true>;
+            static size_t enabled[2][kMaxDevices];
             static std::mutex mu;
             {
                 std::lock_guard<std::mutex> lock(mu);
-                if (smem > enabled[dev]) {
+                if (smem > enabled[small][dev]) {
                     const cudaError_t a = cudaFuncSetAttribute(
-                        plan_eviction_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                        (int)smem);
+                        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
                     if (a != cudaSuccess)
                         return record_cuda(a);
-                    enabled[dev] = smem;
+                    enabled[small][dev] = smem;
                 }
             }
-            st = launch_pdl(plan_eviction_kernel<true>, dim3(num_seqs), dim3(kPlanThreads), smem,
-                            q, p);
+            st = launch_pdl(kernel, dim3(num_seqs), dim3(small ? 256 : 1024), smem, q, p);
         } else {
-            st = launch_pdl(plan_eviction_kernel<false>, dim3(num_seqs), dim3(kPlanThreads), 0, q,
-                            p);
+            st = launch_pdl(plan_eviction_kernel<1024, false>, dim3(num_seqs), dim3(1024), 0, q, p);
         }
         if (st != PA_OK)
             return st;
     }
     if (!p.apply_later)
         return PA_OK;
-    return launch_pdl(apply_eviction_kernel, dim3(1), dim3(kPlanThreads), 0, q, p);
+    return launch_pdl(apply_eviction_kernel<1024>, dim3(1), dim3(1024), 0, q, p);
 }
 
 extern "C" pa_status pa_move_tokens(void *key_cache, void *value_cache, const int32_t *moves,
@@ -483,8 +482,9 @@ extern "C" pa_status pa_move_tokens(void *key_cache, void *value_cache, const in
     const pa_status st = device_info(dev, &info);
     if (st != PA_OK)
         return st;
-    const long long runs = (num_moves + kMoveRun - 1) / kMoveRun, warps = kMoveThreads / 32;
-    const int grid = (int)std::min<long long>(kMoveCtas * (long long)info.sms, (runs + warps - 1) / warps);
+    const long long warps = kMoveThreads / 32;
+    const int grid = (int)std::min<long long>(kMoveCtas * (long long)info.sms,
+                                              (num_moves + warps - 1) / warps);
     return launch_pdl(move_tokens_kernel, dim3(grid), dim3(kMoveThreads), 0, as_stream(stream),
                       static_cast<uint4 *>(key_cache), static_cast<uint4 *>(value_cache),
                       reinterpret_cast<const int2 *>(moves), (long long)num_moves,
