@@ -51,7 +51,8 @@ __device__ __forceinline__ CodeScale code_scale(float top)
 
 // ---- bounds ---------------------------------------------------------------------
 //
-// What bounds it: HBM, each key of a touched block read once.  A warp takes one
+// What bounds it: HBM, each key of a touched block read once (128 contexts, 904 MB of
+// keys: 159 us, 90 % of the measured copy rate).  A warp takes one
 // (block, KV head): its rows of d keys are runs of 64 to 256 bytes, so a group of
 // lanes has one row and the warp several, 16 bytes a lane, eight loads in flight;
 // minima and maxima are taken on packed pairs in the pools' own type (FP8 codes as
@@ -320,11 +321,12 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas)
 //    are small, several on an SM, so that one's selection hides behind the others' loads
 //    (copies into rings of shared memory in place of loads to registers leave room for
 //    fewer, and a second tile's registers cost what they bring).
-//  * The score product runs on the tensor cores as blocks x heads.  A lane's 16 bytes are
-//    taken in the order in which they lie (the sum over d is in a permuted order, which
-//    whole numbers allow), widened to fp16 (exact) and multiplied with the coded heads,
-//    kept in shared memory in the lanes' order.  fp16 products of codes are exact, and so
-//    are their sums in fp32.
+//  * The score product runs on the tensor cores as blocks x heads, on the codes as they
+//    are (mma m16n8k32 on signed bytes).  A lane's 16 bytes are taken in the order in which
+//    they lie (the sum over d is in a permuted order, which whole numbers allow) and
+//    multiplied with the coded heads, kept in shared memory in the lanes' order.  Widened
+//    to fp16 the same products took as long (21.3 us for 128 decode rows and 33.0 for 24
+//    long ones, against 22.0 and 32.3) in twice the instructions: they are not the limit.
 //  * Each CTA selects from its own candidates as many as are wanted of all, by one warp
 //    from its registers where they are few; the first CTA of a cluster selects from those
 //    lists, which come to its shared memory.
@@ -360,16 +362,14 @@ __device__ __forceinline__ uint32_t score_key(float x)
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// Four signed bytes to two fp16 pairs: u = code + 128 below fp16 1024 + u, less 1152.
-__device__ __forceinline__ void widen_codes(uint32_t w, uint32_t &a, uint32_t &b)
+// d[16 x 8] += a[16 x 32] b[32 x 8] on signed bytes, in 32 bits.
+__device__ __forceinline__ void mma_bytes(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    const uint32_t u = w ^ 0x80808080u;
-    const __half2 bias = __half2half2(__ushort_as_half(0x6480));  // 1152
-    uint32_t x = byte_perm(u, 0x64646464u, 0x4140u), y = byte_perm(u, 0x64646464u, 0x4342u);
-    const __half2 hx = __hsub2(*reinterpret_cast<__half2 *>(&x), bias);
-    const __half2 hy = __hsub2(*reinterpret_cast<__half2 *>(&y), bias);
-    a = *reinterpret_cast<const uint32_t *>(&hx);
-    b = *reinterpret_cast<const uint32_t *>(&hy);
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 "
+                 "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 struct SelectShared {
@@ -473,9 +473,9 @@ __global__ void __launch_bounds__(sel_threads(kClusters), sel_resident(kClusters
         ctas = (int)cg::this_cluster().num_blocks();
     }
     __shared__ SelectShared sh;
-    // B fragments of the coded heads: head 8 nt + g; product step (seg, k) of lane t4
-    // stands for codes 64 seg + 16 t4 + 4 k .. + 3 of a block's 2 D
-    __shared__ __align__(16) uint2 qf[NT][kSegs][4][32];
+    // B fragments of the coded heads: head 8 nt + g, codes 64 seg + 16 t4 .. + 15 of a
+    // block's 2 D for the lane (g, t4)
+    __shared__ __align__(16) uint4 qf[NT][kSegs][32];
     extern __shared__ uint32_t keys[];  // of this CTA's candidates; first, pool blocks
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t4 = lane & 3;
@@ -548,17 +548,15 @@ __global__ void __launch_bounds__(sel_threads(kClusters), sel_resident(kClusters
             top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
         ok = __all_sync(kFull, ok);
         const CodeScale cs = ok ? code_scale(top) : CodeScale{0.f, 0.f};
-        // element k = 32 e + lane of a side: product step k % 16 / 4 of run k / 64, lane
-        // 4 (h % 8) + k % 64 / 16 of the fragment, half k % 4 of its four
-        __half *frag = reinterpret_cast<__half *>(&qf[h / 8][0][(lane & 15) >> 2][0]) +
-                       4 * (4 * (h & 7) + (lane >> 4)) + (lane & 3);
+        // element k = 32 e + lane of a side: run k / 64, lane 4 (h % 8) + k % 64 / 16
+        int8_t *frag = reinterpret_cast<int8_t *>(&qf[h / 8][0][4 * (h & 7) + (lane >> 4)]) +
+                       (lane & 15);
 #pragma unroll
         for (int e = 0; e < D / 32; ++e) {
             const int code = ok ? __float2int_rn(__fmul_rn(x[r][e], cs.inv)) : 0;
-            // (a run is 4 x 32 fragments of four halves)
-            __half *at = frag + e / 2 * 512 + e % 2 * 8;
-            at[0] = __int2half_rn(min(code, 0));
-            at[D / 64 * 512] = __int2half_rn(max(code, 0));
+            int8_t *at = frag + e / 2 * 512 + e % 2 * 32;
+            at[0] = (int8_t)min(code, 0);
+            at[D / 64 * 512] = (int8_t)max(code, 0);
         }
         if (lane == 0)
             sh.q_scale[h] = cs.scale;
@@ -589,24 +587,18 @@ __global__ void __launch_bounds__(sel_threads(kClusters), sel_resident(kClusters
                 w[r][sg] = __ldg(src + sg * 4);
             scale[r] = __ldg(p.scales + at);
         }
-        float acc[NT][4];
+        int acc[NT][4];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
-            acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0.f;
+            acc[nt][0] = acc[nt][1] = acc[nt][2] = acc[nt][3] = 0;
 #pragma unroll
         for (int sg = 0; sg < kSegs; ++sg) {
-            const uint32_t a_lo[4] = {w[0][sg].x, w[0][sg].y, w[0][sg].z, w[0][sg].w};
-            const uint32_t a_hi[4] = {w[1][sg].x, w[1][sg].y, w[1][sg].z, w[1][sg].w};
+            const uint4 a = w[0][sg], b = w[1][sg];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t a[4];
-                widen_codes(a_lo[j], a[0], a[2]);
-                widen_codes(a_hi[j], a[1], a[3]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const uint2 b = qf[nt][sg][j][lane];
-                    MmaOp<__half>::run(acc[nt], a, b.x, b.y);
-                }
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint4 q = qf[nt][sg][lane];
+                mma_bytes(acc[nt], a.x, b.x, a.y, b.y, q.x, q.y);
+                mma_bytes(acc[nt], a.z, b.z, a.w, b.w, q.z, q.w);
             }
         }
 #pragma unroll
@@ -617,7 +609,8 @@ __global__ void __launch_bounds__(sel_threads(kClusters), sel_resident(kClusters
 #pragma unroll
                 for (int e = 0; e < 2; ++e)
                     if (nt * 8 + 2 * t4 + e < G)
-                        best = fmaxf(best, __fmul_rn(acc[nt][2 * r + e], q_scale[nt][e]));
+                        best = fmaxf(best, __fmul_rn((float)acc[nt][2 * r + e],
+                                                     q_scale[nt][e]));
             best = fmaxf(best, __shfl_xor_sync(kFull, best, 1));
             best = fmaxf(best, __shfl_xor_sync(kFull, best, 2));
             const int i = tile * 16 + g + 8 * r;
@@ -709,7 +702,7 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     const pa_status st = current_device(&dev, &info);
     if (st != PA_OK)
         return st;
-    const size_t room = (size_t)info.optin - (sizeof(SelectShared) + 32 * NT * D + 1024);
+    const size_t room = (size_t)info.optin - (sizeof(SelectShared) + 16 * NT * D + 1024);
     const int bs = 1 << p.block_shift;
     // candidates of a row, at most
     const int most = (int)std::min<long long>(p.max_blocks_per_seq,
@@ -795,7 +788,7 @@ extern "C" pa_status pa_summarize_blocks(int8_t *summaries, float *summary_scale
         !aligned16(summaries) || !aligned16(key_cache))
         return PA_ERR_INVALID_ARG;
     if (!pool_block(block_size, head_dim) || (long long)num_blocks * block_size >= (1ll << 31) ||
-        (long long)num_seqs * max_blocks_per_seq >= (1ll << 31))
+        (long long)num_seqs * max_blocks_per_seq >= (1ll << 31) - (1 << 20))
         return PA_ERR_UNSUPPORTED;
     SummaryParams p{};
     p.codes = summaries;

@@ -1056,6 +1056,8 @@ static pa_status launch_list_pass(const ListParams &prm, const CUtensorMap &mk,
 static pa_status launch_add_weights(const ListParams &prm, cudaStream_t stream)
 {
     const long long runs = ((long long)prm.pitch + kWeightThreads - 1) / kWeightThreads;
+    if (runs * prm.num_seqs > INT32_MAX)
+        return PA_ERR_UNSUPPORTED;
     const size_t smem = (size_t)prm.num_heads * 8;
     auto kernel = prm.group == 4    ? add_weights_kernel<4, 1>
                   : prm.group == 8  ? add_weights_kernel<4, 2>
@@ -1141,10 +1143,12 @@ static ListWorkspace list_workspace(int rows, int H, int Hkv, int D, int parts, 
     return w;
 }
 
-// Positions of a sequence in the workspace's scores.
+// Positions of a sequence in the workspace's scores: a tile at least, so that a call on
+// contexts of no token has its counts' place too.
 static long long score_pitch(int max_context_len)
 {
-    return ((long long)max_context_len + kTileTokens - 1) / kTileTokens * kTileTokens;
+    return ((long long)std::max(1, max_context_len) + kTileTokens - 1) / kTileTokens *
+           kTileTokens;
 }
 
 static bool scales_ok(float scale, bool fp8, float k_scale, float v_scale)

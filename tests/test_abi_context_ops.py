@@ -147,6 +147,10 @@ def test_weights_refuses(B):
     need = B.pa_weights_workspace_bytes(2, 8, 2, 128, 128, 16)
     assert need == B.pa_decode_workspace_bytes(2, 8, 2, 128, 128, 16) + 256 + 2 * 8 * 128 * 4
     refuses(f, B.PA_ERR_WORKSPACE, dict(ws=None), dict(wsb=need - 1), P=16)
+    for P in (0, 16):                                       # contexts of no token have counts
+        need = B.pa_weights_workspace_bytes(2, 8, 2, 128, 0, P)
+        assert need == 3 * 256 + 2 * 8 * 16 * 4
+        refuses(f, B.PA_ERR_WORKSPACE, dict(ws=None), dict(wsb=need - 1), dict(wsb=0), P=P, maxctx=0)
     for bad in ((-1, 8, 2, 128, 128, 16), (2, 8, 2, 128, -1, 16), (2, 8, 2, 128, 128, -16)):
         assert B.pa_weights_workspace_bytes(*bad) == 0
 

@@ -214,6 +214,8 @@ SELECT = [
     (5, 5, 128, 16, [1030], 64, 1, 1),                      # 65 blocks of which 64
     (24, 2, 64, 16, [40000, 17, 12345], 100, 1, 4),         # clusters of several CTAs
     (2, 1, 128, 16, [100000], 129, 3, 0),
+    (4, 2, 64, 16, [90000, 5000], 4, 2, 2),                 # the same in clusters
+    (16, 1, 128, 16, [60000, 300], 1500, 10, 20),           # lists longer than a CTA's share
 ]
 
 
@@ -285,3 +287,30 @@ def test_selection_repeats_and_takes_any_stream(B):
         b = x.select(B, q, [0, 1], [29999, 8999], 64, 1, 2)
     c = x.select(B, q, [0, 1], [29999, 8999], 64, 1, 2, stream=side)
     assert np.array_equal(a, b) and np.array_equal(a, c)
+
+
+def test_blocks_past_32_bits(B):
+    """Codes and keys whose bytes lie past 4 GB of their pools."""
+    if torch.cuda.mem_get_info()[0] < 16 << 30:
+        pytest.skip("not enough memory")
+    N, K, D, bs = 2_200_000, 8, 128, 16
+    codes = torch.zeros((N, K, 2, D), dtype=torch.int8, device="cuda")
+    scales = torch.ones((N, K), device="cuda")
+    tables = np.array([[N - 1 - 3 * j for j in range(40)]])
+    for j, level in ((7, 90), (23, 100), (24, 80)):
+        codes[int(tables[0, j]), :, 1] = level
+    q = torch.ones((1, 16, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.full((1, K, 4), 9, dtype=torch.int32, device="cuda")
+    B.pa_select_blocks(out, q, codes, scales, i32(tables), i32([0]), i32([639]), 640, bs, 0, 1)
+    assert out.tolist() == [[[7, 23, 24, 39]] * K]
+    del codes, scales
+    N, K = 40000, 32
+    keys = torch.zeros((N, bs, K, D), dtype=torch.bfloat16, device="cuda")
+    keys[N - 1, 3, :, 5] = -2.0
+    codes = torch.full((N, K, 2, D), 1, dtype=torch.int8, device="cuda")
+    scales = torch.full((N, K), 3.0, device="cuda")
+    B.pa_summarize_blocks(codes, scales, keys, i32([[N - 1, N - 2]]), i32([20]))
+    assert codes[N - 1, :, 0, 5].eq(-127).all() and codes[N - 1].ne(0).sum() == K
+    assert scales[N - 2].eq(0).all() and scales[N - 3].eq(3).all()
+    assert torch.equal(scales[N - 1], torch.full((K,), 2.0, device="cuda") *
+                       torch.tensor(1 / 127.0, device="cuda"))

@@ -223,3 +223,42 @@ def test_two_steps_on_two_streams(B):
     torch.cuda.synchronize()
     for c in cs:
         c.check()
+
+
+@pytest.mark.parametrize("P", [0, 64])
+def test_no_token_at_all(B, P):
+    """Empty contexts, and a longest context of 0."""
+    c = Case([0, 0, 0], [0, 5, -3], 4, 2, 64, 16, torch.float16, False, seed=1, slack=100)
+    c.run(B, P)
+    c.check()
+    c.max_ctx = 0
+    c.out.fill_(7.0)
+    c.run(B, P)
+    c.check()
+    assert not c.out.any() and (c.weights_out == -5.0).all()
+
+
+def test_scores_past_32_bits(B):
+    """A longest context that puts the second sequence's scores past 4 GB."""
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("not enough memory")
+    c = Case([33, 700], [0, 699], 128, 8, 64, 16, torch.bfloat16, False, seed=4)
+    c.max_ctx = 10_000_000
+    c.tables = np.concatenate([c.tables, np.full((2, 625_000 - c.tables.shape[1]), -1,
+                                                 dtype=np.int32)], 1)
+    for P in (0, 512):
+        c.out.fill_(7.0)
+        c.weights_out.fill_(-5.0)
+        c.run(B, P)
+        c.check(what=f"partition {P}")
+
+
+def test_one_long_sequence_among_many(B):
+    """Shares of a batch in which one context holds most tokens, and its partials pass
+    what the pass merges itself."""
+    ctx = [3] * 40 + [30000] + [1] * 30
+    c = Case(ctx, [2] * 40 + [29999] + [0] * 30, 8, 8, 64, 32, torch.bfloat16, True, seed=5)
+    for P in (0, 16, 256):
+        c.out.fill_(7.0)
+        c.run(B, P)
+        c.check(what=f"partition {P}")
