@@ -278,3 +278,50 @@ def test_sparse_over_all_blocks_is_decode(B, fp8):
     torch.cuda.synchronize()
     _, tol = c.want()
     assert_within(a, dense.double().cpu().numpy(), 2 * tol)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("P", [0, 32])
+def test_a_wait_runs_out_and_the_next_call_answers(B, P, fp8):
+    ctx = np.array([500, 90, 333])
+    c = Case(ctx, np.arange(3), ctx - 1, 8, 2, 128, 16, 9, torch.bfloat16, fp8, seed=6)
+    ws = c.workspace(B, P)
+    try:
+        B.pa_set_stage_wait_limit_ns(2_000_000)
+        B.pa_debug_withhold_first_fill(True)
+        c.run(B, P, ws)
+    finally:
+        B.pa_debug_withhold_first_fill(False)
+        B.pa_set_stage_wait_limit_ns(0)
+    assert int(c.err.item()) == B.DEVERR_TIMEOUT
+    c.err.zero_()
+    c.run(B, P, ws)
+    c.check()
+
+
+def test_graphs_that_share_a_workspace(B):
+    """Two captured calls of different sizes over one workspace, replayed in turn."""
+    cs = [Case([700, 33, 512], [0, 1, 2], np.array([699, 32, 511]), 8, 2, 128, 16, 40,
+               torch.bfloat16, False, seed=1),
+          Case([900], [0, 0], np.array([899, 898]), 16, 1, 64, 32, 12, torch.float16, True,
+               seed=2)]
+    ws = max((c.workspace(B, 64) for c in cs), key=lambda w: w.numel())
+    args = [[i32(x) for x in (c.tables, c.seq, c.pos, c.chosen)] for c in cs]
+    graphs = []
+    for c, a in zip(cs, args):
+        call = lambda: B.pa_decode_attention_sparse(  # noqa: E731
+            c.out, c.q, c.kc, c.vc, *a, c.scale, 64, ws, k_scale=c.kv, v_scale=c.kv,
+            error_word=c.err)
+        call()
+        torch.cuda.synchronize()
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            call()
+    for _ in range(3):
+        for c in cs:
+            c.out.fill_(7.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for c in cs:
+            c.check()

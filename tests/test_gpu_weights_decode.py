@@ -262,3 +262,21 @@ def test_one_long_sequence_among_many(B):
         c.out.fill_(7.0)
         c.run(B, P)
         c.check(what=f"partition {P}")
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("P", [0, 32])
+def test_a_wait_runs_out_and_the_next_call_answers(B, P, fp8):
+    c = Case([500, 90, 333], [499, 0, 332], 8, 2, 128, 16, torch.bfloat16, fp8, seed=6)
+    ws = c.workspace(B, P)
+    try:
+        B.pa_set_stage_wait_limit_ns(2_000_000)
+        B.pa_debug_withhold_first_fill(True)
+        c.run(B, P, ws)
+    finally:
+        B.pa_debug_withhold_first_fill(False)
+        B.pa_set_stage_wait_limit_ns(0)
+    assert int(c.err.item()) == B.DEVERR_TIMEOUT
+    c.err.zero_()
+    c.run(B, P, ws)
+    c.check()
