@@ -848,8 +848,9 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
             if (un < u_end)
                 named_barrier_arrive(kRecFree, kThreads);
             if (split && !by_kernel(x.nparts))
-                // records loaded per lane at once: fewer under the FP8 register cap
-                arrive_and_merge<T, D, kHeads, kFp8 ? 2 : 8>(p, x.r, x.kh, x.nparts, lane);
+                // (eight records loaded per lane at once: of two, long contexts over FP8 pools
+                // 138 us for 131)
+                arrive_and_merge<T, D, kHeads, 8>(p, x.r, x.kh, x.nparts, lane);
             u = un;
         }
     }
