@@ -1152,6 +1152,35 @@ static long long score_pitch(int max_context_len)
            kTileTokens;
 }
 
+// encode_pool_map for pools whose KV heads are read from blocks of their own: a miss brings
+// the head's own elements of a token into L2 and not its neighbour's, which the shared
+// map's promotion to 256 bytes does (16 lists of 4,096 tokens, FP8: 175 MB from memory for
+// 133 MB of listed keys and values).
+static bool encode_list_map(CUtensorMap *map, const void *pool, pa_dtype dtype, int num_blocks,
+                            int block_size, int num_kv_heads, int head_dim)
+{
+    EncodeTiledFn fn = get_encode_fn();
+    if (!fn)
+        return false;
+    const bool fp8 = dtype == PA_FP8_E4M3;
+    const cuuint64_t e = fp8 ? 1 : 2, row = (cuuint64_t)num_kv_heads * head_dim * e;
+    const CUtensorMapDataType ty = fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : dtype == PA_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                                      : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    const cuuint64_t dims[4] = {(cuuint64_t)head_dim, (cuuint64_t)num_kv_heads,
+                                (cuuint64_t)block_size, (cuuint64_t)num_blocks};
+    const cuuint64_t strides[3] = {(cuuint64_t)head_dim * e, row, row * block_size};
+    const cuuint32_t box[4] = {fp8 ? (cuuint32_t)head_dim : 64u, 1, (cuuint32_t)kTileTokens, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUtensorMapL2promotion wide = head_dim * e >= 256   ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                        : head_dim * e >= 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B
+                                                              : CU_TENSOR_MAP_L2_PROMOTION_L2_64B;
+    return fn(map, ty, 4, const_cast<void *>(pool), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE,
+              fp8 && head_dim == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, wide,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 static bool scales_ok(float scale, bool fp8, float k_scale, float v_scale)
 {
     if (fp8 && !(std::isfinite(k_scale) && std::isfinite(v_scale) && k_scale > 0.f &&
@@ -1241,8 +1270,9 @@ static pa_status run_list(ListParams &prm, void *out, const void *query, const v
     }
     CUtensorMap mk, mv;
     const pa_dtype pool = fp8 ? PA_FP8_E4M3 : dtype;
-    if (!encode_pool_map(&mk, key_cache, pool, num_blocks, block_size, num_kv_heads, head_dim) ||
-        !encode_pool_map(&mv, value_cache, pool, num_blocks, block_size, num_kv_heads, head_dim))
+    const auto encode = kSparse ? encode_list_map : encode_pool_map;
+    if (!encode(&mk, key_cache, pool, num_blocks, block_size, num_kv_heads, head_dim) ||
+        !encode(&mv, value_cache, pool, num_blocks, block_size, num_kv_heads, head_dim))
         return PA_ERR_CUDA;
     cudaStream_t st = as_stream(stream);
     using B16 = __nv_bfloat16;
