@@ -638,10 +638,11 @@ PA_API pa_status pa_select_blocks(int32_t *selected, int top_k, const void *quer
  *   token_seq, token_pos, selected : as pa_select_blocks takes and gives them; an
  *                    entry past the row's own block is left out and sets
  *                    PA_DEVERR_CONTEXT_RANGE
- *   partition_size : as pa_decode_attention, in tokens of the list (top_k * block_size
- *                    of them at most); a remainder of less than half a partition joins
- *                    the one before, and partitions are longer where fewer of them fill
- *                    the GPU
+ *   partition_size : 0: one pass over each list.  Otherwise (a multiple of 16
+ *                    tokens) lists are split among CTAs, into equal shares of all
+ *                    of them with at least so many tokens of a list each (at most
+ *                    8,192 rows; more are not split); partials are merged as
+ *                    pa_decode_attention's
  *   workspace      : >= pa_sparse_workspace_bytes(...) bytes, 256-byte aligned, its
  *                    first bytes (the arrival counters of pa_decode_workspace_bytes, the
  *                    same region) zeroed before first use; may be NULL when that size
@@ -689,8 +690,7 @@ PA_API pa_status pa_decode_attention_sparse_fp8(
  *   workspace      : >= pa_weights_workspace_bytes(...) bytes (the scores of every
  *                    head and position among them), 256-byte aligned, its first bytes
  *                    zeroed before first use as pa_decode_attention's
- *   partition_size : as pa_decode_attention; a remainder of less than half a
- *                    partition joins the one before
+ *   partition_size : as pa_decode_attention_sparse, of the contexts
  * num_heads <= 4,096, and the limits of pa_decode_attention_sparse.  Other arguments
  * and errors as pa_decode_attention(_fp8).
  */

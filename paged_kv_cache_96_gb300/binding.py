@@ -5,7 +5,8 @@ Argument marshalling only: every function takes torch CUDA tensors, checks
 their dtype, device and contiguity, and passes raw pointers, sizes and the
 current CUDA stream to the library of the same name.  All computation runs
 in the library's kernels.  The serving-step calls (step maps, rotary cache write,
-windowed attention) do the same in C++ (``pyext/calls.cpp``), since the host's part
+windowed attention) and the long-context ones (block selection, attention over lists,
+accumulated weights, eviction) do the same in C++ (``pyext/calls.cpp``), since the host's part
 is most of what a small one takes; that extension is loaded when one of them is first
 used.  There is no fallback: if the library has not been built, importing this module
 raises, and so do those calls without the extension.

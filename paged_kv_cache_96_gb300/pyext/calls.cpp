@@ -1,5 +1,5 @@
-// calls.cpp -- the serving-step entry points of libpaged_attention called from
-// Python with torch tensors: argument checks and marshalling, as binding.py does
+// calls.cpp -- the serving-step and long-context entry points of libpaged_attention
+// called from Python with torch tensors: argument checks and marshalling, as binding.py does
 // through ctypes for the others.
 //
 // One step of a small batch is a few microseconds of GPU work behind four such
