@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
     // shares of all tiles, numbered through the rows: as many CTAs as there are KV heads
     // take one share, a head each, so that a token's heads, which lie side by side, are
     // read at about the same time (shares numbered through the heads as well: long
-    // contexts over FP8 pools 191 us, so 150).  A unit is what one row has in the share.
+    // contexts over FP8 pools 191 us, so 138).  A unit is what one row has in the share.
     const bool share = p.share_min > 0;
     int W = 0;                          // tiles of a share
     int u_first = blockIdx.x, u_end = S * Hkv;
