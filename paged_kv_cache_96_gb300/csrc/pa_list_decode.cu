@@ -63,7 +63,7 @@ struct ListParams : DecodeParams {
 };
 
 // Rows of at most this many partials are merged by the pass, others by the reduce
-// kernel behind it.
+// kernel behind it (long contexts with weights, FP8: 135 us, up to 8 in the pass 138).
 constexpr int kListMergeMax = 4;
 
 // Rows whose tiles are numbered for shares, at most: 4 bytes each in every CTA's shared
@@ -994,7 +994,9 @@ __global__ void __launch_bounds__(kWeightThreads)
 // ---- host side -------------------------------------------------------------------
 
 // Tile warps per CTA (the merge warp comes on top), ring stages per warp and CTAs per
-// SM the register budget is sized for, as in windowed decode: 16-bit pools, FP8 pools.
+// SM the register budget is sized for: 16-bit pools, FP8 pools.  Windowed decode's 5 warps
+// of 2 stages, and 3 CTAs of 4 over FP8 pools, take 326 us for 311 (128 contexts with
+// weights) and 138 for 136 (long ones, FP8); 3 x 4 stages 339, 3 CTAs of 4 x 4 168.
 constexpr int kListWarps = 4, kListStages = 2, kListMinBlocks = 2;
 constexpr int kListWarpsFp8 = 3, kListStagesFp8 = 3, kListMinBlocksFp8 = 4;
 
@@ -1132,9 +1134,12 @@ static ListWorkspace list_workspace(int rows, int H, int Hkv, int D, int parts, 
     w.l_off = w.decode.l_off;
     w.total = w.decode.total;
     if (pitch > 0 && parts <= 1) {
-        w.m_off = 0;
-        w.l_off = align256((size_t)rows * H * 4);
-        w.total = 2 * w.l_off;
+        // (behind the arrival counters' place all the same: a workspace that calls with
+        // partitions share keeps its zeros)
+        const size_t ml = align256((size_t)rows * H * 4);
+        w.m_off = align256(std::max<size_t>(kCounterWords, (size_t)rows * Hkv) * 4);
+        w.l_off = w.m_off + ml;
+        w.total = w.l_off + ml;
     }
     w.len_off = w.total;  // partials of each row: for the reduce kernel, and of all
     if (parts > 1 || pitch > 0)
@@ -1242,7 +1247,7 @@ static pa_status run_list(ListParams &prm, void *out, const void *query, const v
         if (kSparse) {
             // Lists are of one length, or shorter: with fewer of them than CTAs for a KV
             // head, each is cut into as many shares of its own as fill these (16 rows of
-            // 4,096 tokens, FP8: 38.7 us; shares across rows have a few partials more to
+            // 4,096 tokens, FP8: 39.0 us; shares across rows have a few partials more to
             // merge, 42.3).
             DeviceInfo info;
             int dev = 0;

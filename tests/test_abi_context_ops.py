@@ -141,7 +141,8 @@ def test_weights_refuses(B):
     refuses(f, B.PA_ERR_UNSUPPORTED, dict(H=8192, K=512), dict(maxctx=(1 << 31) - 1))
     assert f(S=0) == B.PA_OK
     need = B.pa_weights_workspace_bytes(2, 8, 2, 128, 128, 0)
-    assert need == 3 * 256 + 2 * 8 * 128 * 4                # sums, partials, scores
+    counters = 1 << 20                                      # kept for calls with partitions
+    assert need == counters + 3 * 256 + 2 * 8 * 128 * 4     # sums, partials, scores
     refuses(f, B.PA_ERR_WORKSPACE, dict(ws=None), dict(wsb=need - 1),
             dict(ws=ctypes.c_void_p(0x40000010)))
     need = B.pa_weights_workspace_bytes(2, 8, 2, 128, 128, 16)
@@ -149,7 +150,7 @@ def test_weights_refuses(B):
     refuses(f, B.PA_ERR_WORKSPACE, dict(ws=None), dict(wsb=need - 1), P=16)
     for P in (0, 16):                                       # contexts of no token have counts
         need = B.pa_weights_workspace_bytes(2, 8, 2, 128, 0, P)
-        assert need == 3 * 256 + 2 * 8 * 16 * 4
+        assert need == counters + 3 * 256 + 2 * 8 * 16 * 4
         refuses(f, B.PA_ERR_WORKSPACE, dict(ws=None), dict(wsb=need - 1), dict(wsb=0), P=P, maxctx=0)
     for bad in ((-1, 8, 2, 128, 128, 16), (2, 8, 2, 128, -1, 16), (2, 8, 2, 128, 128, -16)):
         assert B.pa_weights_workspace_bytes(*bad) == 0

@@ -280,3 +280,15 @@ def test_a_wait_runs_out_and_the_next_call_answers(B, P, fp8):
     c.err.zero_()
     c.run(B, P, ws)
     c.check()
+
+
+def test_one_workspace_for_calls_with_and_without_partitions(B):
+    """A call on whole contexts leaves the arrival counters of the others at zero."""
+    c = Case([900, 333, 16], [899, 0, 15], 16, 2, 128, 16, torch.bfloat16, False, seed=9)
+    ws = max((c.workspace(B, P) for P in (0, 32, 256)), key=lambda w: w.numel())
+    for P in (0, 32, 0, 256, 0, 32):
+        c.out.fill_(7.0)
+        c.weights_out.fill_(-5.0)
+        c.run(B, P, ws)
+        c.check(what=f"partition {P}")
+        assert not ws[:1 << 20].any()
