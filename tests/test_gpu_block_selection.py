@@ -314,3 +314,29 @@ def test_blocks_past_32_bits(B):
     assert scales[N - 2].eq(0).all() and scales[N - 3].eq(3).all()
     assert torch.equal(scales[N - 1], torch.full((K,), 2.0, device="cuda") *
                        torch.tensor(1 / 127.0, device="cuda"))
+
+
+def test_the_longest_contexts(B):
+    """300,000 blocks of one context at lists of 128, beside a short one; more than the
+    shared memory of eight CTAs holds is refused."""
+    N, D, bs = 300_000, 64, 16
+    codes = torch.zeros((N, 2, 2, D), dtype=torch.int8, device="cuda")
+    scales = torch.ones((N, 2), device="cuda")
+    best = [0, 7, 1000, 123_456, 262_143, 262_144, 299_000]
+    for j, b in enumerate(best):
+        codes[b, 1, 1] = 100 - j
+    tables = torch.arange(N, dtype=torch.int32, device="cuda").expand(2, N).contiguous()
+    q = torch.ones((2, 4, D), dtype=torch.float16, device="cuda")
+    out = torch.full((2, 2, 128), 9, dtype=torch.int32, device="cuda")
+    B.pa_select_blocks(out, q, codes, scales, tables, i32([0, 1]), i32([N * bs - 1, 40]), N * bs, bs,
+                       0, 1)
+    # (of equal scores the lower blocks)
+    rest = [b for b in range(200) if b not in best][:127 - len(best)]
+    assert out[0, 1].tolist() == sorted(best + rest) + [N - 1]
+    assert out[0, 0].tolist() == list(range(127)) + [N - 1]
+    assert out[1].tolist() == [[0, 1, 2] + [-1] * 125] * 2
+    wide = torch.zeros((2, 500_000), dtype=torch.int32, device="cuda")
+    with pytest.raises(B.PAError) as e:
+        B.pa_select_blocks(out, q, codes, scales, wide, i32([0, 1]), i32([9, 9]), 500_000 * bs, bs,
+                           0, 1)
+    assert e.value.status == B.PA_ERR_UNSUPPORTED
