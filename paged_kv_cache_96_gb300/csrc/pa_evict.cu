@@ -62,9 +62,8 @@ constexpr int kPlanBatch = 4;
 
 struct PlanShared {
     TopkShared<11> topk;
-    int above[32], ties[32];
+    int above[32], ties[32], low_above[32], low_ties[32];
     long long given[32], before[32];
-    int low_kept;  // tokens between the first and the last ones that stay below the budget
 };
 
 // Blocks that all sequences give back, and those of sequences below s; whether a
@@ -209,25 +208,36 @@ __global__ void __launch_bounds__(THREADS)
             // a warp's run of them; the tokens that stay before each run
             const int run = (n + THREADS - 1) / THREADS * 32;
             const int i0 = min(n, warp * run), i1 = min(n, i0 + run);
-            int above = 0, ties = 0;
+            const int low = p.budget - first;  // candidates below the budget
+            int above = 0, ties = 0, low_above = 0, low_ties = 0;
             for (int i = i0 + lane; i < i1; i += 32) {
                 const uint32_t v = cut.level(key(i));
                 above += v > cut.prefix;
                 ties += v == cut.prefix;
+                low_above += i < low && v > cut.prefix;
+                low_ties += i < low && v == cut.prefix;
             }
             above = __reduce_add_sync(kFull, above);
             ties = __reduce_add_sync(kFull, ties);
+            low_above = __reduce_add_sync(kFull, low_above);
+            low_ties = __reduce_add_sync(kFull, low_ties);
             if (lane == 0) {
                 sh.above[warp] = above;
                 sh.ties[warp] = ties;
+                sh.low_above[warp] = low_above;
+                sh.low_ties[warp] = low_ties;
             }
             __syncthreads();
-            above = ties = 0;
-            for (int w = 0; w < warp; ++w) {
-                above += sh.above[w];
-                ties += sh.ties[w];
+            above = ties = low_above = low_ties = 0;
+#pragma unroll
+            for (int w = 0; w < THREADS / 32; ++w) {
+                above += w < warp ? sh.above[w] : 0;
+                ties += w < warp ? sh.ties[w] : 0;
+                low_above += sh.low_above[w];
+                low_ties += sh.low_ties[w];
             }
-            const int low = p.budget - first;  // candidates below the budget
+            // candidates below the budget that stay (of equal ones the first)
+            const int low_kept = low_above + min(low_ties, cut.rest);
             // visit(i, stays, how many before it do) for every candidate of the run
             auto walk = [&](auto &&visit) {
                 int a = above, t = ties;
@@ -245,15 +255,6 @@ __global__ void __launch_bounds__(THREADS)
                     t += __popc(tie);
                 }
             };
-            if (tid == 0 && low >= n)
-                sh.low_kept = want;
-            if (low >= i0 && low < i1)
-                walk([&](int i, bool, int before) {
-                    if (i == low)
-                        sh.low_kept = before;
-                });
-            __syncthreads();
-            const int low_kept = sh.low_kept;
             walk([&](int i, bool stays, int before) {
                 if (i < low && !stays)
                     moves[2 * (i - before) + 1] = slot_of(first + i);
