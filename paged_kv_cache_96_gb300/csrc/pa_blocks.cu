@@ -52,7 +52,7 @@ __device__ __forceinline__ CodeScale code_scale(float top)
 // ---- bounds ---------------------------------------------------------------------
 //
 // What bounds it: HBM, each key of a touched block read once (128 contexts, 904 MB of
-// keys: 159 us, 90 % of the measured copy rate).  A warp takes one
+// keys: 153 us, 93 % of the measured copy rate).  A warp takes one
 // (block, KV head): its rows of d keys are runs of 64 to 256 bytes, so a group of
 // lanes has one row and the warp several, 16 bytes a lane, eight loads in flight;
 // minima and maxima are taken on packed pairs in the pools' own type (FP8 codes as
@@ -72,7 +72,8 @@ struct SummaryParams {
 };
 
 constexpr int kSumThreads = 256;
-constexpr int kSumCtas = 5;  // resident on an SM, which the grid fills once
+// Resident CTAs of an SM, which the grid fills once (5, with spilled registers: 159 us).
+constexpr int kSumCtas = 4;
 constexpr int kSumSeqs = 2 * kSumThreads;  // sequences numbered at once
 
 // First block and number of blocks that the new tokens of sequence s are in.
