@@ -746,6 +746,11 @@ PA_API pa_status pa_decode_attention_weights_fp8(
  * pass num_blocks or its count is negative (PA_DEVERR_BLOCK_RANGE).  Blocks are taken to
  * have one owner.  block_size: a power of two; max_moves <= 2^29.
  * Bounds of the changed blocks: pa_summarize_blocks over whole contexts.
+ *
+ * The last num_recent are those that lie last.  A plan takes them to the places of evicted
+ * tokens, so that they are also the newest only in a sequence that is evicted from for the
+ * first time, or where limit - budget + 1 >= num_recent: then so many tokens have come
+ * since.  pa_plan_eviction_aged keeps the newest under every rule.
  */
 PA_API pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *context_lens_out,
                                   int32_t *free_count_out, float *weights_out,
@@ -755,6 +760,35 @@ PA_API pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *contex
                                   int max_context_len, int limit, int budget, int num_sinks,
                                   int num_recent, int num_seqs, int block_size, int num_blocks,
                                   int32_t *error_word, void *stream);
+
+/*
+ * pa_plan_eviction_aged -- pa_plan_eviction for sequences that are evicted from again and
+ * again: the last num_recent are, of the cached ones, those of the num_recent tokens that
+ * arrived last, wherever earlier plans have moved them.  Of two tokens the one with the larger number of arrival is the newer; the
+ * token that arrived k-th in its sequence, k = 0, 1, ..., has number k.
+ *   arrivals       : int32 [num_blocks][block_size] (in and out): numbers of arrival, in
+ *                    the tokens' slots.  A plan that evicts from a sequence numbers its
+ *                    tokens that have none and takes the numbers to their new places; the
+ *                    caller writes none.
+ *   numbered_lens  : int32 [num_seqs] (in and out): places of the sequence, from the first
+ *                    on, whose tokens have a number.  0 for a sequence that no plan has
+ *                    evicted from, then the budget of the last one that did.
+ *   evicted        : int32 [num_seqs] (in and out): tokens evicted from the sequence so
+ *                    far.  0 for a new sequence.  The next token's place in the text, which
+ *                    its rotary position is, is its place in the cache plus this number.
+ * numbered_lens and evicted move with a sequence that changes its row of the batch.  A
+ * numbered_lens outside [0, context_lens] of a sequence that is evicted from counts as 0
+ * and sets PA_DEVERR_CONTEXT_RANGE.  A refused plan leaves all three as they were.  For a
+ * sequence that is evicted from for the first time the plan is pa_plan_eviction's.  Other
+ * arguments and errors as pa_plan_eviction.
+ */
+PA_API pa_status pa_plan_eviction_aged(
+    int32_t *moves, int max_moves, int32_t *context_lens_out, int32_t *free_count_out,
+    float *weights_out, int32_t *arrivals, int32_t *numbered_lens, int32_t *evicted,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    const float *weights, int32_t *free_blocks, const int32_t *free_count, int max_context_len,
+    int limit, int budget, int num_sinks, int num_recent, int num_seqs, int block_size,
+    int num_blocks, int32_t *error_word, void *stream);
 
 /*
  * pa_move_tokens -- pa_copy_blocks for single tokens: for every pair (from, to) of

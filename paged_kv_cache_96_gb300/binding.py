@@ -127,6 +127,8 @@ def _load() -> ctypes.CDLL:
                                                   i32, P, P]),
         "pa_plan_eviction": (i32, [P, i32, P, P, P, P, i32, P, P, P, P, i32, i32, i32, i32, i32,
                                    i32, i32, i32, P, P]),
+        "pa_plan_eviction_aged": (i32, [P, i32, P, P, P, P, P, P, P, i32, P, P, P, P, i32, i32, i32,
+                                        i32, i32, i32, i32, i32, P, P]),
         "pa_move_tokens": (i32, [P, P, P, i64, i32, i32, i32, i32, i32, P, P]),
         "pa_prefix_plan_ints": (sz, [i32, i32, i32]),
         "pa_plan_prefix_groups": (i32, [P, i32, P, i32, i32, i32, P, sz, P, P]),
@@ -720,18 +722,26 @@ def pa_plan_eviction(moves: torch.Tensor, context_lens_out: torch.Tensor,
                      weights: torch.Tensor, free_blocks: torch.Tensor, free_count: torch.Tensor,
                      max_context_len: int, limit: int, budget: int, num_sinks: int = 0,
                      num_recent: int = 0, error_word: Optional[torch.Tensor] = None,
-                     stream=None) -> None:
+                     stream=None, arrivals: Optional[torch.Tensor] = None,
+                     numbered_lens: Optional[torch.Tensor] = None,
+                     evicted: Optional[torch.Tensor] = None) -> None:
     """Cut sequences of more than `limit` cached tokens down to `budget`: the first
     num_sinks, the last num_recent and those of the largest weights [N, bs].
     moves int32 [S, M, 2] gets the (from, to) slots for pa_move_tokens (then -1),
     free_blocks the blocks given back; context_lens_out, free_count_out and
-    weights_out may be the inputs."""
+    weights_out may be the inputs.
+
+    Sequences that are evicted from again and again need arrivals int32 [N, bs],
+    numbered_lens [S] and evicted [S] (all three, changed in place; the two lengths 0 for
+    a new sequence): without them the last num_recent are those that lie last, which
+    are the newest only where limit - budget + 1 >= num_recent.  The next token's rotary
+    position is its place in the cache + evicted."""
     status = _calls.plan_eviction(moves, context_lens_out, free_count_out, weights_out,
                                   block_tables, context_lens, weights, free_blocks, free_count,
                                   max_context_len, limit, budget, num_sinks, num_recent,
-                                  error_word, stream)
+                                  error_word, stream, arrivals, numbered_lens, evicted)
     if status:
-        raise PAError("pa_plan_eviction", status)
+        raise PAError("pa_plan_eviction" + ("" if arrivals is None else "_aged"), status)
 
 
 def pa_move_tokens(key_cache: torch.Tensor, value_cache: torch.Tensor, moves: torch.Tensor,

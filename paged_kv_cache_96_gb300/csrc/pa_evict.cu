@@ -10,8 +10,15 @@
 // go by the order of cached tokens (their positions are in the rotated keys), so rows
 // below `budget` that stay are not moved: the i-th row that stays at or past it takes
 // the place of the i-th evicted one before it.  A sequence one step past its limit
-// costs a handful of rows, not a copy of the context.  Blocks behind the budget go back
-// on the free stack, sequences in batch order, blocks in logical order.
+// costs a handful of rows, not a copy of the context (step by step: the aged form).
+// Blocks behind the budget go back on the free stack, sequences in batch order, blocks in
+// logical order.
+//
+// That also takes the newest tokens to places of evicted ones, behind which older ones
+// lie: by place alone the next plan's last num_recent are the newest only where at least
+// as many tokens come between two evictions of a sequence (limit - budget + 1 >=
+// num_recent).  The aged form keeps each token's number of arrival beside its weight and
+// guards by that.
 //
 // What bounds it: the plan, latency (a sequence's weights are 4 bytes a token, and
 // selection is a chain of passes over them); the moves, HBM: 4 rows of num_kv_heads *
@@ -34,6 +41,9 @@ struct PlanParams {
     int max_moves, max_blocks_per_seq, max_context_len, limit, budget, num_sinks, num_recent;
     int num_seqs, block_shift, num_blocks;
     int apply_later;  // the outputs are the inputs: they are written behind the plan
+    // aged form, or null: number of arrival of each token, of those that have one; of each
+    // sequence the tokens that have one, and those evicted so far
+    int32_t *arrivals, *numbered_lens, *evicted;
 };
 
 // What a sequence's length asks for.
@@ -111,8 +121,10 @@ __device__ __forceinline__ int plan_refusal(const PlanParams &p, const PlanTotal
 }
 
 // One CTA per sequence.  kKept: the keys of the whole context, and its table row, fit in
-// shared memory; else each pass reads the weights again, through L2.
-template <int THREADS, bool kKept>
+// shared memory; else each pass reads the weights again, through L2.  kAged: the last
+// num_recent are those that arrived last, wherever they lie: candidates whose key is above
+// any weight's.  (A template of its own, so that the form by place has no test of it.)
+template <int THREADS, bool kKept, bool kAged>
 __global__ void __launch_bounds__(THREADS)
     plan_eviction_kernel(const __grid_constant__ PlanParams p)
 {
@@ -139,6 +151,9 @@ __global__ void __launch_bounds__(THREADS)
     if (kKept)
         for (int b = tid; b < q.have; b += THREADS)
             row[b] = block_of(b);
+    // the token at place i >= numbered has number i + gone
+    const int gone = kAged ? p.evicted[s] : 0;
+    int numbered = kAged ? p.numbered_lens[s] : 0;
     const PlanTotal sum = plan_total<THREADS>(sh, p, s);  // (with a barrier)
     const int refuse = plan_refusal(p, sum);
     const int slots = p.num_blocks << p.block_shift;
@@ -164,12 +179,37 @@ __global__ void __launch_bounds__(THREADS)
                 flag_error(p.error_word, PA_DEVERR_BLOCK_RANGE);
             top[i] = id;
         }
-        const int first = p.num_sinks, tail = q.c - p.num_recent;  // chosen from [first, tail)
+        // chosen from [first, tail)
+        const int first = p.num_sinks, tail = kAged ? q.c : q.c - p.num_recent;
         const int n = q.end != q.c ? tail - first : 0;
+        if (kAged && n > 0) {
+            if (numbered < 0 || numbered > q.c) {
+                if (tid == 0)
+                    flag_error(p.error_word, PA_DEVERR_CONTEXT_RANGE);
+                numbered = 0;
+            }
+            for (int i = numbered + tid; i < q.c; i += THREADS) {
+                const int at = slot_of(i);
+                if (at >= 0)
+                    p.arrivals[at] = (int)((uint32_t)i + (uint32_t)gone);
+            }
+            __syncthreads();
+            if (tid == 0) {
+                p.numbered_lens[s] = q.end;
+                p.evicted[s] = (int)((uint32_t)gone + (uint32_t)(q.c - q.end));
+            }
+        }
         // (by its bits: a comparison would take subnormal weights for 0)
         auto weight_key = [](float weight) {
             const int w = __float_as_int(weight);
             return w > 0 && w <= 0x7f800000 ? (uint32_t)w : 0u;
+        };
+        // (numbers of arrival are taken modulo 2^32: of the last num_recent a difference is
+        // below it)
+        const uint32_t oldest = (uint32_t)q.c + (uint32_t)gone - (uint32_t)p.num_recent;
+        auto token_key = [&](float weight, int number) {
+            return kAged && (uint32_t)number - oldest < (uint32_t)p.num_recent
+                       ? 0xffffffffu : weight_key(weight);
         };
         // keys of the candidates, and the weights below the new length in their places;
         // kPlanBatch tokens of a thread at a time
@@ -178,12 +218,15 @@ __global__ void __launch_bounds__(THREADS)
         for (int i0 = tid; i0 < reach; i0 += kPlanBatch * THREADS) {
             int at[kPlanBatch];
             float w[kPlanBatch];
+            int age[kPlanBatch];
 #pragma unroll
             for (int u = 0; u < kPlanBatch; ++u)
                 at[u] = slot_of(min(i0 + u * THREADS, reach - 1));
 #pragma unroll
-            for (int u = 0; u < kPlanBatch; ++u)
+            for (int u = 0; u < kPlanBatch; ++u) {
                 w[u] = at[u] >= 0 ? p.weights[at[u]] : 0.f;
+                age[u] = kAged && n > 0 && at[u] >= 0 ? p.arrivals[at[u]] : (int)oldest - 1;
+            }
 #pragma unroll
             for (int u = 0; u < kPlanBatch; ++u) {
                 const int i = i0 + u * THREADS;
@@ -192,17 +235,19 @@ __global__ void __launch_bounds__(THREADS)
                 if (apart && i < q.end && at[u] >= 0)
                     p.weights_out[at[u]] = w[u];
                 if (kKept && i >= first && i < first + n)
-                    keys[i - first] = weight_key(w[u]);
+                    keys[i - first] = token_key(w[u], age[u]);
             }
         }
         __syncthreads();
         if (n > 0) {
-            const int want = p.budget - p.num_sinks - p.num_recent;
+            const int want = p.budget - first - (kAged ? 0 : p.num_recent);
             auto key = [&](int i) {
                 if (kKept)
                     return keys[i];
                 const int at = slot_of(first + i);
-                return at >= 0 ? weight_key(p.weights[at]) : 0u;
+                if (at < 0)
+                    return 0u;
+                return token_key(p.weights[at], kAged ? p.arrivals[at] : 0);
             };
             const Threshold cut = top_threshold<THREADS, 11>(sh.topk, key, n, want);
             // a warp's run of them; the tokens that stay before each run
@@ -270,8 +315,11 @@ __global__ void __launch_bounds__(THREADS)
             __syncthreads();
             for (int i = tid; i < count; i += THREADS) {
                 const int src = moves[2 * i], dst = moves[2 * i + 1];
-                if (src >= 0 && src < slots && dst >= 0 && dst < slots)
+                if (src >= 0 && src < slots && dst >= 0 && dst < slots) {
                     p.weights_out[dst] = p.weights[src];
+                    if (kAged)
+                        p.arrivals[dst] = p.arrivals[src];
+                }
             }
         }
     }
@@ -361,18 +409,53 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas)
     }
 }
 
-} // namespace pa
+// ---- host side -------------------------------------------------------------------
 
-using namespace pa;
+template <bool kAged>
+static pa_status launch_plan(const PlanParams &p, cudaStream_t stream)
+{
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return record_cuda(e);
+    DeviceInfo info;
+    const pa_status st = device_info(dev, &info);
+    if (st != PA_OK)
+        return st;
+    const size_t blocks =
+        ((size_t)p.max_context_len + (((size_t)1 << p.block_shift) - 1)) >> p.block_shift;
+    const size_t smem =
+        ((size_t)p.max_context_len + std::min<size_t>((size_t)p.max_blocks_per_seq, blocks)) * 4;
+    if (smem + sizeof(PlanShared) + 1024 > (size_t)info.optin)
+        return launch_pdl(plan_eviction_kernel<1024, false, kAged>, dim3(p.num_seqs), dim3(1024), 0,
+                          stream, p);
+    const bool small = p.max_context_len <= kPlanShort;
+    auto kernel = small ? plan_eviction_kernel<256, true, kAged>
+                        : plan_eviction_kernel<1024, true, kAged>;
+    static size_t enabled[2][kMaxDevices];
+    static std::mutex mu;
+    {
+        std::lock_guard<std::mutex> lock(mu);
+        if (smem > enabled[small][dev]) {
+            const cudaError_t a = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (a != cudaSuccess)
+                return record_cuda(a);
+            enabled[small][dev] = smem;
+        }
+    }
+    return launch_pdl(kernel, dim3(p.num_seqs), dim3(small ? 256 : 1024), smem, stream, p);
+}
 
-extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *context_lens_out,
-                                      int32_t *free_count_out, float *weights_out,
-                                      const int32_t *block_tables, int max_blocks_per_seq,
-                                      const int32_t *context_lens, const float *weights,
-                                      int32_t *free_blocks, const int32_t *free_count,
-                                      int max_context_len, int limit, int budget, int num_sinks,
-                                      int num_recent, int num_seqs, int block_size,
-                                      int num_blocks, int32_t *error_word, void *stream)
+static pa_status run_plan(int32_t *moves, int max_moves, int32_t *context_lens_out,
+                          int32_t *free_count_out, float *weights_out,
+                          const int32_t *block_tables, int max_blocks_per_seq,
+                          const int32_t *context_lens, const float *weights,
+                          int32_t *free_blocks, const int32_t *free_count, int max_context_len,
+                          int limit, int budget, int num_sinks, int num_recent, int num_seqs,
+                          int block_size, int num_blocks, int32_t *arrivals,
+                          int32_t *numbered_lens, int32_t *evicted, int32_t *error_word,
+                          void *stream)
 {
     if (num_seqs < 0 || max_moves < 0 || max_blocks_per_seq <= 0 || block_size <= 0 ||
         num_blocks <= 0 || max_context_len < 0 || budget <= 0 || limit < budget ||
@@ -398,6 +481,9 @@ extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *co
     p.context_lens = context_lens;
     p.free_count = free_count;
     p.weights = weights;
+    p.arrivals = arrivals;
+    p.numbered_lens = numbered_lens;
+    p.evicted = evicted;
     p.error_word = error_word;
     p.max_moves = max_moves;
     p.max_blocks_per_seq = max_blocks_per_seq;
@@ -419,43 +505,48 @@ extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *co
                     !apart(free_count_out, 1, context_lens, num_seqs);
     cudaStream_t q = as_stream(stream);
     if (num_seqs > 0) {
-        int dev = 0;
-        const cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess)
-            return record_cuda(e);
-        DeviceInfo info;
-        pa_status st = device_info(dev, &info);
-        if (st != PA_OK)
-            return st;
-        const size_t smem = ((size_t)max_context_len +
-                             std::min<size_t>((size_t)max_blocks_per_seq,
-                                              ((size_t)max_context_len + block_size - 1) /
-                                                  block_size)) * 4;
-        if (smem + sizeof(PlanShared) + 1024 <= (size_t)info.optin) {
-            const bool small = max_context_len <= kPlanShort;
-            auto kernel = small ? plan_eviction_kernel<256, true> : plan_eviction_kernel<1024, true>;
-            static size_t enabled[2][kMaxDevices];
-            static std::mutex mu;
-            {
-                std::lock_guard<std::mutex> lock(mu);
-                if (smem > enabled[small][dev]) {
-                    const cudaError_t a = cudaFuncSetAttribute(
-                        kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-                    if (a != cudaSuccess)
-                        return record_cuda(a);
-                    enabled[small][dev] = smem;
-                }
-            }
-            st = launch_pdl(kernel, dim3(num_seqs), dim3(small ? 256 : 1024), smem, q, p);
-        } else {
-            st = launch_pdl(plan_eviction_kernel<1024, false>, dim3(num_seqs), dim3(1024), 0, q, p);
-        }
+        const pa_status st = arrivals != nullptr ? launch_plan<true>(p, q) : launch_plan<false>(p, q);
         if (st != PA_OK)
             return st;
     }
     if (!p.apply_later)
         return PA_OK;
     return launch_pdl(apply_eviction_kernel<1024>, dim3(1), dim3(1024), 0, q, p);
+}
+
+} // namespace pa
+
+using namespace pa;
+
+extern "C" pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *context_lens_out,
+                                      int32_t *free_count_out, float *weights_out,
+                                      const int32_t *block_tables, int max_blocks_per_seq,
+                                      const int32_t *context_lens, const float *weights,
+                                      int32_t *free_blocks, const int32_t *free_count,
+                                      int max_context_len, int limit, int budget, int num_sinks,
+                                      int num_recent, int num_seqs, int block_size,
+                                      int num_blocks, int32_t *error_word, void *stream)
+{
+    return run_plan(moves, max_moves, context_lens_out, free_count_out, weights_out, block_tables,
+                    max_blocks_per_seq, context_lens, weights, free_blocks, free_count,
+                    max_context_len, limit, budget, num_sinks, num_recent, num_seqs, block_size,
+                    num_blocks, nullptr, nullptr, nullptr, error_word, stream);
+}
+
+extern "C" pa_status pa_plan_eviction_aged(
+    int32_t *moves, int max_moves, int32_t *context_lens_out, int32_t *free_count_out,
+    float *weights_out, int32_t *arrivals, int32_t *numbered_lens, int32_t *evicted,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    const float *weights, int32_t *free_blocks, const int32_t *free_count, int max_context_len,
+    int limit, int budget, int num_sinks, int num_recent, int num_seqs, int block_size,
+    int num_blocks, int32_t *error_word, void *stream)
+{
+    if (num_seqs > 0 && (!arrivals || !numbered_lens || !evicted))
+        return PA_ERR_INVALID_ARG;
+    return run_plan(moves, max_moves, context_lens_out, free_count_out, weights_out, block_tables,
+                    max_blocks_per_seq, context_lens, weights, free_blocks, free_count,
+                    max_context_len, limit, budget, num_sinks, num_recent, num_seqs, block_size,
+                    num_blocks, arrivals, numbered_lens, evicted, error_word, stream);
 }
 
 extern "C" pa_status pa_move_tokens(void *key_cache, void *value_cache, const int32_t *moves,

@@ -53,6 +53,7 @@ struct Library {
     decltype(&pa_decode_attention_weights) weights;
     decltype(&pa_decode_attention_weights_fp8) weights_fp8;
     decltype(&pa_plan_eviction) plan;
+    decltype(&pa_plan_eviction_aged) plan_aged;
     decltype(&pa_move_tokens) move;
 };
 Library lib;
@@ -553,13 +554,19 @@ pa_status decode_sparse(PyObject *const *a)
                       x.num_blocks, scale, partition, w.at, w.bytes, x.dtype, err, stream);
 }
 
-// A pool of one weight a slot, [num_blocks, block_size].
-float *weight_pool(PyObject *o, const char *name, int num_blocks, int block_size, int dev)
+// A pool of one number a slot, [num_blocks, block_size].
+void *slot_pool(PyObject *o, const char *name, at::ScalarType type, int num_blocks, int block_size,
+                int dev)
 {
     const at::Tensor &w = tensor(o, name);
-    need(w.dim() == 2 && w.size(0) == num_blocks && w.size(1) == block_size,
-         "weights: [num_blocks, block_size] expected");
-    return static_cast<float *>(address(w, name, at::kFloat, dev));
+    if (w.dim() != 2 || w.size(0) != num_blocks || w.size(1) != block_size)
+        fail(PyExc_ValueError, "%s: [num_blocks, block_size] expected", name);
+    return address(w, name, type, dev);
+}
+
+float *weight_pool(PyObject *o, const char *name, int num_blocks, int block_size, int dev)
+{
+    return static_cast<float *>(slot_pool(o, name, at::kFloat, num_blocks, block_size, dev));
 }
 
 pa_status decode_weights(PyObject *const *a)
@@ -619,7 +626,18 @@ pa_status plan_eviction(PyObject *const *a)
               seqs = size_int(S, "block_tables");
     int32_t *err = optional_ints(a[14], "error_word", dev);
     void *stream = queue(a[15], dev);
+    int32_t *ages = nullptr, *numbered = nullptr, *gone = nullptr;
+    if (a[16] != Py_None || a[17] != Py_None || a[18] != Py_None) {
+        const at::Tensor &n = tensor(a[17], "numbered_lens"), &g = tensor(a[18], "evicted");
+        need(n.numel() == S && g.numel() == S, "numbered_lens, evicted: one per sequence expected");
+        ages = static_cast<int32_t *>(slot_pool(a[16], "arrivals", at::kInt, N, bs, dev));
+        numbered = ints(n, "numbered_lens", dev);
+        gone = ints(g, "evicted", dev);
+    }
     const Unlocked unlocked;
+    if (ages != nullptr)
+        return lib.plan_aged(pm, most, pco, pno, pw_out, ages, numbered, gone, pt, mb, pc, pw, ps,
+                             pn, max_ctx, limit, budget, sinks, recent, seqs, bs, N, err, stream);
     return lib.plan(pm, most, pco, pno, pw_out, pt, mb, pc, pw, ps, pn, max_ctx, limit, budget,
                     sinks, recent, seqs, bs, N, err, stream);
 }
@@ -686,6 +704,7 @@ PyObject *bind(PyObject *, PyObject *path)
         find(h, "pa_decode_attention_weights", found.weights);
         find(h, "pa_decode_attention_weights_fp8", found.weights_fp8);
         find(h, "pa_plan_eviction", found.plan);
+        find(h, "pa_plan_eviction_aged", found.plan_aged);
         find(h, "pa_move_tokens", found.move);
         lib = found;
         Py_RETURN_NONE;
@@ -707,7 +726,7 @@ PyMethodDef methods[] = {{"bind", bind, METH_O, nullptr},
                          PA_ENTRY(select_blocks, 13),
                          PA_ENTRY(decode_sparse, 15),
                          PA_ENTRY(decode_weights, 17),
-                         PA_ENTRY(plan_eviction, 16),
+                         PA_ENTRY(plan_eviction, 19),
                          PA_ENTRY(move_tokens, 5),
                          {nullptr, nullptr, 0, nullptr}};
 
