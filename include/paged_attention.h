@@ -740,12 +740,20 @@ PA_API pa_status pa_decode_attention_weights_fp8(
  *   max_context_len : (host) >= every context_lens[s]
  * budget >= 1, limit >= budget >= num_sinks + num_recent (PA_ERR_INVALID_ARG
  * otherwise).  A table entry outside [0, num_blocks) sets PA_DEVERR_BLOCK_RANGE; its
- * tokens have weight 0 and their moves are -1.  The plan is refused as a whole, with the
- * lengths, stack and weights as they were and every move -1, when a length is negative,
- * past max_context_len or past its table (PA_DEVERR_CONTEXT_RANGE), or the stack would
- * pass num_blocks or its count is negative (PA_DEVERR_BLOCK_RANGE).  Blocks are taken to
- * have one owner.  block_size: a power of two; max_moves <= 2^29.
+ * tokens have weight 0 and their moves are -1 (one that is given back goes on the stack as
+ * it is, as pa_build_step_maps').  The plan is refused as a whole, with the lengths, stack
+ * and weights as they were (context_lens_out and free_count_out get the inputs' values, a
+ * weights_out of its own is not written) and every move -1, when a length is negative, past
+ * max_context_len or past its table (PA_DEVERR_CONTEXT_RANGE), or the stack would pass
+ * num_blocks or its count is negative (PA_DEVERR_BLOCK_RANGE).  Blocks are taken to have
+ * one owner.  No other arrays may overlap.  block_size: a power of two; max_moves <= 2^29.
  * Bounds of the changed blocks: pa_summarize_blocks over whole contexts.
+ *
+ * A place in the cache is no longer a place in the text then.  The rotary position of a
+ * sequence's next token is token_pos (pa_build_step_maps) plus the tokens evicted from the
+ * sequence so far, the sum of its context_lens - context_lens_out; its weighted_lens
+ * (pa_decode_attention_weights) are at most context_lens_out; and windowed attention, whose
+ * window is one of places, does not fit it.
  *
  * The last num_recent are those that lie last.  A plan takes them to the places of evicted
  * tokens, so that they are also the newest only in a sequence that is evicted from for the
