@@ -356,11 +356,12 @@ constexpr int kSelWarp = 512;    // candidates of which one warp selects by itse
 constexpr int kSelCluster = 8;   // CTAs of a row and KV head, at most
 constexpr int kSelShare = 256;   // candidates of a CTA in a cluster, at least
 
-// Keys in the scores' order.
+// Keys in the scores' order.  -0 (a negative product beside a scale of 0) is +0: they are
+// equal scores, of which the lower block goes first.
 __device__ __forceinline__ uint32_t score_key(float x)
 {
     const uint32_t u = __float_as_uint(x);
-    return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+    return u == 0x80000000u ? u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
 // d[16 x 8] += a[16 x 32] b[32 x 8] on signed bytes, in 32 bits.
