@@ -1272,7 +1272,11 @@ static pa_status run_list(ListParams &prm, void *out, const void *query, const v
                 prm.share_min = (int)std::max<long long>(prm.share_min, (tiles + per - 1) / per);
             }
         }
-        if ((tiles + prm.share_min - 2) / prm.share_min + !prm.aligned > prm.merge_max)
+        // shares that the longest row is in: its own, or (n - 2) / W + 2 that begin anywhere
+        const long long longest = prm.aligned
+                                      ? (tiles + prm.share_min - 1) / prm.share_min
+                                      : (tiles + prm.share_min - 2) / prm.share_min + 1;
+        if (longest > prm.merge_max)
             prm.len_out = counts;
     }
     prm.max_context_len = (int)most;

@@ -1,4 +1,6 @@
 """Edges of the long-context operators."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -6,6 +8,7 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from test_gpu_block_selection import Bounds  # noqa: E402
+from test_gpu_sparse_decode import Case as Lists  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -35,3 +38,34 @@ def test_scores_of_either_zero_are_equal(B, ctx, rows, top_k):
     last = -(-ctx // 16) - 1
     assert got[0, 0].tolist() == [0] + list(range(10, 10 + top_k - 2)) + [last]
     assert (got == got[0]).all()
+
+
+def kernels_of(call):
+    """Launches of a call, as a captured graph holds them."""
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    n = ctypes.c_size_t()
+    status = ctypes.CDLL("libcuda.so.1").cuGraphGetNodes(
+        ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(n))
+    assert status == 0
+    return n.value
+
+
+@pytest.mark.parametrize("top_k,parts", [(4, 2), (6, 3), (8, 4), (9, 5), (10, 4), (11, 6)])
+def test_rows_of_more_than_four_partials_go_to_the_reduce_kernel(B, top_k, parts):
+    """Lists in shares of their own, of 2 tiles (10 tiles: of 3); a last tile by itself is a
+    share too."""
+    ctx = np.array([400, 333])
+    c = Lists(ctx, [0, 1], ctx - 1, 4, 1, 64, 16, top_k, torch.bfloat16, False, seed=top_k)
+    ws = c.workspace(B, 32)
+    args = [torch.as_tensor(np.asarray(a, dtype=np.int32)).cuda()
+            for a in (c.tables, c.seq, c.pos, c.chosen)]
+    call = lambda: B.pa_decode_attention_sparse(  # noqa: E731
+        c.out, c.q, c.kc, c.vc, *args, c.scale, 32, ws, error_word=c.err)
+    assert kernels_of(call) == (2 if parts > 4 else 1)
+    c.out.fill_(7.0)
+    c.run(B, 32, ws)
+    c.check()
