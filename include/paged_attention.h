@@ -746,7 +746,8 @@ PA_API pa_status pa_decode_attention_weights_fp8(
  * weights_out of its own is not written) and every move -1, when a length is negative, past
  * max_context_len or past its table (PA_DEVERR_CONTEXT_RANGE), or the stack would pass
  * num_blocks or its count is negative (PA_DEVERR_BLOCK_RANGE).  Blocks are taken to have
- * one owner.  No other arrays may overlap.  block_size: a power of two; max_moves <= 2^29.
+ * one owner.  No other arrays may overlap.  block_size: a power of two; max_moves <= 2^29;
+ * the lesser of max_context_len and max_blocks_per_seq * block_size <= 2^31 - 65,537.
  * Bounds of the changed blocks: pa_summarize_blocks over whole contexts.
  *
  * A place in the cache is no longer a place in the text then.  The rotary position of a

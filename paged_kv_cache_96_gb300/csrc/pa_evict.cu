@@ -69,6 +69,10 @@ __device__ __forceinline__ PlanSeq plan_seq(const PlanParams &p, int s)
 // short and barriers most of the time, else 1,024.
 constexpr int kPlanShort = 2048;
 constexpr int kPlanBatch = 4;
+// Longest context: places are counted in 32 bits, in steps of kPlanBatch tokens a thread
+// past its end.
+constexpr int kPlanLongest = INT32_MAX - 65536;
+static_assert(kPlanBatch * 1024 <= 65536, "a step past the longest context");
 
 struct PlanShared {
     TopkShared<11> topk;
@@ -469,7 +473,8 @@ static pa_status run_plan(int32_t *moves, int max_moves, int32_t *context_lens_o
                          !weights_out || (max_moves > 0 && !moves)))
         return PA_ERR_INVALID_ARG;
     if ((block_size & (block_size - 1)) != 0 || (long long)num_blocks * block_size > INT32_MAX ||
-        (long long)max_blocks_per_seq * block_size > INT32_MAX || max_moves > (1 << 29))
+        (long long)max_blocks_per_seq * block_size > INT32_MAX || max_moves > (1 << 29) ||
+        std::min(max_context_len, max_blocks_per_seq * block_size) > kPlanLongest)
         return PA_ERR_UNSUPPORTED;
     PlanParams p{};
     p.moves = moves;

@@ -34,6 +34,19 @@ def test_aged_plan_refuses(B):
         assert _plan(B, **kw) == B.PA_ERR_UNSUPPORTED, kw
 
 
+def test_contexts_whose_counting_would_pass_32_bits_are_refused(B):
+    """Places are counted in steps of up to 4,096 past the longest context."""
+    top = (1 << 31) - 1
+    for bs, mb in ((16, (1 << 27) - 1), (1, top), (1, top - 65535)):
+        big = dict(bs=bs, mb=mb, N=mb, maxctx=top)
+        assert _plan(B, **big) == B.PA_ERR_UNSUPPORTED, big
+        a = dict(moves=FAKE, M=50, co=FAKE, no=FAKE, wo=FAKE, bt=FAKE, mb=8, ctx=FAKE, w=FAKE,
+                 free=FAKE, cnt=FAKE, maxctx=128, limit=100, budget=50, sinks=4, recent=10, S=2,
+                 bs=16, N=8)
+        a.update(big)
+        assert B.lib().pa_plan_eviction(*a.values(), None, None) == B.PA_ERR_UNSUPPORTED, big
+
+
 def test_ages_are_keywords_of_the_plan(B):
     z = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
     w = torch.zeros((8, 16))
