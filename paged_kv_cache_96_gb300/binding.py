@@ -656,9 +656,9 @@ def pa_select_blocks(selected: torch.Tensor, query: torch.Tensor, summaries: tor
     [T, Hkv, top_k]: the first num_first and last num_last of its context and
     those with the largest score their summaries allow, ascending, then -1.
     token_seq / token_pos [T]: as pa_build_step_maps gives them (-1: padding)."""
-    status = _calls.select_blocks(selected, query, summaries, summary_scales, block_tables, token_seq,
-                           token_pos, max_context_len, block_size, num_first, num_last,
-                           error_word, stream)
+    status = _calls.select_blocks(selected, query, summaries, summary_scales, block_tables,
+                                  token_seq, token_pos, max_context_len, block_size, num_first,
+                                  num_last, error_word, stream)
     if status:
         raise PAError("pa_select_blocks", status)
 

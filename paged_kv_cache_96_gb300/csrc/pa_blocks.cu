@@ -72,7 +72,7 @@ struct SummaryParams {
 };
 
 constexpr int kSumThreads = 256;
-// Resident CTAs of an SM, which the grid fills once (5, with spilled registers: 159 us).
+// Resident CTAs of an SM, which the grid fills once (5, with spilled registers: 160 us).
 constexpr int kSumCtas = 4;
 constexpr int kSumSeqs = 2 * kSumThreads;  // sequences numbered at once
 
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas)
 //    they lie (the sum over d is in a permuted order, which whole numbers allow) and
 //    multiplied with the coded heads, kept in shared memory in the lanes' order.  Widened
 //    to fp16 the same products took as long (21.3 us for 128 decode rows and 33.0 for 24
-//    long ones, against 22.0 and 32.3) in twice the instructions: they are not the limit.
+//    long ones, against 22.0 and 32.3 now) in twice the instructions: they are not the limit.
 //  * Each CTA selects from its own candidates as many as are wanted of all, by one warp
 //    from its registers where they are few; the first CTA of a cluster selects from those
 //    lists, which come to its shared memory.
@@ -343,14 +343,14 @@ struct SelectParams {
     int num_heads, num_kv_heads, group, top_k, num_first, num_last;
 };
 
-// Threads of a CTA and CTAs that an SM holds.  Without clusters: 6 of 128 threads 21.2 us
-// for 128 decode rows, 4 of 256 22.1, 8 of 128 (which spill) 23.5; in clusters, whose
-// first CTA selects from more: 4 of 256 33 us for 24 rows of up to 4,096 blocks, 6 of
-// 128 39.
+// Threads of a CTA and CTAs that an SM holds.  Without clusters: 6 of 128 threads 22.0 us
+// for 128 decode rows, 4 of 256 21.5 (with the products in fp16 21.2 and 22.1), 8 of 128
+// (which spill) 22.8; in clusters, whose first CTA selects from more: 4 of 256 32.3 us for
+// 24 rows of up to 4,096 blocks, 6 of 128 37.8.
 __host__ __device__ constexpr int sel_threads(bool clusters) { return clusters ? 256 : 128; }
 __host__ __device__ constexpr int sel_resident(bool clusters) { return clusters ? 4 : 6; }
 // Shared memory of an SM in percent: the L1 takes the loads under way, and a larger share
-// than the CTAs need cuts them short (128 decode rows 35 us with all of it).
+// than the CTAs need cuts them short (128 decode rows 35 us with all of it, long ones 38).
 constexpr int kSelCarveout = 50;
 constexpr int kSelWarp = 512;    // candidates of which one warp selects by itself
 constexpr int kSelCluster = 8;   // CTAs of a row and KV head, at most
@@ -713,11 +713,12 @@ static pa_status launch_select(const SelectParams &p, int num_tokens, cudaStream
     auto bytes = [&](int ctas) {
         return select_bytes(((most + 15) / 16 + ctas - 1) / ctas * 16, ctas, want);
     };
-    // Clusters where the rows and KV heads leave SMs with fewer CTAs than they hold and contexts are long, or where one CTA's memory does not hold their keys.
+    // Clusters where the rows and KV heads leave SMs with fewer CTAs than they hold and
+    // contexts are long, or where one CTA's memory does not hold their keys.
     const long long units = (long long)num_tokens * p.num_kv_heads;
     int ctas = 1;
-    while (ctas < kSelCluster && units * ctas < sel_resident(true) * info.sms && most >= 2 * ctas * kSelShare &&
-           bytes(2 * ctas) <= room)
+    while (ctas < kSelCluster && units * ctas < sel_resident(true) * info.sms &&
+           most >= 2 * ctas * kSelShare && bytes(2 * ctas) <= room)
         ctas *= 2;
     while (ctas < kSelCluster && bytes(ctas) > room)
         ctas *= 2;

@@ -63,11 +63,12 @@ struct ListParams : DecodeParams {
 };
 
 // Rows of at most this many partials are merged by the pass, others by the reduce
-// kernel behind it (long contexts with weights, FP8: 135 us, up to 8 in the pass 138).
+// kernel behind it (long contexts with weights, FP8: 130.5 us, up to 8 in the pass 132.5).
 constexpr int kListMergeMax = 4;
 
 // Rows whose tiles are numbered for shares, at most: 4 bytes each in every CTA's shared
-// memory (as many CTAs fit an SM as without them up to about 1,900).
+// memory (as many CTAs fit an SM as without them up to about 1,600, which FP8 pools with a
+// head_dim of 128 set: 4 CTAs of 51 KB in 228, less 1 KB each).
 constexpr int kListShareRows = 8192;
 
 // m of a partial without a visible token, and of one whose scores are all -inf: the
@@ -160,9 +161,11 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
         prefetch_tensormap(&tmap_k);
         prefetch_tensormap(&tmap_v);
     }
-    // Listed blocks are read once, and need not stay in L2 (128 rows of 64 blocks 88.8 -> 85.6
-    // us, 16 FP8 lists 35.2 -> 32.9); with weights the hint costs more than the scores that
-    // stay there bring (307 -> 324 us).
+    // A row's listed blocks are read once, and need not stay in L2 (128 rows of 64 blocks 88.2
+    // -> 85.3 us, 16 FP8 lists 35.3 -> 32.9).  Where rows of a sequence list the same blocks
+    // they read them at about the same time, and the hint still pays (3 rows of 128 sequences
+    // with a list each sequence 153.1 -> 150.8, of 16 over FP8 pools 89.1 -> 87.6).  With
+    // weights it costs more than the scores that stay there bring (305 -> 324 us).
     const uint64_t once = kSparse ? policy_evict_first() : 0;
     auto load = [&](uint32_t dst, const void *map, uint32_t bar, int d, int kh, int row, int phys) {
         if constexpr (kSparse)
@@ -206,8 +209,9 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
     // Whole rows in turn (a unit: a row and KV head), or, where rows are split, equal
     // shares of all tiles, numbered through the rows: as many CTAs as there are KV heads
     // take one share, a head each, so that a token's heads, which lie side by side, are
-    // read at about the same time (shares numbered through the heads as well: long
-    // contexts over FP8 pools 191 us, so 138).  A unit is what one row has in the share.
+    // read at about the same time (when this came, long contexts with weights over FP8
+    // pools took 138 us, now 130.5; shares numbered through the heads as well took 191).  A
+    // unit is what one row has in the share.
     const bool share = p.share_min > 0;
     int W = 0;                          // tiles of a share
     int u_first = blockIdx.x, u_end = S * Hkv;
@@ -857,8 +861,8 @@ __global__ void __launch_bounds__(list_bound_threads(NW + 1, MINB), MINB)
             if (un < u_end)
                 named_barrier_arrive(kRecFree, kThreads);
             if (split && !by_kernel(x.nparts))
-                // (eight records loaded per lane at once: of two, long contexts over FP8 pools
-                // 138 us for 131)
+                // (eight records loaded per lane at once: of two, long contexts with weights
+                // over FP8 pools take 138.4 us for 130.5)
                 arrive_and_merge<T, D, kHeads, 8>(p, x.r, x.kh, x.nparts, lane);
             u = un;
         }
@@ -1004,8 +1008,8 @@ __global__ void __launch_bounds__(kWeightThreads)
 
 // Tile warps per CTA (the merge warp comes on top), ring stages per warp and CTAs per
 // SM the register budget is sized for: 16-bit pools, FP8 pools.  Windowed decode's 5 warps
-// of 2 stages, and 3 CTAs of 4 over FP8 pools, take 326 us for 311 (128 contexts with
-// weights) and 138 for 136 (long ones, FP8); 3 x 4 stages 339, 3 CTAs of 4 x 4 168.
+// of 2 stages, and 3 CTAs of 4 over FP8 pools, take 319 us for 305 (128 contexts with
+// weights) and 132.9 for 130.5 (long ones, FP8); 3 x 4 stages 333, 3 CTAs of 4 x 4 159.
 constexpr int kListWarps = 4, kListStages = 2, kListMinBlocks = 2;
 constexpr int kListWarpsFp8 = 3, kListStagesFp8 = 3, kListMinBlocksFp8 = 4;
 
@@ -1256,8 +1260,8 @@ static pa_status run_list(ListParams &prm, void *out, const void *query, const v
         if (kSparse) {
             // Lists are of one length, or shorter: with fewer of them than CTAs for a KV
             // head, each is cut into as many shares of its own as fill these (16 rows of
-            // 4,096 tokens, FP8: 39.0 us; shares across rows have a few partials more to
-            // merge, 42.3).
+            // 4,096 tokens, FP8: 32.9 us; shares across rows have a few partials more to
+            // merge, 35.8).
             DeviceInfo info;
             int dev = 0;
             const cudaError_t e = cudaGetDevice(&dev);

@@ -8,7 +8,8 @@ import torch
 pytestmark = pytest.mark.gpu
 
 from test_gpu_block_selection import Bounds  # noqa: E402
-from test_gpu_sparse_decode import Case as Lists  # noqa: E402
+from test_gpu_sparse_decode import IDS, TYPES, Case as Lists  # noqa: E402
+from test_gpu_weights_decode import SHAPES, Case as Weights  # noqa: E402
 
 
 @pytest.fixture(scope="module")
@@ -69,3 +70,23 @@ def test_rows_of_more_than_four_partials_go_to_the_reduce_kernel(B, top_k, parts
     c.out.fill_(7.0)
     c.run(B, 32, ws)
     c.check()
+
+
+@pytest.mark.parametrize("dtype,fp8", TYPES, ids=IDS)
+@pytest.mark.parametrize("H,K,D,bs,ctx", [x[:5] for x in SHAPES])
+def test_a_steps_weights_add_up_to_the_heads(B, dtype, fp8, H, K, D, bs, ctx):
+    """Each head's weights over a context have a sum of 1, however the scores are rounded:
+    what is counted is the sums' own error (a term for every second token of a lane, every
+    head and a few partials), that of three exponentials, and their arguments' for scores
+    of at most 32."""
+    c = Weights(ctx, np.zeros(len(ctx), dtype=int), H, K, D, bs, dtype, fp8, seed=H * D)
+    for P in (0, 16, 256):
+        c.weights_out.fill_(-5.0)
+        c.run(B, P)
+        assert int(c.err.item()) == 0
+        got = c.weights_out.double().cpu().numpy()
+        for s, n in enumerate(ctx):
+            p = np.arange(n)
+            tol = H * ((2 * -(-n // 16) + H + 16 + 128) * 2.0 ** -24 + 3 * 2.0 ** -21)
+            total = got[c.tables[s][p // bs], p % bs].sum()
+            assert abs(total - (H if n else 0)) <= tol, (s, n, P)
