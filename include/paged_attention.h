@@ -772,9 +772,9 @@ PA_API pa_status pa_plan_eviction(int32_t *moves, int max_moves, int32_t *contex
 
 /*
  * pa_plan_eviction_aged -- pa_plan_eviction for sequences that are evicted from again and
- * again: the last num_recent are, of the cached ones, those of the num_recent tokens that
- * arrived last, wherever earlier plans have moved them.  Of two tokens the one with the larger number of arrival is the newer; the
- * token that arrived k-th in its sequence, k = 0, 1, ..., has number k.
+ * again: the last num_recent are those of the num_recent tokens that arrived last that
+ * are cached, wherever earlier plans have moved them.  Tokens are numbered in the order
+ * of their arrival in the sequence, from 0 on.
  *   arrivals       : int32 [num_blocks][block_size] (in and out): numbers of arrival, in
  *                    the tokens' slots.  A plan that evicts from a sequence numbers its
  *                    tokens that have none and takes the numbers to their new places; the
